@@ -10,6 +10,10 @@
  *                                  position; rope or mrope mode; GPT-NeoX or GPT-J style
  *   rope_with_cos_sin_cache_v2     the same with the cacheMode argument (sectioned or
  *                                  interleaved mrope stitching)
+ *   rope_append_paged_cache        rotates a batch's new keys (and queries) by position and
+ *                                  appends keys and values to a paged cache
+ *   rope_latent_attention_paged    attention of those queries over the paged cache where keys and
+ *                                  values come from one latent row a token (absorbed form)
  *
  * Pages defining the operations:
  *   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码
@@ -194,6 +198,80 @@ int rope_with_cos_sin_cache_v2(const rope_tensor *positions, const rope_tensor *
                                int64_t head_size, int is_neox_style, int64_t cache_mode,
                                const rope_tensor *query_out, const rope_tensor *key_out,
                                void *stream);
+
+/*
+ * rope_append_paged_cache -- rotate by position, append to a paged cache.
+ *
+ * For token t with cos_sin_cache row [c | s] of positions[t] (split in halves as in
+ * rope_with_cos_sin_cache), every key head, and every query head if there is a query, has its
+ * elements [rot_start, rot_start + rotaryDim) rotated, rotaryDim = cache width:
+ *       o1 = x1*c - x2*s,  o2 = x2*c + x1*s
+ * with pairs (i, i + rotaryDim/2) of the slice for is_neox_style != 0 and (2i, 2i+1) otherwise;
+ * the rest of a head, and the value, are copied bit for bit.  Keys and values are written to
+ * row slots[t] % pageSize of page slots[t] / pageSize.
+ *
+ * positions      INT64 [T], any non-negative stride; out-of-range values are clamped as in
+ *                rope_with_cos_sin_cache.
+ * slots          INT64 [T], any non-negative stride.  A slot below 0 or beyond the last page's
+ *                last row is skipped (padding tokens; their queries are still rotated).  The
+ *                slots in range must be distinct -- a precondition that is not checked: a slot
+ *                given twice ends up with elements of either token.
+ * query          [T, Nq, Dq] or NULL, with query_out [T, Nq, Dq] (NULL exactly if query is).
+ * key            [T, Nk, D]; value [T, Nk, Dv] or NULL, with its cache NULL exactly if it is.
+ * cos_sin_cache  [maxSeqLen, rotaryDim], rotaryDim even and positive.
+ * key_cache      [pages, pageSize, Nk, D], value_cache [pages, pageSize, Nk, Dv].
+ * All floating-point tensors share one dtype, F32, F16 or BF16.  Every one may have any
+ * non-negative strides with unit inner stride (columns of one projection's output, caches that
+ * keep heads before rows, or keys and values in one allocation); 16-byte aligned rows, slices and
+ * widths take wide accesses.  query_out may be the query itself (same view).  Outputs whose
+ * strides reach an element twice, and any other overlap with an output, are refused
+ * (ROPE_ERR_PARAM_INVALID).  T = 0 is a no-op.
+ */
+int rope_append_paged_cache(const rope_tensor *positions, const rope_tensor *slots,
+                            const rope_tensor *query, const rope_tensor *key,
+                            const rope_tensor *value, const rope_tensor *cos_sin_cache,
+                            int64_t query_rot_start, int64_t key_rot_start, int is_neox_style,
+                            const rope_tensor *query_out, const rope_tensor *key_cache,
+                            const rope_tensor *value_cache, void *stream);
+
+/*
+ * rope_latent_attention_paged -- attention over a paged cache of latent rows, absorbed form.
+ *
+ * A cached token j of a sequence is one row c_j of latent_dim + 64 elements: a latent part and a
+ * rotated tail.  The row is the key, its latent part the value, of every head.  Query token i
+ * (of n, in a sequence of len cached tokens, its own n among them) sees rows j < len - n + 1 + i:
+ *       s_j = scale * <query[i, h], c_j>,   p = softmax_j(s),   out[i, h] = sum_j p_j c_j[0 : latent_dim]
+ *       lse[i, h] = log sum_j exp(s_j)
+ * Products accumulate in float32; maxima, sums and outputs are float32 until one rounding to the
+ * output's dtype; the weights p are rounded to the dtype for the second product.  A query that
+ * sees no row gets zeros and lse = -infinity.  What no query sees is never read into a result:
+ * rows past len may hold anything.
+ *
+ * query          [T, heads, latent_dim + 64], F16 or BF16, unit inner stride, rows on 16-byte
+ *                boundaries, any non-negative strides.
+ * latent_cache   [pages, pageSize, latent_dim + 64], same dtype, same rule for rows; any pageSize.
+ * page_table     INT64 [B, maxPages]: pages of each sequence, in order, any non-negative strides.
+ *                Entries in use must lie in [0, pages): not checked; others are clamped, so
+ *                that nothing outside the cache is read, and give meaningless results.
+ * seq_lens       INT64 [B]: cached tokens, clamped to [0, maxPages * pageSize].
+ * query_offsets  INT64 [B + 1], ascending: sequence b's queries are rows offsets[b] to
+ *                offsets[b+1] of query and out; rows outside all of them are left as they are.
+ *                Out-of-range values are clamped.  NULL: T / B queries each (T % B == 0).
+ * latent_dim     128, 256 or 512.     scale   finite.
+ * out            [T, heads, latent_dim] contiguous, 16-byte aligned; lse F32 [T, heads]
+ *                contiguous, or NULL.  Outputs may not overlap anything else.
+ * workspace      device memory of at least rope_latent_attention_paged_workspace() bytes, 16-byte
+ *                aligned, free for this call from its enqueueing to its end: calls that may run
+ *                at the same time need one each.  Its contents need not be initialised.
+ * Results do not depend on timing: every sum is taken in a fixed order.
+ */
+int64_t rope_latent_attention_paged_workspace(int64_t num_tokens, int64_t num_heads,
+                                              int64_t latent_dim, int64_t num_sequences);
+int rope_latent_attention_paged(const rope_tensor *query, const rope_tensor *latent_cache,
+                                const rope_tensor *page_table, const rope_tensor *seq_lens,
+                                const rope_tensor *query_offsets, int64_t latent_dim,
+                                double scale, const rope_tensor *out, const rope_tensor *lse,
+                                void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Text describing the last failing call on the calling thread ("" if none).  The pointer
  * stays valid until the next call on this thread. */

@@ -17,6 +17,11 @@ streams.  There is no fallback: if the library is not built this import fails.
   rope_with_cos_sin_cache(positions, query_in, key_in, cos_sin_cache, mrope_section,
                           head_size, is_neox_style, query_out=None, key_out=None, stream=None)
   rope_with_cos_sin_cache_v2(..., is_neox_style, cache_mode, query_out=None, ...)
+  rope_append_paged_cache(positions, slots, key, key_cache, cos_sin_cache, value=None,
+                          value_cache=None, query=None, query_out=None, query_rot_start=0,
+                          key_rot_start=0, is_neox_style=True, stream=None)
+  rope_latent_attention_paged(query, latent_cache, page_table, seq_lens, latent_dim, scale,
+                              query_offsets=None, out=None, lse=None, stream=None)
 
 Pages defining the operations:
   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码接口详解与实现剖析"
@@ -77,6 +82,16 @@ def _load() -> ctypes.CDLL:
                                                ctypes.c_int64, ctypes.c_int, ctypes.c_int64,
                                                P(RopeTensor), P(RopeTensor), ctypes.c_void_p]
     lib.rope_with_cos_sin_cache_v2.restype = ctypes.c_int
+    T = P(RopeTensor)
+    lib.rope_append_paged_cache.argtypes = [T, T, T, T, T, T, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_int, T, T, T, ctypes.c_void_p]
+    lib.rope_append_paged_cache.restype = ctypes.c_int
+    lib.rope_latent_attention_paged_workspace.argtypes = [ctypes.c_int64] * 4
+    lib.rope_latent_attention_paged_workspace.restype = ctypes.c_int64
+    lib.rope_latent_attention_paged.argtypes = [T, T, T, T, T, ctypes.c_int64, ctypes.c_double,
+                                                T, T, ctypes.c_void_p, ctypes.c_int64,
+                                                ctypes.c_void_p]
+    lib.rope_latent_attention_paged.restype = ctypes.c_int
     lib.rope_last_error.argtypes = []
     lib.rope_last_error.restype = ctypes.c_char_p
     return lib
@@ -99,14 +114,8 @@ def describe(t) -> RopeTensor:
     """A ``rope_tensor`` describing a torch tensor (which must outlive the call)."""
     if t.dim() > 4:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "tensors of more than 4 dims are not supported")
-    d = RopeTensor()
-    d.data = t.data_ptr() if t.numel() > 0 else None
-    d.dtype = _dtype_code(t)
-    d.ndim = t.dim()
-    for i in range(t.dim()):
-        d.shape[i] = t.shape[i]
-        d.stride[i] = t.stride(i)
-    return d
+    return RopeTensor(t.data_ptr() if t.numel() > 0 else None, _dtype_code(t), t.dim(),
+                      tuple(t.shape), t.stride())
 
 
 def _int_array(values):
@@ -299,6 +308,89 @@ def rope_with_cos_sin_cache_v2(positions, query_in, key_in, cos_sin_cache, mrope
     return _with_cos_sin_cache(positions, query_in, key_in, cos_sin_cache, mrope_section,
                                head_size, is_neox_style, int(cache_mode), query_out, key_out,
                                stream)
+
+
+# ---- paged cache and latent attention ---------------------------------------------------------
+
+def _describe_all(tensors):
+    """References to the descriptions of tensors (None stays None), and the descriptions."""
+    descs = [None if t is None else describe(t) for t in tensors]
+    return [None if d is None else ctypes.byref(d) for d in descs], descs
+
+
+def _allocating_on(stream, dev):
+    """Context in which torch allocates for work on `stream`: outputs and workspaces that a call
+    makes belong to the stream it runs on."""
+    import contextlib
+
+    import torch
+    if stream is None or dev is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = getattr(stream, "cuda_stream", stream)
+        if not handle:
+            return torch.cuda.stream(torch.cuda.default_stream(dev))
+        stream = torch.cuda.ExternalStream(handle, device=dev)
+    return torch.cuda.stream(stream)
+
+
+def rope_append_paged_cache(positions, slots, key, key_cache, cos_sin_cache, value=None,
+                            value_cache=None, query=None, query_out=None,
+                            query_rot_start: int = 0, key_rot_start: int = 0,
+                            is_neox_style: bool = True, stream=None):
+    """Rotate a batch's keys (and queries) by position and append keys and values to a paged
+    cache: key [T, Nk, D] and value [T, Nk, Dv] go to row slots[t] % pageSize of page
+    slots[t] // pageSize of key_cache [pages, pageSize, Nk, D] and value_cache
+    [pages, pageSize, Nk, Dv]; a slot out of range is skipped.  Elements
+    [rot_start, rot_start + rotaryDim) of every head are rotated, rotaryDim the width of
+    cos_sin_cache [maxSeqLen, rotaryDim].  Returns query_out [T, Nq, Dq] (allocated when not
+    given; it may be query itself), or None without a query."""
+    import torch
+    dev = _device_of([positions, slots, query, key, value, cos_sin_cache, query_out, key_cache,
+                      value_cache])
+    if query is not None and query_out is None:
+        with _allocating_on(stream, dev):
+            query_out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+    refs, _keep = _describe_all([positions, slots, query, key, value, cos_sin_cache, query_out,
+                                 key_cache, value_cache])
+    _check(_on_device(dev, LIB.rope_append_paged_cache,
+                      (*refs[:6], int(query_rot_start), int(key_rot_start),
+                       int(bool(is_neox_style)), *refs[6:], _stream_handle(stream, dev))))
+    return query_out
+
+
+def rope_latent_attention_paged(query, latent_cache, page_table, seq_lens, latent_dim: int,
+                                scale: float, query_offsets=None, out=None, lse=None,
+                                stream=None):
+    """Latent attention over a paged cache, absorbed form: query [T, heads, latent_dim + 64]
+    against latent_cache [pages, pageSize, latent_dim + 64] (or [pages, pageSize, 1, ...], as the
+    append fills it), whose rows are keys and, in their first latent_dim elements, values of every
+    head.  page_table [B, maxPages], seq_lens [B] (the queries' own tokens included) and
+    query_offsets [B + 1] are int64; without offsets every sequence has T / B queries.  Query i of
+    n sees the cached rows below seq_len - n + 1 + i.  Returns (out [T, heads, latent_dim],
+    lse [T, heads] float32)."""
+    import torch
+    dev = _device_of([query, latent_cache, page_table, seq_lens, query_offsets, out, lse])
+    if latent_cache.dim() == 4 and latent_cache.shape[2] == 1:
+        latent_cache = latent_cache.squeeze(2)
+    if query.dim() != 3 or seq_lens.dim() != 1:
+        raise RopeError(ROPE_ERR_PARAM_INVALID, "query must be 3-D and seq_lens 1-D")
+    T, heads = query.shape[0], query.shape[1]
+    need = LIB.rope_latent_attention_paged_workspace(T, heads, int(latent_dim), seq_lens.shape[0])
+    with _allocating_on(stream, dev):
+        if out is None:
+            out = torch.empty((T, heads, max(0, int(latent_dim))), dtype=query.dtype,
+                              device=query.device)
+        if lse is None:
+            lse = torch.empty((T, heads), dtype=torch.float32, device=query.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    refs, _keep = _describe_all([query, latent_cache, page_table, seq_lens, query_offsets, out,
+                                 lse])
+    _check(_on_device(dev, LIB.rope_latent_attention_paged,
+                      (*refs[:5], int(latent_dim), float(scale), *refs[5:],
+                       workspace.data_ptr() if need else None, need,
+                       _stream_handle(stream, dev))))
+    return out, lse
 
 
 class PreparedCall:

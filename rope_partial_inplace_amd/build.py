@@ -9,6 +9,7 @@ disabled (so the compiler never emits packed fp32 adds/multiplies).
 """
 from __future__ import annotations
 
+import concurrent.futures
 import hashlib
 import os
 import subprocess
@@ -20,11 +21,17 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "librope_amd.so")
 ARCH = "gfx950"
 
-SOURCES = [os.path.join(CSRC, "rope_plan.cpp"), os.path.join(CSRC, "rope_kernels.hip")]
+HOST_SOURCES = [os.path.join(CSRC, n) for n in
+                ("rope_plan.cpp", "rope_append_plan.cpp", "rope_latent_plan.cpp")]
+KERNEL_SOURCES = [os.path.join(CSRC, n) for n in
+                  ("rope_kernels.hip", "rope_append.hip", "rope_latent_paged.hip")]
+HEADERS = [os.path.join(CSRC, n) for n in
+           ("rope_plan.h", "rope_append_plan.h", "rope_latent_plan.h", "rope_check.h", "rope_io.h",
+            "rope_launch.h", "rope_mfma.h")]
+SOURCES = HOST_SOURCES + KERNEL_SOURCES
 # Everything the library is built from; its digest is written beside the library (STAMP_PATH)
 # so that a library older than its sources is noticed before it is tested.
-BUILD_INPUTS = SOURCES + [os.path.join(CSRC, "rope_plan.h"), os.path.join(INCLUDE, "rope.h"),
-                          os.path.abspath(__file__)]
+BUILD_INPUTS = SOURCES + HEADERS + [os.path.join(INCLUDE, "rope.h"), os.path.abspath(__file__)]
 STAMP_PATH = LIB_PATH + ".sources"
 
 HIPCC_FLAGS = [
@@ -42,20 +49,24 @@ def hipcc() -> str:
 
 
 def bundled_targets(path: str) -> list[str]:
-    """Target ids of the clang offload bundle embedded in a built library."""
+    """Target ids of the clang offload bundles embedded in a built library (one bundle for each
+    kernel source), each once."""
     import struct
     with open(path, "rb") as f:
         data = f.read()
+    out = []
     i = data.find(b"__CLANG_OFFLOAD_BUNDLE__")
-    if i < 0:
-        return []
-    n = struct.unpack_from("<Q", data, i + 24)[0]
-    off, out = i + 32, []
-    for _ in range(n):
-        _, _, idlen = struct.unpack_from("<QQQ", data, off)
-        off += 24
-        out.append(data[off:off + idlen].decode())
-        off += idlen
+    while i >= 0:
+        n = struct.unpack_from("<Q", data, i + 24)[0]
+        off = i + 32
+        for _ in range(n):
+            _, _, idlen = struct.unpack_from("<QQQ", data, off)
+            off += 24
+            name = data[off:off + idlen].decode()
+            off += idlen
+            if name not in out:
+                out.append(name)
+        i = data.find(b"__CLANG_OFFLOAD_BUNDLE__", off)
     return out
 
 
@@ -89,14 +100,18 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     device code in the result is for gfx950 only."""
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    plan_o = os.path.join(objdir, "rope_plan.o")
-    kern_o = os.path.join(objdir, "rope_kernels.o")
     tmp = LIB_PATH + ".tmp"
     inc = ["-I", INCLUDE, "-I", CSRC]
-    _run(["g++", *HOST_FLAGS, *inc, "-c", SOURCES[0], "-o", plan_o], verbose)
-    _run([hipcc(), *HIPCC_FLAGS, *(extra_flags or []), *inc, "-c", SOURCES[1], "-o", kern_o],
-         verbose)
-    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", kern_o, plan_o, "-o", tmp],
+
+    def obj(src):
+        return os.path.join(objdir, os.path.splitext(os.path.basename(src))[0] + ".o")
+
+    commands = [["g++", *HOST_FLAGS, *inc, "-c", src, "-o", obj(src)] for src in HOST_SOURCES]
+    commands += [[hipcc(), *HIPCC_FLAGS, *(extra_flags or []), *inc, "-c", src, "-o", obj(src)]
+                 for src in KERNEL_SOURCES]
+    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), commands))
+    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *map(obj, SOURCES), "-o", tmp],
          verbose)
     devices = [t for t in bundled_targets(tmp) if not t.startswith("host-")]
     if devices != [f"hipv4-amdgcn-amd-amdhsa--{ARCH}"]:

@@ -10,100 +10,11 @@
 #include <cstdint>
 #include <string>
 
+#include "rope_check.h"
 #include "rope_plan.h"
 
 namespace ropeamd {
 namespace {
-
-int bytes_of(rope_dtype dt) {
-  switch (dt) {
-    case ROPE_F32: return 4;
-    case ROPE_F16: return 2;
-    case ROPE_BF16: return 2;
-    case ROPE_I64: return 8;
-  }
-  return 0;
-}
-
-bool is_float(rope_dtype dt) { return dt == ROPE_F32 || dt == ROPE_F16 || dt == ROPE_BF16; }
-
-bool valid_rank(const rope_tensor *t) {
-  if (t->ndim < 1 || t->ndim > 4) return false;
-  for (int d = 0; d < t->ndim; ++d)
-    if (t->shape[d] < 0) return false;
-  return true;
-}
-
-// Elements of t (saturating at INT64_MAX instead of overflowing).
-int64_t count(const rope_tensor *t) {
-  int64_t n = 1;
-  for (int d = 0; d < t->ndim; ++d)
-    if (__builtin_mul_overflow(n, t->shape[d], &n)) return INT64_MAX;
-  return n;
-}
-
-// The element count and the offset of the furthest element are at most 2^53 (byte offsets of
-// elements of up to 8 bytes stay below 2^56, far beyond any device memory), computed without
-// overflow.  A descriptor outside that cannot describe real memory, and the planning
-// arithmetic on it would overflow.
-bool addressable(const rope_tensor *t) {
-  constexpr int64_t kLimit = int64_t(1) << 53;
-  int64_t n = 1, far = 0;
-  for (int d = 0; d < t->ndim; ++d) {
-    int64_t off;
-    if (__builtin_mul_overflow(n, t->shape[d], &n) || n > kLimit) return false;
-    if (t->shape[d] == 0) continue;
-    if (__builtin_mul_overflow(t->shape[d] - 1, t->stride[d], &off) || off < -kLimit ||
-        off > kLimit)
-      return false;
-    far += off < 0 ? -off : off;  // at most 4 * 2^53: no overflow
-    if (far >= kLimit) return false;
-  }
-  return true;
-}
-
-// Row-major contiguity; a dimension of size 1 may have any stride, and a view with no
-// elements has no layout to check (reading R12: an empty x is a successful no-op).
-bool row_major(const rope_tensor *t) {
-  if (count(t) == 0) return true;
-  int64_t want = 1;
-  for (int d = t->ndim - 1; d >= 0; --d) {
-    if (t->shape[d] > 1 && t->stride[d] != want) return false;
-    want *= t->shape[d];
-  }
-  return true;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int reject(std::string *err, int code, const char *why) {
-  if (err) *err = why;
-  return code;
-}
-
-// Bytes [first, last) an N-d view reaches (non-negative strides).
-void extent(const rope_tensor *t, uintptr_t *first, uintptr_t *last) {
-  int64_t far = 0;
-  for (int d = 0; d < t->ndim; ++d) far += (t->shape[d] - 1) * t->stride[d];
-  *first = reinterpret_cast<uintptr_t>(t->data);
-  *last = *first + uintptr_t((far + 1) * bytes_of(t->dtype));
-}
-
-bool overlap(const rope_tensor *a, const rope_tensor *b) {
-  uintptr_t a0, a1, b0, b1;
-  extent(a, &a0, &a1);
-  extent(b, &b0, &b1);
-  return a0 < b1 && b0 < a1;
-}
-
-bool identical_view(const rope_tensor *a, const rope_tensor *b) {
-  if (a->data != b->data || a->ndim != b->ndim || a->dtype != b->dtype) return false;
-  for (int d = 0; d < a->ndim; ++d) {
-    if (a->shape[d] != b->shape[d]) return false;
-    if (a->shape[d] > 1 && a->stride[d] != b->stride[d]) return false;
-  }
-  return true;
-}
 
 const int64_t kMropeLists[5][4] = {
     {16, 24, 24, 0}, {8, 12, 12, 0}, {24, 20, 20, 0}, {11, 11, 10, 0}, {16, 16, 16, 16}};
