@@ -14,6 +14,9 @@
  *                                  appends keys and values to a paged cache
  *   rope_latent_attention_paged    attention of those queries over the paged cache where keys and
  *                                  values come from one latent row a token (absorbed form)
+ *   rope_latent_attention          the expanded form, for prompts and training: a key and value
+ *                                  of every head and one rotated key part shared by the heads
+ *   rope_latent_attention_backward its gradients
  *
  * Pages defining the operations:
  *   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码
@@ -272,6 +275,52 @@ int rope_latent_attention_paged(const rope_tensor *query, const rope_tensor *lat
                                 const rope_tensor *query_offsets, int64_t latent_dim,
                                 double scale, const rope_tensor *out, const rope_tensor *lse,
                                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rope_latent_attention -- latent attention, expanded form.
+ *
+ * Head h of query token i (of n, in a sequence with m key tokens) attends to its sequence's keys:
+ *       s_ij = scale * (<query[i, h, 0 : dim], key[j, h]> + <query[i, h, dim : dim + 64], key_rope[j]>)
+ *       p = softmax_j(s),  out[i, h] = sum_j p_ij value[j, h],  lse[i, h] = log sum_j exp(s_ij)
+ * With causal != 0 query i sees keys j < m - n + 1 + i (the last query sees them all), else all.
+ * Precision as in rope_latent_attention_paged.  A query that sees no key gets zeros and
+ * lse = -infinity.  A NaN or infinity in a token reaches results of its own sequence only.
+ *
+ * query      [Tq, heads, dim + 64], key [Tk, heads, dim], key_rope [Tk, 64], value
+ *            [Tk, heads, dim]: F16 or BF16, one dtype, dim 64 or 128, unit inner stride, rows on
+ *            16-byte boundaries, any other non-negative strides (key and value may be the two
+ *            parts of one projection's rows).
+ * query_offsets, key_offsets   INT64 [B + 1] each, ascending: sequence b is query rows
+ *            query_offsets[b] to [b+1] and key rows key_offsets[b] to [b+1]; rows outside are
+ *            left as they are; out-of-range values are clamped.  Both NULL: num_sequences
+ *            sequences of Tq / B and Tk / B tokens.
+ * num_sequences   B; may be 0 when there are offsets.
+ * out        [Tq, heads, dim] contiguous, 16-byte aligned; lse F32 [Tq, heads] contiguous.
+ */
+int rope_latent_attention(const rope_tensor *query, const rope_tensor *key,
+                          const rope_tensor *key_rope, const rope_tensor *value,
+                          const rope_tensor *query_offsets, const rope_tensor *key_offsets,
+                          int64_t num_sequences, double scale, int causal, const rope_tensor *out,
+                          const rope_tensor *lse, void *stream);
+
+/*
+ * rope_latent_attention_backward -- gradients of rope_latent_attention with respect to query, key,
+ * key_rope (summed over the heads) and value, for the gradient `grad` [Tq, heads, dim] of out.
+ * out and lse are the forward call's.  Gradients are contiguous, 16-byte aligned, of their input's
+ * shape and dtype, each summed in float32 in a fixed order and rounded once (the probabilities and
+ * their gradients are rounded to the dtype between the products).  Rows outside all sequences get
+ * zero gradients.  workspace: at least rope_latent_attention_backward_workspace() bytes, under
+ * the rules of rope_latent_attention_paged's.
+ */
+int64_t rope_latent_attention_backward_workspace(int64_t query_tokens, int64_t key_tokens,
+                                                 int64_t num_heads);
+int rope_latent_attention_backward(
+    const rope_tensor *grad, const rope_tensor *query, const rope_tensor *key,
+    const rope_tensor *key_rope, const rope_tensor *value, const rope_tensor *out,
+    const rope_tensor *lse, const rope_tensor *query_offsets, const rope_tensor *key_offsets,
+    int64_t num_sequences, double scale, int causal, const rope_tensor *dquery,
+    const rope_tensor *dkey, const rope_tensor *dkey_rope, const rope_tensor *dvalue,
+    void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Text describing the last failing call on the calling thread ("" if none).  The pointer
  * stays valid until the next call on this thread. */

@@ -22,6 +22,12 @@ streams.  There is no fallback: if the library is not built this import fails.
                           key_rot_start=0, is_neox_style=True, stream=None)
   rope_latent_attention_paged(query, latent_cache, page_table, seq_lens, latent_dim, scale,
                               query_offsets=None, out=None, lse=None, stream=None)
+  rope_latent_attention(query, key, key_rope, value, scale, causal=True, num_sequences=None,
+                        query_offsets=None, key_offsets=None, out=None, lse=None, stream=None)
+  rope_latent_attention_backward(grad, query, key, key_rope, value, out, lse, scale, causal=True,
+                                 num_sequences=None, query_offsets=None, key_offsets=None,
+                                 stream=None)
+  latent_attention(query, key, key_rope, value, scale, ...)      (the same, with autograd)
 
 Pages defining the operations:
   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码接口详解与实现剖析"
@@ -92,6 +98,14 @@ def _load() -> ctypes.CDLL:
                                                 T, T, ctypes.c_void_p, ctypes.c_int64,
                                                 ctypes.c_void_p]
     lib.rope_latent_attention_paged.restype = ctypes.c_int
+    where = [T, T, ctypes.c_int64, ctypes.c_double, ctypes.c_int]  # offsets, B, scale, causal
+    lib.rope_latent_attention.argtypes = [T, T, T, T, *where, T, T, ctypes.c_void_p]
+    lib.rope_latent_attention.restype = ctypes.c_int
+    lib.rope_latent_attention_backward_workspace.argtypes = [ctypes.c_int64] * 3
+    lib.rope_latent_attention_backward_workspace.restype = ctypes.c_int64
+    lib.rope_latent_attention_backward.argtypes = [T] * 7 + where + [T] * 4 + [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+    lib.rope_latent_attention_backward.restype = ctypes.c_int
     lib.rope_last_error.argtypes = []
     lib.rope_last_error.restype = ctypes.c_char_p
     return lib
@@ -214,9 +228,11 @@ def _autograd_function():
     return InplacePartialRotaryMul
 
 
-def __getattr__(name):
-    if name == "InplacePartialRotaryMul":
-        fn = _autograd_function()
+def __getattr__(name):  # autograd functions are made on first use (torch is imported then)
+    make = {"InplacePartialRotaryMul": _autograd_function,
+            "LatentAttention": _latent_autograd_function}.get(name)
+    if make is not None:
+        fn = make()
         globals()[name] = fn
         return fn
     raise AttributeError(name)
@@ -391,6 +407,104 @@ def rope_latent_attention_paged(query, latent_cache, page_table, seq_lens, laten
                        workspace.data_ptr() if need else None, need,
                        _stream_handle(stream, dev))))
     return out, lse
+
+
+def _sequences(num_sequences, query_offsets):
+    """num_sequences of the C call: 1 by default, 0 where the offsets give it."""
+    if num_sequences is None:
+        return 1 if query_offsets is None else 0
+    return int(num_sequences)
+
+
+def rope_latent_attention(query, key, key_rope, value, scale: float, causal: bool = True,
+                          num_sequences: int | None = None, query_offsets=None, key_offsets=None,
+                          out=None, lse=None, stream=None):
+    """Latent attention, expanded form: query [Tq, heads, dim + 64] against key [Tk, heads, dim]
+    and, in the last 64 elements, key_rope [Tk, 64], which all heads share; value [Tk, heads, dim].
+    Sequences are packed one behind the other: int64 query_offsets and key_offsets [B + 1], or
+    num_sequences (1 by default) of equal length.  Causal: of n queries and m keys query i sees the
+    first m - n + 1 + i keys.  Returns (out [Tq, heads, dim], lse [Tq, heads] float32).  Not
+    recorded by autograd: that is latent_attention."""
+    import torch
+    dev = _device_of([query, key, key_rope, value, query_offsets, key_offsets, out, lse])
+    if query.dim() != 3 or value.dim() != 3:
+        raise RopeError(ROPE_ERR_PARAM_INVALID, "query and value must be 3-D")
+    with _allocating_on(stream, dev):
+        if out is None:
+            out = torch.empty((*query.shape[:2], value.shape[2]), dtype=query.dtype,
+                              device=query.device)
+        if lse is None:
+            lse = torch.empty(query.shape[:2], dtype=torch.float32, device=query.device)
+    refs, _keep = _describe_all([query, key, key_rope, value, query_offsets, key_offsets, out, lse])
+    _check(_on_device(dev, LIB.rope_latent_attention,
+                      (*refs[:6], _sequences(num_sequences, query_offsets), float(scale),
+                       int(bool(causal)), *refs[6:], _stream_handle(stream, dev))))
+    return out, lse
+
+
+def rope_latent_attention_backward(grad, query, key, key_rope, value, out, lse, scale: float,
+                                   causal: bool = True, num_sequences: int | None = None,
+                                   query_offsets=None, key_offsets=None, stream=None):
+    """Gradients of rope_latent_attention's out with respect to (query, key, key_rope, value), for
+    the gradient ``grad`` of out; out and lse are the forward call's."""
+    import torch
+    tensors = [grad, query, key, key_rope, value, out, lse, query_offsets, key_offsets]
+    dev = _device_of(tensors)
+    if query.dim() != 3:
+        raise RopeError(ROPE_ERR_PARAM_INVALID, "query must be 3-D")
+    need = LIB.rope_latent_attention_backward_workspace(query.shape[0], key.shape[0],
+                                                        query.shape[1])
+    with _allocating_on(stream, dev):
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                 for t in (query, key, key_rope, value)]
+        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    refs, _keep = _describe_all(tensors + grads)
+    _check(_on_device(dev, LIB.rope_latent_attention_backward,
+                      (*refs[:9], _sequences(num_sequences, query_offsets), float(scale),
+                       int(bool(causal)), *refs[9:], workspace.data_ptr() if need else None, need,
+                       _stream_handle(stream, dev))))
+    return tuple(grads)
+
+
+def _latent_autograd_function():
+    import torch
+
+    class LatentAttention(torch.autograd.Function):
+        """Autograd wrapper of the expanded form; rows outside all sequences are zero in the
+        output and in the gradients."""
+
+        @staticmethod
+        def forward(ctx, query, key, key_rope, value, scale, causal=True, num_sequences=None,
+                    query_offsets=None, key_offsets=None):
+            out = lse = None
+            if query_offsets is not None:
+                out = torch.zeros((*query.shape[:2], value.shape[2]), dtype=query.dtype,
+                                  device=query.device)
+            out, lse = rope_latent_attention(query, key, key_rope, value, scale, causal,
+                                             num_sequences, query_offsets, key_offsets, out=out)
+            ctx.save_for_backward(query, key, key_rope, value, out, lse, query_offsets,
+                                  key_offsets)
+            ctx.where = (scale, causal, num_sequences)
+            return out
+
+        @staticmethod
+        def backward(ctx, grad):
+            *saved, q_off, k_off = ctx.saved_tensors
+            if grad.stride(-1) != 1 or any(s * grad.element_size() % 16 for s in grad.stride()[:-1]):
+                grad = grad.contiguous()  # an expanded or transposed gradient
+            grads = rope_latent_attention_backward(grad, *saved, *ctx.where, q_off, k_off)
+            return (*grads, None, None, None, None, None)
+
+    return LatentAttention
+
+
+def latent_attention(query, key, key_rope, value, scale: float, causal: bool = True,
+                     num_sequences: int | None = None, query_offsets=None, key_offsets=None):
+    """rope_latent_attention with autograd: returns out [Tq, heads, dim]; query, key, key_rope and
+    value get gradients from the backward kernels."""
+    fn = globals().get("LatentAttention") or __getattr__("LatentAttention")
+    return fn.apply(query, key, key_rope, value, scale, causal, num_sequences, query_offsets,
+                    key_offsets)
 
 
 class PreparedCall:

@@ -24,7 +24,8 @@ ARCH = "gfx950"
 HOST_SOURCES = [os.path.join(CSRC, n) for n in
                 ("rope_plan.cpp", "rope_append_plan.cpp", "rope_latent_plan.cpp")]
 KERNEL_SOURCES = [os.path.join(CSRC, n) for n in
-                  ("rope_kernels.hip", "rope_append.hip", "rope_latent_paged.hip")]
+                  ("rope_kernels.hip", "rope_append.hip", "rope_latent_paged.hip",
+                   "rope_latent_attn.hip")]
 HEADERS = [os.path.join(CSRC, n) for n in
            ("rope_plan.h", "rope_append_plan.h", "rope_latent_plan.h", "rope_check.h", "rope_io.h",
             "rope_launch.h", "rope_mfma.h")]

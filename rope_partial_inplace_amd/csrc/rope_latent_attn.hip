@@ -1,0 +1,630 @@
+// rope_latent_attn.hip -- latent attention, expanded form, forward and gradients (gfx950).
+//
+// Head h of query token i attends to its sequence's tokens j, whose keys are an expanded part of
+// its own and a rotated part shared by all heads:
+//   s_ij = scale (<qn_ih, k_jh> + <qr_ih, r_j>),  p = softmax_j(s),  o_ih = sum_j p_ij v_jh
+// causal: the last query sees every key and each earlier one a key less.  With g the gradient of
+// o and D_ih = <g_ih, o_ih>:
+//   dv_jh = sum_i p_ij g_ih,   ds_ij = p_ij (<g_ih, v_jh> - D_ih)
+//   dq_ih = scale sum_j ds_ij [k_jh | r_j],  dk_jh = scale sum_i ds_ij qn_ih,
+//   dr_j  = scale sum_h sum_i ds_ij qr_ih
+//
+// All of it is matrix products (2 (2 dim + 64) operations a visible pair forward, 2.5 times that
+// backward with the probabilities computed again), bound by MFMA, by the LDS reads that feed it
+// and by the exponentials between the products.  The shared key part is read as it is, never
+// repeated for each head in memory.
+//
+// Forward, and dq: a workgroup is four wavefronts of 32 query rows of one head; 64 keys and
+// values at a time pass through LDS in two buffers.  dk and dv: four wavefronts of 32 keys, over
+// 64 query rows at a time.  dq and dk/dv are two kernels that both compute p again: seven
+// products where atomics on dq would need five, for sums in a fixed order.  Probabilities and ds
+// are rounded to the storage type between the products, as P is in the absorbed form.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "rope.h"
+#include "rope_latent_plan.h"
+#include "rope_launch.h"
+#include "rope_mfma.h"
+
+namespace ropeamd {
+namespace {
+
+constexpr int kBlockThreads = 256;
+constexpr int kRows = 128;  // query rows (or keys) of a workgroup
+constexpr int kTile = 64;   // keys (or query rows) in LDS at a time
+constexpr float kLog2eF = 1.44269504f, kLn2F = 0.693147180f;
+
+struct Span {
+  int32_t first, count;
+};
+
+// Tokens of sequence b; offsets are device data, so values out of range are clamped.
+__device__ inline Span span(const int64_t *off, int64_t stride, int64_t total, int64_t each,
+                            int32_t b) {
+  if (off == nullptr) return {int32_t(b * each), int32_t(each)};
+  const int64_t o0 = min(max(off[b * stride], int64_t(0)), total);
+  const int64_t o1 = min(max(off[(b + 1) * stride], o0), total);
+  return {int32_t(o0), int32_t(o1 - o0)};
+}
+
+__device__ inline int32_t wave_scan32(int32_t x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// The sequence and the tile within it that tile number `t` of all sequences' tiles is, by query
+// (or key) tokens; sequence -1: there are fewer tiles.
+struct TileAt {
+  int32_t seq, tile;
+};
+
+// `scratch`: six words of LDS, free again on return.
+template <bool QUERY>
+__device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scratch) {
+  const int64_t *off = QUERY ? p.q_off : p.k_off;
+  const int64_t each = QUERY ? p.q_each : p.k_each;
+  if (off == nullptr) {
+    const int32_t per = int32_t((each + kRows - 1) / kRows);
+    if (per == 0 || t / per >= p.B) return {-1, 0};
+    return {t / per, t % per};
+  }
+  int32_t *sums = static_cast<int32_t *>(scratch), *found = sums + 4;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  if (tid == 0) found[0] = -1;
+  int32_t before = 0;
+  for (int32_t b0 = 0; b0 < p.B; b0 += kBlockThreads) {
+    const int32_t b = b0 + tid;
+    int32_t n = 0;
+    if (b < p.B) {
+      const Span s = span(off, QUERY ? p.q_off_stride : p.k_off_stride, QUERY ? p.Tq : p.Tk, 0, b);
+      n = (s.count + kRows - 1) / kRows;
+    }
+    const int32_t incl = wave_scan32(n, lane);
+    if (lane == 63) sums[wave] = incl;
+    __syncthreads();
+    int32_t base = before;
+    for (int w = 0; w < wave; ++w) base += sums[w];
+    before += sums[0] + sums[1] + sums[2] + sums[3];
+    if (base + incl - n <= t && t < base + incl) {
+      found[0] = b;
+      found[1] = t - (base + incl - n);
+    }
+    __syncthreads();
+    if (t < before) break;  // the same for all threads
+  }
+  const TileAt at = {__builtin_amdgcn_readfirstlane(found[0]),
+                     __builtin_amdgcn_readfirstlane(found[1])};
+  __syncthreads();
+  return at;
+}
+
+// Workgroup number -> (head, tile): the workgroups of a head, which share its keys and values,
+// follow each other on one XCD, the longest (last) tiles first.
+__device__ inline bool head_and_tile(const ExpandedPlan &p, int64_t tiles, int32_t &head,
+                                     int32_t &tile) {
+  const int64_t total = int64_t(p.heads) * tiles;
+  const int64_t per = (total + kXcds - 1) / kXcds;
+  const int64_t at = int64_t(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (blockIdx.x / kXcds >= per || at >= total) return false;
+  head = int32_t(at / tiles);
+  tile = int32_t(tiles - 1 - at % tiles);
+  return true;
+}
+
+// Rows [row0, row0 + 64) of a strided matrix into LDS panels 0 .. PANELS - 1 (8 KB each), this
+// wavefront's quarter; rows past `last` repeat it.
+template <typename T, int PANELS>
+__device__ __forceinline__ void fetch_rows(const void *base, int64_t stride, int32_t row0,
+                                           int32_t last, int wave, int lane,
+                                           char *__restrict__ lds) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int rb = wave * 2 + i;
+    const int32_t row = min(row0 + 8 * rb + (lane >> 3), last);
+    const char *at = static_cast<const char *>(base) + int64_t(row) * stride * int64_t(sizeof(T)) +
+                     ((uint32_t(lane & 7) ^ chunk_key(uint32_t(lane >> 3))) << 4);
+#pragma unroll
+    for (int n = 0; n < PANELS; ++n) load_lds16(at + n * 128, lds + n * 8192 + rb * 1024);
+  }
+}
+
+// C (32 x 32) of 32 rows of LDS panels (from row `row0`) times register operands.
+template <typename T, int PANELS>
+__device__ __forceinline__ f32x16 row_product(const char *__restrict__ lds, int row0, int lane,
+                                              const s16x8 *b, f32x16 c) {
+#pragma unroll
+  for (int n = 0; n < PANELS; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const s16x8 a = as_operand(*reinterpret_cast<const uint4 *>(
+          lds + n * 8192 + panel_chunk(uint32_t(row0 + (lane & 31)), 2u * k + (uint32_t(lane) >> 5))));
+      c = Mfma<T>::mul(a, b[n * 4 + k], c);
+    }
+  return c;
+}
+
+// acc[d] += (32 columns d of 32 LDS rows from row0, transposed) times the 32 x 32 operand whose
+// two steps of 16 are b0, b1.
+template <typename T, int BLOCKS>
+__device__ __forceinline__ void column_product(const char *__restrict__ lds, int row0, int lane,
+                                               s16x8 b0, s16x8 b1, f32x16 *acc) {
+#pragma unroll
+  for (int d = 0; d < BLOCKS; ++d) {
+    const char *at = lds + (d / 2) * 8192 + row0 * 128 +
+                     panel_transposed(uint32_t(lane), uint32_t(d & 1));
+    acc[d] = Mfma<T>::mul(join(read_transposed(at), read_transposed(at + 1024)), b0, acc[d]);
+    acc[d] = Mfma<T>::mul(join(read_transposed(at + 2048), read_transposed(at + 3072)), b1, acc[d]);
+  }
+}
+
+// 16-byte pieces of a row as register operands: 8 (lane / 32) elements into every 16.
+template <int STEPS>
+__device__ __forceinline__ void load_operands(const char *row, bool live, int lane, s16x8 *f) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k)
+    f[k] = live ? as_operand(*reinterpret_cast<const uint4 *>(row + k * 32 + 16 * (lane >> 5)))
+                : s16x8{};
+}
+
+// Row of this lane's column, four consecutive elements at a time: scaled, rounded, stored.
+template <typename T, int BLOCKS>
+__device__ __forceinline__ void store_columns(char *row, const f32x16 *acc, float f, int lane) {
+#pragma unroll
+  for (int d = 0; d < BLOCKS; ++d)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint2 *>(row + (d * 8 + c * 2 + (lane >> 5)) * 8) =
+          make_uint2(Mfma<T>::pack(acc[d][4 * c] * f, acc[d][4 * c + 1] * f),
+                     Mfma<T>::pack(acc[d][4 * c + 2] * f, acc[d][4 * c + 3] * f));
+}
+
+// ---- forward ------------------------------------------------------------------------------
+
+template <typename T, int DIM>
+__global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(ExpandedPlan p) {
+  constexpr int NP = DIM / 64;             // panels of a key's own part, and of a value
+  constexpr int TILE = (2 * NP + 1) * 8192;  // keys, shared key part, values
+  __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
+  int32_t head, tile;
+  if (!head_and_tile(p, p.q_tiles, head, tile)) return;
+  const TileAt at = find_tile<true>(p, tile, tiles);
+  if (at.seq < 0) return;
+  const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
+  const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
+
+  const int tid = int(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t row = at.tile * kRows + wave * 32 + (lane & 31);
+  const bool live = row < q.count;
+  s16x8 qf[NP * 4 + 4];
+  load_operands<NP * 4 + 4>(static_cast<const char *>(p.q) +
+                                (int64_t(q.first + row) * p.q_tok + head * p.q_head) *
+                                    int64_t(sizeof(T)),
+                            live, lane, qf);
+  // keys a row sees, the fewest and the most of the workgroup's rows
+  const int32_t shift = k.count - q.count + 1;
+  const int32_t limit = !live ? 0 : p.causal ? row + shift : k.count;
+  const int32_t least = p.causal ? at.tile * kRows + shift : k.count;
+  const int32_t most =
+      p.causal ? min(min(at.tile * kRows + kRows, q.count) - 1 + shift, k.count) : k.count;
+
+  const int64_t es = sizeof(T);
+  const char *kb = static_cast<const char *>(p.k) + (int64_t(k.first) * p.k_tok + head * p.k_head) * es;
+  const char *rb = static_cast<const char *>(p.kr) + int64_t(k.first) * p.kr_tok * es;
+  const char *vb = static_cast<const char *>(p.v) + (int64_t(k.first) * p.v_tok + head * p.v_head) * es;
+  auto fetch = [&](int32_t j0, char *__restrict__ to) {
+    fetch_rows<T, NP>(kb, p.k_tok, j0, k.count - 1, wave, lane, to);
+    fetch_rows<T, 1>(rb, p.kr_tok, j0, k.count - 1, wave, lane, to + NP * 8192);
+    fetch_rows<T, NP>(vb, p.v_tok, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
+  };
+
+  float top = kNegInf, sum = 0.0f;
+  f32x16 acc[NP * 2];
+#pragma unroll
+  for (int d = 0; d < NP * 2; ++d) acc[d] = f32x16{};
+
+  auto step = [&](const char *__restrict__ cur, char *__restrict__ other, int32_t j0) {
+    if (j0 + kTile < most) fetch(j0 + kTile, other);
+    f32x16 s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      s[i] = row_product<T, NP + 1>(cur, i * 32, lane, qf, f32x16{});
+    const bool whole = j0 + kTile <= min(least, k.count);
+    float e[32], best = kNegInf;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      float x = s[r / 16][r % 16] * p.scale_log2;
+      if (!whole) x = j0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < limit ? x : kNegInf;
+      e[r] = x;
+      best = fmaxf(best, x);
+    }
+    best = fmaxf(best, other_half(best));
+    // rescale only when the maximum rises by more than 8 (weights of up to 2^8 are carried)
+    if (__any(best > top + 8.0f)) {
+      float f = 1.0f;
+      if (best > top + 8.0f) {
+        f = __builtin_amdgcn_exp2f(top - best);
+        top = best;
+      }
+      sum *= f;
+#pragma unroll
+      for (int d = 0; d < NP * 2; ++d) acc[d] *= f;
+    }
+    const float ref = top == kNegInf ? 0.0f : top;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      e[r] = __builtin_amdgcn_exp2f(e[r] - ref);
+      sum += e[r];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      column_product<T, NP * 2>(cur + (NP + 1) * 8192, i * 32, lane, round8<T>(e + 16 * i),
+                                round8<T>(e + 16 * i + 8), acc);
+  };
+
+  if (most > 0) fetch(0, tiles);
+  for (int32_t n = 0; n * kTile < most; ++n) {
+    wait_loads_all();
+    lds_barrier();
+    step(tiles + (n & 1) * TILE, tiles + (~n & 1) * TILE, n * kTile);
+  }
+  sum += other_half(sum);
+  if (!live) return;
+  const bool some = sum > 0.0f || sum != sum;  // a row that sees nothing gets zeros
+  const int64_t out_row = int64_t(q.first + row) * p.heads + head;
+  store_columns<T, NP * 2>(static_cast<char *>(p.out) + out_row * DIM * es, acc,
+                           some ? 1.0f / sum : 0.0f, lane);
+  if (lane < 32) p.lse[out_row] = some ? top * kLn2F + logf(sum) : kNegInf;
+}
+
+// ---- backward: D and dq -------------------------------------------------------------------
+
+template <typename T, int DIM>
+__global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(ExpandedPlan p) {
+  constexpr int NP = DIM / 64;
+  constexpr int TILE = (2 * NP + 1) * 8192;
+  __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
+  int32_t head, tile;
+  if (!head_and_tile(p, p.q_tiles, head, tile)) return;
+  const TileAt at = find_tile<true>(p, tile, tiles);
+  if (at.seq < 0) return;
+  const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
+  const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
+
+  const int tid = int(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t es = sizeof(T);
+  const int32_t row = at.tile * kRows + wave * 32 + (lane & 31);
+  const bool live = row < q.count;
+  const int64_t tok = q.first + row, out_row = tok * p.heads + head;
+  s16x8 qf[NP * 4 + 4], gf[NP * 4];
+  load_operands<NP * 4 + 4>(
+      static_cast<const char *>(p.q) + (tok * p.q_tok + head * p.q_head) * es, live, lane, qf);
+  load_operands<NP * 4>(
+      static_cast<const char *>(p.grad) + (tok * p.g_tok + head * p.g_head) * es, live, lane, gf);
+  float delta = 0.0f;
+  {
+    s16x8 of[NP * 4];
+    load_operands<NP * 4>(static_cast<const char *>(p.fwd_out) + out_row * DIM * es, live, lane, of);
+#pragma unroll
+    for (int i = 0; i < NP * 4; ++i) {
+      const uint4 a = __builtin_bit_cast(uint4, gf[i]), b = __builtin_bit_cast(uint4, of[i]);
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        delta += Mfma<T>::low(x[c]) * Mfma<T>::low(y[c]);
+        delta += Mfma<T>::high(x[c]) * Mfma<T>::high(y[c]);
+      }
+    }
+    delta += other_half(delta);
+  }
+  float lse2 = __builtin_huge_valf();  // rows that see nothing, or do not exist: p = 0
+  if (live) {
+    const float l = p.lse[out_row];
+    if (l != kNegInf) lse2 = l * kLog2eF;
+    if (lane < 32) p.delta[out_row] = delta;
+  }
+  const int32_t shift = k.count - q.count + 1;
+  const int32_t limit = !live ? 0 : p.causal ? row + shift : k.count;
+  const int32_t least = p.causal ? at.tile * kRows + shift : k.count;
+  const int32_t most =
+      p.causal ? min(min(at.tile * kRows + kRows, q.count) - 1 + shift, k.count) : k.count;
+
+  const char *kb = static_cast<const char *>(p.k) + (int64_t(k.first) * p.k_tok + head * p.k_head) * es;
+  const char *rb = static_cast<const char *>(p.kr) + int64_t(k.first) * p.kr_tok * es;
+  const char *vb = static_cast<const char *>(p.v) + (int64_t(k.first) * p.v_tok + head * p.v_head) * es;
+  auto fetch = [&](int32_t j0, char *__restrict__ to) {
+    fetch_rows<T, NP>(kb, p.k_tok, j0, k.count - 1, wave, lane, to);
+    fetch_rows<T, 1>(rb, p.kr_tok, j0, k.count - 1, wave, lane, to + NP * 8192);
+    fetch_rows<T, NP>(vb, p.v_tok, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
+  };
+  f32x16 acc[NP * 2 + 2];
+#pragma unroll
+  for (int d = 0; d < NP * 2 + 2; ++d) acc[d] = f32x16{};
+
+  auto step = [&](const char *__restrict__ cur, char *__restrict__ other, int32_t j0) {
+    if (j0 + kTile < most) fetch(j0 + kTile, other);
+    const bool whole = j0 + kTile <= min(least, k.count);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x16 s = row_product<T, NP + 1>(cur, i * 32, lane, qf, f32x16{});
+      const f32x16 dp = row_product<T, NP>(cur + (NP + 1) * 8192, i * 32, lane, gf, f32x16{});
+      float e[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float w = __builtin_amdgcn_exp2f(s[r] * p.scale_log2 - lse2);
+        if (!whole) w = j0 + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < limit ? w : 0.0f;
+        e[r] = w * (dp[r] - delta);
+      }
+      column_product<T, NP * 2 + 2>(cur, i * 32, lane, round8<T>(e), round8<T>(e + 8), acc);
+    }
+  };
+  if (most > 0) fetch(0, tiles);
+  for (int32_t n = 0; n * kTile < most; ++n) {
+    wait_loads_all();
+    lds_barrier();
+    step(tiles + (n & 1) * TILE, tiles + (~n & 1) * TILE, n * kTile);
+  }
+  if (live)
+    store_columns<T, NP * 2 + 2>(static_cast<char *>(p.dq) + out_row * (DIM + 64) * es, acc,
+                                 p.scale, lane);
+}
+
+// ---- backward: dk, dv and each head's share of the shared key part's gradient ---------------
+
+template <typename T, int DIM>
+__global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedPlan p) {
+  constexpr int NP = DIM / 64;
+  constexpr int TILE = (2 * NP + 1) * 8192;  // queries (own part, shared part), gradients
+  __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
+  __shared__ __attribute__((aligned(16))) float stats[2][2][kTile];  // lse * log2(e), D
+  int32_t head, tile;
+  if (!head_and_tile(p, p.k_tiles, head, tile)) return;
+  // the first keys are seen by the most queries: those tiles first
+  tile = int32_t(p.k_tiles - 1 - tile);
+  const TileAt at = find_tile<false>(p, tile, tiles);
+  if (at.seq < 0) return;
+  const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
+  const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
+
+  const int tid = int(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t es = sizeof(T);
+  const int32_t key = at.tile * kRows + wave * 32 + (lane & 31);
+  const bool live = key < k.count;
+  const int64_t tok = k.first + key;
+  s16x8 kf[NP * 4 + 4], vf[NP * 4];
+  load_operands<NP * 4>(static_cast<const char *>(p.k) + (tok * p.k_tok + head * p.k_head) * es,
+                        live, lane, kf);
+  load_operands<4>(static_cast<const char *>(p.kr) + tok * p.kr_tok * es, live, lane, kf + NP * 4);
+  load_operands<NP * 4>(static_cast<const char *>(p.v) + (tok * p.v_tok + head * p.v_head) * es,
+                        live, lane, vf);
+  // query i sees key j if j < i + shift; i0: the first 64-row tile with a row that sees one
+  const int32_t shift = k.count - q.count + 1;
+  const int32_t first_i = p.causal ? max(0, at.tile * kRows - shift + 1) : 0;
+  const int32_t n0 = first_i / kTile;
+  const int32_t last_key = min(at.tile * kRows + kRows, k.count) - 1;
+
+  const char *qb = static_cast<const char *>(p.q) + (int64_t(q.first) * p.q_tok + head * p.q_head) * es;
+  const char *gb = static_cast<const char *>(p.grad) + (int64_t(q.first) * p.g_tok + head * p.g_head) * es;
+  const float *lse = p.lse + int64_t(q.first) * p.heads + head;
+  const float *del = p.delta + int64_t(q.first) * p.heads + head;
+  // the statistics of a tile's rows: read by the first wavefront, one row a lane
+  float next_lse = 0.0f, next_delta = 0.0f;
+  auto fetch = [&](int32_t i0, char *__restrict__ to) {
+    fetch_rows<T, NP + 1>(qb, p.q_tok, i0, q.count - 1, wave, lane, to);
+    fetch_rows<T, NP>(gb, p.g_tok, i0, q.count - 1, wave, lane, to + (NP + 1) * 8192);
+  };
+  auto fetch_stats = [&](int32_t i0) {
+    if (wave == 0) {
+      const int32_t i = i0 + lane;
+      next_lse = i < q.count ? lse[int64_t(i) * p.heads] : kNegInf;
+      next_delta = i < q.count ? del[int64_t(i) * p.heads] : 0.0f;
+    }
+  };
+  auto put_stats = [&](int slot) {
+    if (wave == 0) {  // rows that see nothing, or do not exist: p = exp2(s - infinity) = 0
+      stats[slot][0][lane] = next_lse == kNegInf ? __builtin_huge_valf() : next_lse * kLog2eF;
+      stats[slot][1][lane] = next_delta;
+    }
+  };
+  f32x16 dk[NP * 2 + 2], dv[NP * 2];
+#pragma unroll
+  for (int d = 0; d < NP * 2 + 2; ++d) dk[d] = f32x16{};
+#pragma unroll
+  for (int d = 0; d < NP * 2; ++d) dv[d] = f32x16{};
+
+  auto step = [&](const char *__restrict__ cur, char *__restrict__ other, const float *st,
+                  int32_t i0) {
+    if (i0 + kTile < q.count) fetch(i0 + kTile, other);
+    const bool whole = !p.causal || last_key < i0 + shift;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x16 s = row_product<T, NP + 1>(cur, i * 32, lane, kf, f32x16{});
+      const f32x16 dp = row_product<T, NP>(cur + (NP + 1) * 8192, i * 32, lane, vf, f32x16{});
+      float w[16], e[16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int at_row = i * 32 + 8 * c + 4 * (lane >> 5);
+        const f32x4 l = *reinterpret_cast<const f32x4 *>(st + at_row);
+        const f32x4 d = *reinterpret_cast<const f32x4 *>(st + kTile + at_row);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = __builtin_amdgcn_exp2f(s[4 * c + r] * p.scale_log2 - l[r]);
+          if (!whole) x = key < i0 + at_row + r + shift ? x : 0.0f;
+          w[4 * c + r] = x;
+          e[4 * c + r] = x * (dp[4 * c + r] - d[r]);
+        }
+      }
+      column_product<T, NP * 2>(cur + (NP + 1) * 8192, i * 32, lane, round8<T>(w), round8<T>(w + 8),
+                                dv);
+      column_product<T, NP * 2 + 2>(cur, i * 32, lane, round8<T>(e), round8<T>(e + 8), dk);
+    }
+  };
+  if (n0 * kTile < q.count) {
+    fetch_stats(n0 * kTile);
+    fetch(n0 * kTile, tiles);
+  }
+  for (int32_t n = n0; n * kTile < q.count; ++n) {
+    const int slot = (n - n0) & 1;
+    wait_loads_all();
+    put_stats(slot);
+    lds_barrier();
+    if ((n + 1) * kTile < q.count) fetch_stats((n + 1) * kTile);
+    step(tiles + slot * TILE, tiles + (slot ^ 1) * TILE, &stats[slot][0][0], n * kTile);
+  }
+  if (!live) return;
+  const int64_t out_row = tok * p.heads + head;
+  store_columns<T, NP * 2>(static_cast<char *>(p.dv) + out_row * DIM * es, dv, 1.0f, lane);
+  store_columns<T, NP * 2>(static_cast<char *>(p.dk) + out_row * DIM * es, dk, p.scale, lane);
+  float *part = p.dkr_part + (int64_t(head) * p.Tk + tok) * 64;
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const f32x16 &a = dk[NP * 2 + d];
+      *reinterpret_cast<float4 *>(part + (d * 8 + c * 2 + (lane >> 5)) * 4) =
+          make_float4(a[4 * c] * p.scale, a[4 * c + 1] * p.scale, a[4 * c + 2] * p.scale,
+                      a[4 * c + 3] * p.scale);
+    }
+}
+
+// The shared key part's gradient: the heads' shares added in order.  One thread for four
+// elements of a token.  Tokens outside all sequences get zero gradients, here and (rows of
+// dq, dk, dv) by the threads beyond.
+template <typename T>
+__global__ __launch_bounds__(kBlockThreads) void latent_dshared_kernel(ExpandedPlan p) {
+  const int64_t i = int64_t(blockIdx.x) * kBlockThreads + threadIdx.x;
+  const int64_t es = sizeof(T);
+  const int64_t row = i / 16;
+  const bool key = row < p.Tk;
+  const int64_t tok = key ? row : row - p.Tk;
+  if (!key && tok >= p.Tq) return;
+  const int64_t *off = key ? p.k_off : p.q_off;
+  bool inside = true;
+  if (off != nullptr) {
+    const int64_t stride = key ? p.k_off_stride : p.q_off_stride;
+    inside = tok >= off[0] && tok < off[p.B * stride];
+  }
+  if (!key) {
+    if (inside) return;
+    const int64_t n = int64_t(p.heads) * (p.dim + 64) * es / 16;
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<char *>(p.dq) + tok * n * 16);
+    for (int64_t j = i % 16; j < n; j += 16) to[j] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (inside) {
+    const float *part = p.dkr_part + tok * 64 + (i % 16) * 4;
+#pragma unroll 4
+    for (int32_t h = 0; h < p.heads; ++h) {
+      const float4 x = *reinterpret_cast<const float4 *>(part + int64_t(h) * p.Tk * 64);
+      t.x += x.x;
+      t.y += x.y;
+      t.z += x.z;
+      t.w += x.w;
+    }
+  } else {
+    const int64_t n = int64_t(p.heads) * p.dim * es / 16;
+    for (void *out : {p.dk, p.dv}) {
+      uint4 *to = reinterpret_cast<uint4 *>(static_cast<char *>(out) + tok * n * 16);
+      for (int64_t j = i % 16; j < n; j += 16) to[j] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  *reinterpret_cast<uint2 *>(static_cast<char *>(p.dkr) + (tok * 64 + (i % 16) * 4) * es) =
+      make_uint2(Mfma<T>::pack(t.x, t.y), Mfma<T>::pack(t.z, t.w));
+}
+
+// ---- launches -------------------------------------------------------------------------------
+
+uint32_t head_grid(int64_t heads, int64_t tiles) {
+  return uint32_t((heads * tiles + kXcds - 1) / kXcds * kXcds);
+}
+
+template <typename T, int DIM>
+int run_forward(ExpandedPlan &p, void *stream) {
+  return launch_kernel(reinterpret_cast<const void *>(&latent_forward_kernel<T, DIM>),
+                       dim3(head_grid(p.heads, p.q_tiles)), kBlockThreads, 0, stream, &p);
+}
+
+template <typename T, int DIM>
+int run_backward(ExpandedPlan &p, void *stream) {
+  int st = ROPE_OK;
+  if (p.q_tiles > 0)
+    st = launch_kernel(reinterpret_cast<const void *>(&latent_dquery_kernel<T, DIM>),
+                       dim3(head_grid(p.heads, p.q_tiles)), kBlockThreads, 0, stream, &p);
+  if (st == ROPE_OK && p.k_tiles > 0)
+    st = launch_kernel(reinterpret_cast<const void *>(&latent_dkey_kernel<T, DIM>),
+                       dim3(head_grid(p.heads, p.k_tiles)), kBlockThreads, 0, stream, &p);
+  if (st != ROPE_OK) return st;
+  const int64_t threads = (p.Tk + (p.q_off != nullptr ? p.Tq : 0)) * 16;
+  if (threads == 0) return ROPE_OK;
+  return launch_kernel(reinterpret_cast<const void *>(&latent_dshared_kernel<T>),
+                       dim3(uint32_t((threads + kBlockThreads - 1) / kBlockThreads)), kBlockThreads,
+                       0, stream, &p);
+}
+
+}  // namespace
+}  // namespace ropeamd
+
+using namespace ropeamd;
+
+ROPE_API int rope_latent_attention(const rope_tensor *query, const rope_tensor *key,
+                                   const rope_tensor *key_rope, const rope_tensor *value,
+                                   const rope_tensor *query_offsets,
+                                   const rope_tensor *key_offsets, int64_t num_sequences,
+                                   double scale, int causal, const rope_tensor *out,
+                                   const rope_tensor *lse, void *stream) {
+  ExpandedPlan plan;
+  std::string err;
+  const int st = plan_expanded(query, key, key_rope, value, query_offsets, key_offsets,
+                               num_sequences, scale, causal, out, lse, &plan, &err);
+  if (st != ROPE_OK) {
+    g_last_error = err;
+    return st;
+  }
+  g_last_error.clear();
+  if (plan.noop) return ROPE_OK;
+  if (plan.dt == ROPE_F16)
+    return plan.dim == 128 ? run_forward<_Float16, 128>(plan, stream)
+                           : run_forward<_Float16, 64>(plan, stream);
+  return plan.dim == 128 ? run_forward<__bf16, 128>(plan, stream)
+                         : run_forward<__bf16, 64>(plan, stream);
+}
+
+ROPE_API int64_t rope_latent_attention_backward_workspace(int64_t query_tokens, int64_t key_tokens,
+                                                          int64_t num_heads) {
+  return expanded_workspace(query_tokens, key_tokens, num_heads);
+}
+
+ROPE_API int rope_latent_attention_backward(
+    const rope_tensor *grad, const rope_tensor *query, const rope_tensor *key,
+    const rope_tensor *key_rope, const rope_tensor *value, const rope_tensor *out,
+    const rope_tensor *lse, const rope_tensor *query_offsets, const rope_tensor *key_offsets,
+    int64_t num_sequences, double scale, int causal, const rope_tensor *dquery,
+    const rope_tensor *dkey, const rope_tensor *dkey_rope, const rope_tensor *dvalue,
+    void *workspace, int64_t workspace_bytes, void *stream) {
+  ExpandedPlan plan;
+  std::string err;
+  const int st = plan_expanded_backward(grad, query, key, key_rope, value, out, lse, query_offsets,
+                                        key_offsets, num_sequences, scale, causal, dquery, dkey,
+                                        dkey_rope, dvalue, workspace, workspace_bytes, &plan, &err);
+  if (st != ROPE_OK) {
+    g_last_error = err;
+    return st;
+  }
+  g_last_error.clear();
+  if (plan.noop) return ROPE_OK;
+  if (plan.dt == ROPE_F16)
+    return plan.dim == 128 ? run_backward<_Float16, 128>(plan, stream)
+                           : run_backward<_Float16, 64>(plan, stream);
+  return plan.dim == 128 ? run_backward<__bf16, 128>(plan, stream)
+                         : run_backward<__bf16, 64>(plan, stream);
+}

@@ -188,4 +188,188 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
   return ROPE_OK;
 }
 
+// ---- expanded form --------------------------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kExpandedRows = 128;  // query rows (or keys) of a workgroup
+
+int64_t tiles_bound(int64_t tokens, int64_t sequences, int64_t each, bool offsets) {
+  return offsets ? tokens / kExpandedRows + sequences
+                 : sequences * ((each + kExpandedRows - 1) / kExpandedRows);
+}
+
+}  // namespace
+
+int64_t expanded_workspace(int64_t query_tokens, int64_t key_tokens, int64_t heads) {
+  if (query_tokens < 0 || key_tokens < 0 || heads <= 0) return 0;
+  return up(query_tokens * heads * 4, 256) + key_tokens * heads * kLatentRope * 4;
+}
+
+int plan_expanded(const rope_tensor *query, const rope_tensor *key, const rope_tensor *key_rope,
+                  const rope_tensor *value, const rope_tensor *query_offsets,
+                  const rope_tensor *key_offsets, int64_t num_sequences, double scale, int causal,
+                  const rope_tensor *out, const rope_tensor *lse, ExpandedPlan *plan,
+                  std::string *err) {
+  *plan = ExpandedPlan();
+  for (const rope_tensor *t : {query, key, key_rope, value, out, lse})
+    if (t == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "a tensor argument is NULL");
+  if ((query_offsets == nullptr) != (key_offsets == nullptr))
+    return reject(err, ROPE_ERR_PARAM_NULLPTR, "query_offsets and key_offsets come together");
+  const int st =
+      common_checks({query, key, key_rope, value, query_offsets, key_offsets, out, lse}, err);
+  if (st != ROPE_OK) return st;
+  const rope_dtype dt = query->dtype;
+  if (!half_precision(dt))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "query must be float16 or bfloat16");
+  for (const rope_tensor *t : {key, key_rope, value, out})
+    if (t->dtype != dt)
+      return reject(err, ROPE_ERR_PARAM_INVALID, "key, value and out must share query's dtype");
+  if (lse->dtype != ROPE_F32) return reject(err, ROPE_ERR_PARAM_INVALID, "lse must be float32");
+  for (const rope_tensor *t : {query_offsets, key_offsets})
+    if (t != nullptr && !is_i64_vector(t))
+      return reject(err, ROPE_ERR_PARAM_INVALID, "offsets must be int64 [B + 1]");
+  if (query->ndim != 3 || key->ndim != 3 || key_rope->ndim != 2 || value->ndim != 3 ||
+      out->ndim != 3 || lse->ndim != 2)
+    return reject(err, ROPE_ERR_PARAM_INVALID,
+                  "query, key, value and out must be 3-D, key_rope and lse 2-D");
+  const int64_t Tq = query->shape[0], H = query->shape[1], Tk = key->shape[0];
+  const int64_t dim = key->shape[2];
+  if (dim != 64 && dim != 128)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "key heads must be 64 or 128 wide");
+  if (query->shape[2] != dim + kLatentRope || key_rope->shape[1] != kLatentRope ||
+      value->shape[2] != dim)
+    return reject(err, ROPE_ERR_PARAM_INVALID,
+                  "widths: query key + 64, key_rope 64, value that of key");
+  if (key->shape[1] != H || value->shape[1] != H || key_rope->shape[0] != Tk ||
+      value->shape[0] != Tk)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "heads or key tokens differ");
+  if (out->shape[0] != Tq || out->shape[1] != H || out->shape[2] != dim || lse->shape[0] != Tq ||
+      lse->shape[1] != H)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "out must be [Tq, heads, dim], lse [Tq, heads]");
+  int64_t B = num_sequences;
+  if (query_offsets != nullptr) {
+    B = query_offsets->shape[0] - 1;
+    if (B < 0 || key_offsets->shape[0] != B + 1 || (num_sequences != 0 && num_sequences != B))
+      return reject(err, ROPE_ERR_PARAM_INVALID,
+                    "offsets must be [B + 1] each, num_sequences B or 0 with them");
+  } else if (B < 1 || Tq % B != 0 || Tk % B != 0) {
+    return reject(err, ROPE_ERR_PARAM_INVALID,
+                  "without offsets num_sequences must divide both token counts");
+  }
+  if (!std::isfinite(scale)) return reject(err, ROPE_ERR_PARAM_INVALID, "scale must be finite");
+  if (Tq >= kIndexLimit || Tk >= kIndexLimit || H >= kIndexLimit || B >= kIndexLimit)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "too many tokens, heads or sequences");
+  for (const rope_tensor *t : {query, key, key_rope, value})
+    if (!unit_inner(t) || !rows_aligned16(t))
+      return reject(err, ROPE_ERR_PARAM_INVALID,
+                    "rows need unit inner stride and 16-byte aligned starts");
+  if (!row_major(out) || !row_major(lse) || !aligned16(out->data))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "out and lse must be contiguous, out 16-byte aligned");
+  ExpandedPlan &p = *plan;
+  p.q_tiles = tiles_bound(Tq, B, query_offsets != nullptr ? 0 : Tq / std::max<int64_t>(B, 1),
+                          query_offsets != nullptr);
+  p.k_tiles = tiles_bound(Tk, B, query_offsets != nullptr ? 0 : Tk / std::max<int64_t>(B, 1),
+                          query_offsets != nullptr);
+  if (H * std::max(p.q_tiles, p.k_tiles) > 0x7fffff00)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "too many tokens and heads for one launch");
+  if (!outputs_apart({out, lse}, {query, key, key_rope, value, query_offsets, key_offsets}))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "an output overlaps another tensor");
+  p.noop = Tq == 0 || H == 0 || B == 0;
+  p.dt = dt;
+  p.causal = causal != 0;
+  p.q = query->data;
+  p.q_tok = query->stride[0];
+  p.q_head = query->stride[1];
+  p.k = key->data;
+  p.k_tok = key->stride[0];
+  p.k_head = key->stride[1];
+  p.kr = key_rope->data;
+  p.kr_tok = key_rope->stride[0];
+  p.v = value->data;
+  p.v_tok = value->stride[0];
+  p.v_head = value->stride[1];
+  if (query_offsets != nullptr) {
+    p.q_off = static_cast<const int64_t *>(query_offsets->data);
+    p.k_off = static_cast<const int64_t *>(key_offsets->data);
+    p.q_off_stride = query_offsets->stride[0];
+    p.k_off_stride = key_offsets->stride[0];
+  } else {
+    p.q_each = Tq / B;
+    p.k_each = Tk / B;
+  }
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.B = B;
+  p.heads = int32_t(H);
+  p.dim = int32_t(dim);
+  p.scale = float(scale);
+  p.scale_log2 = float(scale * kLog2e);
+  p.out = out->data;
+  p.lse = static_cast<float *>(lse->data);
+  return ROPE_OK;
+}
+
+int plan_expanded_backward(const rope_tensor *grad, const rope_tensor *query,
+                           const rope_tensor *key, const rope_tensor *key_rope,
+                           const rope_tensor *value, const rope_tensor *out,
+                           const rope_tensor *lse, const rope_tensor *query_offsets,
+                           const rope_tensor *key_offsets, int64_t num_sequences, double scale,
+                           int causal, const rope_tensor *dquery, const rope_tensor *dkey,
+                           const rope_tensor *dkey_rope, const rope_tensor *dvalue,
+                           void *workspace, int64_t workspace_bytes, ExpandedPlan *plan,
+                           std::string *err) {
+  for (const rope_tensor *t : {grad, dquery, dkey, dkey_rope, dvalue})
+    if (t == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "a tensor argument is NULL");
+  int st = plan_expanded(query, key, key_rope, value, query_offsets, key_offsets, num_sequences,
+                         scale, causal, out, lse, plan, err);
+  if (st != ROPE_OK) return st;
+  st = common_checks({grad, dquery, dkey, dkey_rope, dvalue}, err);
+  if (st != ROPE_OK) return st;
+  const rope_tensor *outs[4] = {dquery, dkey, dkey_rope, dvalue};
+  const rope_tensor *like[4] = {query, key, key_rope, value};
+  for (int i = 0; i < 4; ++i) {
+    if (outs[i]->dtype != query->dtype || outs[i]->ndim != like[i]->ndim)
+      return reject(err, ROPE_ERR_PARAM_INVALID, "gradients must have their input's dtype and rank");
+    for (int d = 0; d < like[i]->ndim; ++d)
+      if (outs[i]->shape[d] != like[i]->shape[d])
+        return reject(err, ROPE_ERR_PARAM_INVALID, "gradients must have their input's shape");
+    if (!row_major(outs[i]) || !aligned16(outs[i]->data))
+      return reject(err, ROPE_ERR_PARAM_INVALID, "gradients must be contiguous, 16-byte aligned");
+  }
+  if (grad->dtype != query->dtype || grad->ndim != 3)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "grad must have out's dtype and shape");
+  for (int d = 0; d < 3; ++d)
+    if (grad->shape[d] != out->shape[d])
+      return reject(err, ROPE_ERR_PARAM_INVALID, "grad must have out's dtype and shape");
+  if (!unit_inner(grad) || !rows_aligned16(grad))
+    return reject(err, ROPE_ERR_PARAM_INVALID,
+                  "rows need unit inner stride and 16-byte aligned starts");
+  if (!outputs_apart({dquery, dkey, dkey_rope, dvalue},
+                     {grad, query, key, key_rope, value, out, lse, query_offsets, key_offsets}))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "an output overlaps another tensor");
+  ExpandedPlan &p = *plan;
+  p.noop = (p.Tq == 0 && p.Tk == 0) || p.heads == 0 || p.B == 0;
+  if (p.noop) return ROPE_OK;
+  const int64_t need = expanded_workspace(p.Tq, p.Tk, p.heads);
+  if (workspace == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "workspace is NULL");
+  if (workspace_bytes < need || !aligned16(workspace))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "workspace too small or not 16-byte aligned");
+  for (const rope_tensor *t : {grad, query, key, key_rope, value, out, lse, query_offsets,
+                               key_offsets, dquery, dkey, dkey_rope, dvalue})
+    if (touches(workspace, need, t))
+      return reject(err, ROPE_ERR_PARAM_INVALID, "workspace overlaps a tensor");
+  p.grad = grad->data;
+  p.g_tok = grad->stride[0];
+  p.g_head = grad->stride[1];
+  p.fwd_out = out->data;
+  p.dq = dquery->data;
+  p.dk = dkey->data;
+  p.dkr = dkey_rope->data;
+  p.dv = dvalue->data;
+  p.delta = static_cast<float *>(workspace);
+  p.dkr_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + up(p.Tq * p.heads * 4, 256));
+  return ROPE_OK;
+}
+
 }  // namespace ropeamd

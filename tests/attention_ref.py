@@ -96,3 +96,55 @@ def assert_within(got, want, bound, what):
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside the bound, first at "
                              f"{i}: got {got[tuple(i)]:.9g}, want {want[tuple(i)]:.9g}, bound "
                              f"{bound[tuple(i)]:.3g}; worst {err[bad].max():.3g} x")
+
+
+def expanded_reference(q, k, kr, v, scale, causal, dtype, grad=None):
+    """One sequence in float64: q [n, H, dim + 64], k, v [m, H, dim], kr [m, 64], grad [n, H, dim].
+    Returns a dict of (value, bound) pairs: out, lse and, with grad, dq, dk, dkr, dv.
+
+    Backward bounds, beyond those of the module's head: dp_ij = <g, v_j> and D = <g, o> carry their
+    float32 sums' errors and D the output's own error; ds = p (dp - D) is rounded once to the type;
+    every gradient is a sum of products in float32, rounded once."""
+    u, f16 = U[dtype], dtype == torch.float16
+    n, m, h = q.shape[0], k.shape[0], q.shape[1]
+    dim = k.shape[2]
+    tiny = 2.0 ** -25 if f16 else 0.0
+    q, v = q.double().transpose(0, 1), v.double().transpose(0, 1)
+    k = torch.cat([k.double(), kr.double()[:, None, :].expand(m, h, ROPE)], dim=-1).transpose(0, 1)
+    s = torch.matmul(q, k.transpose(1, 2)) * scale
+    if causal:
+        i, j = torch.arange(n, device=s.device), torch.arange(m, device=s.device)
+        s = s.masked_fill(j[None, :] > i[:, None] + (m - n), -math.inf)
+    p, lse = softmax_rows(s)
+    o = torch.matmul(p, v)
+    mag = torch.matmul(q.abs(), k.abs().transpose(1, 2)) * abs(scale)
+    ds = (dim + ROPE + 4) * E32 * (mag.amax(-1) if m else torch.zeros_like(lse))
+    ob = output_bound(p, v, o, ds, u, m, f16)
+    flat_lse = torch.where(torch.isinf(lse), torch.zeros_like(lse), lse)
+    lb = ds + (m + 8) * E32 + 2 * E32 * flat_lse.abs()
+    back = lambda x: x.transpose(0, 1)
+    r = {"out": (back(o), back(ob)), "lse": (back(lse), back(lb))}
+    if grad is None:
+        return r
+    g = grad.double().transpose(0, 1)
+    dP = torch.matmul(g, v.transpose(1, 2))
+    D = (g * o).sum(-1, keepdim=True)
+    dS = p * (dP - D)
+    dp = (2 * ds + lb + 4 * E32 * flat_lse.abs() + 8 * E32)[..., None]  # weights from the saved lse
+    eP = (dim + 4) * E32 * torch.matmul(g.abs(), v.abs().transpose(1, 2))
+    eD = (g.abs() * (ob + (dim + 4) * E32 * o.abs())).sum(-1, keepdim=True)
+    eS = p * (dp * (dP.abs() + D.abs()) + eP + eD + 4 * E32 * (dP.abs() + D.abs()))
+    eS = eS + u * (dS.abs() + eS) + tiny
+    sums = lambda a, b, eA, length: (torch.matmul(eA, b.abs()) +
+                                     (length + 4) * E32 * torch.matmul(a.abs(), b.abs()))
+    dq, eq = torch.matmul(dS, k) * scale, sums(dS, k, eS, m) * abs(scale)
+    dSt, pt = dS.transpose(1, 2), p.transpose(1, 2)
+    dk, ek = torch.matmul(dSt, q) * scale, sums(dSt, q, eS.transpose(1, 2), n) * abs(scale)
+    dv = torch.matmul(pt, g)
+    ev = sums(pt, g, ((u + dp) * p + tiny).transpose(1, 2), n)
+    final = lambda x, e: (x, e + u * (x.abs() + e) + 2.0 ** -24)
+    r["dq"] = final(back(dq), back(eq))
+    r["dk"] = final(back(dk[..., :dim]), back(ek[..., :dim]))
+    r["dv"] = final(back(dv), back(ev))
+    r["dkr"] = final(dk[..., dim:].sum(0), ek[..., dim:].sum(0) + h * E32 * dk[..., dim:].abs().sum(0))
+    return r
