@@ -289,7 +289,7 @@ int rope_latent_attention_paged(const rope_tensor *query, const rope_tensor *lat
  * query      [Tq, heads, dim + 64], key [Tk, heads, dim], key_rope [Tk, 64], value
  *            [Tk, heads, dim]: F16 or BF16, one dtype, dim 64 or 128, unit inner stride, rows on
  *            16-byte boundaries, any other non-negative strides (key and value may be the two
- *            parts of one projection's rows).
+ *            parts of one projection's rows), a token's below 32 MiB.
  * query_offsets, key_offsets   INT64 [B + 1] each, ascending: sequence b is query rows
  *            query_offsets[b] to [b+1] and key rows key_offsets[b] to [b+1]; rows outside are
  *            left as they are; out-of-range values are clamped.  Both NULL: num_sequences

@@ -41,6 +41,9 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-command-line-argument",
 ]
+# The attention kernels rescale their accumulators with vector instructions, which reach the first
+# 256 registers only: products write those, and operands move to the others.
+MFMA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra"]
 
 
@@ -108,7 +111,7 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         return os.path.join(objdir, os.path.splitext(os.path.basename(src))[0] + ".o")
 
     commands = [["g++", *HOST_FLAGS, *inc, "-c", src, "-o", obj(src)] for src in HOST_SOURCES]
-    commands += [[hipcc(), *HIPCC_FLAGS, *(extra_flags or []), *inc, "-c", src, "-o", obj(src)]
+    commands += [[hipcc(), *HIPCC_FLAGS, *MFMA_FLAGS, *(extra_flags or []), *inc, "-c", src, "-o", obj(src)]
                  for src in KERNEL_SOURCES]
     with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
         list(pool.map(lambda cmd: _run(cmd, verbose), commands))

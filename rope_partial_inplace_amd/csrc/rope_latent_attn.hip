@@ -50,15 +50,6 @@ __device__ inline Span span(const int64_t *off, int64_t stride, int64_t total, i
   return {int32_t(o0), int32_t(o1 - o0)};
 }
 
-__device__ inline int32_t wave_scan32(int32_t x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int32_t y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
-  }
-  return x;
-}
-
 // The sequence and the tile within it that tile number `t` of all sequences' tiles is, by query
 // (or key) tokens; sequence -1: there are fewer tiles.
 struct TileAt {
@@ -86,7 +77,7 @@ __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scrat
       const Span s = span(off, QUERY ? p.q_off_stride : p.k_off_stride, QUERY ? p.Tq : p.Tk, 0, b);
       n = (s.count + kRows - 1) / kRows;
     }
-    const int32_t incl = wave_scan32(n, lane);
+    const int32_t incl = wave_scan(n);
     if (lane == 63) sums[wave] = incl;
     __syncthreads();
     int32_t base = before;
@@ -119,19 +110,21 @@ __device__ inline bool head_and_tile(const ExpandedPlan &p, int64_t tiles, int32
 }
 
 // Rows [row0, row0 + 64) of a strided matrix into LDS panels 0 .. PANELS - 1 (8 KB each), this
-// wavefront's quarter; rows past `last` repeat it.
-template <typename T, int PANELS>
-__device__ __forceinline__ void fetch_rows(const void *base, int64_t stride, int32_t row0,
+// wavefront's quarter; rows past `last` repeat it.  stride in bytes, below 2^25 (plan): the rows
+// of a tile lie within 2^31 bytes.
+template <int PANELS>
+__device__ __forceinline__ void fetch_rows(const char *base, int64_t stride, int32_t row0,
                                            int32_t last, int wave, int lane,
                                            char *__restrict__ lds) {
+  const auto buffer = buffer_at(base + int64_t(row0) * stride);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int rb = wave * 2 + i;
-    const int32_t row = min(row0 + 8 * rb + (lane >> 3), last);
-    const char *at = static_cast<const char *>(base) + int64_t(row) * stride * int64_t(sizeof(T)) +
-                     ((uint32_t(lane & 7) ^ chunk_key(uint32_t(lane >> 3))) << 4);
+    const uint32_t row = uint32_t(min(8 * rb + (lane >> 3), last - row0));
+    const uint32_t at = row * uint32_t(stride) +
+                        ((uint32_t(lane & 7) ^ chunk_key(uint32_t(8 * rb + (lane >> 3)))) << 4);
 #pragma unroll
-    for (int n = 0; n < PANELS; ++n) load_lds16(at + n * 128, lds + n * 8192 + rb * 1024);
+    for (int n = 0; n < PANELS; ++n) load_lds16(buffer, at, n * 128, lds + n * 8192 + rb * 1024);
   }
 }
 
@@ -157,10 +150,9 @@ __device__ __forceinline__ void column_product(const char *__restrict__ lds, int
                                                s16x8 b0, s16x8 b1, f32x16 *acc) {
 #pragma unroll
   for (int d = 0; d < BLOCKS; ++d) {
-    const char *at = lds + (d / 2) * 8192 + row0 * 128 +
-                     panel_transposed(uint32_t(lane), uint32_t(d & 1));
-    acc[d] = Mfma<T>::mul(join(read_transposed(at), read_transposed(at + 1024)), b0, acc[d]);
-    acc[d] = Mfma<T>::mul(join(read_transposed(at + 2048), read_transposed(at + 3072)), b1, acc[d]);
+    const char *at = lds + (d / 2) * 8192 + row0 * 128;
+    acc[d] = Mfma<T>::mul(transposed_operand(at, uint32_t(lane), uint32_t(d & 1)), b0, acc[d]);
+    acc[d] = Mfma<T>::mul(transposed_operand(at + 2048, uint32_t(lane), uint32_t(d & 1)), b1, acc[d]);
   }
 }
 
@@ -220,9 +212,9 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
   const char *rb = static_cast<const char *>(p.kr) + int64_t(k.first) * p.kr_tok * es;
   const char *vb = static_cast<const char *>(p.v) + (int64_t(k.first) * p.v_tok + head * p.v_head) * es;
   auto fetch = [&](int32_t j0, char *__restrict__ to) {
-    fetch_rows<T, NP>(kb, p.k_tok, j0, k.count - 1, wave, lane, to);
-    fetch_rows<T, 1>(rb, p.kr_tok, j0, k.count - 1, wave, lane, to + NP * 8192);
-    fetch_rows<T, NP>(vb, p.v_tok, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
+    fetch_rows<NP>(kb, p.k_tok * es, j0, k.count - 1, wave, lane, to);
+    fetch_rows<1>(rb, p.kr_tok * es, j0, k.count - 1, wave, lane, to + NP * 8192);
+    fetch_rows<NP>(vb, p.v_tok * es, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
   };
 
   float top = kNegInf, sum = 0.0f;
@@ -245,7 +237,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
       e[r] = x;
       best = fmaxf(best, x);
     }
-    best = fmaxf(best, other_half(best));
+    best = max_halves(best);
     // rescale only when the maximum rises by more than 8 (weights of up to 2^8 are carried)
     if (__any(best > top + 8.0f)) {
       float f = 1.0f;
@@ -275,7 +267,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
     lds_barrier();
     step(tiles + (n & 1) * TILE, tiles + (~n & 1) * TILE, n * kTile);
   }
-  sum += other_half(sum);
+  sum = sum_halves(sum);
   if (!live) return;
   const bool some = sum > 0.0f || sum != sum;  // a row that sees nothing gets zeros
   const int64_t out_row = int64_t(q.first + row) * p.heads + head;
@@ -323,7 +315,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
         delta += Mfma<T>::high(x[c]) * Mfma<T>::high(y[c]);
       }
     }
-    delta += other_half(delta);
+    delta = sum_halves(delta);
   }
   float lse2 = __builtin_huge_valf();  // rows that see nothing, or do not exist: p = 0
   if (live) {
@@ -341,9 +333,9 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
   const char *rb = static_cast<const char *>(p.kr) + int64_t(k.first) * p.kr_tok * es;
   const char *vb = static_cast<const char *>(p.v) + (int64_t(k.first) * p.v_tok + head * p.v_head) * es;
   auto fetch = [&](int32_t j0, char *__restrict__ to) {
-    fetch_rows<T, NP>(kb, p.k_tok, j0, k.count - 1, wave, lane, to);
-    fetch_rows<T, 1>(rb, p.kr_tok, j0, k.count - 1, wave, lane, to + NP * 8192);
-    fetch_rows<T, NP>(vb, p.v_tok, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
+    fetch_rows<NP>(kb, p.k_tok * es, j0, k.count - 1, wave, lane, to);
+    fetch_rows<1>(rb, p.kr_tok * es, j0, k.count - 1, wave, lane, to + NP * 8192);
+    fetch_rows<NP>(vb, p.v_tok * es, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
   };
   f32x16 acc[NP * 2 + 2];
 #pragma unroll
@@ -383,8 +375,15 @@ template <typename T, int DIM>
 __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedPlan p) {
   constexpr int NP = DIM / 64;
   constexpr int TILE = (2 * NP + 1) * 8192;  // queries (own part, shared part), gradients
-  __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
-  __shared__ __attribute__((aligned(16))) float stats[2][2][kTile];  // lse * log2(e), D
+  // (one LDS variable: with several the compiler would wait for the loads into the other buffer
+  // before it reads this one)
+  struct Lds {
+    char tiles[2 * TILE];
+    float stats[2][2][kTile];  // lse * log2(e), D
+  };
+  __shared__ __attribute__((aligned(16))) Lds lds;
+  char *tiles = lds.tiles;
+  auto &stats = lds.stats;
   int32_t head, tile;
   if (!head_and_tile(p, p.k_tiles, head, tile)) return;
   // the first keys are seen by the most queries: those tiles first
@@ -419,8 +418,8 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
   // the statistics of a tile's rows: read by the first wavefront, one row a lane
   float next_lse = 0.0f, next_delta = 0.0f;
   auto fetch = [&](int32_t i0, char *__restrict__ to) {
-    fetch_rows<T, NP + 1>(qb, p.q_tok, i0, q.count - 1, wave, lane, to);
-    fetch_rows<T, NP>(gb, p.g_tok, i0, q.count - 1, wave, lane, to + (NP + 1) * 8192);
+    fetch_rows<NP + 1>(qb, p.q_tok * es, i0, q.count - 1, wave, lane, to);
+    fetch_rows<NP>(gb, p.g_tok * es, i0, q.count - 1, wave, lane, to + (NP + 1) * 8192);
   };
   auto fetch_stats = [&](int32_t i0) {
     if (wave == 0) {

@@ -9,14 +9,15 @@
 // a row of 1152 bytes (latent_dim 512) leave the call bound by HBM up to about 128 heads, if the
 // loads never pause.
 //
-// One pass, running maximum and sum in float32.  A workgroup is four wavefronts and 32 or 64
-// query rows.  Cache rows pass through LDS, 64 at a time in two buffers that direct-to-LDS loads
-// fill one step ahead.  S^T = K Q^T is split between the wavefronts by cache rows (and query
-// rows), so that Q stays in registers as the second operand (144 of them at latent_dim 512);
-// O^T = V^T P^T is split by columns of V, so that a wavefront accumulates a quarter of the
-// latent for all rows (64 or 128 registers) and every byte of the tile is read for it once, by
-// transposed LDS reads.  In between P goes through LDS, rounded to the storage type: a relative
-// error of at most half a step on each weight, as on the output itself.
+// One pass, running maximum and sum in float32.  A workgroup is eight wavefronts, two on each
+// SIMD, and 32 or 64 query rows.  Cache rows pass through LDS, 64 at a time in two buffers that
+// direct-to-LDS loads fill one step ahead.  S^T = K Q^T is split between the wavefronts by cache
+// rows (four strips of 16) and query rows (two halves), so that Q stays in registers as the second
+// operand (144 of them for 64 rows at latent_dim 512); O^T = V^T P^T is split by columns of V, so
+// that a wavefront accumulates an eighth of the latent for all rows (64 registers) and every byte
+// of the tile is read for it once, by transposed LDS reads.  In between P goes through LDS,
+// rounded to the storage type: a relative error of at most half a step on each weight, as on the
+// output itself.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -30,7 +31,8 @@
 namespace ropeamd {
 namespace {
 
-constexpr int kPagedBlock = 256;
+constexpr int kPagedBlock = 512;
+constexpr int kPagedWaves = kPagedBlock / 64;
 constexpr int kPageIds = 1024;  // page numbers held in LDS at a time
 
 __device__ inline uint32_t div_by(const FastDiv &f, uint32_t n) {
@@ -67,33 +69,36 @@ __device__ inline Sequence sequence(const PagedPlan &p, int32_t b, int rows, int
   return s;
 }
 
-// Inclusive sum over the wavefront.
-__device__ inline int64_t wave_scan(int64_t x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
-  }
-  return x;
+// A wavefront's eighth of a tile of 64 cache rows is 8 of them (tokens tile0 .. tile0 + 63 of the
+// sequence, the last one repeated past `len`).  This lane's piece: its row's byte offset in the
+// cache.
+template <typename T>
+__device__ __forceinline__ int64_t tile_piece(const PagedPlan &p, const int32_t *ids, int32_t page0,
+                                              int32_t tile0, int32_t len, int wave, int lane) {
+  const int32_t tok = min(tile0 + 8 * wave + (lane >> 3), len - 1);
+  const int32_t page = int32_t(div_by(p.div_page, uint32_t(tok)));
+  return (int64_t(ids[page - page0]) * p.c_page +
+          int64_t(tok - page * int32_t(p.page_size)) * p.c_row) * int64_t(sizeof(T));
 }
 
-// A wavefront's quarter of a tile of 64 cache rows (tokens tile0 .. tile0 + 63, the last one
-// repeated past `len`) into LDS: 16 rows of each 64-element panel.
-template <typename T, int PANELS>
-__device__ __forceinline__ void fetch_tile(const PagedPlan &p, const int32_t *ids, int32_t page0,
-                                           int32_t tile0, int32_t len, int wave, int lane,
+// The pieces' way into LDS, 128 bytes of every row at a time.  A buffer reaches 4 GiB, a cache may
+// be larger: rows are fetched by 2 GiB blocks, nearly always all of them in one.
+template <int PANELS>
+__device__ __forceinline__ void fetch_tile(const char *cache, int64_t piece, int wave, int lane,
                                            char *__restrict__ tile) {
+  const int32_t block = int32_t(piece >> 31);
+  const uint32_t offset = (uint32_t(piece) & 0x7fffffffu) +
+                          ((uint32_t(lane & 7) ^ chunk_key(uint32_t(8 * wave + (lane >> 3)))) << 4);
+  bool left = true;
+  while (left) {  // ends: every turn serves the first lane left
+    const int32_t now = __builtin_amdgcn_readfirstlane(block);
+    if (block == now) {
+      const auto buffer = buffer_at(cache + (int64_t(now) << 31));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int rb = wave * 2 + i;  // 8-row block
-    const int32_t tok = min(tile0 + 8 * rb + (lane >> 3), len - 1);
-    const int32_t page = int32_t(div_by(p.div_page, uint32_t(tok)));
-    const int64_t off = int64_t(ids[page - page0]) * p.c_page +
-                        int64_t(tok - page * int32_t(p.page_size)) * p.c_row;
-    const char *row = static_cast<const char *>(p.cache) + off * int64_t(sizeof(T)) +
-                      ((uint32_t(lane & 7) ^ chunk_key(uint32_t(lane >> 3))) << 4);
-#pragma unroll
-    for (int n = 0; n < PANELS; ++n) load_lds16(row + n * 128, tile + n * 8192 + rb * 1024);
+      for (int n = 0; n < PANELS; ++n)
+        load_lds16(buffer, offset, n * 128, tile + n * 8192 + wave * 1024);
+      left = false;
+    }
   }
 }
 
@@ -109,76 +114,94 @@ __device__ inline float raise(float &top, float best) {
   return f;
 }
 
-// One tile.  seen: cache rows of the tile that a query row may see (per lane and row block);
-// whole: whether every row sees all of it.
+// How the wavefronts share a tile of 64 cache rows, DB 32-column blocks of the latent and RB
+// 32-row blocks of queries.
 template <typename T, int DB, int RB>
 struct Step {
   static constexpr int PANELS = DB / 2 + 1;
   static constexpr int ROWS = 32 * RB;
-  static constexpr int SB = RB == 1 ? 2 : 1;    // row blocks of a wavefront in S
-  static constexpr int PARTS = RB == 1 ? 4 : 2;  // wavefronts that share a row's cache rows in S
-  static constexpr int QF = RB == 1 ? PANELS * 2 : PANELS * 4;
-  static constexpr int COLS = DB / 4;            // 32-column blocks of a wavefront in O
+  // S: a wavefront multiplies ST strips of 16 cache rows by one block of 16 query rows, WR of them
+  // side by side over the query rows, PARTS over the cache rows
+  static constexpr int WR = 2 * RB, PARTS = kPagedWaves / WR, ST = 4 / PARTS;
+  static constexpr int QF = PANELS * 2;
+  // O: COLS column blocks and OB row blocks of a wavefront
+  static constexpr bool SPLIT = DB < kPagedWaves;  // fewer column blocks than wavefronts
+  static constexpr int COLS = SPLIT ? 1 : DB / kPagedWaves;
+  static constexpr int OB = SPLIT ? 1 : RB;
+  static_assert(!SPLIT || DB == kPagedWaves / 2, "column blocks");
 
-  // Row of the workgroup that this lane owns in S (block i), and in O (block i).
-  __device__ static int s_row(int wave, int lane, int i) {
-    return RB == 1 ? i * 16 + (lane & 15) : (wave >> 1) * 32 + (lane & 31);
+  __device__ static int part(int wave) { return wave / WR; }
+  // Row of the workgroup that this lane owns in its S, and in block i of its O.
+  __device__ static int s_row(int wave, int lane) { return wave % WR * 16 + (lane & 15); }
+  __device__ static int o_row(int wave, int lane, int i) {
+    return (SPLIT ? wave / DB : i) * 32 + (lane & 31);
   }
-  __device__ static int s_part(int wave) { return RB == 1 ? wave : wave & 1; }
+  __device__ static int column(int wave, int d) { return SPLIT ? wave % DB : wave * COLS + d; }
+  // wavefronts without a share of O (one row block, four column blocks)
+  __device__ static bool has_output(int wave) { return !SPLIT || wave / DB < RB; }
 
-  // S^T of the wavefront's cache rows; scaled, masked; returns the rows' maxima.
-  __device__ __forceinline__ static void scores(const char *__restrict__ tile,
-                                                const s16x8 (&qf)[SB][QF], int wave, int lane,
-                                                const int32_t (&seen)[SB], bool whole,
-                                                float scale_log2, float (&e)[SB][RB == 1 ? 4 : 16],
-                                                float (&best)[SB]) {
-    if constexpr (RB == 1) {
-      f32x4 s[SB] = {};
-      const uint32_t row = uint32_t(wave * 16 + (lane & 15));
+  // Operands out of LDS: panel n of the strips' rows; P of the 16 cache rows of step k; and for
+  // product n (step n / COLS, column block n % COLS) the values.  The tile goes in as an argument
+  // everywhere, never captured: only so does the compiler see that these reads and the loads
+  // into the other buffer do not meet, and does not wait for those loads here.
+  __device__ __forceinline__ static void load_keys(const char *tile, int wave, int lane, int n,
+                                                   s16x8 (&f)[ST][2]) {
 #pragma unroll
-      for (int n = 0; n < PANELS; ++n)
+    for (int j = 0; j < ST; ++j)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const s16x8 kf = as_operand(*reinterpret_cast<const uint4 *>(
-              tile + n * 8192 + panel_chunk(row, 4u * c + (uint32_t(lane) >> 4))));
+      for (int c = 0; c < 2; ++c)
+        f[j][c] = as_operand(*reinterpret_cast<const uint4 *>(
+            tile + n * 8192 + j * 2048 +
+            panel_chunk(uint32_t(part(wave) * ST * 16 + (lane & 15)),
+                        4u * c + (uint32_t(lane) >> 4))));
+  }
+  __device__ __forceinline__ static void load_weights(const char *pt, int wave, int lane, int k,
+                                                      s16x8 *f) {
 #pragma unroll
-          for (int i = 0; i < SB; ++i) s[i] = Mfma<T>::mul16(kf, qf[i][n * 2 + c], s[i]);
-        }
+    for (int i = 0; i < OB; ++i)
+      f[i] = as_operand(*reinterpret_cast<const uint4 *>(
+          pt + panel_chunk(uint32_t(o_row(wave, lane, i)), uint32_t(2 * k + (lane >> 5)))));
+  }
+  __device__ __forceinline__ static s16x8 load_values(const char *tile, int wave, int lane, int n) {
+    const int block = column(wave, n % COLS);
+    return transposed_operand(tile + (block >> 1) * 8192 + n / COLS * 2048, uint32_t(lane),
+                              uint32_t(block & 1));
+  }
+
+  // S^T of the wavefront's strips and rows; scaled, masked (seen: rows of the tile that the query
+  // row may see; whole: every query row sees all of them); returns the row's maximum.
+  __device__ __forceinline__ static float scores(const char *__restrict__ tile,
+                                                 const s16x8 (&qf)[QF], int wave, int lane,
+                                                 int32_t seen, bool whole, float scale_log2,
+                                                 float (&e)[ST][4]) {
+    f32x4 s[ST] = {};
+    constexpr int AHEAD = 2;  // panels read ahead
+    s16x8 kf[AHEAD + 1][ST][2];
 #pragma unroll
-      for (int i = 0; i < SB; ++i) {
-        best[i] = kNegInf;
+    for (int n = 0; n < AHEAD; ++n) load_keys(tile, wave, lane, n, kf[n]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float x = s[i][r] * scale_log2;
-          if (!whole) x = wave * 16 + 4 * (lane >> 4) + r < seen[i] ? x : kNegInf;
-          e[i][r] = x;
-          best[i] = fmaxf(best[i], x);
-        }
-        best[i] = fmaxf(best[i], __shfl_xor(best[i], 16, 64));
-        best[i] = fmaxf(best[i], other_half(best[i]));
-      }
-    } else {
-      f32x16 s = {};
-      const uint32_t row = uint32_t((wave & 1) * 32 + (lane & 31));
+    for (int n = 0; n < PANELS; ++n) {
+      if (n + AHEAD < PANELS)
+        load_keys(tile, wave, lane, n + AHEAD, kf[(n + AHEAD) % (AHEAD + 1)]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < PANELS; ++n)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const s16x8 kf = as_operand(*reinterpret_cast<const uint4 *>(
-              tile + n * 8192 + panel_chunk(row, 2u * c + (uint32_t(lane) >> 5))));
-          s = Mfma<T>::mul(kf, qf[0][n * 4 + c], s);
-        }
-      best[0] = kNegInf;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float x = s[r] * scale_log2;
-        if (!whole)
-          x = (wave & 1) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < seen[0] ? x : kNegInf;
-        e[0][r] = x;
-        best[0] = fmaxf(best[0], x);
-      }
-      best[0] = fmaxf(best[0], other_half(best[0]));
+        for (int j = 0; j < ST; ++j)
+          s[j] = Mfma<T>::mul16(kf[n % (AHEAD + 1)][j][c], qf[n * 2 + c], s[j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    float best = kNegInf;
+#pragma unroll
+    for (int j = 0; j < ST; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float x = s[j][r] * scale_log2;
+        if (!whole) x = (part(wave) * ST + j) * 16 + 4 * (lane >> 4) + r < seen ? x : kNegInf;
+        e[j][r] = x;
+        best = fmaxf(best, x);
+      }
+    return max_quarters(best);
   }
 
   // Weights of four cache rows (4 g4 .. + 3 of the tile) of query row `row` into the P tile, in
@@ -193,44 +216,48 @@ struct Step {
   // O^T += V^T P^T over the tile.
   __device__ __forceinline__ static void outputs(const char *__restrict__ tile,
                                                  const char *__restrict__ pt, int wave, int lane,
-                                                 f32x16 (&acc)[RB][COLS]) {
+                                                 f32x16 (&acc)[OB][COLS]) {
+    s16x8 pf[2][OB], vf[2];  // read one product ahead
+    load_weights(pt, wave, lane, 0, pf[0]);
+    vf[0] = load_values(tile, wave, lane, 0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s16x8 pf[RB];
+    for (int n = 0; n < 4 * COLS; ++n) {
+      const int k = n / COLS;
+      if (n + 1 < 4 * COLS) vf[(n + 1) % 2] = load_values(tile, wave, lane, n + 1);
+      if (n % COLS == 0 && k < 3) load_weights(pt, wave, lane, k + 1, pf[(k + 1) % 2]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < RB; ++i)
-        pf[i] = as_operand(*reinterpret_cast<const uint4 *>(
-            pt + panel_chunk(uint32_t(i * 32 + (lane & 31)), uint32_t(2 * k + (lane >> 5)))));
-#pragma unroll
-      for (int d = 0; d < COLS; ++d) {
-        const int block = wave * COLS + d;
-        const char *at = tile + (block >> 1) * 8192 + k * 2048 +
-                         panel_transposed(uint32_t(lane), uint32_t(block & 1));
-        const s16x8 vf = join(read_transposed(at), read_transposed(at + 1024));
-#pragma unroll
-        for (int i = 0; i < RB; ++i) acc[i][d] = Mfma<T>::mul(vf, pf[i], acc[i][d]);
-      }
+      for (int i = 0; i < OB; ++i)
+        acc[i][n % COLS] = Mfma<T>::mul(vf[n % 2], pf[k % 2][i], acc[i][n % COLS]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
 
 template <typename T, int DB, int RB>
-__global__ __launch_bounds__(kPagedBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) void
+__global__ __launch_bounds__(kPagedBlock) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 latent_paged_kernel(PagedPlan p) {
   using S = Step<T, DB, RB>;
-  constexpr int PANELS = S::PANELS, ROWS = S::ROWS, SB = S::SB;
+  constexpr int PANELS = S::PANELS, ROWS = S::ROWS, OB = S::OB, COLS = S::COLS;
   constexpr int STEP = int(kPagedStep);
   constexpr int TILE = PANELS * 8192;  // bytes
-  constexpr int SE = RB == 1 ? 4 : 16;
-  __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
-  __shared__ __attribute__((aligned(16))) char weights[ROWS * 128];
-  __shared__ int32_t ids[kPageIds];
-  __shared__ float row_max[S::PARTS][ROWS];
-  __shared__ int64_t wave_total[4];
-  __shared__ int64_t found_before;
-  __shared__ int32_t found_seq;
+  // One LDS variable: with several the compiler would mark accesses by variable, and lose what it
+  // knows about the two halves of `tiles`.
+  struct Lds {
+    char tiles[2 * TILE];
+    char weights[ROWS * 128];
+    int32_t ids[kPageIds];
+    float row_max[S::PARTS][ROWS];
+    int32_t wave_total[kPagedWaves];
+    int32_t found[7];
+  };
+  __shared__ __attribute__((aligned(16))) Lds lds;
+  char *tiles = lds.tiles, *weights = lds.weights;
+  int32_t *ids = lds.ids, *found = lds.found;
+  auto &row_max = lds.row_max;
+  int32_t *wave_total = lds.wave_total;
 
-  const int tid = int(threadIdx.x), lane = tid & 63;
+  const int tid = int(threadIdx.x), lane = tid & 63, lane_id = lane;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // the workgroups of a cluster are kXcds apart: on one XCD, they share its L2
   const int32_t turn = int32_t(blockIdx.x / kXcds);
@@ -238,235 +265,270 @@ latent_paged_kernel(PagedPlan p) {
   const int32_t member = turn % p.cluster;
   const int32_t item_rows = ROWS * p.cluster;
 
-  // ---- the cluster's share [w0, w1) of all steps ----
-  int64_t mine = 0;
-  for (int32_t b = tid; b < p.B; b += kPagedBlock) {
-    const Sequence s = sequence(p, b, item_rows, STEP);
-    mine += int64_t(s.items) * s.steps;
+  // ---- the cluster's share [w0, w1) of all steps (their number fits 31 bits: plan) ----
+  Sequence sq = {};
+  int32_t mine = 0, n = 0;
+  if (tid < p.B) {
+    sq = sequence(p, tid, item_rows, STEP);
+    n = sq.items * sq.steps;
   }
-  const int64_t wave_sum = __shfl(wave_scan(mine, lane), 63, 64);
-  if (lane == 0) wave_total[wave] = wave_sum;
+  for (int32_t b = tid + kPagedBlock; b < p.B; b += kPagedBlock) {
+    const Sequence s = sequence(p, b, item_rows, STEP);
+    mine += s.items * s.steps;
+  }
+  int32_t incl = wave_scan(n);
+  const int32_t rest = p.B > kPagedBlock ? wave_scan(mine) : 0;
+  if (lane == 63) wave_total[wave] = incl + rest;
   __syncthreads();
-  const int64_t total = wave_total[0] + wave_total[1] + wave_total[2] + wave_total[3];
-  const int64_t per = (total + p.clusters - 1) / p.clusters;
-  const int64_t w0 = g * per, w1 = min(total, w0 + per);
-  if (w0 >= w1) {
-    if (tid == 0 && member == 0) p.joins[g * 4 + 3] = 0;
+  int32_t total = 0;
+#pragma unroll
+  for (int v = 0; v < kPagedWaves; ++v) total += wave_total[v];
+  auto uniform = [](int32_t x) { return __builtin_amdgcn_readfirstlane(x); };
+  total = uniform(total);
+  const int32_t per = uniform(int32_t((uint32_t(total) + p.clusters - 1) / uint32_t(p.clusters)));
+  const int64_t start = int64_t(g) * per;
+  if (start >= total) {
+    if (tid < 2 && member == 0) p.joins[(g * 2 + tid) * kJoinWords] = 0;
     return;
   }
+  const int32_t w0 = int32_t(start), w1 = int32_t(min(int64_t(total), start + per));
   // the sequence that holds step w0
-  int64_t before = 0;
+  int32_t before = 0;
   for (int32_t b0 = 0; b0 < p.B; b0 += kPagedBlock) {
-    const int32_t b = b0 + tid;
-    int64_t n = 0;
-    if (b < p.B) {
-      const Sequence s = sequence(p, b, item_rows, STEP);
-      n = int64_t(s.items) * s.steps;
+    if (b0 > 0) {
+      n = 0;
+      if (b0 + tid < p.B) {
+        sq = sequence(p, b0 + tid, item_rows, STEP);
+        n = sq.items * sq.steps;
+      }
+      incl = wave_scan(n);
     }
-    const int64_t incl = wave_scan(n, lane);
-    __syncthreads();
-    if (lane == 63) wave_total[wave] = incl;
-    __syncthreads();
-    int64_t base = before;
-    for (int v = 0; v < wave; ++v) base += wave_total[v];
-    const int64_t chunk = wave_total[0] + wave_total[1] + wave_total[2] + wave_total[3];
+    if (p.B > kPagedBlock) {  // else wave_total holds the first (only) round's sums already
+      __syncthreads();
+      if (lane == 63) wave_total[wave] = incl;
+      __syncthreads();
+    }
+    int32_t base = before;
+    for (int v = 0; v < kPagedWaves; ++v) {
+      if (v < wave) base += wave_total[v];
+      before += wave_total[v];
+    }
     if (n > 0 && base + incl - n <= w0 && w0 < base + incl) {
-      found_seq = b;
-      found_before = base + incl - n;
+      found[0] = b0 + tid;
+      found[1] = sq.len;
+      found[2] = sq.first;
+      found[3] = sq.count;
+      found[4] = sq.items;
+      found[5] = sq.steps;
+      found[6] = base + incl - n;
     }
-    before += chunk;
-    if (w0 < before) break;
+    if (w0 < before) break;  // the same for all threads
   }
   __syncthreads();
-  int32_t b = __builtin_amdgcn_readfirstlane(found_seq);
-  Sequence sq = sequence(p, b, item_rows, STEP);
-  const int64_t into = w0 - found_before;
-  int32_t item = int32_t(into / sq.steps);
-  int32_t st0 = int32_t(into - int64_t(item) * sq.steps);
-  int64_t w = w0;
-  bool joined = false;
+  int32_t b = uniform(found[0]);
+  sq = {uniform(found[1]), uniform(found[2]), uniform(found[3]), uniform(found[4]),
+        uniform(found[5])};
+  const int32_t into = w0 - uniform(found[6]);
+  int32_t item = uniform(int32_t(uint32_t(into) / uint32_t(sq.steps)));
+  int32_t st0 = into - item * sq.steps;
+  int32_t w = w0;
+  uint32_t partial = 0;  // bit s: part s of this cluster is one of an item's several
 
   while (true) {
-    const int32_t st1 = int32_t(min(int64_t(sq.steps), st0 + (w1 - w)));
+    const int32_t st1 = min(sq.steps, st0 + (w1 - w));
     const int32_t rows = sq.count * p.heads;
     const int32_t row0 = item * item_rows + member * ROWS;
     if (row0 < rows) {
+      // page numbers of as many of the steps from `st` on as the table holds; returns the step
+      // that they end before
+      int32_t page0 = 0;
+      auto load_ids = [&](int32_t st) {
+        page0 = int32_t(div_by(p.div_page, uint32_t(st * STEP)));
+        const int32_t last_tok = min(st1 * STEP, sq.len) - 1;
+        const int32_t pages = min(int32_t(kPageIds),
+                                  int32_t(div_by(p.div_page, uint32_t(last_tok))) - page0 + 1);
+        for (int32_t i = tid; i < pages; i += kPagedBlock) {
+          const int64_t id = p.table[b * p.table_seq + (page0 + i) * p.table_page];
+          ids[i] = int32_t(min(max(id, int64_t(0)), p.num_pages - 1));
+        }
+        return int64_t(page0 + pages) * p.page_size <= last_tok
+                   ? int32_t((int64_t(page0 + pages) * p.page_size) / STEP)
+                   : st1;
+      };
+      __syncthreads();  // what the last segment read of ids, tiles and row_max
+      int32_t end = st1;
+      if (sq.len > 0) end = load_ids(st0);
+
       // ---- this wavefront's query rows, and how much of the cache each may see ----
-      s16x8 qf[SB][S::QF];
-      int32_t limit[SB];
-#pragma unroll
-      for (int i = 0; i < SB; ++i) {
-        const int32_t r = row0 + S::s_row(wave, lane, i);
-        const bool live = r < rows;
-        const int32_t qi = live ? int32_t(div_by(p.div_heads, uint32_t(r))) : 0;
-        const int32_t head = live ? r - qi * p.heads : 0;
-        limit[i] = live ? sq.len - sq.count + qi + 1 : 0;
+      s16x8 qf[S::QF];
+      const int32_t s_r = row0 + S::s_row(wave, lane);
+      const bool live = s_r < rows;
+      const int32_t qi = live ? int32_t(div_by(p.div_heads, uint32_t(s_r))) : 0;
+      const int32_t limit = live ? sq.len - sq.count + qi + 1 : 0;
+      {
+        const int32_t head = live ? s_r - qi * p.heads : 0;
         const T *q = static_cast<const T *>(p.q) + int64_t(sq.first + qi) * p.q_tok +
-                     int64_t(head) * p.q_head + 8 * (RB == 1 ? lane >> 4 : lane >> 5);
+                     int64_t(head) * p.q_head + 8 * (lane >> 4);
 #pragma unroll
         for (int k = 0; k < S::QF; ++k)
-          qf[i][k] = live ? as_operand(*reinterpret_cast<const uint4 *>(q + k * (RB == 1 ? 32 : 16)))
-                          : s16x8{};
+          qf[k] = live ? as_operand(*reinterpret_cast<const uint4 *>(q + k * 32)) : s16x8{};
       }
       // fewest cache rows that any row of the workgroup sees
       const int32_t floor = row0 + ROWS > rows
                                 ? 0
                                 : sq.len - sq.count + int32_t(div_by(p.div_heads, uint32_t(row0))) + 1;
 
-      float s_top[SB], s_sum[SB], o_top[RB];
-      f32x16 acc[RB][S::COLS];
+      float s_top = kNegInf, s_sum = 0.0f, o_top[OB];
+      f32x16 acc[OB][COLS];
 #pragma unroll
-      for (int i = 0; i < SB; ++i) s_top[i] = kNegInf, s_sum[i] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
+      for (int i = 0; i < OB; ++i) {
         o_top[i] = kNegInf;
 #pragma unroll
-        for (int d = 0; d < S::COLS; ++d) acc[i][d] = f32x16{};
+        for (int d = 0; d < COLS; ++d) acc[i][d] = f32x16{};
       }
 
       auto step = [&](const char *__restrict__ cur, char *__restrict__ other,
-                      char *__restrict__ pt, int32_t tile0, int32_t next0, int32_t page0) {
-        if (next0 >= 0) fetch_tile<T, PANELS>(p, ids, page0, next0, sq.len, wave, lane, other);
-        int32_t seen[SB];
-#pragma unroll
-        for (int i = 0; i < SB; ++i) seen[i] = limit[i] - tile0;
-        float e[SB][SE], best[SB];
-        S::scores(cur, qf, wave, lane, seen, tile0 + STEP <= floor, p.scale_log2, e, best);
-#pragma unroll
-        for (int i = 0; i < SB; ++i)
-          if (lane < (RB == 1 ? 16 : 32))
-            row_max[S::s_part(wave)][S::s_row(wave, lane, i)] = best[i];
+                      char *__restrict__ pt, float *__restrict__ rm,
+                      const int32_t *__restrict__ pages, const char *cache, int64_t piece,
+                      int32_t st) {
+        if (st + 1 < end) fetch_tile<PANELS>(cache, piece, wave, lane_id, other);
+        const int32_t tile0 = st * STEP;
+        // LDS addresses are worked out again in every step: kept from step to step they would
+        // take the registers that Q and the accumulators need
+        int lane = lane_id;
+        asm volatile("" : "+v"(lane));
+        float e[S::ST][4];
+        const int row = S::s_row(wave, lane);
+        const float best = S::scores(cur, qf, wave, lane, limit - tile0, tile0 + STEP <= floor,
+                                     p.scale_log2, e);
+        if (lane < 16) rm[S::part(wave) * ROWS + row] = best;
+        // where the tile after the next one comes from
+        const int64_t after = st + 2 < end ? tile_piece<T>(p, pages, page0, (st + 2) * STEP,
+                                                           sq.len, wave, lane)
+                                           : 0;
         lds_barrier();
+        {
+          float high = rm[row];
 #pragma unroll
-        for (int i = 0; i < SB; ++i) {
-          const int row = S::s_row(wave, lane, i);
-          float high = row_max[0][row];
+          for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, rm[k * ROWS + row]);
+          s_sum *= raise(s_top, high);
+          const float ref = s_top == kNegInf ? 0.0f : s_top;
 #pragma unroll
-          for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, row_max[k][row]);
-          s_sum[i] *= raise(s_top[i], high);
-          const float ref = s_top[i] == kNegInf ? 0.0f : s_top[i];
+          for (int j = 0; j < S::ST; ++j) {
 #pragma unroll
-          for (int r = 0; r < SE; ++r) {
-            e[i][r] = __builtin_amdgcn_exp2f(e[i][r] - ref);
-            s_sum[i] += e[i][r];
-          }
-          if constexpr (RB == 1) {
-            S::put_weights(pt, row, wave * 4 + (lane >> 4), e[i]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              S::put_weights(pt, row, (wave & 1) * 8 + 2 * c + (lane >> 5), e[i] + 4 * c);
+            for (int r = 0; r < 4; ++r) {
+              e[j][r] = __builtin_amdgcn_exp2f(e[j][r] - ref);
+              s_sum += e[j][r];
+            }
+            S::put_weights(pt, row, (S::part(wave) * S::ST + j) * 4 + (lane >> 4), e[j]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          const int row = i * 32 + (lane & 31);
-          float high = row_max[0][row];
+        for (int i = 0; i < OB; ++i) {
+          const int o_row = S::o_row(wave, lane, i) % ROWS;
+          float high = rm[o_row];
 #pragma unroll
-          for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, row_max[k][row]);
+          for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, rm[k * ROWS + o_row]);
           const float f = raise(o_top[i], high);
           if (__any(f != 1.0f)) {
 #pragma unroll
-            for (int d = 0; d < S::COLS; ++d) acc[i][d] *= f;
+            for (int d = 0; d < COLS; ++d) acc[i][d] *= f;
           }
         }
         lds_barrier();
-        S::outputs(cur, pt, wave, lane, acc);
+        if (S::has_output(wave)) S::outputs(cur, pt, wave, lane, acc);
+        return after;
       };
 
       if (sq.len > 0) {
         int32_t st = st0;
-        while (st < st1) {
-          // ---- page numbers of as many of the segment's steps as the table holds ----
-          const int32_t page0 = int32_t(div_by(p.div_page, uint32_t(st * STEP)));
-          const int32_t last_tok = min(st1 * STEP, sq.len) - 1;
-          const int32_t pages = min(int32_t(kPageIds),
-                                    int32_t(div_by(p.div_page, uint32_t(last_tok))) - page0 + 1);
-          __syncthreads();
-          for (int32_t i = tid; i < pages; i += kPagedBlock) {
-            const int64_t id = p.table[b * p.table_seq + (page0 + i) * p.table_page];
-            ids[i] = int32_t(min(max(id, int64_t(0)), p.num_pages - 1));
-          }
-          __syncthreads();
-          int32_t end = st1;
-          if (int64_t(page0 + pages) * p.page_size <= last_tok)
-            end = int32_t((int64_t(page0 + pages) * p.page_size) / STEP);
+        while (true) {
           // ---- the steps: the next tile is on its way while one is multiplied ----
-          fetch_tile<T, PANELS>(p, ids, page0, st * STEP, sq.len, wave, lane, tiles);
-          for (int32_t n = 0; st < end; ++st, ++n) {
+          __syncthreads();
+          const char *cache = static_cast<const char *>(p.cache);
+          fetch_tile<PANELS>(cache, tile_piece<T>(p, ids, page0, st * STEP, sq.len, wave, lane),
+                             wave, lane, tiles);
+          int64_t next = st + 1 < end ? tile_piece<T>(p, ids, page0, (st + 1) * STEP, sq.len, wave,
+                                                      lane)
+                                      : 0;
+          for (int32_t i = 0; st < end; ++st, ++i) {
             wait_loads_all();
             lds_barrier();
-            step(tiles + (n & 1) * TILE, tiles + (~n & 1) * TILE, weights, st * STEP,
-                 st + 1 < end ? (st + 1) * STEP : -1, page0);
+            next = step(tiles + (i & 1) * TILE, tiles + (~i & 1) * TILE, weights, &row_max[0][0],
+                        ids, cache, next, st);
           }
+          if (st >= st1) break;
+          __syncthreads();
+          end = load_ids(st);
         }
       }
 
       // ---- sums of the wavefronts that shared a row ----
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < SB; ++i) {
-        if constexpr (RB == 1) s_sum[i] += __shfl_xor(s_sum[i], 16, 64);
-        s_sum[i] += other_half(s_sum[i]);
-        if (lane < (RB == 1 ? 16 : 32))
-          row_max[S::s_part(wave)][S::s_row(wave, lane, i)] = s_sum[i];
-      }
+      s_sum = sum_quarters(s_sum);
+      if (lane < 16) row_max[S::part(wave)][S::s_row(wave, lane)] = s_sum;
       __syncthreads();
 
       // ---- the segment's result: a whole item's output, or a part for the joining kernel ----
       const bool whole = st0 == 0 && st1 == sq.steps;
       const int64_t slot = (int64_t(g) * p.cluster + member) * 2 + (w == w0 ? 0 : 1);
+      if (S::has_output(wave)) {
 #pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const int m = i * 32 + (lane & 31);
-        float sum = row_max[0][m];
+        for (int i = 0; i < OB; ++i) {
+          const int m = S::o_row(wave, lane, i);
+          float sum = row_max[0][m];
 #pragma unroll
-        for (int k = 1; k < S::PARTS; ++k) sum += row_max[k][m];
-        const int32_t r = row0 + m;
-        const int64_t out_row = int64_t(sq.first) * p.heads + r;
-        const bool some = sum > 0.0f || sum != sum;  // a row that sees nothing gets zeros
-        if (whole) {
-          if (r < rows) {
-            const float inv = some ? 1.0f / sum : 0.0f;
-            char *out = static_cast<char *>(p.out) + out_row * p.latent * int64_t(sizeof(T));
+          for (int k = 1; k < S::PARTS; ++k) sum += row_max[k][m];
+          const int32_t r = row0 + m;
+          const int64_t out_row = int64_t(sq.first) * p.heads + r;
+          const bool some = sum > 0.0f || sum != sum;  // a row that sees nothing gets zeros
+          const bool first_column = S::column(wave, 0) == 0;
+          if (whole) {
+            if (r < rows) {
+              const float inv = some ? 1.0f / sum : 0.0f;
+              char *out = static_cast<char *>(p.out) + out_row * p.latent * int64_t(sizeof(T));
 #pragma unroll
-            for (int d = 0; d < S::COLS; ++d)
+              for (int d = 0; d < COLS; ++d)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const f32x16 &a = acc[i][d];
+                  const int d4 = S::column(wave, d) * 8 + c * 2 + (lane >> 5);
+                  *reinterpret_cast<uint2 *>(out + d4 * 8) =
+                      make_uint2(Mfma<T>::pack(a[4 * c] * inv, a[4 * c + 1] * inv),
+                                 Mfma<T>::pack(a[4 * c + 2] * inv, a[4 * c + 3] * inv));
+                }
+              if (first_column && lane < 32 && p.lse != nullptr)
+                p.lse[out_row] = some ? o_top[i] * 0.693147180559945f + logf(sum) : kNegInf;
+            }
+          } else {
+            float *part = p.parts + slot * ROWS * p.latent + m * 4;
+#pragma unroll
+            for (int d = 0; d < COLS; ++d)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const f32x16 &a = acc[i][d];
-                const int d4 = (wave * S::COLS + d) * 8 + c * 2 + (lane >> 5);
-                *reinterpret_cast<uint2 *>(out + d4 * 8) =
-                    make_uint2(Mfma<T>::pack(a[4 * c] * inv, a[4 * c + 1] * inv),
-                               Mfma<T>::pack(a[4 * c + 2] * inv, a[4 * c + 3] * inv));
+                const int d4 = S::column(wave, d) * 8 + c * 2 + (lane >> 5);
+                *reinterpret_cast<float4 *>(part + d4 * (ROWS * 4)) =
+                    make_float4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
               }
-            if (wave == 0 && lane < 32 && p.lse != nullptr)
-              p.lse[out_row] = some ? o_top[i] * 0.693147180559945f + logf(sum) : kNegInf;
+            if (first_column && lane < 32)
+              *reinterpret_cast<float2 *>(p.stats + (slot * ROWS + m) * 2) =
+                  make_float2(o_top[i], sum);
           }
-        } else {
-          float *part = p.parts + slot * ROWS * p.latent + m * 4;
-#pragma unroll
-          for (int d = 0; d < S::COLS; ++d)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const f32x16 &a = acc[i][d];
-              const int d4 = (wave * S::COLS + d) * 8 + c * 2 + (lane >> 5);
-              *reinterpret_cast<float4 *>(part + d4 * (ROWS * 4)) =
-                  make_float4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
-            }
-          if (wave == 0 && lane < 32)
-            *reinterpret_cast<float2 *>(p.stats + (slot * ROWS + m) * 2) =
-                make_float2(o_top[i], sum);
         }
       }
     }
-    // an item that began here and goes on in the next clusters is joined afterwards
-    if (st0 == 0 && st1 < sq.steps) {
-      joined = true;
+    if (st0 != 0 || st1 != sq.steps) {
+      const int part = w == w0 ? 0 : 1;
+      partial |= 1u << part;
       if (tid == 0 && member == 0) {
-        p.joins[g * 4 + 0] = b;
-        p.joins[g * 4 + 1] = item;
-        p.joins[g * 4 + 2] = w == w0 ? 0 : 1;
-        p.joins[g * 4 + 3] = int32_t((w + sq.steps - 1) / per - g + 1);
+        const uint32_t begin = uint32_t(w - st0), first_g = begin / uint32_t(per);
+        int32_t *rec = p.joins + (g * 2 + part) * kJoinWords;
+        rec[0] = int32_t((begin + uint32_t(sq.steps) - 1) / uint32_t(per) - first_g + 1);
+        rec[1] = int32_t(first_g);
+        rec[2] = begin == first_g * uint32_t(per) ? 0 : 1;
+        rec[3] = sq.first * p.heads + item * item_rows;
+        rec[4] = rows - item * item_rows;
       }
     }
     w += st1 - st0;
@@ -480,83 +542,91 @@ latent_paged_kernel(PagedPlan p) {
       } while (sq.items == 0);
     }
   }
-  if (!joined && tid == 0 && member == 0) p.joins[g * 4 + 3] = 0;
+  if (tid < 2 && member == 0 && (partial >> tid & 1u) == 0)
+    p.joins[(g * 2 + tid) * kJoinWords] = 0;
 }
 
-// Joins the parts of the item that began in a cluster's share: a part k holds
-// unnormalised outputs o_k at maximum m_k with weight sum l_k, and
+// Joins the parts of items that several clusters had a share of: a part k holds unnormalised
+// outputs o_k at maximum m_k with weight sum l_k, and
 //   out = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k,   m = max_k m_k.
-// Four wavefronts share the parts of one (4-column group, row) and add up through LDS in a fixed
-// order, so results do not depend on timing.
+// One workgroup for each part joins the n-th part of the item's (4-column group, row) cells, so
+// that all workgroups have about one part's bytes to read.  It is a launch of a few dependent
+// reads: `share` wavefronts take the parts of a cell in turn, as many as the workgroup has to
+// spare, eight parts' reads under way at once, and add up through LDS in a fixed order.
+constexpr int kJoinBlock = 1024;
+constexpr int kJoinAhead = 8;
+
 template <typename T, int DB, int RB>
-__global__ __launch_bounds__(kPagedBlock) void latent_paged_join_kernel(PagedPlan p) {
+__global__ __launch_bounds__(kJoinBlock) void latent_paged_join_kernel(PagedPlan p) {
   constexpr int ROWS = 32 * RB;
-  constexpr int CELLS = DB * 8 * ROWS;  // (4-column group, row) pairs
-  __shared__ float4 add[4][64];
-  __shared__ float add_l[4][64], add_top[4][64];
-  const int32_t g = int32_t(blockIdx.x) / p.cluster, member = int32_t(blockIdx.x) % p.cluster;
-  const int32_t n = p.joins[g * 4 + 3];
+  constexpr int CELLS = DB * 8 * ROWS;
+  constexpr int WAVES = kJoinBlock / 64;
+  __shared__ float4 add[WAVES][64];
+  __shared__ float2 add_stat[WAVES][64];
+  const int32_t member = int32_t(blockIdx.y);
+  const int32_t g = int32_t(blockIdx.x) >> 1;
+  const int32_t *rec = p.joins + int32_t(blockIdx.x) * kJoinWords;
+  const int32_t n = rec[0], g0 = rec[1], first = rec[2];
   if (n <= 1) return;
-  const int32_t b = p.joins[g * 4], item = p.joins[g * 4 + 1], first = p.joins[g * 4 + 2];
-  const Sequence sq = sequence(p, b, ROWS * p.cluster, int(kPagedStep));
-  const int32_t rows = sq.count * p.heads, row0 = (item * p.cluster + member) * ROWS;
-  if (row0 >= rows) return;
+  const int32_t live = rec[4] - member * ROWS;  // rows of the item from this member's on
   const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
-  auto slot = [&](int32_t k) {
-    return (int64_t(g + k) * p.cluster + member) * 2 + (k == 0 ? first : 0);
-  };
-  for (int c0 = int(blockIdx.y) * 64; c0 < CELLS; c0 += int(gridDim.y) * 64) {
-    const int cell = c0 + lane;
+  const int c0 = int(int64_t(CELLS) * (g - g0) / n), c1 = int(int64_t(CELLS) * (g - g0 + 1) / n);
+  const int groups = (c1 - c0 + 63) / 64;  // of 64 cells
+  int share = 1;
+  while (share < WAVES && 2 * share * groups <= WAVES) share *= 2;
+  const int side = WAVES / share;  // groups at a time
+  for (int at = 0; at < groups; at += side) {
+    const int cell = c0 + (at + wave / share) * 64 + lane;
     const int m = cell % ROWS;
-    // every wavefront joins its share of the parts at a maximum of its own
+    const bool mine = cell < c1 && m < live;
     float top = kNegInf, l = 0.0f;
     float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int32_t k = wave; k < n; k += 4) {
-      const float2 stat = *reinterpret_cast<const float2 *>(p.stats + (slot(k) * ROWS + m) * 2);
-      const float4 o =
-          *reinterpret_cast<const float4 *>(p.parts + slot(k) * ROWS * p.latent + int64_t(cell) * 4);
-      const float next = fmaxf(top, stat.x), ref = next == kNegInf ? 0.0f : next;
-      const float fa = __builtin_amdgcn_exp2f(top - ref), fb = __builtin_amdgcn_exp2f(stat.x - ref);
+    auto take = [&](float top_k, float l_k, const float4 &o) {
+      const float next = fmaxf(top, top_k), ref = next == kNegInf ? 0.0f : next;
+      const float fa = __builtin_amdgcn_exp2f(top - ref), fb = __builtin_amdgcn_exp2f(top_k - ref);
       top = next;
-      l = l * fa + stat.y * fb;
+      l = l * fa + l_k * fb;
       t.x = t.x * fa + o.x * fb;
       t.y = t.y * fa + o.y * fb;
       t.z = t.z * fa + o.z * fb;
       t.w = t.w * fa + o.w * fb;
-    }
-    add[wave][lane] = t;
-    add_l[wave][lane] = l;
-    add_top[wave][lane] = top;
-    __syncthreads();
-    const int32_t r = row0 + m;
-    if (wave == 0 && r < rows) {
-      float high = top;
+    };
+    if (mine) {
+      for (int32_t k0 = wave % share; k0 < n; k0 += kJoinAhead * share) {
+        float2 stat[kJoinAhead];
+        float4 o[kJoinAhead];
 #pragma unroll
-      for (int k = 1; k < 4; ++k) high = fmaxf(high, add_top[k][lane]);
-      const float ref = high == kNegInf ? 0.0f : high;
-      l = 0.0f;
-      t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int u = 0; u < kJoinAhead; ++u) {
+          const int32_t k = min(k0 + u * share, n - 1);
+          const int64_t slot = (int64_t(g0 + k) * p.cluster + member) * 2 + (k == 0 ? first : 0);
+          stat[u] = *reinterpret_cast<const float2 *>(p.stats + (slot * ROWS + m) * 2);
+          o[u] = *reinterpret_cast<const float4 *>(p.parts + slot * ROWS * p.latent +
+                                                   int64_t(cell) * 4);
+        }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = __builtin_amdgcn_exp2f(add_top[k][lane] - ref);
-        const float4 y = add[k][lane];
-        t.x += f * y.x;
-        t.y += f * y.y;
-        t.z += f * y.z;
-        t.w += f * y.w;
-        l += f * add_l[k][lane];
+        for (int u = 0; u < kJoinAhead; ++u)
+          if (k0 + u * share < n) take(stat[u].x, stat[u].y, o[u]);
       }
+    }
+    if (share > 1) {
+      add[wave][lane] = t;
+      add_stat[wave][lane] = make_float2(top, l);
+      __syncthreads();
+      if (wave % share == 0)
+        for (int k = 1; k < share; ++k)
+          take(add_stat[wave + k][lane].x, add_stat[wave + k][lane].y, add[wave + k][lane]);
+      __syncthreads();
+    }
+    if (mine && wave % share == 0) {
       const bool some = l > 0.0f || l != l;
       const float inv = some ? 1.0f / l : 0.0f;
-      const int64_t row = int64_t(sq.first) * p.heads + r;
+      const int64_t row = int64_t(rec[3]) + member * ROWS + m;
       *reinterpret_cast<uint2 *>(static_cast<char *>(p.out) +
                                  row * p.latent * int64_t(sizeof(T)) + (cell / ROWS) * 8) =
           make_uint2(Mfma<T>::pack(t.x * inv, t.y * inv), Mfma<T>::pack(t.z * inv, t.w * inv));
       if (cell < ROWS && p.lse != nullptr)
-        p.lse[row] = some ? high * 0.693147180559945f + logf(l) : kNegInf;
+        p.lse[row] = some ? top * 0.693147180559945f + logf(l) : kNegInf;
     }
-    __syncthreads();
   }
 }
 
@@ -570,7 +640,8 @@ int run_paged(PagedPlan &p, void *stream) {
                          : reinterpret_cast<const void *>(&latent_paged_join_kernel<T, DB, 1>);
   const int st = launch_kernel(fn, dim3(groups), kPagedBlock, 0, stream, &p);
   if (st != ROPE_OK) return st;
-  return launch_kernel(join, dim3(groups, uint32_t(p.join_slices)), kPagedBlock, 0, stream, &p);
+  return launch_kernel(join, dim3(uint32_t(p.clusters) * 2, uint32_t(p.cluster)), kJoinBlock, 0,
+                       stream, &p);
 }
 
 template <typename T>

@@ -67,7 +67,7 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t paged_workspace(int64_t tokens, int64_t heads, int64_t latent, int64_t sequences) {
   if (tokens <= 0 || heads <= 0 || latent <= 0 || sequences <= 0) return 0;
   const int64_t rows = std::min<int64_t>(64, paged_rows(tokens, heads, sequences));
-  return up(kPagedGroups * 16, 256) + up(2 * kPagedGroups * rows * 8, 256) +
+  return up(kPagedGroups * 2 * kJoinWords * 4, 256) + up(2 * kPagedGroups * rows * 8, 256) +
          2 * kPagedGroups * rows * latent * 4;
 }
 
@@ -173,15 +173,14 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
   const int64_t items = B + T * H / item_rows;
   const int64_t steps =
       std::max<int64_t>(1, up(p.max_pages * p.page_size, kPagedStep) / kPagedStep);
+  if (items > 0x7fffffff / steps)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "too many query rows and pages for one call");
   const int64_t most = kPagedGroups / p.cluster;
   p.clusters = int32_t(
       steps >= most ? most : std::min<int64_t>(most, up(items * steps, kXcds)));
-  // Parts of one item are few when there are many items, many when there is one: the fewer
-  // items, the more workgroups share the joining of one.
-  p.join_slices = int32_t(items <= 8 ? 32 : items <= 64 ? 16 : 8);
   char *w = static_cast<char *>(workspace);
   p.joins = reinterpret_cast<int32_t *>(w);
-  w += up(kPagedGroups * 16, 256);
+  w += up(kPagedGroups * 2 * kJoinWords * 4, 256);
   p.stats = reinterpret_cast<float *>(w);
   w += up(2 * kPagedGroups * rows * 8, 256);
   p.parts = reinterpret_cast<float *>(w);
@@ -193,6 +192,11 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
 namespace {
 
 constexpr int64_t kExpandedRows = 128;  // query rows (or keys) of a workgroup
+
+// The rows of a tile of 64 tokens are addressed by 32-bit byte offsets from its first.
+bool token_stride_fits(const rope_tensor *t) {
+  return t->shape[0] <= 1 || t->stride[0] * bytes_of(t->dtype) < (int64_t(1) << 25);
+}
 
 int64_t tiles_bound(int64_t tokens, int64_t sequences, int64_t each, bool offsets) {
   return offsets ? tokens / kExpandedRows + sequences
@@ -264,6 +268,9 @@ int plan_expanded(const rope_tensor *query, const rope_tensor *key, const rope_t
     if (!unit_inner(t) || !rows_aligned16(t))
       return reject(err, ROPE_ERR_PARAM_INVALID,
                     "rows need unit inner stride and 16-byte aligned starts");
+  for (const rope_tensor *t : {query, key, key_rope, value})
+    if (!token_stride_fits(t))
+      return reject(err, ROPE_ERR_PARAM_INVALID, "a token's stride is 32 MiB or more");
   if (!row_major(out) || !row_major(lse) || !aligned16(out->data))
     return reject(err, ROPE_ERR_PARAM_INVALID, "out and lse must be contiguous, out 16-byte aligned");
   ExpandedPlan &p = *plan;
@@ -342,9 +349,9 @@ int plan_expanded_backward(const rope_tensor *grad, const rope_tensor *query,
   for (int d = 0; d < 3; ++d)
     if (grad->shape[d] != out->shape[d])
       return reject(err, ROPE_ERR_PARAM_INVALID, "grad must have out's dtype and shape");
-  if (!unit_inner(grad) || !rows_aligned16(grad))
+  if (!unit_inner(grad) || !rows_aligned16(grad) || !token_stride_fits(grad))
     return reject(err, ROPE_ERR_PARAM_INVALID,
-                  "rows need unit inner stride and 16-byte aligned starts");
+                  "rows need unit inner stride, 16-byte aligned starts, token strides below 32 MiB");
   if (!outputs_apart({dquery, dkey, dkey_rope, dvalue},
                      {grad, query, key, key_rope, value, out, lse, query_offsets, key_offsets}))
     return reject(err, ROPE_ERR_PARAM_INVALID, "an output overlaps another tensor");

@@ -20,6 +20,7 @@ constexpr int64_t kLatentRope = 64;  // rotated tail of a latent row and of an e
 // is joined by a second kernel.
 constexpr int64_t kPagedGroups = kComputeUnits;  // one workgroup per compute unit (LDS)
 constexpr int64_t kPagedStep = 64;
+constexpr int64_t kJoinWords = 8;
 constexpr int64_t kXcds = 8;  // consecutive workgroups go to the eight XCDs in turn
 
 struct PagedPlan {
@@ -39,9 +40,10 @@ struct PagedPlan {
   int32_t row_blocks = 1;  // 32-row blocks of a workgroup (1 or 2)
   int32_t cluster = 1;     // workgroups of an item (1 or 2), on one XCD
   int32_t clusters = 0;
-  int32_t join_slices = 0;
   // workspace
-  int32_t *joins = nullptr;   // [clusters][4]: sequence, item, first part (0 or 1), parts
+  // [clusters][2][kJoinWords], for a cluster's first and last part: clusters that share the item
+  // (0: no part), the first of them, its part, the item's first row, rows from there
+  int32_t *joins = nullptr;
   float *stats = nullptr;     // [2 * groups][rows][2]: running maximum and sum of a part
   float *parts = nullptr;     // [2 * groups][latent / 4][rows][4]: unnormalised output of a part
 };

@@ -12,9 +12,12 @@
 // k values in the order of those rows -- 4 (l / 32) + {0..3, 8..11} -- which is what two
 // transposed LDS reads of four rows deliver.
 //
-// An LDS tile is cut into panels of 64 elements (128 bytes) a row.  The eight 16-byte chunks of
-// a row are permuted by the bit-reversed row number, so that neither 32 rows' reads of one chunk
-// nor a transposed read of four rows meets in the same banks.
+// An LDS tile is cut into panels of 64 elements (128 bytes) a row: two rows are one pass over the
+// 64 banks.  The eight 16-byte chunks of a row are permuted by a key so that no access meets
+// itself in a bank (SQ_LDS_BANK_CONFLICT 0): it takes all eight values over 16 rows, which keeps
+// 32 rows' reads of one chunk apart; it moves rows 0 and 2 (1 and 3) of four to different halves
+// of a row, for the transposed reads; and it differs by 1 only between rows 12 apart, for 16 rows'
+// reads of two neighbouring chunks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -95,16 +98,26 @@ __device__ inline s16x8 round8(const float *f) {
                                Mfma<T>::pack(f[4], f[5]), Mfma<T>::pack(f[6], f[7])));
 }
 
-// Permutation of a row's eight 16-byte chunks: chunk c of row r lies at c ^ chunk_key(r).
+// Permutation of a row's eight 16-byte chunks: chunk c of row r lies at c ^ chunk_key(r).  Rows
+// 16 apart share a key.
 __device__ inline uint32_t chunk_key(uint32_t row) {
-  return ((row & 1u) << 2) | (row & 2u) | ((row >> 2) & 1u);
+  return ((row & 2u) << 1) ^ ((row >> 1) & 2u) ^ (3u & (0u - ((row >> 3) & 1u)));
 }
 
-// 16 bytes per lane from global memory straight into LDS: lane l's bytes land at lds + 16 l.
-// `lds` is the same for all lanes of the wavefront.
-__device__ inline void load_lds16(const void *g, void *lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
-                                   (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+// Memory from `base` (the same for all lanes) on, addressed by 32-bit byte offsets.
+__device__ inline __amdgpu_buffer_rsrc_t buffer_at(const void *base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(0xffffffff),
+                                           0x00027000);
+}
+
+// 16 bytes per lane from global memory straight into LDS, from offset + uniform of the buffer:
+// lane l's bytes land at lds + 16 l.  `lds` and `uniform` are the same for all lanes of the
+// wavefront.  (Buffer loads: after the flat form, global_load_lds, the compiler cannot count LDS
+// reads and waits for all of them before each use.)
+__device__ inline void load_lds16(__amdgpu_buffer_rsrc_t buffer, uint32_t offset, int uniform,
+                                  void *lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (__attribute__((address_space(3))) void *)lds,
+                                           16, int(offset), uniform, 0, 0);
 }
 
 // Four rows of a 16-column block, transposed: lane i of each group of 16 points at row i / 4,
@@ -124,25 +137,61 @@ __device__ inline uint32_t panel_chunk(uint32_t row, uint32_t c) {
 }
 
 // Byte offset, inside a panel, that a lane supplies for a transposed read of rows
-// 4 (lane / 32) + {0..3} (+8, +16, ... rows: + 1024 bytes each) of the 32 columns of half
-// `e` (0 or 1) of the panel.
-__device__ inline uint32_t panel_transposed(uint32_t lane, uint32_t e) {
+// 4 (lane / 32) + {0..3} + 8 `up` (+ 16, 32, ... rows: + 2048 bytes each) of the 32 columns of
+// half `e` (0 or 1) of the panel.
+__device__ inline uint32_t panel_transposed(uint32_t lane, uint32_t e, uint32_t up) {
   const uint32_t i = lane & 15u;
-  const uint32_t row = 4u * (lane >> 5) + (i >> 2);
+  const uint32_t row = 4u * (lane >> 5) + (i >> 2) + 8u * up;
   const uint32_t c = 4u * e + 2u * ((lane >> 4) & 1u) + ((i & 3u) >> 1);
   return row * 128u + ((c ^ chunk_key(row)) << 4) + (i & 1u) * 8u;
 }
 
-// Value held by the lane 32 away.
-__device__ inline float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// The operand of 16 rows (from a multiple of 16) of 32 columns, transposed: k values in the order
+// 4 (lane / 32) + {0..3, 8..11}.
+__device__ inline s16x8 transposed_operand(const char *panel, uint32_t lane, uint32_t e) {
+  return join(read_transposed(panel + panel_transposed(lane, e, 0)),
+              read_transposed(panel + panel_transposed(lane, e, 1)));
+}
+
+// Maximum and sum over the two lanes 32 apart, and (max16) over the four 16 apart.
+__device__ inline float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline float max_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ inline float sum_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// Inclusive sum over the wavefront: shifts within 16 lanes, then each row's last lane to the
+// rows behind it.
+__device__ inline int32_t wave_scan(int32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
+}
 
 __device__ inline void wait_loads_all() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
-// Workgroup barrier that orders LDS accesses (direct-to-LDS loads are waited for separately).
+// Workgroup barrier that orders LDS accesses.  Direct-to-LDS loads are waited for separately:
+// written as waits and a barrier, since a fence would wait for those under way as well.
 __device__ inline void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  asm volatile("" ::: "memory");
 }
 
 }  // namespace
