@@ -40,6 +40,10 @@ __device__ inline uint32_t div_by(const FastDiv &f, uint32_t n) {
   return (t + ((n - t) >> f.s1)) >> f.s2;
 }
 
+// Beginning an item (its page numbers, its queries, a first tile that nothing hides) costs about
+// as much as two steps: the shares of the clusters are cut by steps and this.
+constexpr int32_t kItemCost = 2;
+
 // What a sequence asks for.
 struct Sequence {
   int32_t len;     // cached tokens
@@ -47,6 +51,7 @@ struct Sequence {
   int32_t count;   // query tokens
   int32_t items;
   int32_t steps;   // of one item
+  __device__ int32_t cost() const { return steps + kItemCost; }
 };
 
 // Lengths and offsets are device data: values outside their ranges are clamped, so that no
@@ -89,15 +94,18 @@ __device__ __forceinline__ void fetch_tile(const char *cache, int64_t piece, int
   const int32_t block = int32_t(piece >> 31);
   const uint32_t offset = (uint32_t(piece) & 0x7fffffffu) +
                           ((uint32_t(lane & 7) ^ chunk_key(uint32_t(8 * wave + (lane >> 3)))) << 4);
-  bool left = true;
-  while (left) {  // ends: every turn serves the first lane left
-    const int32_t now = __builtin_amdgcn_readfirstlane(block);
-    if (block == now) {
+  uint64_t left = __ballot(true);
+  while (left != 0) {  // ends: every turn serves the first lane left
+    const int32_t first = __builtin_amdgcn_readlane(block, __builtin_ctzll(left));
+    // opaque, or the compiler would take the lanes' own `block` for the address in the branch
+    int32_t now = first;
+    asm volatile("" : "+s"(now));
+    left &= ~__ballot(block == first);
+    if (block == first) {
       const auto buffer = buffer_at(cache + (int64_t(now) << 31));
 #pragma unroll
       for (int n = 0; n < PANELS; ++n)
         load_lds16(buffer, offset, n * 128, tile + n * 8192 + wave * 1024);
-      left = false;
     }
   }
 }
@@ -265,16 +273,16 @@ latent_paged_kernel(PagedPlan p) {
   const int32_t member = turn % p.cluster;
   const int32_t item_rows = ROWS * p.cluster;
 
-  // ---- the cluster's share [w0, w1) of all steps (their number fits 31 bits: plan) ----
+  // ---- the cluster's share [w0, w1) of all items' cost (it fits 31 bits: plan) ----
   Sequence sq = {};
   int32_t mine = 0, n = 0;
   if (tid < p.B) {
     sq = sequence(p, tid, item_rows, STEP);
-    n = sq.items * sq.steps;
+    n = sq.items * sq.cost();
   }
   for (int32_t b = tid + kPagedBlock; b < p.B; b += kPagedBlock) {
     const Sequence s = sequence(p, b, item_rows, STEP);
-    mine += s.items * s.steps;
+    mine += s.items * s.cost();
   }
   int32_t incl = wave_scan(n);
   const int32_t rest = p.B > kPagedBlock ? wave_scan(mine) : 0;
@@ -292,14 +300,14 @@ latent_paged_kernel(PagedPlan p) {
     return;
   }
   const int32_t w0 = int32_t(start), w1 = int32_t(min(int64_t(total), start + per));
-  // the sequence that holds step w0
+  // the sequence that w0 falls into
   int32_t before = 0;
   for (int32_t b0 = 0; b0 < p.B; b0 += kPagedBlock) {
     if (b0 > 0) {
       n = 0;
       if (b0 + tid < p.B) {
         sq = sequence(p, b0 + tid, item_rows, STEP);
-        n = sq.items * sq.steps;
+        n = sq.items * sq.cost();
       }
       incl = wave_scan(n);
     }
@@ -329,16 +337,17 @@ latent_paged_kernel(PagedPlan p) {
   sq = {uniform(found[1]), uniform(found[2]), uniform(found[3]), uniform(found[4]),
         uniform(found[5])};
   const int32_t into = w0 - uniform(found[6]);
-  int32_t item = uniform(int32_t(uint32_t(into) / uint32_t(sq.steps)));
-  int32_t st0 = into - item * sq.steps;
+  int32_t item = uniform(int32_t(uint32_t(into) / uint32_t(sq.cost())));
+  int32_t x0 = into - item * sq.cost();  // where in the item
   int32_t w = w0;
   uint32_t partial = 0;  // bit s: part s of this cluster is one of an item's several
 
   while (true) {
-    const int32_t st1 = min(sq.steps, st0 + (w1 - w));
+    const int32_t x1 = min(sq.cost(), x0 + (w1 - w));
+    const int32_t st0 = max(0, x0 - kItemCost), st1 = max(0, x1 - kItemCost);  // steps
     const int32_t rows = sq.count * p.heads;
     const int32_t row0 = item * item_rows + member * ROWS;
-    if (row0 < rows) {
+    if (row0 < rows && st0 < st1) {
       // page numbers of as many of the steps from `st` on as the table holds; returns the step
       // that they end before
       int32_t page0 = 0;
@@ -355,7 +364,7 @@ latent_paged_kernel(PagedPlan p) {
                    ? int32_t((int64_t(page0 + pages) * p.page_size) / STEP)
                    : st1;
       };
-      __syncthreads();  // what the last segment read of ids, tiles and row_max
+      lds_barrier();  // what the last segment read of ids, tiles and row_max
       int32_t end = st1;
       if (sq.len > 0) end = load_ids(st0);
 
@@ -444,7 +453,7 @@ latent_paged_kernel(PagedPlan p) {
         int32_t st = st0;
         while (true) {
           // ---- the steps: the next tile is on its way while one is multiplied ----
-          __syncthreads();
+          lds_barrier();
           const char *cache = static_cast<const char *>(p.cache);
           fetch_tile<PANELS>(cache, tile_piece<T>(p, ids, page0, st * STEP, sq.len, wave, lane),
                              wave, lane, tiles);
@@ -458,16 +467,16 @@ latent_paged_kernel(PagedPlan p) {
                         ids, cache, next, st);
           }
           if (st >= st1) break;
-          __syncthreads();
+          lds_barrier();
           end = load_ids(st);
         }
       }
 
       // ---- sums of the wavefronts that shared a row ----
-      __syncthreads();
+      lds_barrier();
       s_sum = sum_quarters(s_sum);
       if (lane < 16) row_max[S::part(wave)][S::s_row(wave, lane)] = s_sum;
-      __syncthreads();
+      lds_barrier();
 
       // ---- the segment's result: a whole item's output, or a part for the joining kernel ----
       const bool whole = st0 == 0 && st1 == sq.steps;
@@ -518,22 +527,23 @@ latent_paged_kernel(PagedPlan p) {
         }
       }
     }
-    if (st0 != 0 || st1 != sq.steps) {
+    if (st0 < st1 && (st0 != 0 || st1 != sq.steps)) {
       const int part = w == w0 ? 0 : 1;
       partial |= 1u << part;
       if (tid == 0 && member == 0) {
-        const uint32_t begin = uint32_t(w - st0), first_g = begin / uint32_t(per);
+        const uint32_t begin = uint32_t(w - x0), u_per = uint32_t(per);
+        const uint32_t first_g = (begin + kItemCost) / u_per;
         int32_t *rec = p.joins + (g * 2 + part) * kJoinWords;
-        rec[0] = int32_t((begin + uint32_t(sq.steps) - 1) / uint32_t(per) - first_g + 1);
+        rec[0] = int32_t((begin + uint32_t(sq.cost()) - 1) / u_per - first_g + 1);
         rec[1] = int32_t(first_g);
-        rec[2] = begin == first_g * uint32_t(per) ? 0 : 1;
+        rec[2] = begin <= first_g * u_per ? 0 : 1;
         rec[3] = sq.first * p.heads + item * item_rows;
         rec[4] = rows - item * item_rows;
       }
     }
-    w += st1 - st0;
+    w += x1 - x0;
     if (w >= w1) break;
-    st0 = 0;
+    x0 = 0;
     if (++item >= sq.items) {
       item = 0;
       do {  // ends: w < w1 <= total, so a later sequence has items

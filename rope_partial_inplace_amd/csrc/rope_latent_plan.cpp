@@ -173,7 +173,7 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
   const int64_t items = B + T * H / item_rows;
   const int64_t steps =
       std::max<int64_t>(1, up(p.max_pages * p.page_size, kPagedStep) / kPagedStep);
-  if (items > 0x7fffffff / steps)
+  if (items > 0x7fffffff / (steps + 8))
     return reject(err, ROPE_ERR_PARAM_INVALID, "too many query rows and pages for one call");
   const int64_t most = kPagedGroups / p.cluster;
   p.clusters = int32_t(

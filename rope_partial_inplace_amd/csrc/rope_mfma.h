@@ -106,7 +106,10 @@ __device__ inline uint32_t chunk_key(uint32_t row) {
 
 // Memory from `base` (the same for all lanes) on, addressed by 32-bit byte offsets.
 __device__ inline __amdgpu_buffer_rsrc_t buffer_at(const void *base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(0xffffffff),
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(b >> 32))))) << 32 |
+                     uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(b))));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(u), 0, int(0xffffffff),
                                            0x00027000);
 }
 

@@ -287,18 +287,23 @@ def test_paged_repeats_are_identical():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
-def test_paged_past_32_bit_offsets():
-    """A cache of 9 GiB whose used pages lie at both ends."""
-    latent, page, pages = 512, 64, 65536
+@pytest.mark.parametrize("page", [1, 5, 64])
+def test_paged_past_32_bit_offsets(page):
+    """A cache of 4.5 GiB whose used pages are scattered over all of it (neighbouring tokens of a
+    sequence 2 GiB and more apart)."""
+    latent, row_bytes, n = 512, 1152, 250
+    pages = (9 << 29) // (row_bytes * page)
     cache = torch.zeros(pages, page, latent + ROPE, dtype=BF16, device=DEV)
     g = gen_of(2)
-    table = torch.tensor([[pages - 1, 0, pages // 2, pages - 2]], device=DEV)
-    cache[table[0]] = randn(g, BF16, 4, page, latent + ROPE)
-    rows = [cache[table[0]].reshape(-1, latent + ROPE)[:250]]
+    need = -(-n // page)
+    table = torch.randperm(pages, generator=g, device=DEV)[:need]
+    table[0], table[-1] = pages - 1, 0
+    cache[table] = randn(g, BF16, need, page, latent + ROPE)
+    rows = [cache[table].reshape(-1, latent + ROPE)[:n]]
     q = randn(g, BF16, 1, 16, latent + ROPE)
-    out, lse = ra.rope_latent_attention_paged(q, cache, table, torch.tensor([250], device=DEV),
+    out, lse = ra.rope_latent_attention_paged(q, cache, table[None], torch.tensor([n], device=DEV),
                                               latent, 0.07)
-    want, wl, bound, lb = paged_reference(q, rows, [250], [1], 0.07, latent, BF16)
+    want, wl, bound, lb = paged_reference(q, rows, [n], [1], 0.07, latent, BF16)
     assert_within(out, want, bound, "out")
     assert_within(lse, wl, lb, "lse")
 
