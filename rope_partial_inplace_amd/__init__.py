@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from .build import LIB_PATH
 
@@ -88,7 +89,7 @@ def _load() -> ctypes.CDLL:
                                                ctypes.c_int64, ctypes.c_int, ctypes.c_int64,
                                                P(RopeTensor), P(RopeTensor), ctypes.c_void_p]
     lib.rope_with_cos_sin_cache_v2.restype = ctypes.c_int
-    T = P(RopeTensor)
+    T = ctypes.c_void_p  # a RopeTensor by reference, or its bytes
     lib.rope_append_paged_cache.argtypes = [T, T, T, T, T, T, ctypes.c_int64, ctypes.c_int64,
                                             ctypes.c_int, T, T, T, ctypes.c_void_p]
     lib.rope_append_paged_cache.restype = ctypes.c_int
@@ -327,27 +328,78 @@ def rope_with_cos_sin_cache_v2(positions, query_in, key_in, cos_sin_cache, mrope
 
 
 # ---- paged cache and latent attention ---------------------------------------------------------
+# A decoding step's calls take the GPU a few microseconds, so their marshalling is kept short:
+# descriptions are packed as bytes, and the device and stream read as numbers.
 
-def _describe_all(tensors):
-    """References to the descriptions of tensors (None stays None), and the descriptions."""
-    descs = [None if t is None else describe(t) for t in tensors]
-    return [None if d is None else ctypes.byref(d) for d in descs], descs
+_PACK = [None] + [struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack
+                  for n in range(1, 5)]
+_DTYPE_CODES = {}
 
 
-def _allocating_on(stream, dev):
-    """Context in which torch allocates for work on `stream`: outputs and workspaces that a call
-    makes belong to the stream it runs on."""
-    import contextlib
+def _pack(t):
+    """The bytes of a ``rope_tensor`` describing a torch tensor (None stays None)."""
+    if t is None:
+        return None
+    n = t.dim()
+    if not 1 <= n <= 4:
+        raise RopeError(ROPE_ERR_PARAM_INVALID, "tensors must have 1 to 4 dims")
+    dtype = t.dtype
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        code = _DTYPE_CODES[dtype] = _dtype_code(t)
+    return _PACK[n](t.data_ptr(), code, n, *t.shape, *t.stride())
 
+
+def _device_index(tensors) -> int:
+    """GPU of the tensors (-1: none of them has elements)."""
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d != dev:
+            if t.numel() == 0:
+                continue
+            if d < 0:
+                raise RopeError(ROPE_ERR_PARAM_INVALID,
+                                "tensors must live in GPU memory (torch device 'cuda')")
+            if dev >= 0:
+                raise RopeError(ROPE_ERR_PARAM_INVALID, "tensors are on different devices")
+            dev = d
+    return dev
+
+
+def _raw_stream(stream, dev: int):
     import torch
-    if stream is None or dev is None:
-        return contextlib.nullcontext()
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _run_on(dev: int, fn, *args):
+    """One C call with GPU `dev` as the current HIP device."""
+    import torch
+    if dev < 0 or dev == torch.cuda.current_device():
+        code = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args)
+    if code != ROPE_OK:
+        raise RopeError(code, last_error())
+
+
+def _new(stream, dev: int, *specs):
+    """New tensors of (shape, dtype, device), None for a spec of None.  Torch allocates them for
+    the stream that the call runs on: outputs and workspaces belong to it."""
+    import torch
+    if stream is None or dev < 0:
+        return [s and torch.empty(s[0], dtype=s[1], device=s[2]) for s in specs]
     if not isinstance(stream, torch.cuda.Stream):
         handle = getattr(stream, "cuda_stream", stream)
-        if not handle:
-            return torch.cuda.stream(torch.cuda.default_stream(dev))
-        stream = torch.cuda.ExternalStream(handle, device=dev)
-    return torch.cuda.stream(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
+                  else torch.cuda.default_stream(dev))
+    with torch.cuda.stream(stream):
+        return [s and torch.empty(s[0], dtype=s[1], device=s[2]) for s in specs]
 
 
 def rope_append_paged_cache(positions, slots, key, key_cache, cos_sin_cache, value=None,
@@ -361,17 +413,14 @@ def rope_append_paged_cache(positions, slots, key, key_cache, cos_sin_cache, val
     [rot_start, rot_start + rotaryDim) of every head are rotated, rotaryDim the width of
     cos_sin_cache [maxSeqLen, rotaryDim].  Returns query_out [T, Nq, Dq] (allocated when not
     given; it may be query itself), or None without a query."""
-    import torch
-    dev = _device_of([positions, slots, query, key, value, cos_sin_cache, query_out, key_cache,
-                      value_cache])
+    dev = _device_index((positions, slots, query, key, value, cos_sin_cache, query_out, key_cache,
+                         value_cache))
     if query is not None and query_out is None:
-        with _allocating_on(stream, dev):
-            query_out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
-    refs, _keep = _describe_all([positions, slots, query, key, value, cos_sin_cache, query_out,
-                                 key_cache, value_cache])
-    _check(_on_device(dev, LIB.rope_append_paged_cache,
-                      (*refs[:6], int(query_rot_start), int(key_rot_start),
-                       int(bool(is_neox_style)), *refs[6:], _stream_handle(stream, dev))))
+        query_out, = _new(stream, dev, (query.shape, query.dtype, query.device))
+    _run_on(dev, LIB.rope_append_paged_cache, _pack(positions), _pack(slots), _pack(query),
+            _pack(key), _pack(value), _pack(cos_sin_cache), query_rot_start, key_rot_start,
+            bool(is_neox_style), _pack(query_out), _pack(key_cache), _pack(value_cache),
+            _raw_stream(stream, dev))
     return query_out
 
 
@@ -386,26 +435,22 @@ def rope_latent_attention_paged(query, latent_cache, page_table, seq_lens, laten
     n sees the cached rows below seq_len - n + 1 + i.  Returns (out [T, heads, latent_dim],
     lse [T, heads] float32)."""
     import torch
-    dev = _device_of([query, latent_cache, page_table, seq_lens, query_offsets, out, lse])
+    dev = _device_index((query, latent_cache, page_table, seq_lens, query_offsets, out, lse))
     if latent_cache.dim() == 4 and latent_cache.shape[2] == 1:
         latent_cache = latent_cache.squeeze(2)
     if query.dim() != 3 or seq_lens.dim() != 1:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "query must be 3-D and seq_lens 1-D")
-    T, heads = query.shape[0], query.shape[1]
-    need = LIB.rope_latent_attention_paged_workspace(T, heads, int(latent_dim), seq_lens.shape[0])
-    with _allocating_on(stream, dev):
-        if out is None:
-            out = torch.empty((T, heads, max(0, int(latent_dim))), dtype=query.dtype,
-                              device=query.device)
-        if lse is None:
-            lse = torch.empty((T, heads), dtype=torch.float32, device=query.device)
-        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
-    refs, _keep = _describe_all([query, latent_cache, page_table, seq_lens, query_offsets, out,
-                                 lse])
-    _check(_on_device(dev, LIB.rope_latent_attention_paged,
-                      (*refs[:5], int(latent_dim), float(scale), *refs[5:],
-                       workspace.data_ptr() if need else None, need,
-                       _stream_handle(stream, dev))))
+    T, heads, _ = query.shape
+    need = LIB.rope_latent_attention_paged_workspace(T, heads, latent_dim, seq_lens.shape[0])
+    d = query.device
+    new_out, new_lse, workspace = _new(
+        stream, dev,
+        ((T, heads, max(0, latent_dim)), query.dtype, d) if out is None else None,
+        ((T, heads), torch.float32, d) if lse is None else None, (need, torch.uint8, d))
+    out, lse = out if new_out is None else new_out, lse if new_lse is None else new_lse
+    _run_on(dev, LIB.rope_latent_attention_paged, _pack(query), _pack(latent_cache),
+            _pack(page_table), _pack(seq_lens), _pack(query_offsets), latent_dim, scale,
+            _pack(out), _pack(lse), workspace.data_ptr(), need, _raw_stream(stream, dev))
     return out, lse
 
 
@@ -426,19 +471,20 @@ def rope_latent_attention(query, key, key_rope, value, scale: float, causal: boo
     first m - n + 1 + i keys.  Returns (out [Tq, heads, dim], lse [Tq, heads] float32).  Not
     recorded by autograd: that is latent_attention."""
     import torch
-    dev = _device_of([query, key, key_rope, value, query_offsets, key_offsets, out, lse])
+    dev = _device_index((query, key, key_rope, value, query_offsets, key_offsets, out, lse))
     if query.dim() != 3 or value.dim() != 3:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "query and value must be 3-D")
-    with _allocating_on(stream, dev):
-        if out is None:
-            out = torch.empty((*query.shape[:2], value.shape[2]), dtype=query.dtype,
-                              device=query.device)
-        if lse is None:
-            lse = torch.empty(query.shape[:2], dtype=torch.float32, device=query.device)
-    refs, _keep = _describe_all([query, key, key_rope, value, query_offsets, key_offsets, out, lse])
-    _check(_on_device(dev, LIB.rope_latent_attention,
-                      (*refs[:6], _sequences(num_sequences, query_offsets), float(scale),
-                       int(bool(causal)), *refs[6:], _stream_handle(stream, dev))))
+    T, heads, _ = query.shape
+    d = query.device
+    new_out, new_lse = _new(
+        stream, dev,
+        ((T, heads, value.shape[2]), query.dtype, d) if out is None else None,
+        ((T, heads), torch.float32, d) if lse is None else None)
+    out, lse = out if new_out is None else new_out, lse if new_lse is None else new_lse
+    _run_on(dev, LIB.rope_latent_attention, _pack(query), _pack(key), _pack(key_rope),
+            _pack(value), _pack(query_offsets), _pack(key_offsets),
+            _sequences(num_sequences, query_offsets), scale, bool(causal), _pack(out), _pack(lse),
+            _raw_stream(stream, dev))
     return out, lse
 
 
@@ -448,21 +494,18 @@ def rope_latent_attention_backward(grad, query, key, key_rope, value, out, lse, 
     """Gradients of rope_latent_attention's out with respect to (query, key, key_rope, value), for
     the gradient ``grad`` of out; out and lse are the forward call's."""
     import torch
-    tensors = [grad, query, key, key_rope, value, out, lse, query_offsets, key_offsets]
-    dev = _device_of(tensors)
+    dev = _device_index((grad, query, key, key_rope, value, out, lse, query_offsets, key_offsets))
     if query.dim() != 3:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "query must be 3-D")
     need = LIB.rope_latent_attention_backward_workspace(query.shape[0], key.shape[0],
                                                         query.shape[1])
-    with _allocating_on(stream, dev):
-        grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                 for t in (query, key, key_rope, value)]
-        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
-    refs, _keep = _describe_all(tensors + grads)
-    _check(_on_device(dev, LIB.rope_latent_attention_backward,
-                      (*refs[:9], _sequences(num_sequences, query_offsets), float(scale),
-                       int(bool(causal)), *refs[9:], workspace.data_ptr() if need else None, need,
-                       _stream_handle(stream, dev))))
+    *grads, workspace = _new(stream, dev,
+                             *((t.shape, t.dtype, t.device) for t in (query, key, key_rope, value)),
+                             (need, torch.uint8, query.device))
+    _run_on(dev, LIB.rope_latent_attention_backward, _pack(grad), _pack(query), _pack(key),
+            _pack(key_rope), _pack(value), _pack(out), _pack(lse), _pack(query_offsets),
+            _pack(key_offsets), _sequences(num_sequences, query_offsets), scale, bool(causal),
+            *map(_pack, grads), workspace.data_ptr(), need, _raw_stream(stream, dev))
     return tuple(grads)
 
 
