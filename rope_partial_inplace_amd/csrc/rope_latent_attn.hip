@@ -128,32 +128,69 @@ __device__ __forceinline__ void fetch_rows(const char *base, int64_t stride, int
   }
 }
 
-// C (32 x 32) of 32 rows of LDS panels (from row `row0`) times register operands.
-template <typename T, int PANELS>
-__device__ __forceinline__ f32x16 row_product(const char *__restrict__ lds, int row0, int lane,
-                                              const s16x8 *b, f32x16 c) {
+// The compiler would read every operand just before its product; the barriers keep the reads of
+// the next operands ahead of the products of these.
+__device__ __forceinline__ void hold_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// Row operands of panel n: 32 rows from row0, k values 16 c .. + 15.
+__device__ __forceinline__ void load_panel(const char *lds, int row0, int n, int lane,
+                                           s16x8 (&f)[4]) {
 #pragma unroll
-  for (int n = 0; n < PANELS; ++n)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const s16x8 a = as_operand(*reinterpret_cast<const uint4 *>(
-          lds + n * 8192 + panel_chunk(uint32_t(row0 + (lane & 31)), 2u * k + (uint32_t(lane) >> 5))));
-      c = Mfma<T>::mul(a, b[n * 4 + k], c);
-    }
-  return c;
+  for (int c = 0; c < 4; ++c)
+    f[c] = as_operand(*reinterpret_cast<const uint4 *>(
+        lds + n * 8192 + panel_chunk(uint32_t(row0 + (lane & 31)), 2u * c + (uint32_t(lane) >> 5))));
 }
 
-// acc[d] += (32 columns d of 32 LDS rows from row0, transposed) times the 32 x 32 operand whose
-// two steps of 16 are b0, b1.
+// Transposed operand of 32 columns d of the 16 rows from row0.
+__device__ __forceinline__ s16x8 load_column(const char *lds, int row0, int d, int lane) {
+  return transposed_operand(lds + (d / 2) * 8192 + row0 * 128, uint32_t(lane), uint32_t(d & 1));
+}
+
+// acc[d] += (column blocks d of 32 LDS rows from row0) times the 32 x 32 operand whose two steps
+// of 16 are b0, b1.
 template <typename T, int BLOCKS>
-__device__ __forceinline__ void column_product(const char *__restrict__ lds, int row0, int lane,
-                                               s16x8 b0, s16x8 b1, f32x16 *acc) {
+__device__ __forceinline__ void column_product(const char *lds, int row0, int lane, s16x8 b0,
+                                               s16x8 b1, f32x16 *acc) {
+  s16x8 f[2][2];
+  f[0][0] = load_column(lds, row0, 0, lane);
+  f[0][1] = load_column(lds, row0 + 16, 0, lane);
 #pragma unroll
   for (int d = 0; d < BLOCKS; ++d) {
-    const char *at = lds + (d / 2) * 8192 + row0 * 128;
-    acc[d] = Mfma<T>::mul(transposed_operand(at, uint32_t(lane), uint32_t(d & 1)), b0, acc[d]);
-    acc[d] = Mfma<T>::mul(transposed_operand(at + 2048, uint32_t(lane), uint32_t(d & 1)), b1, acc[d]);
+    if (d + 1 < BLOCKS) {
+      f[(d + 1) % 2][0] = load_column(lds, row0, d + 1, lane);
+      f[(d + 1) % 2][1] = load_column(lds, row0 + 16, d + 1, lane);
+    }
+    hold_order();
+    acc[d] = Mfma<T>::mul(f[d % 2][0], b0, acc[d]);
+    acc[d] = Mfma<T>::mul(f[d % 2][1], b1, acc[d]);
+    hold_order();
   }
+}
+
+// C += 32 rows of LDS panels (from row0) times register operands, AHEAD of them read ahead.
+template <typename T, int PANELS, int AHEAD = 4>
+__device__ __forceinline__ f32x16 row_product(const char *lds, int row0, int lane, const s16x8 *b,
+                                              f32x16 c) {
+  constexpr int STEPS = PANELS * 4 / AHEAD;
+  s16x8 f[2][AHEAD];
+  auto load = [](const char *lds, int row0, int lane, int n, s16x8 *to) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      to[k] = as_operand(*reinterpret_cast<const uint4 *>(
+          lds + (n * AHEAD + k) / 4 * 8192 +
+          panel_chunk(uint32_t(row0 + (lane & 31)),
+                      2u * ((n * AHEAD + k) % 4) + (uint32_t(lane) >> 5))));
+  };
+  load(lds, row0, lane, 0, f[0]);
+#pragma unroll
+  for (int n = 0; n < STEPS; ++n) {
+    if (n + 1 < STEPS) load(lds, row0, lane, n + 1, f[(n + 1) % 2]);
+    hold_order();
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) c = Mfma<T>::mul(f[n % 2][k], b[n * AHEAD + k], c);
+    hold_order();
+  }
+  return c;
 }
 
 // 16-byte pieces of a row as register operands: 8 (lane / 32) elements into every 16.
@@ -200,6 +237,10 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
                                 (int64_t(q.first + row) * p.q_tok + head * p.q_head) *
                                     int64_t(sizeof(T)),
                             live, lane, qf);
+  if (p.negative) {  // a negative scale becomes the queries' sign, so that maxima stay maxima
+#pragma unroll
+    for (int i = 0; i < NP * 4 + 4; ++i) qf[i] ^= short(0x8000);
+  }
   // keys a row sees, the fewest and the most of the workgroup's rows
   const int32_t shift = k.count - q.count + 1;
   const int32_t limit = !live ? 0 : p.causal ? row + shift : k.count;
@@ -224,20 +265,36 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
 
   auto step = [&](const char *__restrict__ cur, char *__restrict__ other, int32_t j0) {
     if (j0 + kTile < most) fetch(j0 + kTile, other);
-    f32x16 s[2];
+    // S^T of the tile's two halves, a panel's operands read ahead
+    f32x16 s[2] = {};
+    {
+      s16x8 f[2][2][4];
+      load_panel(cur, 0, 0, lane, f[0][0]);
+      load_panel(cur, 32, 0, lane, f[0][1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      s[i] = row_product<T, NP + 1>(cur, i * 32, lane, qf, f32x16{});
-    const bool whole = j0 + kTile <= min(least, k.count);
-    float e[32], best = kNegInf;
+      for (int n = 0; n < NP + 1; ++n) {
+        if (n < NP) {
+          load_panel(cur, 0, n + 1, lane, f[(n + 1) % 2][0]);
+          load_panel(cur, 32, n + 1, lane, f[(n + 1) % 2][1]);
+        }
+        hold_order();
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      float x = s[r / 16][r % 16] * p.scale_log2;
-      if (!whole) x = j0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < limit ? x : kNegInf;
-      e[r] = x;
-      best = fmaxf(best, x);
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) s[i] = Mfma<T>::mul(f[n % 2][i][k], qf[n * 4 + k], s[i]);
+        hold_order();
+      }
     }
-    best = max_halves(best);
+    if (j0 + kTile > min(least, k.count)) {  // some row does not see all of it
+      asm volatile("");  // a branch: most tiles need no masks
+#pragma unroll
+      for (int r = 0; r < 32; ++r)
+        if (j0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 >= limit) s[r / 16][r % 16] = kNegInf;
+    }
+    float best = kNegInf;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) best = fmaxf(best, s[r / 16][r % 16]);
+    best = max_halves(best) * p.scale_log2;  // the scale is not negative: see the operands
     // rescale only when the maximum rises by more than 8 (weights of up to 2^8 are carried)
     if (__any(best > top + 8.0f)) {
       float f = 1.0f;
@@ -251,14 +308,17 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
     }
     const float ref = top == kNegInf ? 0.0f : top;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      e[r] = __builtin_amdgcn_exp2f(e[r] - ref);
-      sum += e[r];
-    }
+    for (int i = 0; i < 2; ++i) {
+      float e[16], part = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      column_product<T, NP * 2>(cur + (NP + 1) * 8192, i * 32, lane, round8<T>(e + 16 * i),
-                                round8<T>(e + 16 * i + 8), acc);
+      for (int r = 0; r < 16; ++r) {
+        e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][r], p.scale_log2, -ref));
+        part += e[r];
+      }
+      sum += part;
+      column_product<T, NP * 2>(cur + (NP + 1) * 8192, i * 32, lane, round8<T>(e),
+                                round8<T>(e + 8), acc);
+    }
   };
 
   if (most > 0) fetch(0, tiles);
@@ -337,6 +397,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
     fetch_rows<1>(rb, p.kr_tok * es, j0, k.count - 1, wave, lane, to + NP * 8192);
     fetch_rows<NP>(vb, p.v_tok * es, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
   };
+  const float scale2 = p.negative ? -p.scale_log2 : p.scale_log2;
   f32x16 acc[NP * 2 + 2];
 #pragma unroll
   for (int d = 0; d < NP * 2 + 2; ++d) acc[d] = f32x16{};
@@ -346,12 +407,12 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
     const bool whole = j0 + kTile <= min(least, k.count);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const f32x16 s = row_product<T, NP + 1>(cur, i * 32, lane, qf, f32x16{});
-      const f32x16 dp = row_product<T, NP>(cur + (NP + 1) * 8192, i * 32, lane, gf, f32x16{});
+      const f32x16 s = row_product<T, NP + 1, 2>(cur, i * 32, lane, qf, f32x16{});
+      const f32x16 dp = row_product<T, NP, 2>(cur + (NP + 1) * 8192, i * 32, lane, gf, f32x16{});
       float e[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        float w = __builtin_amdgcn_exp2f(s[r] * p.scale_log2 - lse2);
+        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, -lse2));
         if (!whole) w = j0 + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < limit ? w : 0.0f;
         e[r] = w * (dp[r] - delta);
       }
@@ -415,7 +476,8 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
   const char *gb = static_cast<const char *>(p.grad) + (int64_t(q.first) * p.g_tok + head * p.g_head) * es;
   const float *lse = p.lse + int64_t(q.first) * p.heads + head;
   const float *del = p.delta + int64_t(q.first) * p.heads + head;
-  // the statistics of a tile's rows: read by the first wavefront, one row a lane
+  // The statistics of a tile's rows: read by the first wavefront, one row a lane, a tile ahead
+  // (and only looked at when that tile's turn comes, so that nothing waits for them before).
   float next_lse = 0.0f, next_delta = 0.0f;
   auto fetch = [&](int32_t i0, char *__restrict__ to) {
     fetch_rows<NP + 1>(qb, p.q_tok * es, i0, q.count - 1, wave, lane, to);
@@ -423,17 +485,20 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
   };
   auto fetch_stats = [&](int32_t i0) {
     if (wave == 0) {
-      const int32_t i = i0 + lane;
-      next_lse = i < q.count ? lse[int64_t(i) * p.heads] : kNegInf;
-      next_delta = i < q.count ? del[int64_t(i) * p.heads] : 0.0f;
+      const int64_t i = int64_t(min(i0 + lane, q.count - 1)) * p.heads;
+      next_lse = lse[i];
+      next_delta = del[i];
     }
   };
-  auto put_stats = [&](int slot) {
+  auto put_stats = [&](int slot, int32_t i0) {
     if (wave == 0) {  // rows that see nothing, or do not exist: p = exp2(s - infinity) = 0
-      stats[slot][0][lane] = next_lse == kNegInf ? __builtin_huge_valf() : next_lse * kLog2eF;
-      stats[slot][1][lane] = next_delta;
+      const bool real = i0 + lane < q.count;
+      stats[slot][0][lane] =
+          real && next_lse != kNegInf ? next_lse * kLog2eF : __builtin_huge_valf();
+      stats[slot][1][lane] = real ? next_delta : 0.0f;
     }
   };
+  const float scale2 = p.negative ? -p.scale_log2 : p.scale_log2;
   f32x16 dk[NP * 2 + 2], dv[NP * 2];
 #pragma unroll
   for (int d = 0; d < NP * 2 + 2; ++d) dk[d] = f32x16{};
@@ -456,7 +521,7 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
         const f32x4 d = *reinterpret_cast<const f32x4 *>(st + kTile + at_row);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = __builtin_amdgcn_exp2f(s[4 * c + r] * p.scale_log2 - l[r]);
+          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * c + r], scale2, -l[r]));
           if (!whole) x = key < i0 + at_row + r + shift ? x : 0.0f;
           w[4 * c + r] = x;
           e[4 * c + r] = x * (dp[4 * c + r] - d[r]);
@@ -474,7 +539,7 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
   for (int32_t n = n0; n * kTile < q.count; ++n) {
     const int slot = (n - n0) & 1;
     wait_loads_all();
-    put_stats(slot);
+    put_stats(slot, n * kTile);
     lds_barrier();
     if ((n + 1) * kTile < q.count) fetch_stats((n + 1) * kTile);
     step(tiles + slot * TILE, tiles + (slot ^ 1) * TILE, &stats[slot][0][0], n * kTile);

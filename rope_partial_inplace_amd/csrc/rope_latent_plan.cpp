@@ -311,7 +311,10 @@ int plan_expanded(const rope_tensor *query, const rope_tensor *key, const rope_t
   p.heads = int32_t(H);
   p.dim = int32_t(dim);
   p.scale = float(scale);
-  p.scale_log2 = float(scale * kLog2e);
+  // (not 0, which would turn a masked score of -infinity into a NaN; no score is large enough for
+  // 1e-30 to differ from it)
+  p.scale_log2 = float(std::max(std::fabs(scale) * kLog2e, 1e-30));
+  p.negative = scale < 0;
   p.out = out->data;
   p.lse = static_cast<float *>(lse->data);
   return ROPE_OK;

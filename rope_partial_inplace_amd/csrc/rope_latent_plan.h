@@ -66,7 +66,9 @@ struct ExpandedPlan {
   int64_t q_off_stride = 0, k_off_stride = 0;
   int64_t Tq = 0, Tk = 0, B = 0, q_each = 0, k_each = 0;  // *_each: tokens without offsets
   int32_t heads = 0, dim = 0;
-  float scale = 0, scale_log2 = 0;
+  float scale = 0;
+  float scale_log2 = 0;   // |scale| * log2(e), at least 1e-30
+  bool negative = false;  // scale < 0: the forward kernel turns the queries' signs
   void *out = nullptr;
   float *lse = nullptr;
   // backward

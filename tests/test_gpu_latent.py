@@ -120,6 +120,12 @@ def test_equal_sequences_without_offsets():
     check([1] * 5, [77] * 5, 4, 64, F16, False, seed=6, spare=0, use_offsets=False)
 
 
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30])
+def test_other_scales(scale):
+    check([100, 7], [150, 7], 2, 64, BF16, True, seed=3, scale=scale)
+    check([70], [200], 2, 128, F16, False, seed=4, scale=scale)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_large_scores_and_a_rising_maximum(dtype):
     """Scores of +-100 and more (weights down to zero), and keys ordered so that the running

@@ -235,6 +235,11 @@ def test_paged_rising_and_falling_scores():
         assert_within(out, want, bound, "out")
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30])
+def test_paged_other_scales(scale):
+    check_paged([300, 5, 77], [1, 2, 1], 16, 128, BF16, 16, seed=5, scale=scale)
+
+
 def test_paged_without_offsets_and_strided_views():
     lens, heads, latent = [100, 260, 31], 12, 256
     q, cache, table, sl, rows = paged_inputs(lens, [2, 2, 2], heads, latent, BF16, 16, 8)
