@@ -33,6 +33,7 @@ namespace ropeamd {
 namespace {
 
 constexpr int kBlockThreads = 256;
+constexpr int kKeyThreads = 512;  // of the kernel of dk and dv
 constexpr int kRows = 128;  // query rows (or keys) of a workgroup
 constexpr int kTile = 64;   // keys (or query rows) in LDS at a time
 constexpr float kLog2eF = 1.44269504f, kLn2F = 0.693147180f;
@@ -56,8 +57,8 @@ struct TileAt {
   int32_t seq, tile;
 };
 
-// `scratch`: six words of LDS, free again on return.
-template <bool QUERY>
+// `scratch`: ten words of LDS, free again on return.
+template <bool QUERY, int THREADS>
 __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scratch) {
   const int64_t *off = QUERY ? p.q_off : p.k_off;
   const int64_t each = QUERY ? p.q_each : p.k_each;
@@ -66,11 +67,11 @@ __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scrat
     if (per == 0 || t / per >= p.B) return {-1, 0};
     return {t / per, t % per};
   }
-  int32_t *sums = static_cast<int32_t *>(scratch), *found = sums + 4;
+  int32_t *sums = static_cast<int32_t *>(scratch), *found = sums + THREADS / 64;
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
   if (tid == 0) found[0] = -1;
   int32_t before = 0;
-  for (int32_t b0 = 0; b0 < p.B; b0 += kBlockThreads) {
+  for (int32_t b0 = 0; b0 < p.B; b0 += THREADS) {
     const int32_t b = b0 + tid;
     int32_t n = 0;
     if (b < p.B) {
@@ -81,8 +82,10 @@ __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scrat
     if (lane == 63) sums[wave] = incl;
     __syncthreads();
     int32_t base = before;
-    for (int w = 0; w < wave; ++w) base += sums[w];
-    before += sums[0] + sums[1] + sums[2] + sums[3];
+    for (int w = 0; w < THREADS / 64; ++w) {
+      if (w < wave) base += sums[w];
+      before += sums[w];
+    }
     if (base + incl - n <= t && t < base + incl) {
       found[0] = b;
       found[1] = t - (base + incl - n);
@@ -110,16 +113,16 @@ __device__ inline bool head_and_tile(const ExpandedPlan &p, int64_t tiles, int32
 }
 
 // Rows [row0, row0 + 64) of a strided matrix into LDS panels 0 .. PANELS - 1 (8 KB each), this
-// wavefront's quarter; rows past `last` repeat it.  stride in bytes, below 2^25 (plan): the rows
+// wavefront's share (of WAVES); rows past `last` repeat it.  stride in bytes, below 2^25 (plan): the rows
 // of a tile lie within 2^31 bytes.
-template <int PANELS>
+template <int PANELS, int WAVES = 4>
 __device__ __forceinline__ void fetch_rows(const char *base, int64_t stride, int32_t row0,
                                            int32_t last, int wave, int lane,
                                            char *__restrict__ lds) {
   const auto buffer = buffer_at(base + int64_t(row0) * stride);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int rb = wave * 2 + i;
+  for (int i = 0; i < 8 / WAVES; ++i) {
+    const int rb = wave * (8 / WAVES) + i;
     const uint32_t row = uint32_t(min(8 * rb + (lane >> 3), last - row0));
     const uint32_t at = row * uint32_t(stride) +
                         ((uint32_t(lane & 7) ^ chunk_key(uint32_t(8 * rb + (lane >> 3)))) << 4);
@@ -214,6 +217,79 @@ __device__ __forceinline__ void store_columns(char *row, const f32x16 *acc, floa
                      Mfma<T>::pack(acc[d][4 * c + 2] * f, acc[d][4 * c + 3] * f));
 }
 
+// ---- the same with 16 x 16 tiles (32 k values a product) ----
+
+template <int STEPS>
+__device__ __forceinline__ void load_operands16(const char *row, bool live, int lane, s16x8 *f) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k)
+    f[k] = live ? as_operand(*reinterpret_cast<const uint4 *>(row + k * 64 + 16 * (lane >> 4)))
+                : s16x8{};
+}
+
+// c[t] += rows row0 + 16 t .. + 15 of LDS panels times register operands, a panel read ahead.
+template <typename T, int PANELS>
+__device__ __forceinline__ void row_product16(const char *lds, int row0, int lane, const s16x8 *b,
+                                              f32x4 (&c)[2]) {
+  s16x8 f[2][2][2];
+  auto load = [](const char *lds, int row0, int lane, int n, s16x8 (&to)[2][2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        to[k][t] = as_operand(*reinterpret_cast<const uint4 *>(
+            lds + n * 8192 +
+            panel_chunk(uint32_t(row0 + 16 * t + (lane & 15)), 4u * k + (uint32_t(lane) >> 4))));
+  };
+  load(lds, row0, lane, 0, f[0]);
+#pragma unroll
+  for (int n = 0; n < PANELS; ++n) {
+    if (n + 1 < PANELS) load(lds, row0, lane, n + 1, f[(n + 1) % 2]);
+    hold_order();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) c[t] = Mfma<T>::mul16(f[n % 2][k][t], b[n * 2 + k], c[t]);
+    hold_order();
+  }
+}
+
+// acc[d] += (16-column blocks d of the 32 LDS rows from row0, transposed) times the operand b,
+// whose k values stand for rows 4 (lane / 16) + {0..3, 16..19}.
+template <typename T, int BLOCKS>
+__device__ __forceinline__ void column_product16(const char *lds, int row0, int lane, s16x8 b,
+                                                 f32x4 *acc) {
+  s16x8 f[2][4];
+  auto load = [](const char *lds, int row0, int lane, int d) {
+    const uint32_t i = uint32_t(lane) & 15u, row = 4u * (uint32_t(lane) >> 4) + (i >> 2);
+    const uint32_t c = 2u * uint32_t(d % 4) + ((i & 3u) >> 1);
+    const char *at = lds + d / 4 * 8192 + row0 * 128 + row * 128u + ((c ^ chunk_key(row)) << 4) +
+                     (i & 1u) * 8u;
+    return join(read_transposed(at), read_transposed(at + 2048));
+  };
+#pragma unroll
+  for (int d = 0; d < 4; ++d) f[0][d] = load(lds, row0, lane, d);
+#pragma unroll
+  for (int n = 0; n < BLOCKS / 4; ++n) {
+    if (n + 1 < BLOCKS / 4)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) f[(n + 1) % 2][d] = load(lds, row0, lane, n * 4 + 4 + d);
+    hold_order();
+#pragma unroll
+    for (int d = 0; d < 4; ++d) acc[n * 4 + d] = Mfma<T>::mul16(f[n % 2][d], b, acc[n * 4 + d]);
+    hold_order();
+  }
+}
+
+template <typename T, int BLOCKS>
+__device__ __forceinline__ void store_columns16(char *row, const f32x4 *acc, float f, int lane) {
+#pragma unroll
+  for (int d = 0; d < BLOCKS; ++d)
+    *reinterpret_cast<uint2 *>(row + (d * 4 + (lane >> 4)) * 8) =
+        make_uint2(Mfma<T>::pack(acc[d][0] * f, acc[d][1] * f),
+                   Mfma<T>::pack(acc[d][2] * f, acc[d][3] * f));
+}
+
 // ---- forward ------------------------------------------------------------------------------
 
 template <typename T, int DIM>
@@ -223,7 +299,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
   __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
   int32_t head, tile;
   if (!head_and_tile(p, p.q_tiles, head, tile)) return;
-  const TileAt at = find_tile<true>(p, tile, tiles);
+  const TileAt at = find_tile<true, kBlockThreads>(p, tile, tiles);
   if (at.seq < 0) return;
   const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
   const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
@@ -345,7 +421,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
   __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
   int32_t head, tile;
   if (!head_and_tile(p, p.q_tiles, head, tile)) return;
-  const TileAt at = find_tile<true>(p, tile, tiles);
+  const TileAt at = find_tile<true, kBlockThreads>(p, tile, tiles);
   if (at.seq < 0) return;
   const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
   const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
@@ -432,10 +508,14 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
 
 // ---- backward: dk, dv and each head's share of the shared key part's gradient ---------------
 
+// Products of 16 keys a wavefront (rope_mfma.h's 16 x 16 tiles, 32 k values each): half the
+// accumulators of 32 keys, so that two wavefronts fit a SIMD and one's exponentials run beside the
+// other's products.
 template <typename T, int DIM>
-__global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedPlan p) {
+__global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPlan p) {
   constexpr int NP = DIM / 64;
   constexpr int TILE = (2 * NP + 1) * 8192;  // queries (own part, shared part), gradients
+  constexpr int WAVES = kKeyThreads / 64;
   // (one LDS variable: with several the compiler would wait for the loads into the other buffer
   // before it reads this one)
   struct Lds {
@@ -449,7 +529,7 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
   if (!head_and_tile(p, p.k_tiles, head, tile)) return;
   // the first keys are seen by the most queries: those tiles first
   tile = int32_t(p.k_tiles - 1 - tile);
-  const TileAt at = find_tile<false>(p, tile, tiles);
+  const TileAt at = find_tile<false, kKeyThreads>(p, tile, tiles);
   if (at.seq < 0) return;
   const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
   const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
@@ -457,16 +537,17 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t es = sizeof(T);
-  const int32_t key = at.tile * kRows + wave * 32 + (lane & 31);
+  const int32_t key = at.tile * kRows + wave * 16 + (lane & 15);
   const bool live = key < k.count;
   const int64_t tok = k.first + key;
-  s16x8 kf[NP * 4 + 4], vf[NP * 4];
-  load_operands<NP * 4>(static_cast<const char *>(p.k) + (tok * p.k_tok + head * p.k_head) * es,
-                        live, lane, kf);
-  load_operands<4>(static_cast<const char *>(p.kr) + tok * p.kr_tok * es, live, lane, kf + NP * 4);
-  load_operands<NP * 4>(static_cast<const char *>(p.v) + (tok * p.v_tok + head * p.v_head) * es,
-                        live, lane, vf);
-  // query i sees key j if j < i + shift; i0: the first 64-row tile with a row that sees one
+  s16x8 kf[NP * 2 + 2], vf[NP * 2];
+  load_operands16<NP * 2>(static_cast<const char *>(p.k) + (tok * p.k_tok + head * p.k_head) * es,
+                          live, lane, kf);
+  load_operands16<2>(static_cast<const char *>(p.kr) + tok * p.kr_tok * es, live, lane,
+                     kf + NP * 2);
+  load_operands16<NP * 2>(static_cast<const char *>(p.v) + (tok * p.v_tok + head * p.v_head) * es,
+                          live, lane, vf);
+  // query i sees key j if j < i + shift; n0: the first 64-row tile with a row that sees one
   const int32_t shift = k.count - q.count + 1;
   const int32_t first_i = p.causal ? max(0, at.tile * kRows - shift + 1) : 0;
   const int32_t n0 = first_i / kTile;
@@ -476,19 +557,17 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
   const char *gb = static_cast<const char *>(p.grad) + (int64_t(q.first) * p.g_tok + head * p.g_head) * es;
   const float *lse = p.lse + int64_t(q.first) * p.heads + head;
   const float *del = p.delta + int64_t(q.first) * p.heads + head;
-  // The statistics of a tile's rows: read by the first wavefront, one row a lane, a tile ahead
-  // (and only looked at when that tile's turn comes, so that nothing waits for them before).
+  // The statistics of a tile's rows, one row a lane, read a tile ahead by every wavefront (under a
+  // condition the compiler would wait for them at its end) and put into LDS by the first.
   float next_lse = 0.0f, next_delta = 0.0f;
   auto fetch = [&](int32_t i0, char *__restrict__ to) {
-    fetch_rows<NP + 1>(qb, p.q_tok * es, i0, q.count - 1, wave, lane, to);
-    fetch_rows<NP>(gb, p.g_tok * es, i0, q.count - 1, wave, lane, to + (NP + 1) * 8192);
+    fetch_rows<NP + 1, WAVES>(qb, p.q_tok * es, i0, q.count - 1, wave, lane, to);
+    fetch_rows<NP, WAVES>(gb, p.g_tok * es, i0, q.count - 1, wave, lane, to + (NP + 1) * 8192);
   };
   auto fetch_stats = [&](int32_t i0) {
-    if (wave == 0) {
-      const int64_t i = int64_t(min(i0 + lane, q.count - 1)) * p.heads;
-      next_lse = lse[i];
-      next_delta = del[i];
-    }
+    const int64_t i = int64_t(min(i0 + lane, q.count - 1)) * p.heads;
+    next_lse = lse[i];
+    next_delta = del[i];
   };
   auto put_stats = [&](int slot, int32_t i0) {
     if (wave == 0) {  // rows that see nothing, or do not exist: p = exp2(s - infinity) = 0
@@ -499,37 +578,37 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
     }
   };
   const float scale2 = p.negative ? -p.scale_log2 : p.scale_log2;
-  f32x16 dk[NP * 2 + 2], dv[NP * 2];
+  f32x4 dk[NP * 4 + 4], dv[NP * 4];
 #pragma unroll
-  for (int d = 0; d < NP * 2 + 2; ++d) dk[d] = f32x16{};
+  for (int d = 0; d < NP * 4 + 4; ++d) dk[d] = f32x4{};
 #pragma unroll
-  for (int d = 0; d < NP * 2; ++d) dv[d] = f32x16{};
+  for (int d = 0; d < NP * 4; ++d) dv[d] = f32x4{};
 
   auto step = [&](const char *__restrict__ cur, char *__restrict__ other, const float *st,
                   int32_t i0) {
     if (i0 + kTile < q.count) fetch(i0 + kTile, other);
     const bool whole = !p.causal || last_key < i0 + shift;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const f32x16 s = row_product<T, NP + 1>(cur, i * 32, lane, kf, f32x16{});
-      const f32x16 dp = row_product<T, NP>(cur + (NP + 1) * 8192, i * 32, lane, vf, f32x16{});
-      float w[16], e[16];
+    for (int i = 0; i < 2; ++i) {  // 32 query rows, in two products of 16
+      f32x4 s[2] = {}, dp[2] = {};
+      row_product16<T, NP + 1>(cur, i * 32, lane, kf, s);
+      row_product16<T, NP>(cur + (NP + 1) * 8192, i * 32, lane, vf, dp);
+      float w[8], e[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int at_row = i * 32 + 8 * c + 4 * (lane >> 5);
+      for (int t = 0; t < 2; ++t) {
+        const int at_row = i * 32 + 16 * t + 4 * (lane >> 4);
         const f32x4 l = *reinterpret_cast<const f32x4 *>(st + at_row);
         const f32x4 d = *reinterpret_cast<const f32x4 *>(st + kTile + at_row);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * c + r], scale2, -l[r]));
+          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], scale2, -l[r]));
           if (!whole) x = key < i0 + at_row + r + shift ? x : 0.0f;
-          w[4 * c + r] = x;
-          e[4 * c + r] = x * (dp[4 * c + r] - d[r]);
+          w[4 * t + r] = x;
+          e[4 * t + r] = x * (dp[t][r] - d[r]);
         }
       }
-      column_product<T, NP * 2>(cur + (NP + 1) * 8192, i * 32, lane, round8<T>(w), round8<T>(w + 8),
-                                dv);
-      column_product<T, NP * 2 + 2>(cur, i * 32, lane, round8<T>(e), round8<T>(e + 8), dk);
+      column_product16<T, NP * 4>(cur + (NP + 1) * 8192, i * 32, lane, round8<T>(w), dv);
+      column_product16<T, NP * 4 + 4>(cur, i * 32, lane, round8<T>(e), dk);
     }
   };
   if (n0 * kTile < q.count) {
@@ -541,23 +620,20 @@ __global__ __launch_bounds__(kBlockThreads, 1) void latent_dkey_kernel(ExpandedP
     wait_loads_all();
     put_stats(slot, n * kTile);
     lds_barrier();
-    if ((n + 1) * kTile < q.count) fetch_stats((n + 1) * kTile);
+    fetch_stats((n + 1) * kTile);
     step(tiles + slot * TILE, tiles + (slot ^ 1) * TILE, &stats[slot][0][0], n * kTile);
   }
   if (!live) return;
   const int64_t out_row = tok * p.heads + head;
-  store_columns<T, NP * 2>(static_cast<char *>(p.dv) + out_row * DIM * es, dv, 1.0f, lane);
-  store_columns<T, NP * 2>(static_cast<char *>(p.dk) + out_row * DIM * es, dk, p.scale, lane);
+  store_columns16<T, NP * 4>(static_cast<char *>(p.dv) + out_row * DIM * es, dv, 1.0f, lane);
+  store_columns16<T, NP * 4>(static_cast<char *>(p.dk) + out_row * DIM * es, dk, p.scale, lane);
   float *part = p.dkr_part + (int64_t(head) * p.Tk + tok) * 64;
 #pragma unroll
-  for (int d = 0; d < 2; ++d)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const f32x16 &a = dk[NP * 2 + d];
-      *reinterpret_cast<float4 *>(part + (d * 8 + c * 2 + (lane >> 5)) * 4) =
-          make_float4(a[4 * c] * p.scale, a[4 * c + 1] * p.scale, a[4 * c + 2] * p.scale,
-                      a[4 * c + 3] * p.scale);
-    }
+  for (int d = 0; d < 4; ++d) {
+    const f32x4 &a = dk[NP * 4 + d];
+    *reinterpret_cast<float4 *>(part + d * 16 + 4 * (lane >> 4)) =
+        make_float4(a[0] * p.scale, a[1] * p.scale, a[2] * p.scale, a[3] * p.scale);
+  }
 }
 
 // The shared key part's gradient: the heads' shares added in order.  One thread for four
@@ -626,7 +702,7 @@ int run_backward(ExpandedPlan &p, void *stream) {
                        dim3(head_grid(p.heads, p.q_tiles)), kBlockThreads, 0, stream, &p);
   if (st == ROPE_OK && p.k_tiles > 0)
     st = launch_kernel(reinterpret_cast<const void *>(&latent_dkey_kernel<T, DIM>),
-                       dim3(head_grid(p.heads, p.k_tiles)), kBlockThreads, 0, stream, &p);
+                       dim3(head_grid(p.heads, p.k_tiles)), kKeyThreads, 0, stream, &p);
   if (st != ROPE_OK) return st;
   const int64_t threads = (p.Tk + (p.q_off != nullptr ? p.Tq : 0)) * 16;
   if (threads == 0) return ROPE_OK;
