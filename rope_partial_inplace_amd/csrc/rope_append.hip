@@ -7,8 +7,8 @@
 // copied bit for bit.  Keys and values go to slot slots[t] of the cache: page slot / pageSize,
 // row slot % pageSize.
 //
-// A few flops for every 4 bytes moved: bound by HBM.  One lane carries one 16-byte vector (two
-// for a NeoX pair), so nothing is staged and a wavefront's accesses are runs of whole lines; all
+// A few flops for every 4 bytes moved: bound by HBM.  An item is one 16-byte vector (two for a
+// NeoX pair), so nothing is staged and a wavefront's accesses are runs of whole lines; all
 // of a token's groups go into one launch because a decoding step's batch is bound by launch
 // latency (64 tokens of 32 + 8 + 8 heads: one launch in place of two or three).
 #include <hip/hip_runtime.h>
@@ -27,124 +27,142 @@
 namespace ropeamd {
 namespace {
 
-constexpr int kAppendBlock = 256;
-
 __device__ inline uint32_t div_by(const FastDiv &f, uint32_t n) {
   const uint32_t t = __umulhi(f.m, n);
   return (t + ((n - t) >> f.s1)) >> f.s2;
 }
 
-// V elements of a row as floats, and back (one 16-byte access, or one element).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// V elements of a row, as they lie in memory: one 16-byte access, or one element.
 template <typename T, int V>
-__device__ inline void load_row(const T *p, float *f) {
-  if constexpr (V == 1) {
-    f[0] = Io<T>::load1(p, 0);
-  } else {
-    Io<T>::unpack(*reinterpret_cast<const uint4 *>(p), f);
+struct Item {
+  uint4 raw;
+  __device__ void load(const T *p) { raw = *reinterpret_cast<const uint4 *>(p); }
+  // streamed: what is written here is read by later launches (32768 latent rows 45.6 -> 39.0 us;
+  // streamed loads were slower, 34 -> 44 us at 8192 tokens of 48 heads)
+  __device__ void store(T *p) const {
+    const u32x4 v = {raw.x, raw.y, raw.z, raw.w};
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
   }
-}
-
-template <typename T, int V>
-__device__ inline void store_row(T *p, const float *f) {
-  if constexpr (V == 1) {
-    Io<T>::store1(p, 0, f[0]);
-  } else {
-    *reinterpret_cast<uint4 *>(p) = Io<T>::pack(f);
+  __device__ void floats(float *f) const { Io<T>::unpack(raw, f); }
+  __device__ void set(const float *f) { raw = Io<T>::pack(f); }
+  // the V/2 cos (or sin) values of a GPT-J vector: 8 bytes
+  __device__ void load_half(const T *p) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    raw.x = w.x;
+    raw.y = w.y;
   }
-}
+  __device__ void half_floats(float *f) const {
+    Io<T>::word_to_floats(raw.x, f);
+    Io<T>::word_to_floats(raw.y, f + Io<T>::kPerWord);
+  }
+};
 
-// The V/2 cos (or sin) values of a GPT-J vector: 8 bytes.
-template <typename T, int V>
-__device__ inline void load_half(const T *p, float *f) {
-  const uint2 w = *reinterpret_cast<const uint2 *>(p);
-  Io<T>::word_to_floats(w.x, f);
-  Io<T>::word_to_floats(w.y, f + Io<T>::kPerWord);
-}
+template <typename T>
+struct Item<T, 1> {
+  typename Io<T>::raw raw;
+  __device__ void load(const T *p) { raw = *reinterpret_cast<const typename Io<T>::raw *>(p); }
+  __device__ void store(T *p) const { *reinterpret_cast<typename Io<T>::raw *>(p) = raw; }
+  __device__ void floats(float *f) const { f[0] = Io<T>::from_raw(raw); }
+  __device__ void set(const float *f) {
+    T v;
+    Io<T>::store1(&v, 0, f[0]);
+    raw = __builtin_bit_cast(typename Io<T>::raw, v);
+  }
+};
 
+// Workgroups are dealt to the three groups of rows one after the other (plan), so that a group's
+// pointers and strides are scalars, and a lane carries one item (two: no faster at 8192 tokens of
+// 48 heads, 8% slower at 32768 latent rows).
 template <typename T, int V, bool NEOX>
 __global__ __launch_bounds__(kAppendBlock) void append_paged_kernel(AppendPlan p) {
-  const int64_t stride = int64_t(gridDim.x) * kAppendBlock;
-  for (int64_t it = int64_t(blockIdx.x) * kAppendBlock + threadIdx.x; it < p.items; it += stride) {
+  const int64_t blocks0 = p.rows[0].blocks, blocks01 = blocks0 + p.rows[1].blocks;
+  const int64_t all = blocks01 + p.rows[2].blocks;
+  for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
+    const int group = block < blocks0 ? 0 : block < blocks01 ? 1 : 2;
+    const AppendRows &r = p.rows[group];
+    const int64_t it = (block - (group == 0 ? 0 : group == 1 ? blocks0 : blocks01)) * kAppendBlock +
+                       threadIdx.x;
+    if (it >= r.all) continue;
     int64_t t;
     uint32_t i;  // item of the token
     if (p.idx32) {
-      const uint32_t q = div_by(p.div_token, uint32_t(it));
+      const uint32_t q = div_by(r.div_total, uint32_t(it));
       t = q;
-      i = uint32_t(it) - q * p.items_per_token;
+      i = uint32_t(it) - q * r.total;
     } else {
-      t = it / p.items_per_token;
-      i = uint32_t(it - t * p.items_per_token);
+      t = it / r.total;
+      i = uint32_t(it - t * r.total);
     }
-    const int64_t pos_raw = p.positions[t * p.pos_stride];
-    // the row group the item belongs to (fields picked apart: the plan is read with scalar loads)
-    const uint32_t n0 = p.rows[0].total, n01 = n0 + p.rows[1].total;
-    const bool is_q = i < n0, is_k = !is_q && i < n01;
-    const AppendRows &r = is_q ? p.rows[0] : is_k ? p.rows[1] : p.rows[2];
-    const uint32_t j = i - (is_q ? 0u : is_k ? n0 : n01);
-    const uint32_t h = div_by(r.div_items, j), u = j - h * r.items;
+    const uint32_t h = div_by(r.div_items, i), unit = i - h * r.items;
     const T *in = static_cast<const T *>(r.in) + t * r.in_tok + int64_t(h) * r.in_head;
-    T *out = static_cast<T *>(r.out) + int64_t(h) * r.out_head;
-    bool keep = true;
-    if (is_q) {
-      out += t * r.out_tok;
-    } else {
-      // a slot outside the cache (negative: a padding token) takes nothing
-      const int64_t s = p.slots[t * p.slot_stride];
-      keep = s >= 0 && s < p.num_slots;
-      if (p.linear) {
-        out += s * r.out_tok;
-      } else {
-        const int64_t page = p.page32 ? int64_t(div_by(p.div_page, uint32_t(s))) : s / p.page_size;
-        out += page * r.out_page + (s - page * p.page_size) * r.out_tok;
-      }
-    }
-    if (!keep) continue;
-    if (u >= r.rot_items) {  // outside the slice: copied bit for bit
-      int64_t e = int64_t(u - r.rot_items) * V;
+    // the loads that depend on nothing first: position, slot, the row's elements
+    const int64_t pos = r.rot_items != 0 ? p.positions[t * p.pos_stride] : 0;
+    const int64_t slot = group != 0 ? p.slots[t * p.slot_stride] : 0;
+    // an item's elements: from e on, and (pairs) from e + partner on
+    const bool turn = unit < r.rot_items;
+    int64_t e;
+    if (turn) {
+      e = r.rot_start + int64_t(unit) * (V == 1 && !NEOX ? 2 : V);
+    } else {  // outside the slice
+      e = int64_t(unit - r.rot_items) * V;
       if (e >= r.rot_start && r.rot_items != 0) e += 2 * p.half;
-      if constexpr (V == 1) {
-        reinterpret_cast<typename Io<T>::raw *>(out)[e] =
-            reinterpret_cast<const typename Io<T>::raw *>(in)[e];
-      } else {
-        *reinterpret_cast<uint4 *>(out + e) = *reinterpret_cast<const uint4 *>(in + e);
-      }
+    }
+    constexpr bool PAIR = NEOX || V == 1;
+    const int64_t partner = NEOX ? int64_t(p.half) : int64_t(1);
+    Item<T, V> x, y, c, s;
+    x.load(in + e);
+    if (PAIR && turn) y.load(in + e + partner);
+
+    T *out = static_cast<T *>(r.out) + int64_t(h) * r.out_head;
+    if (group == 0) {
+      out += t * r.out_tok;
+    } else if (p.linear) {
+      out += slot * r.out_tok;
+    } else {
+      const int64_t page =
+          p.page32 ? int64_t(div_by(p.div_page, uint32_t(slot))) : slot / p.page_size;
+      out += page * r.out_page + (slot - page * p.page_size) * r.out_tok;
+    }
+    // a slot outside the cache (negative: a padding token) takes nothing
+    const bool keep = group == 0 || (slot >= 0 && slot < p.num_slots);
+    if (!turn) {  // copied bit for bit
+      if (keep) x.store(out + e);
       continue;
     }
-    const int64_t pos = min(max(pos_raw, int64_t(0)), p.max_seq - 1);
-    const T *row = static_cast<const T *>(p.table) + pos * p.table_stride;
-    if constexpr (NEOX) {
-      const int64_t e = r.rot_start + int64_t(u) * V;
-      float a[V], b[V], c[V], s[V], x[V], y[V];
-      load_row<T, V>(in + e, a);
-      load_row<T, V>(in + e + p.half, b);
-      load_row<T, V>(row + int64_t(u) * V, c);
-      load_row<T, V>(row + p.half + int64_t(u) * V, s);
+    const int64_t at = min(max(pos, int64_t(0)), p.max_seq - 1);
+    const T *row = static_cast<const T *>(p.table) + at * p.table_stride;
+    float a[V], cv[V], sv[V], u[V];
+    if constexpr (PAIR) {
+      float b[V], w[V];
+      c.load(row + int64_t(unit) * V);
+      s.load(row + p.half + int64_t(unit) * V);
+      x.floats(a);
+      y.floats(b);
+      c.floats(cv);
+      s.floats(sv);
 #pragma unroll
       for (int m = 0; m < V; ++m) {
-        x[m] = a[m] * c[m] - b[m] * s[m];
-        y[m] = b[m] * c[m] + a[m] * s[m];
+        u[m] = a[m] * cv[m] - b[m] * sv[m];
+        w[m] = b[m] * cv[m] + a[m] * sv[m];
       }
-      store_row<T, V>(out + e, x);
-      store_row<T, V>(out + e + p.half, y);
-    } else if constexpr (V == 1) {
-      const int64_t e = r.rot_start + 2 * int64_t(u);
-      const float a = Io<T>::load1(in, e), b = Io<T>::load1(in, e + 1);
-      const float c = Io<T>::load1(row, u), s = Io<T>::load1(row, p.half + int64_t(u));
-      Io<T>::store1(out, e, a * c - b * s);
-      Io<T>::store1(out, e + 1, b * c + a * s);
+      y.set(w);
+      if (keep) y.store(out + e + partner);
     } else {
-      const int64_t e = r.rot_start + int64_t(u) * V;
-      float a[V], c[V / 2], s[V / 2], x[V];
-      load_row<T, V>(in + e, a);
-      load_half<T, V>(row + int64_t(u) * (V / 2), c);
-      load_half<T, V>(row + p.half + int64_t(u) * (V / 2), s);
+      c.load_half(row + int64_t(unit) * (V / 2));
+      s.load_half(row + p.half + int64_t(unit) * (V / 2));
+      x.floats(a);
+      c.half_floats(cv);
+      s.half_floats(sv);
 #pragma unroll
       for (int m = 0; m < V / 2; ++m) {
-        x[2 * m] = a[2 * m] * c[m] - a[2 * m + 1] * s[m];
-        x[2 * m + 1] = a[2 * m + 1] * c[m] + a[2 * m] * s[m];
+        u[2 * m] = a[2 * m] * cv[m] - a[2 * m + 1] * sv[m];
+        u[2 * m + 1] = a[2 * m + 1] * cv[m] + a[2 * m] * sv[m];
       }
-      store_row<T, V>(out + e, x);
     }
+    x.set(u);
+    if (keep) x.store(out + e);
   }
 }
 
@@ -183,7 +201,7 @@ ROPE_API int rope_append_paged_cache(const rope_tensor *positions, const rope_te
   const void *fn = plan.dt == ROPE_F32   ? pick_append<float>(plan)
                    : plan.dt == ROPE_F16 ? pick_append<_Float16>(plan)
                                          : pick_append<__bf16>(plan);
-  int64_t blocks = (plan.items + kAppendBlock - 1) / kAppendBlock;
+  int64_t blocks = plan.rows[0].blocks + plan.rows[1].blocks + plan.rows[2].blocks;
   if (blocks > kMaxGrid) blocks = kMaxGrid;
   return launch_kernel(fn, dim3(uint32_t(blocks)), kAppendBlock, 0, stream, &plan);
 }

@@ -139,7 +139,7 @@ int plan_append(const rope_tensor *positions, const rope_tensor *slots, const ro
             (count(outs[g]) == 0 || rows_aligned16(outs[g]));
   p.vector_io = vec;
 
-  int64_t per_token = 0;
+  int64_t items = 0;
   for (int g = 0; g < 3; ++g) {
     AppendRows &r = p.rows[g];
     if (ins[g] == nullptr || count(ins[g]) == 0) continue;
@@ -156,17 +156,19 @@ int plan_append(const rope_tensor *positions, const rope_tensor *slots, const ro
     const bool in_place = g == 0 && query_out->data == query->data;
     head_items(&r, in->shape[2], starts[g], g == 2 ? 0 : rd, vec ? v : 1, p.neox, in_place);
     r.total = uint32_t(in->shape[1]) * r.items;
+    r.all = T * int64_t(r.total);  // below 2^31 * 2^24
     r.div_items = make_fastdiv(std::max(1u, r.items));
-    per_token += r.total;
+    r.div_total = make_fastdiv(std::max(1u, r.total));
+    items += r.all;
   }
-  if (per_token == 0) {
+  if (items == 0) {
     p.noop = true;
     return ROPE_OK;
   }
-  p.items_per_token = uint32_t(per_token);  // at most 3 * 2^24
-  p.div_token = make_fastdiv(p.items_per_token);
-  p.items = T * per_token;  // below 2^31 * 2^26
-  p.idx32 = p.items < (int64_t(1) << 31);
+  for (AppendRows &r : p.rows) {
+    r.blocks = (r.all + kAppendBlock - 1) / kAppendBlock;
+    p.idx32 = p.idx32 && r.all + kAppendBlock < (int64_t(1) << 31);
+  }
   p.page32 = p.num_slots < (int64_t(1) << 31);
   p.div_page = make_fastdiv(uint32_t(std::min<int64_t>(std::max<int64_t>(p.page_size, 1),
                                                        0x7fffffff)));

@@ -23,7 +23,9 @@ struct AppendRows {
   uint32_t rot_items = 0;  // rotated items of a head
   uint32_t items = 0;      // items of a head
   uint32_t total = 0;      // items of the group for one token: heads * items
-  FastDiv div_items;
+  int64_t all = 0;         // items of the group for all tokens
+  int64_t blocks = 0;      // workgroups
+  FastDiv div_items, div_total;
 };
 
 struct AppendPlan {
@@ -31,7 +33,7 @@ struct AppendPlan {
   bool neox = true;
   bool vector_io = false;  // 16-byte items (else one element, or one pair, at a time)
   bool noop = false;
-  bool idx32 = true;        // items of the whole call stay below 2^31
+  bool idx32 = true;        // item numbers of a group, and of its last lanes, fit 32 bits
   const int64_t *positions = nullptr, *slots = nullptr;
   int64_t pos_stride = 0, slot_stride = 0;
   const void *table = nullptr;
@@ -43,10 +45,9 @@ struct AppendPlan {
   bool page32 = true;   // slots below 2^32: page number by FastDiv
   FastDiv div_page;
   AppendRows rows[3];  // query, key, value (total 0: absent)
-  uint32_t items_per_token = 0;
-  FastDiv div_token;
-  int64_t items = 0;
 };
+
+constexpr int kAppendBlock = 256;
 
 int plan_append(const rope_tensor *positions, const rope_tensor *slots, const rope_tensor *query,
                 const rope_tensor *key, const rope_tensor *value,

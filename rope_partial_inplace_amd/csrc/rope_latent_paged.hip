@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kPagedBlock = 512;
 constexpr int kPagedWaves = kPagedBlock / 64;
-constexpr int kPageIds = 1024;  // page numbers held in LDS at a time
+constexpr int kPageIds = 512;  // pages' places held in LDS at a time
 
 __device__ inline uint32_t div_by(const FastDiv &f, uint32_t n) {
   const uint32_t t = __umulhi(f.m, n);
@@ -76,14 +76,15 @@ __device__ inline Sequence sequence(const PagedPlan &p, int32_t b, int rows, int
 
 // A wavefront's eighth of a tile of 64 cache rows is 8 of them (tokens tile0 .. tile0 + 63 of the
 // sequence, the last one repeated past `len`).  This lane's piece: its row's byte offset in the
-// cache.
+// cache.  places: byte offsets of the sequence's pages from page0 on.
 template <typename T>
-__device__ __forceinline__ int64_t tile_piece(const PagedPlan &p, const int32_t *ids, int32_t page0,
-                                              int32_t tile0, int32_t len, int wave, int lane) {
-  const int32_t tok = min(tile0 + 8 * wave + (lane >> 3), len - 1);
-  const int32_t page = int32_t(div_by(p.div_page, uint32_t(tok)));
-  return (int64_t(ids[page - page0]) * p.c_page +
-          int64_t(tok - page * int32_t(p.page_size)) * p.c_row) * int64_t(sizeof(T));
+__device__ __forceinline__ int64_t tile_piece(const PagedPlan &p, const int64_t *places,
+                                              int32_t page0, int32_t tile0, int32_t len, int wave,
+                                              int lane) {
+  const uint32_t tok = uint32_t(min(tile0 + 8 * wave + (lane >> 3), len - 1));
+  const uint32_t page = div_by(p.div_page, tok);
+  return places[int32_t(page) - page0] +
+         int64_t(uint64_t(tok - page * uint32_t(p.page_size)) * uint64_t(p.c_row * sizeof(T)));
 }
 
 // The pieces' way into LDS, 128 bytes of every row at a time.  A buffer reaches 4 GiB, a cache may
@@ -108,18 +109,6 @@ __device__ __forceinline__ void fetch_tile(const char *cache, int64_t piece, int
         load_lds16(buffer, offset, n * 128, tile + n * 8192 + wave * 1024);
     }
   }
-}
-
-// Running maximum of a row: raised (and what was summed at the old one rescaled by the returned
-// factor) only when the tile's maximum passes it by more than 8, so that rescaling is rare.
-// Until then weights of up to 2^8 are carried, which changes no result beyond its rounding.
-__device__ inline float raise(float &top, float best) {
-  float f = 1.0f;
-  if (best > top + 8.0f) {
-    f = __builtin_amdgcn_exp2f(top - best);
-    top = best;
-  }
-  return f;
 }
 
 // How the wavefronts share a tile of 64 cache rows, DB 32-column blocks of the latent and RB
@@ -176,15 +165,15 @@ struct Step {
                               uint32_t(block & 1));
   }
 
-  // S^T of the wavefront's strips and rows; scaled, masked (seen: rows of the tile that the query
-  // row may see; whole: every query row sees all of them); returns the row's maximum.
+  // S^T of the wavefront's strips and rows, masked where not every query row sees all of the tile
+  // (seen: rows of the tile that this lane's query row may see); returns the row's maximum.
   __device__ __forceinline__ static float scores(const char *__restrict__ tile,
                                                  const s16x8 (&qf)[QF], int wave, int lane,
-                                                 int32_t seen, bool whole, float scale_log2,
-                                                 float (&e)[ST][4]) {
-    f32x4 s[ST] = {};
+                                                 int32_t seen, bool whole, f32x4 (&s)[ST]) {
     constexpr int AHEAD = 2;  // panels read ahead
     s16x8 kf[AHEAD + 1][ST][2];
+#pragma unroll
+    for (int j = 0; j < ST; ++j) s[j] = f32x4{};
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) load_keys(tile, wave, lane, n, kf[n]);
 #pragma unroll
@@ -199,17 +188,40 @@ struct Step {
           s[j] = Mfma<T>::mul16(kf[n % (AHEAD + 1)][j][c], qf[n * 2 + c], s[j]);
       __builtin_amdgcn_sched_barrier(0);
     }
+    if (!whole) {
+      asm volatile("");  // a branch: most tiles need no masks
+#pragma unroll
+      for (int j = 0; j < ST; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if ((part(wave) * ST + j) * 16 + 4 * (lane >> 4) + r >= seen) s[j][r] = kNegInf;
+    }
     float best = kNegInf;
 #pragma unroll
     for (int j = 0; j < ST; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float x = s[j][r] * scale_log2;
-        if (!whole) x = (part(wave) * ST + j) * 16 + 4 * (lane >> 4) + r < seen ? x : kNegInf;
-        e[j][r] = x;
-        best = fmaxf(best, x);
-      }
+      for (int r = 0; r < 4; ++r) best = fmaxf(best, s[j][r]);
     return max_quarters(best);
+  }
+
+  // The weights of the wavefront's strips at maximum `top`, into the P tile; returns this lane's
+  // share of their sum.
+  __device__ __forceinline__ static float weights(char *__restrict__ pt, const f32x4 (&s)[ST],
+                                                  int wave, int lane, float scale_log2,
+                                                  float top) {
+    const float ref = top == kNegInf ? 0.0f : top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+      float e[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][r], scale_log2, -ref));
+        sum += e[r];
+      }
+      put_weights(pt, s_row(wave, lane), (part(wave) * ST + j) * 4 + (lane >> 4), e);
+    }
+    return sum;
   }
 
   // Weights of four cache rows (4 g4 .. + 3 of the tile) of query row `row` into the P tile, in
@@ -254,14 +266,16 @@ latent_paged_kernel(PagedPlan p) {
   struct Lds {
     char tiles[2 * TILE];
     char weights[ROWS * 128];
-    int32_t ids[kPageIds];
+    int64_t places[kPageIds];
     float row_max[S::PARTS][ROWS];
+    int32_t raised;  // some wavefront's row passed its maximum
     int32_t wave_total[kPagedWaves];
     int32_t found[7];
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
   char *tiles = lds.tiles, *weights = lds.weights;
-  int32_t *ids = lds.ids, *found = lds.found;
+  int64_t *places = lds.places;
+  int32_t *found = lds.found;
   auto &row_max = lds.row_max;
   int32_t *wave_total = lds.wave_total;
 
@@ -348,25 +362,26 @@ latent_paged_kernel(PagedPlan p) {
     const int32_t rows = sq.count * p.heads;
     const int32_t row0 = item * item_rows + member * ROWS;
     if (row0 < rows && st0 < st1) {
-      // page numbers of as many of the steps from `st` on as the table holds; returns the step
-      // that they end before
+      // places of the pages of as many of the steps from `st` on as LDS holds; returns the step that
+      // they end before
       int32_t page0 = 0;
-      auto load_ids = [&](int32_t st) {
+      auto load_places = [&](int32_t st) {
         page0 = int32_t(div_by(p.div_page, uint32_t(st * STEP)));
         const int32_t last_tok = min(st1 * STEP, sq.len) - 1;
         const int32_t pages = min(int32_t(kPageIds),
                                   int32_t(div_by(p.div_page, uint32_t(last_tok))) - page0 + 1);
         for (int32_t i = tid; i < pages; i += kPagedBlock) {
           const int64_t id = p.table[b * p.table_seq + (page0 + i) * p.table_page];
-          ids[i] = int32_t(min(max(id, int64_t(0)), p.num_pages - 1));
+          places[i] = min(max(id, int64_t(0)), p.num_pages - 1) * p.c_page * int64_t(sizeof(T));
         }
         return int64_t(page0 + pages) * p.page_size <= last_tok
                    ? int32_t((int64_t(page0 + pages) * p.page_size) / STEP)
                    : st1;
       };
-      lds_barrier();  // what the last segment read of ids, tiles and row_max
+      lds_barrier();  // what the last segment read of places, tiles and row_max
+      if (tid == 0) lds.raised = 0;
       int32_t end = st1;
-      if (sq.len > 0) end = load_ids(st0);
+      if (sq.len > 0) end = load_places(st0);
 
       // ---- this wavefront's query rows, and how much of the cache each may see ----
       s16x8 qf[S::QF];
@@ -381,24 +396,32 @@ latent_paged_kernel(PagedPlan p) {
 #pragma unroll
         for (int k = 0; k < S::QF; ++k)
           qf[k] = live ? as_operand(*reinterpret_cast<const uint4 *>(q + k * 32)) : s16x8{};
+        if (p.negative) {  // a negative scale becomes the queries' sign: maxima stay maxima
+#pragma unroll
+          for (int k = 0; k < S::QF; ++k) qf[k] ^= short(0x8000);
+        }
       }
       // fewest cache rows that any row of the workgroup sees
       const int32_t floor = row0 + ROWS > rows
                                 ? 0
                                 : sq.len - sq.count + int32_t(div_by(p.div_heads, uint32_t(row0))) + 1;
 
-      float s_top = kNegInf, s_sum = 0.0f, o_top[OB];
+      float s_top = kNegInf, s_sum = 0.0f;
       f32x16 acc[OB][COLS];
 #pragma unroll
-      for (int i = 0; i < OB; ++i) {
-        o_top[i] = kNegInf;
+      for (int i = 0; i < OB; ++i)
 #pragma unroll
         for (int d = 0; d < COLS; ++d) acc[i][d] = f32x16{};
-      }
 
+      // A row's maximum is raised only when a tile passes it by more than 8; until then weights of
+      // up to 2^8 are carried, which changes no result beyond its rounding.  So the wavefronts that
+      // share a row need not agree on a maximum in every tile: each takes the weights at the old
+      // one, and all of them see at the barrier before the second product whether any had to pass
+      // it, which is rare.  Then the maxima are exchanged, accumulators and sums rescaled and the
+      // weights taken again.
       auto step = [&](const char *__restrict__ cur, char *__restrict__ other,
-                      char *__restrict__ pt, float *__restrict__ rm,
-                      const int32_t *__restrict__ pages, const char *cache, int64_t piece,
+                      char *__restrict__ pt, float *__restrict__ rm, int32_t *__restrict__ raised,
+                      const int64_t *__restrict__ pages, const char *cache, int64_t piece,
                       int32_t st) {
         if (st + 1 < end) fetch_tile<PANELS>(cache, piece, wave, lane_id, other);
         const int32_t tile0 = st * STEP;
@@ -406,45 +429,42 @@ latent_paged_kernel(PagedPlan p) {
         // take the registers that Q and the accumulators need
         int lane = lane_id;
         asm volatile("" : "+v"(lane));
-        float e[S::ST][4];
-        const int row = S::s_row(wave, lane);
-        const float best = S::scores(cur, qf, wave, lane, limit - tile0, tile0 + STEP <= floor,
-                                     p.scale_log2, e);
-        if (lane < 16) rm[S::part(wave) * ROWS + row] = best;
+        f32x4 s[S::ST];
+        const float best = S::scores(cur, qf, wave, lane, limit - tile0, tile0 + STEP <= floor, s) *
+                           p.scale_log2;
+        float sum = S::weights(pt, s, wave, lane, p.scale_log2, s_top);
+        if (__any(best > s_top + 8.0f) && lane == 0) *raised = 1;
         // where the tile after the next one comes from
         const int64_t after = st + 2 < end ? tile_piece<T>(p, pages, page0, (st + 2) * STEP,
                                                            sq.len, wave, lane)
                                            : 0;
         lds_barrier();
-        {
+        if (uniform(*raised) != 0) {
+          const int row = S::s_row(wave, lane);
+          if (lane < 16) rm[S::part(wave) * ROWS + row] = best;
+          lds_barrier();
+          if (tid == 0) *raised = 0;
           float high = rm[row];
 #pragma unroll
           for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, rm[k * ROWS + row]);
-          s_sum *= raise(s_top, high);
-          const float ref = s_top == kNegInf ? 0.0f : s_top;
+          float f = 1.0f;
+          if (high > s_top + 8.0f) {
+            f = __builtin_amdgcn_exp2f(s_top - high);
+            s_top = high;
+          }
+          s_sum *= f;
+          sum = S::weights(pt, s, wave, lane, p.scale_log2, s_top);
+          lds_barrier();
+          if (S::part(wave) == 0 && lane < 16) rm[row] = f;
+          lds_barrier();
 #pragma unroll
-          for (int j = 0; j < S::ST; ++j) {
+          for (int i = 0; i < OB; ++i) {
+            const float g = rm[S::o_row(wave, lane, i) % ROWS];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              e[j][r] = __builtin_amdgcn_exp2f(e[j][r] - ref);
-              s_sum += e[j][r];
-            }
-            S::put_weights(pt, row, (S::part(wave) * S::ST + j) * 4 + (lane >> 4), e[j]);
+            for (int d = 0; d < COLS; ++d) acc[i][d] *= g;
           }
         }
-#pragma unroll
-        for (int i = 0; i < OB; ++i) {
-          const int o_row = S::o_row(wave, lane, i) % ROWS;
-          float high = rm[o_row];
-#pragma unroll
-          for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, rm[k * ROWS + o_row]);
-          const float f = raise(o_top[i], high);
-          if (__any(f != 1.0f)) {
-#pragma unroll
-            for (int d = 0; d < COLS; ++d) acc[i][d] *= f;
-          }
-        }
-        lds_barrier();
+        s_sum += sum;
         if (S::has_output(wave)) S::outputs(cur, pt, wave, lane, acc);
         return after;
       };
@@ -455,26 +475,32 @@ latent_paged_kernel(PagedPlan p) {
           // ---- the steps: the next tile is on its way while one is multiplied ----
           lds_barrier();
           const char *cache = static_cast<const char *>(p.cache);
-          fetch_tile<PANELS>(cache, tile_piece<T>(p, ids, page0, st * STEP, sq.len, wave, lane),
+          fetch_tile<PANELS>(cache, tile_piece<T>(p, places, page0, st * STEP, sq.len, wave, lane),
                              wave, lane, tiles);
-          int64_t next = st + 1 < end ? tile_piece<T>(p, ids, page0, (st + 1) * STEP, sq.len, wave,
-                                                      lane)
+          int64_t next = st + 1 < end ? tile_piece<T>(p, places, page0, (st + 1) * STEP, sq.len,
+                                                      wave, lane)
                                       : 0;
           for (int32_t i = 0; st < end; ++st, ++i) {
             wait_loads_all();
             lds_barrier();
             next = step(tiles + (i & 1) * TILE, tiles + (~i & 1) * TILE, weights, &row_max[0][0],
-                        ids, cache, next, st);
+                        &lds.raised, places, cache, next, st);
           }
           if (st >= st1) break;
           lds_barrier();
-          end = load_ids(st);
+          end = load_places(st);
         }
       }
 
-      // ---- sums of the wavefronts that shared a row ----
-      lds_barrier();
+      // ---- maxima, and sums of the wavefronts that shared a row, to those that hold outputs ----
       s_sum = sum_quarters(s_sum);
+      float o_top[OB];
+      lds_barrier();
+      if (S::part(wave) == 0 && lane < 16) row_max[0][S::s_row(wave, lane)] = s_top;
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < OB; ++i) o_top[i] = row_max[0][S::o_row(wave, lane, i) % ROWS];
+      lds_barrier();
       if (lane < 16) row_max[S::part(wave)][S::s_row(wave, lane)] = s_sum;
       lds_barrier();
 

@@ -60,6 +60,13 @@ int64_t paged_rows(int64_t tokens, int64_t heads, int64_t sequences) {
   return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
+// |scale| * log2(e), and whether the scale is negative.  Not 0, which would turn a masked score of
+// -infinity into a NaN; no score is large enough for 1e-30 to differ from it.
+void set_scale(double scale, float *scale_log2, bool *negative) {
+  *scale_log2 = float(std::max(std::fabs(scale) * kLog2e, 1e-30));
+  *negative = scale < 0;
+}
+
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 }  // namespace
@@ -162,7 +169,7 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
   p.queries = query_offsets != nullptr ? 0 : T / B;
   p.heads = int32_t(H);
   p.latent = int32_t(latent_dim);
-  p.scale_log2 = float(scale * kLog2e);
+  set_scale(scale, &p.scale_log2, &p.negative);
   p.out = out->data;
   p.lse = lse != nullptr ? static_cast<float *>(lse->data) : nullptr;
   const int64_t item_rows = paged_rows(T, H, B);
@@ -311,10 +318,7 @@ int plan_expanded(const rope_tensor *query, const rope_tensor *key, const rope_t
   p.heads = int32_t(H);
   p.dim = int32_t(dim);
   p.scale = float(scale);
-  // (not 0, which would turn a masked score of -infinity into a NaN; no score is large enough for
-  // 1e-30 to differ from it)
-  p.scale_log2 = float(std::max(std::fabs(scale) * kLog2e, 1e-30));
-  p.negative = scale < 0;
+  set_scale(scale, &p.scale_log2, &p.negative);
   p.out = out->data;
   p.lse = static_cast<float *>(lse->data);
   return ROPE_OK;

@@ -34,7 +34,8 @@ struct PagedPlan {
   FastDiv div_page, div_heads;
   int64_t T = 0, B = 0, queries = 0;  // queries: tokens of every sequence without offsets
   int32_t heads = 0, latent = 0;
-  float scale_log2 = 0;  // scale * log2(e): the softmax runs in powers of two
+  float scale_log2 = 0;   // |scale| * log2(e), at least 1e-30: the softmax runs in powers of two
+  bool negative = false;  // scale < 0: the kernel turns the queries' signs
   void *out = nullptr;
   float *lse = nullptr;
   int32_t row_blocks = 1;  // 32-row blocks of a workgroup (1 or 2)
