@@ -43,7 +43,6 @@ __device__ inline uint32_t div_by(const FastDiv &f, uint32_t n) {
 // Beginning an item (its page numbers, its queries, a first tile that nothing hides) costs about
 // as much as two steps: the shares of the clusters are cut by steps and this.
 constexpr int32_t kItemCost = 2;
-
 // What a sequence asks for.
 struct Sequence {
   int32_t len;     // cached tokens
@@ -75,8 +74,8 @@ __device__ inline Sequence sequence(const PagedPlan &p, int32_t b, int rows, int
 }
 
 // A wavefront's eighth of a tile of 64 cache rows is 8 of them (tokens tile0 .. tile0 + 63 of the
-// sequence, the last one repeated past `len`).  This lane's piece: its row's byte offset in the
-// cache.  places: byte offsets of the sequence's pages from page0 on.
+// sequence, the last one repeated past `len`).  This lane's piece: where in the cache its 16-byte
+// chunk of the row's first 128 bytes lies.  places: byte offsets of the sequence's pages from page0 on.
 template <typename T>
 __device__ __forceinline__ int64_t tile_piece(const PagedPlan &p, const int64_t *places,
                                               int32_t page0, int32_t tile0, int32_t len, int wave,
@@ -84,17 +83,17 @@ __device__ __forceinline__ int64_t tile_piece(const PagedPlan &p, const int64_t 
   const uint32_t tok = uint32_t(min(tile0 + 8 * wave + (lane >> 3), len - 1));
   const uint32_t page = div_by(p.div_page, tok);
   return places[int32_t(page) - page0] +
-         int64_t(uint64_t(tok - page * uint32_t(p.page_size)) * uint64_t(p.c_row * sizeof(T)));
+         int64_t(uint64_t(tok - page * uint32_t(p.page_size)) * uint64_t(p.c_row * sizeof(T)) +
+                 ((uint32_t(lane & 7) ^ chunk_key(uint32_t(8 * wave + (lane >> 3)))) << 4));
 }
 
 // The pieces' way into LDS, 128 bytes of every row at a time.  A buffer reaches 4 GiB, a cache may
 // be larger: rows are fetched by 2 GiB blocks, nearly always all of them in one.
 template <int PANELS>
-__device__ __forceinline__ void fetch_tile(const char *cache, int64_t piece, int wave, int lane,
+__device__ __forceinline__ void fetch_tile(const char *cache, int64_t piece, int wave,
                                            char *__restrict__ tile) {
   const int32_t block = int32_t(piece >> 31);
-  const uint32_t offset = (uint32_t(piece) & 0x7fffffffu) +
-                          ((uint32_t(lane & 7) ^ chunk_key(uint32_t(8 * wave + (lane >> 3)))) << 4);
+  const uint32_t offset = uint32_t(piece) & 0x7fffffffu;
   uint64_t left = __ballot(true);
   while (left != 0) {  // ends: every turn serves the first lane left
     const int32_t first = __builtin_amdgcn_readlane(block, __builtin_ctzll(left));
@@ -137,49 +136,66 @@ struct Step {
   // wavefronts without a share of O (one row block, four column blocks)
   __device__ static bool has_output(int wave) { return !SPLIT || wave / DB < RB; }
 
+  // A lane's places in the tiles' panels, from which its other chunks differ by an exclusive or:
+  // of its key row, of its transposed values, and of the weights it writes and reads.
+  struct Lanes {
+    uint32_t keys, values, put, get;
+    __device__ Lanes(int wave, int lane)
+        : keys(panel_chunk(uint32_t(part(wave) * ST * 16 + (lane & 15)), uint32_t(lane) >> 4)),
+          values(panel_transposed(uint32_t(lane), 0, 0)),
+          put(panel_chunk(uint32_t(s_row(wave, lane)), (uint32_t(lane) >> 4) & 1u) +
+              (uint32_t(lane) >> 5) * 8u),
+          get(panel_chunk(uint32_t(o_row(wave, lane, 0)), uint32_t(lane) >> 5)) {}
+    // Opaque: what follows from these is worked out again in every step.  Kept from step to step
+    // it would take the registers that Q and the accumulators need.
+    __device__ void fresh() {
+      asm volatile("" : "+v"(keys), "+v"(values), "+v"(put), "+v"(get));
+    }
+  };
+
   // Operands out of LDS: panel n of the strips' rows; P of the 16 cache rows of step k; and for
   // product n (step n / COLS, column block n % COLS) the values.  The tile goes in as an argument
   // everywhere, never captured: only so does the compiler see that these reads and the loads
   // into the other buffer do not meet, and does not wait for those loads here.
-  __device__ __forceinline__ static void load_keys(const char *tile, int wave, int lane, int n,
+  __device__ __forceinline__ static void load_keys(const char *tile, const Lanes &at, int n,
                                                    s16x8 (&f)[ST][2]) {
 #pragma unroll
     for (int j = 0; j < ST; ++j)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        f[j][c] = as_operand(*reinterpret_cast<const uint4 *>(
-            tile + n * 8192 + j * 2048 +
-            panel_chunk(uint32_t(part(wave) * ST * 16 + (lane & 15)),
-                        4u * c + (uint32_t(lane) >> 4))));
+        f[j][c] = as_operand(*reinterpret_cast<const uint4 *>(tile + n * 8192 + j * 2048 +
+                                                              (at.keys ^ (c * 64u))));
   }
-  __device__ __forceinline__ static void load_weights(const char *pt, int wave, int lane, int k,
+  __device__ __forceinline__ static void load_weights(const char *pt, const Lanes &at, int k,
                                                       s16x8 *f) {
 #pragma unroll
     for (int i = 0; i < OB; ++i)
-      f[i] = as_operand(*reinterpret_cast<const uint4 *>(
-          pt + panel_chunk(uint32_t(o_row(wave, lane, i)), uint32_t(2 * k + (lane >> 5)))));
+      f[i] = as_operand(*reinterpret_cast<const uint4 *>(pt + i * 4096 + (at.get ^ (k * 32u))));
   }
-  __device__ __forceinline__ static s16x8 load_values(const char *tile, int wave, int lane, int n) {
+  __device__ __forceinline__ static s16x8 load_values(const char *tile, const Lanes &at, int wave,
+                                                      int n) {
     const int block = column(wave, n % COLS);
-    return transposed_operand(tile + (block >> 1) * 8192 + n / COLS * 2048, uint32_t(lane),
-                              uint32_t(block & 1));
+    const char *from = tile + (block >> 1) * 8192 + n / COLS * 2048;
+    const uint32_t v = at.values ^ (uint32_t(block & 1) * 64u);
+    return join(read_transposed(from + v), read_transposed(from + (v ^ kEightRows)));
   }
 
   // S^T of the wavefront's strips and rows, masked where not every query row sees all of the tile
   // (seen: rows of the tile that this lane's query row may see); returns the row's maximum.
   __device__ __forceinline__ static float scores(const char *__restrict__ tile,
-                                                 const s16x8 (&qf)[QF], int wave, int lane,
-                                                 int32_t seen, bool whole, f32x4 (&s)[ST]) {
+                                                 const Lanes &at, const s16x8 (&qf)[QF], int wave,
+                                                 int lane, int32_t seen, bool whole,
+                                                 f32x4 (&s)[ST]) {
     constexpr int AHEAD = 2;  // panels read ahead
     s16x8 kf[AHEAD + 1][ST][2];
 #pragma unroll
     for (int j = 0; j < ST; ++j) s[j] = f32x4{};
 #pragma unroll
-    for (int n = 0; n < AHEAD; ++n) load_keys(tile, wave, lane, n, kf[n]);
+    for (int n = 0; n < AHEAD; ++n) load_keys(tile, at, n, kf[n]);
 #pragma unroll
     for (int n = 0; n < PANELS; ++n) {
       if (n + AHEAD < PANELS)
-        load_keys(tile, wave, lane, n + AHEAD, kf[(n + AHEAD) % (AHEAD + 1)]);
+        load_keys(tile, at, n + AHEAD, kf[(n + AHEAD) % (AHEAD + 1)]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -205,10 +221,11 @@ struct Step {
   }
 
   // The weights of the wavefront's strips at maximum `top`, into the P tile; returns this lane's
-  // share of their sum.
-  __device__ __forceinline__ static float weights(char *__restrict__ pt, const f32x4 (&s)[ST],
-                                                  int wave, int lane, float scale_log2,
-                                                  float top) {
+  // share of their sum.  P lies in the order the second product takes it: a 16-byte chunk 2 k + h
+  // holds the weights of cache rows 16 k + 4 h + {0..3} and of those 8 further on.
+  __device__ __forceinline__ static float weights(char *__restrict__ pt, const Lanes &at,
+                                                  const f32x4 (&s)[ST], int wave,
+                                                  float scale_log2, float top) {
     const float ref = top == kNegInf ? 0.0f : top;
     float sum = 0.0f;
 #pragma unroll
@@ -219,32 +236,24 @@ struct Step {
         e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][r], scale_log2, -ref));
         sum += e[r];
       }
-      put_weights(pt, s_row(wave, lane), (part(wave) * ST + j) * 4 + (lane >> 4), e);
+      *reinterpret_cast<uint2 *>(pt + (at.put ^ (uint32_t(part(wave) * ST + j) * 32u))) =
+          make_uint2(Mfma<T>::pack(e[0], e[1]), Mfma<T>::pack(e[2], e[3]));
     }
     return sum;
   }
 
-  // Weights of four cache rows (4 g4 .. + 3 of the tile) of query row `row` into the P tile, in
-  // the order the second product takes them: a 16-byte chunk 2 k + h holds cache rows
-  // 16 k + 4 h + {0..3} and those 8 further on.
-  __device__ static void put_weights(char *__restrict__ pt, int row, int g4, const float *e) {
-    const uint32_t chunk = uint32_t(2 * (g4 >> 2) + (g4 & 1));
-    *reinterpret_cast<uint2 *>(pt + panel_chunk(uint32_t(row), chunk) + ((g4 >> 1) & 1) * 8) =
-        make_uint2(Mfma<T>::pack(e[0], e[1]), Mfma<T>::pack(e[2], e[3]));
-  }
-
   // O^T += V^T P^T over the tile.
   __device__ __forceinline__ static void outputs(const char *__restrict__ tile,
-                                                 const char *__restrict__ pt, int wave, int lane,
-                                                 f32x16 (&acc)[OB][COLS]) {
+                                                 const char *__restrict__ pt, const Lanes &at,
+                                                 int wave, f32x16 (&acc)[OB][COLS]) {
     s16x8 pf[2][OB], vf[2];  // read one product ahead
-    load_weights(pt, wave, lane, 0, pf[0]);
-    vf[0] = load_values(tile, wave, lane, 0);
+    load_weights(pt, at, 0, pf[0]);
+    vf[0] = load_values(tile, at, wave, 0);
 #pragma unroll
     for (int n = 0; n < 4 * COLS; ++n) {
       const int k = n / COLS;
-      if (n + 1 < 4 * COLS) vf[(n + 1) % 2] = load_values(tile, wave, lane, n + 1);
-      if (n % COLS == 0 && k < 3) load_weights(pt, wave, lane, k + 1, pf[(k + 1) % 2]);
+      if (n + 1 < 4 * COLS) vf[(n + 1) % 2] = load_values(tile, at, wave, n + 1);
+      if (n % COLS == 0 && k < 3) load_weights(pt, at, k + 1, pf[(k + 1) % 2]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < OB; ++i)
@@ -279,7 +288,7 @@ latent_paged_kernel(PagedPlan p) {
   auto &row_max = lds.row_max;
   int32_t *wave_total = lds.wave_total;
 
-  const int tid = int(threadIdx.x), lane = tid & 63, lane_id = lane;
+  const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // the workgroups of a cluster are kXcds apart: on one XCD, they share its L2
   const int32_t turn = int32_t(blockIdx.x / kXcds);
@@ -354,6 +363,7 @@ latent_paged_kernel(PagedPlan p) {
   int32_t item = uniform(int32_t(uint32_t(into) / uint32_t(sq.cost())));
   int32_t x0 = into - item * sq.cost();  // where in the item
   int32_t w = w0;
+  typename S::Lanes at(wave, lane);
   uint32_t partial = 0;  // bit s: part s of this cluster is one of an item's several
 
   while (true) {
@@ -406,6 +416,7 @@ latent_paged_kernel(PagedPlan p) {
                                 ? 0
                                 : sq.len - sq.count + int32_t(div_by(p.div_heads, uint32_t(row0))) + 1;
 
+      const char *cache = static_cast<const char *>(p.cache);
       float s_top = kNegInf, s_sum = 0.0f;
       f32x16 acc[OB][COLS];
 #pragma unroll
@@ -419,53 +430,76 @@ latent_paged_kernel(PagedPlan p) {
       // one, and all of them see at the barrier before the second product whether any had to pass
       // it, which is rare.  Then the maxima are exchanged, accumulators and sums rescaled and the
       // weights taken again.
-      auto step = [&](const char *__restrict__ cur, char *__restrict__ other,
-                      char *__restrict__ pt, float *__restrict__ rm, int32_t *__restrict__ raised,
-                      const int64_t *__restrict__ pages, const char *cache, int64_t piece,
-                      int32_t st) {
-        if (st + 1 < end) fetch_tile<PANELS>(cache, piece, wave, lane_id, other);
+      //
+      // LDS pointers are arguments, restrict, of what runs between two barriers and of nothing
+      // longer: so the compiler does not wait for the loads into the other buffer at each use, and
+      // moves no access over a barrier.
+      const int s_row = S::s_row(wave, lane), s_part = S::part(wave);
+      f32x4 s[S::ST];
+      float best = 0.0f, sum = 0.0f;
+      // the tile's scores, and weights at the present maxima; returns where the tile after the
+      // next one comes from
+      auto first_half = [&](const char *__restrict__ cur, char *__restrict__ other,
+                            char *__restrict__ pt, int32_t *__restrict__ raised,
+                            const int64_t *__restrict__ pages, const char *cache, int64_t piece,
+                            int32_t st) {
+        if (st + 1 < end) fetch_tile<PANELS>(cache, piece, wave, other);
         const int32_t tile0 = st * STEP;
-        // LDS addresses are worked out again in every step: kept from step to step they would
-        // take the registers that Q and the accumulators need
-        int lane = lane_id;
-        asm volatile("" : "+v"(lane));
-        f32x4 s[S::ST];
-        const float best = S::scores(cur, qf, wave, lane, limit - tile0, tile0 + STEP <= floor, s) *
-                           p.scale_log2;
-        float sum = S::weights(pt, s, wave, lane, p.scale_log2, s_top);
+        at.fresh();
+        best = S::scores(cur, at, qf, wave, lane, limit - tile0, tile0 + STEP <= floor, s) *
+               p.scale_log2;
+        sum = S::weights(pt, at, s, wave, p.scale_log2, s_top);
         if (__any(best > s_top + 8.0f) && lane == 0) *raised = 1;
-        // where the tile after the next one comes from
-        const int64_t after = st + 2 < end ? tile_piece<T>(p, pages, page0, (st + 2) * STEP,
-                                                           sq.len, wave, lane)
-                                           : 0;
+        return st + 2 < end
+                   ? tile_piece<T>(p, pages, page0, (st + 2) * STEP, sq.len, wave, lane)
+                   : 0;
+      };
+      auto any_raised = [&](const int32_t *__restrict__ raised) { return uniform(*raised) != 0; };
+      auto put_row = [&](float *__restrict__ rm, int slot, float x) {
+        if (lane < 16) rm[slot * ROWS + s_row] = x;
+      };
+      // new maxima and weights; returns the factor that what was summed before is rescaled by
+      auto raise = [&](const float *__restrict__ rm, char *__restrict__ pt,
+                       int32_t *__restrict__ raised) {
+        if (tid == 0) *raised = 0;
+        float high = rm[s_row];
+#pragma unroll
+        for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, rm[k * ROWS + s_row]);
+        float f = 1.0f;
+        if (high > s_top + 8.0f) {
+          f = __builtin_amdgcn_exp2f(s_top - high);
+          s_top = high;
+        }
+        s_sum *= f;
+        sum = S::weights(pt, at, s, wave, p.scale_log2, s_top);
+        return f;
+      };
+      auto rescale = [&](const float *__restrict__ rm) {
+#pragma unroll
+        for (int i = 0; i < OB; ++i) {
+          const float f = rm[S::o_row(wave, lane, i) % ROWS];
+#pragma unroll
+          for (int d = 0; d < COLS; ++d) acc[i][d] *= f;
+        }
+      };
+      auto second_half = [&](const char *__restrict__ cur, const char *__restrict__ pt) {
+        if (S::has_output(wave)) S::outputs(cur, pt, at, wave, acc);
+      };
+      auto step = [&](const char *cur, char *other, int64_t piece, int32_t st) {
+        float *rm = &row_max[0][0];
+        const int64_t after = first_half(cur, other, weights, &lds.raised, places, cache, piece, st);
         lds_barrier();
-        if (uniform(*raised) != 0) {
-          const int row = S::s_row(wave, lane);
-          if (lane < 16) rm[S::part(wave) * ROWS + row] = best;
+        if (any_raised(&lds.raised)) {
+          put_row(rm, s_part, best);
           lds_barrier();
-          if (tid == 0) *raised = 0;
-          float high = rm[row];
-#pragma unroll
-          for (int k = 1; k < S::PARTS; ++k) high = fmaxf(high, rm[k * ROWS + row]);
-          float f = 1.0f;
-          if (high > s_top + 8.0f) {
-            f = __builtin_amdgcn_exp2f(s_top - high);
-            s_top = high;
-          }
-          s_sum *= f;
-          sum = S::weights(pt, s, wave, lane, p.scale_log2, s_top);
+          const float f = raise(rm, weights, &lds.raised);
           lds_barrier();
-          if (S::part(wave) == 0 && lane < 16) rm[row] = f;
+          if (s_part == 0) put_row(rm, 0, f);
           lds_barrier();
-#pragma unroll
-          for (int i = 0; i < OB; ++i) {
-            const float g = rm[S::o_row(wave, lane, i) % ROWS];
-#pragma unroll
-            for (int d = 0; d < COLS; ++d) acc[i][d] *= g;
-          }
+          rescale(rm);
         }
         s_sum += sum;
-        if (S::has_output(wave)) S::outputs(cur, pt, wave, lane, acc);
+        second_half(cur, weights);
         return after;
       };
 
@@ -474,17 +508,15 @@ latent_paged_kernel(PagedPlan p) {
         while (true) {
           // ---- the steps: the next tile is on its way while one is multiplied ----
           lds_barrier();
-          const char *cache = static_cast<const char *>(p.cache);
           fetch_tile<PANELS>(cache, tile_piece<T>(p, places, page0, st * STEP, sq.len, wave, lane),
-                             wave, lane, tiles);
+                             wave, tiles);
           int64_t next = st + 1 < end ? tile_piece<T>(p, places, page0, (st + 1) * STEP, sq.len,
                                                       wave, lane)
                                       : 0;
           for (int32_t i = 0; st < end; ++st, ++i) {
             wait_loads_all();
             lds_barrier();
-            next = step(tiles + (i & 1) * TILE, tiles + (~i & 1) * TILE, weights, &row_max[0][0],
-                        &lds.raised, places, cache, next, st);
+            next = step(tiles + (i & 1) * TILE, tiles + (~i & 1) * TILE, next, st);
           }
           if (st >= st1) break;
           lds_barrier();
@@ -496,12 +528,12 @@ latent_paged_kernel(PagedPlan p) {
       s_sum = sum_quarters(s_sum);
       float o_top[OB];
       lds_barrier();
-      if (S::part(wave) == 0 && lane < 16) row_max[0][S::s_row(wave, lane)] = s_top;
+      if (s_part == 0) put_row(&row_max[0][0], 0, s_top);
       lds_barrier();
 #pragma unroll
       for (int i = 0; i < OB; ++i) o_top[i] = row_max[0][S::o_row(wave, lane, i) % ROWS];
       lds_barrier();
-      if (lane < 16) row_max[S::part(wave)][S::s_row(wave, lane)] = s_sum;
+      put_row(&row_max[0][0], s_part, s_sum);
       lds_barrier();
 
       // ---- the segment's result: a whole item's output, or a part for the joining kernel ----
@@ -535,7 +567,7 @@ latent_paged_kernel(PagedPlan p) {
               if (first_column && lane < 32 && p.lse != nullptr)
                 p.lse[out_row] = some ? o_top[i] * 0.693147180559945f + logf(sum) : kNegInf;
             }
-          } else {
+          } else if (r < rows) {
             float *part = p.parts + slot * ROWS * p.latent + m * 4;
 #pragma unroll
             for (int d = 0; d < COLS; ++d)
@@ -543,8 +575,8 @@ latent_paged_kernel(PagedPlan p) {
               for (int c = 0; c < 4; ++c) {
                 const f32x16 &a = acc[i][d];
                 const int d4 = S::column(wave, d) * 8 + c * 2 + (lane >> 5);
-                *reinterpret_cast<float4 *>(part + d4 * (ROWS * 4)) =
-                    make_float4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
+                const f32x4 v = {a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]};
+                *reinterpret_cast<f32x4 *>(part + d4 * (ROWS * 4)) = v;
               }
             if (first_column && lane < 32)
               *reinterpret_cast<float2 *>(p.stats + (slot * ROWS + m) * 2) =

@@ -149,6 +149,9 @@ __device__ inline uint32_t panel_transposed(uint32_t lane, uint32_t e, uint32_t 
   return row * 128u + ((c ^ chunk_key(row)) << 4) + (i & 1u) * 8u;
 }
 
+// What the place of row + 8 differs by from that of a row whose number has the bit 8 clear.
+constexpr uint32_t kEightRows = 8u * 128u | 3u << 4;
+
 // The operand of 16 rows (from a multiple of 16) of 32 columns, transposed: k values in the order
 // 4 (lane / 32) + {0..3, 8..11}.
 __device__ inline s16x8 transposed_operand(const char *panel, uint32_t lane, uint32_t e) {

@@ -206,7 +206,10 @@ def test_paged_many_ragged_sequences():
     g = torch.Generator().manual_seed(0)
     lens = torch.randint(0, 900, (300,), generator=g).tolist()
     counts = torch.randint(0, 3, (300,), generator=g).tolist()
-    check_paged(lens, counts, 16, 128, F16, 16, seed=9)
+    for heads, latent in ((16, 128), (40, 256), (128, 512)):
+        first = check_paged(lens, counts, heads, latent, F16, 16, seed=9)
+        for _ in range(5):
+            assert torch.equal(first, check_paged(lens, counts, heads, latent, F16, 16, seed=9))
 
 
 @pytest.mark.parametrize("heads", [16, 128])
