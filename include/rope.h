@@ -16,15 +16,17 @@
  *                                  values come from one latent row a token (absorbed form)
  *   rope_latent_attention          the expanded form, for prompts and training: a key and value
  *                                  of every head and one rotated key part shared by the heads
- *   rope_latent_attention_backward its gradients
+ *   rope_latent_attention_backward
+ *                                  its gradients
  *
  * Pages defining the operations:
  *   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码
  *           接口详解与实现剖析"
  *   [RSCC] "CANN ops-transformer 旋转位置编码算子 RopeWithSinCosCache 深度解析：cache 化 RoPE 的
  *           计算原理与 aclnn 两段式调用实战"
- * Both pages describe a two-phase interface (workspace size, then execute).  These kernels
- * need no workspace, so the two phases are one call here.
+ * Both pages describe a two-phase interface (workspace size, then execute).  Their kernels
+ * need no workspace here, so the two phases are one call.  Where the attention calls need one,
+ * a function beside them gives its size and the caller passes it.
  *
  * Common rules
  *  - Memory: every tensor `data` pointer is device memory (or memory the GPU can address)
@@ -37,7 +39,7 @@
  *    call returns once the work is enqueued; results are visible after the stream is
  *    synchronized.  The library is stateless and reentrant; calls that touch the same
  *    buffers must be ordered by the caller (same stream or events).
- *  - Arithmetic: operands are raised to float32, each product and each sum of the formulas
+ *  - Arithmetic (of the rotations; the attention calls state theirs): operands are raised to float32, each product and each sum of the formulas
  *    is one float32 operation (no fused multiply-add), and the result is rounded once to
  *    the tensor dtype (round to nearest even).  Data outside the rotated range is never
  *    converted: it is left untouched (in-place op) or copied bit for bit (cache op).
@@ -247,8 +249,9 @@ int rope_append_paged_cache(const rope_tensor *positions, const rope_tensor *slo
  *       lse[i, h] = log sum_j exp(s_j)
  * Products accumulate in float32; maxima, sums and outputs are float32 until one rounding to the
  * output's dtype; the weights p are rounded to the dtype for the second product.  A query that
- * sees no row gets zeros and lse = -infinity.  What no query sees is never read into a result:
- * rows past len may hold anything.
+ * sees no row gets zeros and lse = -infinity.  Rows past len may hold anything: they reach no
+ * result.  A row that a sequence's last query sees and an earlier one does not has weight 0 for
+ * the earlier one, so a NaN or infinity in it makes that query's output NaN too.
  *
  * query          [T, heads, latent_dim + 64], F16 or BF16, unit inner stride, rows on 16-byte
  *                boundaries, any non-negative strides.
@@ -259,7 +262,8 @@ int rope_append_paged_cache(const rope_tensor *positions, const rope_tensor *slo
  * seq_lens       INT64 [B]: cached tokens, clamped to [0, maxPages * pageSize].
  * query_offsets  INT64 [B + 1], ascending: sequence b's queries are rows offsets[b] to
  *                offsets[b+1] of query and out; rows outside all of them are left as they are.
- *                Out-of-range values are clamped.  NULL: T / B queries each (T % B == 0).
+ *                Out-of-range values are clamped; where they descend, the call writes no result.
+ *                NULL: T / B queries each (T % B == 0).
  * latent_dim     128, 256 or 512.     scale   finite.
  * out            [T, heads, latent_dim] contiguous, 16-byte aligned; lse F32 [T, heads]
  *                contiguous, or NULL.  Outputs may not overlap anything else.
@@ -284,7 +288,8 @@ int rope_latent_attention_paged(const rope_tensor *query, const rope_tensor *lat
  *       p = softmax_j(s),  out[i, h] = sum_j p_ij value[j, h],  lse[i, h] = log sum_j exp(s_ij)
  * With causal != 0 query i sees keys j < m - n + 1 + i (the last query sees them all), else all.
  * Precision as in rope_latent_attention_paged.  A query that sees no key gets zeros and
- * lse = -infinity.  A NaN or infinity in a token reaches results of its own sequence only.
+ * lse = -infinity.  A NaN or infinity in a token reaches results of its own sequence only, there
+ * also those of queries that do not see the token.
  *
  * query      [Tq, heads, dim + 64], key [Tk, heads, dim], key_rope [Tk, 64], value
  *            [Tk, heads, dim]: F16 or BF16, one dtype, dim 64 or 128, unit inner stride, rows on

@@ -352,7 +352,7 @@ def _pack(t):
 
 def _device_index(tensors) -> int:
     """GPU of the tensors (-1: none of them has elements)."""
-    dev = -1
+    dev = None
     for t in tensors:
         if t is None:
             continue
@@ -363,10 +363,10 @@ def _device_index(tensors) -> int:
             if d < 0:
                 raise RopeError(ROPE_ERR_PARAM_INVALID,
                                 "tensors must live in GPU memory (torch device 'cuda')")
-            if dev >= 0:
+            if dev is not None:
                 raise RopeError(ROPE_ERR_PARAM_INVALID, "tensors are on different devices")
             dev = d
-    return dev
+    return -1 if dev is None else dev
 
 
 def _raw_stream(stream, dev: int):
@@ -433,7 +433,8 @@ def rope_latent_attention_paged(query, latent_cache, page_table, seq_lens, laten
     head.  page_table [B, maxPages], seq_lens [B] (the queries' own tokens included) and
     query_offsets [B + 1] are int64; without offsets every sequence has T / B queries.  Query i of
     n sees the cached rows below seq_len - n + 1 + i.  Returns (out [T, heads, latent_dim],
-    lse [T, heads] float32)."""
+    lse [T, heads] float32); rows outside all sequences are not written, so pass out and lse where
+    they are to be defined."""
     import torch
     dev = _device_index((query, latent_cache, page_table, seq_lens, query_offsets, out, lse))
     if latent_cache.dim() == 4 and latent_cache.shape[2] == 1:
@@ -468,8 +469,9 @@ def rope_latent_attention(query, key, key_rope, value, scale: float, causal: boo
     and, in the last 64 elements, key_rope [Tk, 64], which all heads share; value [Tk, heads, dim].
     Sequences are packed one behind the other: int64 query_offsets and key_offsets [B + 1], or
     num_sequences (1 by default) of equal length.  Causal: of n queries and m keys query i sees the
-    first m - n + 1 + i keys.  Returns (out [Tq, heads, dim], lse [Tq, heads] float32).  Not
-    recorded by autograd: that is latent_attention."""
+    first m - n + 1 + i keys.  Returns (out [Tq, heads, dim], lse [Tq, heads] float32); rows outside
+    all sequences are not written, so pass out and lse where they are to be defined.  Not recorded
+    by autograd: that is latent_attention."""
     import torch
     dev = _device_index((query, key, key_rope, value, query_offsets, key_offsets, out, lse))
     if query.dim() != 3 or value.dim() != 3:
@@ -531,10 +533,11 @@ def _latent_autograd_function():
             return out
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, grad):
             *saved, q_off, k_off = ctx.saved_tensors
-            if grad.stride(-1) != 1 or any(s * grad.element_size() % 16 for s in grad.stride()[:-1]):
-                grad = grad.contiguous()  # an expanded or transposed gradient
+            if not grad.is_contiguous() or grad.data_ptr() % 16:  # expanded, transposed, a slice
+                grad = grad.clone(memory_format=torch.contiguous_format)
             grads = rope_latent_attention_backward(grad, *saved, *ctx.where, q_off, k_off)
             return (*grads, None, None, None, None, None)
 

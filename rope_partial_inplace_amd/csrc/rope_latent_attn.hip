@@ -697,10 +697,11 @@ int run_forward(ExpandedPlan &p, void *stream) {
 template <typename T, int DIM>
 int run_backward(ExpandedPlan &p, void *stream) {
   int st = ROPE_OK;
-  if (p.q_tiles > 0)
+  const bool any = p.heads > 0 && p.B > 0;
+  if (any && p.q_tiles > 0)
     st = launch_kernel(reinterpret_cast<const void *>(&latent_dquery_kernel<T, DIM>),
                        dim3(head_grid(p.heads, p.q_tiles)), kBlockThreads, 0, stream, &p);
-  if (st == ROPE_OK && p.k_tiles > 0)
+  if (st == ROPE_OK && any && p.k_tiles > 0)
     st = launch_kernel(reinterpret_cast<const void *>(&latent_dkey_kernel<T, DIM>),
                        dim3(head_grid(p.heads, p.k_tiles)), kKeyThreads, 0, stream, &p);
   if (st != ROPE_OK) return st;

@@ -47,7 +47,7 @@ constexpr int32_t kItemCost = 2;
 struct Sequence {
   int32_t len;     // cached tokens
   int32_t first;   // first query token
-  int32_t count;   // query tokens
+  int32_t count;   // query tokens (below 0: the offsets descend here)
   int32_t items;
   int32_t steps;   // of one item
   __device__ int32_t cost() const { return steps + kItemCost; }
@@ -61,14 +61,14 @@ __device__ inline Sequence sequence(const PagedPlan &p, int32_t b, int rows, int
   s.len = int32_t(min(max(p.lens[b * p.len_stride], int64_t(0)), cap));
   if (p.offsets != nullptr) {
     const int64_t o0 = min(max(p.offsets[b * p.off_stride], int64_t(0)), p.T);
-    const int64_t o1 = min(max(p.offsets[(b + 1) * p.off_stride], o0), p.T);
+    const int64_t o1 = min(max(p.offsets[(b + 1) * p.off_stride], int64_t(0)), p.T);
     s.first = int32_t(o0);
     s.count = int32_t(o1 - o0);
   } else {
     s.first = int32_t(b * p.queries);
     s.count = int32_t(p.queries);
   }
-  s.items = (s.count * p.heads + rows - 1) / rows;
+  s.items = (max(s.count, 0) * p.heads + rows - 1) / rows;
   s.steps = max(1, (s.len + step - 1) / step);
   return s;
 }
@@ -299,18 +299,23 @@ latent_paged_kernel(PagedPlan p) {
   // ---- the cluster's share [w0, w1) of all items' cost (it fits 31 bits: plan) ----
   Sequence sq = {};
   int32_t mine = 0, n = 0;
+  bool descends = false;
   if (tid < p.B) {
     sq = sequence(p, tid, item_rows, STEP);
     n = sq.items * sq.cost();
+    descends = sq.count < 0;
   }
   for (int32_t b = tid + kPagedBlock; b < p.B; b += kPagedBlock) {
     const Sequence s = sequence(p, b, item_rows, STEP);
     mine += s.items * s.cost();
+    descends |= s.count < 0;
   }
   int32_t incl = wave_scan(n);
   const int32_t rest = p.B > kPagedBlock ? wave_scan(mine) : 0;
   if (lane == 63) wave_total[wave] = incl + rest;
-  __syncthreads();
+  // Offsets that descend could let the sequences' rows add up to more than the plan's 31 bits
+  // hold: then there is no work.
+  descends = __syncthreads_or(descends);
   int32_t total = 0;
 #pragma unroll
   for (int v = 0; v < kPagedWaves; ++v) total += wave_total[v];
@@ -318,7 +323,7 @@ latent_paged_kernel(PagedPlan p) {
   total = uniform(total);
   const int32_t per = uniform(int32_t((uint32_t(total) + p.clusters - 1) / uint32_t(p.clusters)));
   const int64_t start = int64_t(g) * per;
-  if (start >= total) {
+  if (descends || start >= total) {
     if (tid < 2 && member == 0) p.joins[(g * 2 + tid) * kJoinWords] = 0;
     return;
   }

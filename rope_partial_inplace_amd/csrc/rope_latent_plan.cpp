@@ -363,10 +363,11 @@ int plan_expanded_backward(const rope_tensor *grad, const rope_tensor *query,
                      {grad, query, key, key_rope, value, out, lse, query_offsets, key_offsets}))
     return reject(err, ROPE_ERR_PARAM_INVALID, "an output overlaps another tensor");
   ExpandedPlan &p = *plan;
-  p.noop = (p.Tq == 0 && p.Tk == 0) || p.heads == 0 || p.B == 0;
+  // without heads or sequences there are still zero gradients to write
+  p.noop = p.Tq == 0 && p.Tk == 0;
   if (p.noop) return ROPE_OK;
   const int64_t need = expanded_workspace(p.Tq, p.Tk, p.heads);
-  if (workspace == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "workspace is NULL");
+  if (need > 0 && workspace == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "workspace is NULL");
   if (workspace_bytes < need || !aligned16(workspace))
     return reject(err, ROPE_ERR_PARAM_INVALID, "workspace too small or not 16-byte aligned");
   for (const rope_tensor *t : {grad, query, key, key_rope, value, out, lse, query_offsets,

@@ -210,6 +210,35 @@ def test_autograd_layouts_and_unused_rows():
     assert torch.equal(o2[:54], out[:54])
 
 
+def test_gradients_without_heads_or_sequences_are_zero():
+    q, k, kr, v, grad = inputs([40], [70], 2, 64, BF16, 11)
+    none = torch.zeros(1, dtype=torch.int64, device=DEV)
+    lse = torch.zeros(40, 2, device=DEV)
+    torch.full((1 << 20,), float("nan"), device=DEV)  # freed again: new tensors find it
+    grads = ra.rope_latent_attention_backward(grad, q, k, kr, v, grad, lse, 0.1,
+                                              query_offsets=none, key_offsets=none)
+    assert all((x == 0).all() for x in grads)
+    torch.full((1 << 20,), float("nan"), device=DEV)
+    grads = ra.rope_latent_attention_backward(*(x[:, :0] for x in (grad, q, k)), kr,
+                                              *(x[:, :0] for x in (v, grad, lse)), 0.1)
+    assert (grads[2] == 0).all() and all(grads[i].numel() == 0 for i in (0, 1, 3))
+
+
+def test_autograd_takes_gradients_off_alignment_and_refuses_a_second_order():
+    q, k, kr, v, grad = inputs([30], [30], 2, 64, BF16, 12)
+    x = [t.clone().requires_grad_() for t in (q, k, kr, v)]
+    odd = torch.zeros(3, dtype=BF16, device=DEV, requires_grad=True)
+    out = ra.latent_attention(*x, 0.1)
+    joined = torch.cat([odd, out.reshape(-1)])  # out's gradient begins 6 bytes into its memory
+    one = torch.autograd.grad(joined, x, torch.cat([odd.detach(), grad.reshape(-1)]))
+    two = torch.autograd.grad(ra.latent_attention(*x, 0.1), x, grad)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    first = torch.autograd.grad(ra.latent_attention(*x, 0.1).float().pow(2).sum(), x,
+                                create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(first[0].float().sum(), x)
+
+
 def test_repeats_streams_and_graph_replays():
     """Bit-identical repeats, on another stream too; a captured forward and backward replayed with
     new inputs, eager work in between."""

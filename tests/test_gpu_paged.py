@@ -287,6 +287,16 @@ def test_paged_bad_pages_lengths_and_offsets_stay_inside():
     assert torch.equal(a[0], b[0])
 
 
+def test_paged_descending_offsets_write_nothing():
+    q, cache, table, sl, _ = paged_inputs([100, 50, 70], [2, 1, 1], 16, 128, BF16, 16, 1)
+    for off in ([0, 4, 0, 4], [3, 2, 4, 4], [0, 1, 4, 3]):
+        out = torch.full((4, 16, 128), 3.0, dtype=BF16, device=DEV)
+        lse = torch.full((4, 16), 3.0, device=DEV)
+        ra.rope_latent_attention_paged(q, cache, table, sl, 128, 0.1, out=out, lse=lse,
+                                       query_offsets=torch.tensor(off, device=DEV))
+        assert (out == 3).all() and (lse == 3).all()
+
+
 def test_paged_repeats_are_identical():
     q, cache, table, sl, _ = paged_inputs([5000, 100, 3000], [1, 1, 1], 32, 512, BF16, 64, 6)
     first = ra.rope_latent_attention_paged(q, cache, table, sl, 512, 0.07)
