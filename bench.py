@@ -52,7 +52,8 @@ MALL_DEFEAT_BYTES = 2 << 30
 # The sources that decide what a launch does: the kernels and the launch plans (which kernel,
 # grid and layout a workload gets).
 KERNEL_SOURCES = [os.path.join(ROOT, "rope_partial_inplace_amd", "csrc", f)
-                  for f in ("rope_kernels.hip", "rope_plan.h", "rope_plan.cpp")]
+                  for f in ("rope_kernels.hip", "rope_io.h", "rope_launch.h", "rope_plan.h",
+                            "rope_plan.cpp", "rope_check.h")]
 CEILING_SRC = os.path.join(ROOT, "bench_ceiling.hip")
 CEILING_LIB = os.path.join(ROOT, "libbench_ceiling.so")
 HEADLINE = "cache_rope_gptj_f16_t32768_rd64"
