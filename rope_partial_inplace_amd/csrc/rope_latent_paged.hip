@@ -22,6 +22,7 @@
 
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "rope.h"
 #include "rope_latent_plan.h"
@@ -625,9 +626,9 @@ latent_paged_kernel(PagedPlan p) {
 // One workgroup for each part joins the n-th part of the item's (4-column group, row) cells, so
 // that all workgroups have about one part's bytes to read.  It is a launch of a few dependent
 // reads: `share` wavefronts take the parts of a cell in turn, as many as the workgroup has to
-// spare, eight parts' reads under way at once, and add up through LDS in a fixed order.
+// spare, four parts' reads under way at once, and add up through LDS in a fixed order.
 constexpr int kJoinBlock = 1024;
-constexpr int kJoinAhead = 8;
+constexpr int kJoinAhead = 4;
 
 template <typename T, int DB, int RB>
 __global__ __launch_bounds__(kJoinBlock) void latent_paged_join_kernel(PagedPlan p) {
@@ -654,15 +655,26 @@ __global__ __launch_bounds__(kJoinBlock) void latent_paged_join_kernel(PagedPlan
     const bool mine = cell < c1 && m < live;
     float top = kNegInf, l = 0.0f;
     float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto take = [&](float top_k, float l_k, const float4 &o) {
-      const float next = fmaxf(top, top_k), ref = next == kNegInf ? 0.0f : next;
-      const float fa = __builtin_amdgcn_exp2f(top - ref), fb = __builtin_amdgcn_exp2f(top_k - ref);
+    // what is held so far and `N` parts more, all at the highest maximum among them
+    auto take = [&](auto count, const float2 *stat, const float4 *o) {
+      constexpr int N = decltype(count)::value;
+      float next = top;
+#pragma unroll
+      for (int u = 0; u < N; ++u) next = fmaxf(next, stat[u].x);
+      const float ref = next == kNegInf ? 0.0f : next;
+      const float f = __builtin_amdgcn_exp2f(top - ref);
       top = next;
-      l = l * fa + l_k * fb;
-      t.x = t.x * fa + o.x * fb;
-      t.y = t.y * fa + o.y * fb;
-      t.z = t.z * fa + o.z * fb;
-      t.w = t.w * fa + o.w * fb;
+      l *= f;
+      t = make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const float w = __builtin_amdgcn_exp2f(stat[u].x - ref);
+        l += stat[u].y * w;
+        t.x += o[u].x * w;
+        t.y += o[u].y * w;
+        t.z += o[u].z * w;
+        t.w += o[u].w * w;
+      }
     };
     if (mine) {
       for (int32_t k0 = wave % share; k0 < n; k0 += kJoinAhead * share) {
@@ -670,15 +682,17 @@ __global__ __launch_bounds__(kJoinBlock) void latent_paged_join_kernel(PagedPlan
         float4 o[kJoinAhead];
 #pragma unroll
         for (int u = 0; u < kJoinAhead; ++u) {
-          const int32_t k = min(k0 + u * share, n - 1);
-          const int64_t slot = (int64_t(g0 + k) * p.cluster + member) * 2 + (k == 0 ? first : 0);
-          stat[u] = *reinterpret_cast<const float2 *>(p.stats + (slot * ROWS + m) * 2);
-          o[u] = *reinterpret_cast<const float4 *>(p.parts + slot * ROWS * p.latent +
-                                                   int64_t(cell) * 4);
+          const int32_t k = k0 + u * share;
+          stat[u] = make_float2(kNegInf, 0.0f);
+          o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k < n) {
+            const int64_t slot = (int64_t(g0 + k) * p.cluster + member) * 2 + (k == 0 ? first : 0);
+            stat[u] = *reinterpret_cast<const float2 *>(p.stats + (slot * ROWS + m) * 2);
+            o[u] = *reinterpret_cast<const float4 *>(p.parts + slot * ROWS * p.latent +
+                                                     int64_t(cell) * 4);
+          }
         }
-#pragma unroll
-        for (int u = 0; u < kJoinAhead; ++u)
-          if (k0 + u * share < n) take(stat[u].x, stat[u].y, o[u]);
+        take(std::integral_constant<int, kJoinAhead>(), stat, o);
       }
     }
     if (share > 1) {
@@ -687,7 +701,7 @@ __global__ __launch_bounds__(kJoinBlock) void latent_paged_join_kernel(PagedPlan
       __syncthreads();
       if (wave % share == 0)
         for (int k = 1; k < share; ++k)
-          take(add_stat[wave + k][lane].x, add_stat[wave + k][lane].y, add[wave + k][lane]);
+          take(std::integral_constant<int, 1>(), &add_stat[wave + k][lane], &add[wave + k][lane]);
       __syncthreads();
     }
     if (mine && wave % share == 0) {
