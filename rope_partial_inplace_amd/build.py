@@ -41,8 +41,9 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-command-line-argument",
 ]
-# The attention kernels rescale their accumulators with vector instructions, which reach the first
-# 256 registers only: products write those, and operands move to the others.
+# The attention kernels rescale their accumulators with vector instructions, which do not reach the
+# accumulation registers: the products write ordinary ones (kernels without products stay as they
+# are).
 MFMA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra"]
 

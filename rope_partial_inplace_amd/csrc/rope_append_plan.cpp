@@ -124,7 +124,7 @@ int plan_append(const rope_tensor *positions, const rope_tensor *slots, const ro
   p.max_seq = table->shape[0];
   p.half = int32_t(rd / 2);
   p.T = T;
-  p.page_size = key_cache->shape[1];
+  p.page_size = std::max<int64_t>(key_cache->shape[1], 1);
   p.num_slots = key_cache->shape[0] * key_cache->shape[1];
 
   // 16-byte items where every head row, the slice and the table rows split into whole vectors.
@@ -169,14 +169,6 @@ int plan_append(const rope_tensor *positions, const rope_tensor *slots, const ro
     r.blocks = (r.all + kAppendBlock - 1) / kAppendBlock;
     p.idx32 = p.idx32 && r.all + kAppendBlock < (int64_t(1) << 31);
   }
-  p.page32 = p.num_slots < (int64_t(1) << 31);
-  p.div_page = make_fastdiv(uint32_t(std::min<int64_t>(std::max<int64_t>(p.page_size, 1),
-                                                       0x7fffffff)));
-  p.linear = true;
-  for (int g = 1; g < 3; ++g)
-    if (p.rows[g].total > 0 && outs[g]->shape[0] > 1 &&
-        p.rows[g].out_page != p.page_size * p.rows[g].out_tok)
-      p.linear = false;
   return ROPE_OK;
 }
 

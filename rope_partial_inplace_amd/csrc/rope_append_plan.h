@@ -33,7 +33,9 @@ struct AppendPlan {
   bool neox = true;
   bool vector_io = false;  // 16-byte items (else one element, or one pair, at a time)
   bool noop = false;
-  bool idx32 = true;        // item numbers of a group, and of its last lanes, fit 32 bits
+  // item numbers of a group, and of its last lanes, fit 32 bits: decoded by multiplications
+  // (64-bit divisions: 34.7 in place of 34.3 us at 8192 tokens of 48 heads)
+  bool idx32 = true;
   const int64_t *positions = nullptr, *slots = nullptr;
   int64_t pos_stride = 0, slot_stride = 0;
   const void *table = nullptr;
@@ -41,9 +43,6 @@ struct AppendPlan {
   int32_t half = 0;  // rotaryDim / 2
   int64_t T = 0;
   int64_t num_slots = 0, page_size = 1;
-  bool linear = false;  // slot s lies at s * out_tok in both caches: no page arithmetic
-  bool page32 = true;   // slots below 2^32: page number by FastDiv
-  FastDiv div_page;
   AppendRows rows[3];  // query, key, value (total 0: absent)
 };
 

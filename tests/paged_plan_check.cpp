@@ -6,7 +6,7 @@
 // query_out and of every used slot's rows has to be written exactly once, from the input element
 // the formulas name, and nothing else; every rotated element has to be paired with its partner
 // and its own column of the table.  Both styles, every dtype, vector and element paths, one to
-// many heads, slices inside a head, caches that are linear, padded, or keep heads before rows,
+// many heads, slices inside a head, caches that are contiguous, padded, or keep heads before rows,
 // slots out of range, the query in place.
 //
 // All plans: descriptions of random extreme shapes, strides, ranks, types and addresses have to be
@@ -69,7 +69,7 @@ struct Source {
 
 struct Shape {
   int64_t T, nq, nk, Dq, D, Dv, rd, q_start, k_start, pages, page;
-  int layout;  // 0 linear caches, 1 padded rows and pages, 2 heads before rows
+  int layout;  // 0 contiguous caches, 1 padded rows and pages, 2 heads before rows
   bool in_place, query, value;
 };
 
@@ -143,11 +143,8 @@ static int64_t walk(const Shape &s, rope_dtype dt, bool neox, int64_t shift) {
       int64_t out = int64_t(h) * r.out_head;
       if (g == 0) {
         out += t * r.out_tok;
-      } else if (p.linear) {
-        out += slot * r.out_tok;
       } else {
-        const int64_t page =
-            p.page32 ? int64_t(div_by(p.div_page, uint32_t(slot))) : slot / p.page_size;
+        const int64_t page = slot / p.page_size;
         out += page * r.out_page + (slot - page * p.page_size) * r.out_tok;
       }
       if (g != 0 && (slot < 0 || slot >= p.num_slots)) continue;
