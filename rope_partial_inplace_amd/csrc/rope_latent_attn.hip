@@ -15,22 +15,22 @@
 // repeated for each head in memory.
 //
 // Forward, and dq: a workgroup is four wavefronts of 32 query rows of one head; 64 keys and
-// values at a time pass through LDS in two buffers.  dk and dv: eight wavefronts of 16 keys, two
-// on a SIMD, over 64 query rows at a time (four of 32 keys and one on a SIMD: 550 us in place of
-// 520 at the training step below).  dq and dk/dv are two kernels that both compute p again: seven
-// products where atomics on dq would need five, for sums in a fixed order.  Probabilities and ds
-// are rounded to the storage type between the products, as P is in the absorbed form: a relative
+// values at a time pass through LDS in two buffers.  dk and dv: four pairs of wavefronts for 32
+// keys each, over 64 query rows at a time.  dq and dk/dv are two kernels that both compute p again:
+// seven products where atomics on dq would need five, for sums in a fixed order.  Probabilities and
+// ds are rounded to the storage type between the products, as P is in the absorbed form: a relative
 // error of at most half a step on each.
 //
-// Measured, bfloat16, causal, 32 heads of 128: 7 prompts of 300 to 6000 tokens forward 870 - 920
-// us, 0.87 - 0.91 PF/s (a large library product on this card: 1.2 - 1.35); 4 x 2048 tokens, forward
-// 237 us, dq 341, dk and dv 520 - 555, dr 12: 0.7 PF/s of all nine products.  The clock falls to
-// 1.7 - 2.1 GHz under such kernels.  What the products wait for: LDS reads of the keys and the
-// exponentials of a tile, which only the workgroup's or SIMD's other wavefronts cover.
+// Measured, bfloat16, causal, 32 heads of 128: 7 prompts of 300 to 6000 tokens forward 870 - 1010
+// us, 0.79 - 0.91 PF/s (a large library product on this card: 1.2 - 1.35); 4 x 2048 tokens, forward
+// 217 - 239 us, dq 313 - 340, dk and dv 493 - 556, dr 12: 0.7 - 0.76 PF/s of all nine products.
+// The range is the clock's, which falls to 1.7 - 2.1 GHz under such kernels.  What the products
+// wait for: LDS reads, and the exponentials of a tile, which only the SIMD's other wavefront covers.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "rope.h"
 #include "rope_latent_plan.h"
@@ -59,33 +59,65 @@ __device__ inline Span span(const int64_t *off, int64_t stride, int64_t total, i
   return {int32_t(o0), int32_t(o1 - o0)};
 }
 
-// The sequence and the tile within it that tile number `t` of all sequences' tiles is, by query
-// (or key) tokens; sequence -1: there are fewer tiles.
+// A tile of a sequence's query (or key) tokens; sequence -1: there are fewer tiles.
 struct TileAt {
   int32_t seq, tile;
 };
 
-// `scratch`: ten words of LDS, free again on return.
+__device__ inline int32_t wave_sum(int32_t x) {
+  return __builtin_amdgcn_readlane(wave_scan(x), 63);
+}
+
+// The t-th tile of all sequences, longest first: a causal query tile j sees about j tiles of keys,
+// a key tile as many tiles of queries as its sequence has behind it.  A head's tiles begin
+// together on the compute units of one XCD, and one that began late would hold up the end.  (In the
+// order of the sequences, each one's longest first, compute units idled 21% of a training step of
+// 4 x 2048 tokens, and it took 1100 us in place of 1035; 7 prompts of 300 to 6000 tokens took 1004
+// in place of 1013.)
+//
+// Up to 64 sequences, one a lane: with n_b tiles in sequence b, sum_b max(0, n_b - j) of them have
+// an index (counted from the short end) of at least j, so a bisection over j finds the t-th.  With
+// more sequences they come in their own order.  `scratch`: ten words of LDS, free again on return.
 template <bool QUERY, int THREADS>
 __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scratch) {
   const int64_t *off = QUERY ? p.q_off : p.k_off;
   const int64_t each = QUERY ? p.q_each : p.k_each;
+  const int32_t bound = int32_t(QUERY ? p.q_tiles : p.k_tiles);
   if (off == nullptr) {
-    const int32_t per = int32_t((each + kRows - 1) / kRows);
-    if (per == 0 || t / per >= p.B) return {-1, 0};
-    return {t / per, t % per};
+    const int32_t per = int32_t((each + kRows - 1) / kRows), count = int32_t(p.B);
+    if (t >= per * count) return {-1, 0};
+    return {t % count, QUERY ? per - 1 - t / count : t / count};
   }
-  int32_t *sums = static_cast<int32_t *>(scratch), *found = sums + THREADS / 64;
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  auto tiles = [&](int32_t b) {
+    if (b >= p.B) return 0;
+    const Span s = span(off, QUERY ? p.q_off_stride : p.k_off_stride, QUERY ? p.Tq : p.Tk, 0, b);
+    return (s.count + kRows - 1) / kRows;
+  };
+  if (p.B <= 64) {
+    const int32_t n = tiles(lane);
+    if (t >= wave_sum(n)) return {-1, 0};
+    int32_t j = 0, above = bound;  // more than t tiles from j on, and none from `above` on
+    while (above - j > 1) {
+      const int32_t mid = (j + above) / 2;
+      if (wave_sum(max(0, n - mid)) > t)
+        j = mid;
+      else
+        above = mid;
+    }
+    const int32_t rank = t - wave_sum(max(0, n - j - 1));
+    const uint64_t with = __ballot(n > j);
+    const int32_t place = __builtin_amdgcn_mbcnt_hi(uint32_t(with >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo(uint32_t(with), 0));
+    const int32_t seq = __builtin_ctzll(__ballot(n > j && place == rank));
+    return {seq, QUERY ? j : __builtin_amdgcn_readlane(n, seq) - 1 - j};
+  }
+  if (QUERY) t = bound - 1 - t;  // the last tiles first, at least
+  int32_t *sums = static_cast<int32_t *>(scratch), *found = sums + THREADS / 64;
   if (tid == 0) found[0] = -1;
   int32_t before = 0;
   for (int32_t b0 = 0; b0 < p.B; b0 += THREADS) {
-    const int32_t b = b0 + tid;
-    int32_t n = 0;
-    if (b < p.B) {
-      const Span s = span(off, QUERY ? p.q_off_stride : p.k_off_stride, QUERY ? p.Tq : p.Tk, 0, b);
-      n = (s.count + kRows - 1) / kRows;
-    }
+    const int32_t n = tiles(b0 + tid);
     const int32_t incl = wave_scan(n);
     if (lane == 63) sums[wave] = incl;
     __syncthreads();
@@ -95,7 +127,7 @@ __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scrat
       before += sums[w];
     }
     if (base + incl - n <= t && t < base + incl) {
-      found[0] = b;
+      found[0] = b0 + tid;
       found[1] = t - (base + incl - n);
     }
     __syncthreads();
@@ -107,8 +139,8 @@ __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scrat
   return at;
 }
 
-// Workgroup number -> (head, tile): the workgroups of a head, which share its keys and values,
-// follow each other on one XCD, the longest (last) tiles first.
+// Workgroup number -> (head, tile number): the workgroups of a head, which share its keys and
+// values, follow each other on one XCD.
 __device__ inline bool head_and_tile(const ExpandedPlan &p, int64_t tiles, int32_t &head,
                                      int32_t &tile) {
   const int64_t total = int64_t(p.heads) * tiles;
@@ -116,7 +148,7 @@ __device__ inline bool head_and_tile(const ExpandedPlan &p, int64_t tiles, int32
   const int64_t at = int64_t(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
   if (blockIdx.x / kXcds >= per || at >= total) return false;
   head = int32_t(at / tiles);
-  tile = int32_t(tiles - 1 - at % tiles);
+  tile = int32_t(at % tiles);
   return true;
 }
 
@@ -223,79 +255,6 @@ __device__ __forceinline__ void store_columns(char *row, const f32x16 *acc, floa
       *reinterpret_cast<uint2 *>(row + (d * 8 + c * 2 + (lane >> 5)) * 8) =
           make_uint2(Mfma<T>::pack(acc[d][4 * c] * f, acc[d][4 * c + 1] * f),
                      Mfma<T>::pack(acc[d][4 * c + 2] * f, acc[d][4 * c + 3] * f));
-}
-
-// ---- the same with 16 x 16 tiles (32 k values a product) ----
-
-template <int STEPS>
-__device__ __forceinline__ void load_operands16(const char *row, bool live, int lane, s16x8 *f) {
-#pragma unroll
-  for (int k = 0; k < STEPS; ++k)
-    f[k] = live ? as_operand(*reinterpret_cast<const uint4 *>(row + k * 64 + 16 * (lane >> 4)))
-                : s16x8{};
-}
-
-// c[t] += rows row0 + 16 t .. + 15 of LDS panels times register operands, a panel read ahead.
-template <typename T, int PANELS>
-__device__ __forceinline__ void row_product16(const char *lds, int row0, int lane, const s16x8 *b,
-                                              f32x4 (&c)[2]) {
-  s16x8 f[2][2][2];
-  auto load = [](const char *lds, int row0, int lane, int n, s16x8 (&to)[2][2]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        to[k][t] = as_operand(*reinterpret_cast<const uint4 *>(
-            lds + n * 8192 +
-            panel_chunk(uint32_t(row0 + 16 * t + (lane & 15)), 4u * k + (uint32_t(lane) >> 4))));
-  };
-  load(lds, row0, lane, 0, f[0]);
-#pragma unroll
-  for (int n = 0; n < PANELS; ++n) {
-    if (n + 1 < PANELS) load(lds, row0, lane, n + 1, f[(n + 1) % 2]);
-    hold_order();
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) c[t] = Mfma<T>::mul16(f[n % 2][k][t], b[n * 2 + k], c[t]);
-    hold_order();
-  }
-}
-
-// acc[d] += (16-column blocks d of the 32 LDS rows from row0, transposed) times the operand b,
-// whose k values stand for rows 4 (lane / 16) + {0..3, 16..19}.
-template <typename T, int BLOCKS>
-__device__ __forceinline__ void column_product16(const char *lds, int row0, int lane, s16x8 b,
-                                                 f32x4 *acc) {
-  s16x8 f[2][4];
-  auto load = [](const char *lds, int row0, int lane, int d) {
-    const uint32_t i = uint32_t(lane) & 15u, row = 4u * (uint32_t(lane) >> 4) + (i >> 2);
-    const uint32_t c = 2u * uint32_t(d % 4) + ((i & 3u) >> 1);
-    const char *at = lds + d / 4 * 8192 + row0 * 128 + row * 128u + ((c ^ chunk_key(row)) << 4) +
-                     (i & 1u) * 8u;
-    return join(read_transposed(at), read_transposed(at + 2048));
-  };
-#pragma unroll
-  for (int d = 0; d < 4; ++d) f[0][d] = load(lds, row0, lane, d);
-#pragma unroll
-  for (int n = 0; n < BLOCKS / 4; ++n) {
-    if (n + 1 < BLOCKS / 4)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) f[(n + 1) % 2][d] = load(lds, row0, lane, n * 4 + 4 + d);
-    hold_order();
-#pragma unroll
-    for (int d = 0; d < 4; ++d) acc[n * 4 + d] = Mfma<T>::mul16(f[n % 2][d], b, acc[n * 4 + d]);
-    hold_order();
-  }
-}
-
-template <typename T, int BLOCKS>
-__device__ __forceinline__ void store_columns16(char *row, const f32x4 *acc, float f, int lane) {
-#pragma unroll
-  for (int d = 0; d < BLOCKS; ++d)
-    *reinterpret_cast<uint2 *>(row + (d * 4 + (lane >> 4)) * 8) =
-        make_uint2(Mfma<T>::pack(acc[d][0] * f, acc[d][1] * f),
-                   Mfma<T>::pack(acc[d][2] * f, acc[d][3] * f));
 }
 
 // ---- forward ------------------------------------------------------------------------------
@@ -516,9 +475,12 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
 
 // ---- backward: dk, dv and each head's share of the shared key part's gradient ---------------
 
-// Products of 16 keys a wavefront (rope_mfma.h's 16 x 16 tiles, 32 k values each): half the
-// accumulators of 32 keys, so that two wavefronts fit a SIMD and one's exponentials run beside the
-// other's products.
+// Two wavefronts for 32 keys, on one SIMD: the first computes S, p and dv, the second dP, ds and
+// dk, five products of 32 rows by 64 each (dim 128), and p goes from the first to the second through
+// LDS, in float32, where lane and register are the same on both sides.  One wavefront for both
+// would need more registers than a half of a SIMD's (alone on its SIMD it took 4% longer than two
+// of 16 keys), and 16 keys a wavefront, which do fit, read every tile twice as often: 569 us in
+// place of 546 for 4 x 2048 tokens of 32 heads.
 template <typename T, int DIM>
 __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPlan p) {
   constexpr int NP = DIM / 64;
@@ -528,15 +490,14 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
   // before it reads this one)
   struct Lds {
     char tiles[2 * TILE];
-    float stats[2][2][kTile];  // lse * log2(e), D
+    char weights[kRows / 32 * 8192];  // p: 32 keys and 64 query rows of each pair
+    float stats[2][2][kTile];         // lse * log2(e), D
   };
   __shared__ __attribute__((aligned(16))) Lds lds;
   char *tiles = lds.tiles;
   auto &stats = lds.stats;
   int32_t head, tile;
   if (!head_and_tile(p, p.k_tiles, head, tile)) return;
-  // the first keys are seen by the most queries: those tiles first
-  tile = int32_t(p.k_tiles - 1 - tile);
   const TileAt at = find_tile<false, kKeyThreads>(p, tile, tiles);
   if (at.seq < 0) return;
   const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
@@ -545,16 +506,11 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t es = sizeof(T);
-  const int32_t key = at.tile * kRows + wave * 16 + (lane & 15);
+  const int pair = wave % (WAVES / 2);
+  const bool second = wave >= WAVES / 2;
+  const int32_t key = at.tile * kRows + pair * 32 + (lane & 31);
   const bool live = key < k.count;
   const int64_t tok = k.first + key;
-  s16x8 kf[NP * 2 + 2], vf[NP * 2];
-  load_operands16<NP * 2>(static_cast<const char *>(p.k) + (tok * p.k_tok + head * p.k_head) * es,
-                          live, lane, kf);
-  load_operands16<2>(static_cast<const char *>(p.kr) + tok * p.kr_tok * es, live, lane,
-                     kf + NP * 2);
-  load_operands16<NP * 2>(static_cast<const char *>(p.v) + (tok * p.v_tok + head * p.v_head) * es,
-                          live, lane, vf);
   // query i sees key j if j < i + shift; n0: the first 64-row tile with a row that sees one
   const int32_t shift = k.count - q.count + 1;
   const int32_t first_i = p.causal ? max(0, at.tile * kRows - shift + 1) : 0;
@@ -586,62 +542,127 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
     }
   };
   const float scale2 = p.negative ? -p.scale_log2 : p.scale_log2;
-  f32x4 dk[NP * 4 + 4], dv[NP * 4];
-#pragma unroll
-  for (int d = 0; d < NP * 4 + 4; ++d) dk[d] = f32x4{};
-#pragma unroll
-  for (int d = 0; d < NP * 4; ++d) dv[d] = f32x4{};
 
-  auto step = [&](const char *__restrict__ cur, char *__restrict__ other, const float *st,
-                  int32_t i0) {
-    if (i0 + kTile < q.count) fetch(i0 + kTile, other);
-    const bool whole = !p.causal || last_key < i0 + shift;
+  // The two wavefronts' ways are apart from here on, so that each has registers for its own
+  // operands and accumulators only; they meet at the same barriers.
+  auto run = [&](auto role) {
+    constexpr bool SECOND = decltype(role)::value;
+    constexpr int OPERANDS = SECOND ? NP * 4 : NP * 4 + 4, BLOCKS = SECOND ? NP * 2 + 2 : NP * 2;
+    s16x8 f[OPERANDS];  // values; of the first wavefront, keys
+    const char *row = SECOND ? static_cast<const char *>(p.v) + (tok * p.v_tok + head * p.v_head) * es
+                             : static_cast<const char *>(p.k) + (tok * p.k_tok + head * p.k_head) * es;
+    load_operands<NP * 4>(row, live, lane, f);
+    if constexpr (!SECOND)
+      load_operands<4>(static_cast<const char *>(p.kr) + tok * p.kr_tok * es, live, lane,
+                       f + NP * 4);
+    f32x16 acc[BLOCKS];  // dk and the shared part's gradient; dv
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // 32 query rows, in two products of 16
-      f32x4 s[2] = {}, dp[2] = {};
-      row_product16<T, NP + 1>(cur, i * 32, lane, kf, s);
-      row_product16<T, NP>(cur + (NP + 1) * 8192, i * 32, lane, vf, dp);
-      float w[8], e[8];
+    for (int d = 0; d < BLOCKS; ++d) acc[d] = f32x16{};
+    f32x16 x[2];  // dP of the tile's two halves, then ds; p
+
+    auto first_half = [&](const char *__restrict__ cur, char *__restrict__ other,
+                          char *__restrict__ to, const float *__restrict__ st, int32_t i0) {
+      if (i0 + kTile < q.count) fetch(i0 + kTile, other);
+      const bool whole = !p.causal || last_key < i0 + shift;
+      x[0] = x[1] = f32x16{};
+      {
+        constexpr int N = SECOND ? NP : NP + 1;
+        const char *from = cur + (SECOND ? (NP + 1) * 8192 : 0);
+        s16x8 g[2][2][4];
+        load_panel(from, 0, 0, lane, g[0][0]);
+        load_panel(from, 32, 0, lane, g[0][1]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int at_row = i * 32 + 16 * t + 4 * (lane >> 4);
-        const f32x4 l = *reinterpret_cast<const f32x4 *>(st + at_row);
-        const f32x4 d = *reinterpret_cast<const f32x4 *>(st + kTile + at_row);
+        for (int n = 0; n < N; ++n) {
+          if (n + 1 < N) {
+            load_panel(from, 0, n + 1, lane, g[(n + 1) % 2][0]);
+            load_panel(from, 32, n + 1, lane, g[(n + 1) % 2][1]);
+          }
+          hold_order();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], scale2, -l[r]));
-          if (!whole) x = key < i0 + at_row + r + shift ? x : 0.0f;
-          w[4 * t + r] = x;
-          e[4 * t + r] = x * (dp[t][r] - d[r]);
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[i] = Mfma<T>::mul(g[n % 2][i][k], f[n * 4 + k], x[i]);
+          hold_order();
         }
       }
-      column_product16<T, NP * 4>(cur + (NP + 1) * 8192, i * 32, lane, round8<T>(w), dv);
-      column_product16<T, NP * 4 + 4>(cur, i * 32, lane, round8<T>(e), dk);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (!SECOND) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int at_row = i * 32 + 8 * c + 4 * (lane >> 5);
+            const f32x4 l = *reinterpret_cast<const f32x4 *>(st + at_row);
+            f32x4 w;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][4 * c + r], scale2, -l[r]));
+              if (!whole) w[r] = key < i0 + at_row + r + shift ? w[r] : 0.0f;
+              x[i][4 * c + r] = w[r];
+            }
+            *reinterpret_cast<f32x4 *>(to + i * 4096 + c * 1024 + lane * 16) = w;
+          }
+        }
+      }
+    };
+    auto second_half = [&](const char *__restrict__ cur, const char *__restrict__ from,
+                           const float *__restrict__ st) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float e[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f32x4 w = {1.0f, 1.0f, 1.0f, 1.0f}, d = {};
+          if constexpr (SECOND) {
+            w = *reinterpret_cast<const f32x4 *>(from + i * 4096 + c * 1024 + lane * 16);
+            d = *reinterpret_cast<const f32x4 *>(st + kTile + i * 32 + 8 * c + 4 * (lane >> 5));
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            e[4 * c + r] = SECOND ? w[r] * (x[i][4 * c + r] - d[r]) : x[i][4 * c + r];
+        }
+        column_product<T, BLOCKS>(cur + (SECOND ? 0 : (NP + 1) * 8192), i * 32, lane,
+                                  round8<T>(e), round8<T>(e + 8), acc);
+      }
+    };
+    char *weights = lds.weights + pair * 8192;
+    for (int32_t n = n0; n * kTile < q.count; ++n) {
+      const int slot = (n - n0) & 1;
+      wait_loads_all();
+      put_stats(slot, n * kTile);
+      lds_barrier();
+      fetch_stats((n + 1) * kTile);
+      const char *cur = tiles + slot * TILE;
+      const float *st = &stats[slot][0][0];
+      first_half(cur, tiles + (slot ^ 1) * TILE, weights, st, n * kTile);
+      lds_barrier();
+      second_half(cur, weights, st);
+    }
+    if (!live) return;
+    const int64_t out_row = tok * p.heads + head;
+    if constexpr (!SECOND) {
+      store_columns<T, BLOCKS>(static_cast<char *>(p.dv) + out_row * DIM * es, acc, 1.0f, lane);
+    } else {
+      store_columns<T, NP * 2>(static_cast<char *>(p.dk) + out_row * DIM * es, acc, p.scale, lane);
+      float *part = p.dkr_part + (int64_t(head) * p.Tk + tok) * 64;
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x16 &a = acc[NP * 2 + d];
+          *reinterpret_cast<float4 *>(part + d * 32 + c * 8 + 4 * (lane >> 5)) =
+              make_float4(a[4 * c] * p.scale, a[4 * c + 1] * p.scale, a[4 * c + 2] * p.scale,
+                          a[4 * c + 3] * p.scale);
+        }
     }
   };
   if (n0 * kTile < q.count) {
     fetch_stats(n0 * kTile);
     fetch(n0 * kTile, tiles);
   }
-  for (int32_t n = n0; n * kTile < q.count; ++n) {
-    const int slot = (n - n0) & 1;
-    wait_loads_all();
-    put_stats(slot, n * kTile);
-    lds_barrier();
-    fetch_stats((n + 1) * kTile);
-    step(tiles + slot * TILE, tiles + (slot ^ 1) * TILE, &stats[slot][0][0], n * kTile);
-  }
-  if (!live) return;
-  const int64_t out_row = tok * p.heads + head;
-  store_columns16<T, NP * 4>(static_cast<char *>(p.dv) + out_row * DIM * es, dv, 1.0f, lane);
-  store_columns16<T, NP * 4>(static_cast<char *>(p.dk) + out_row * DIM * es, dk, p.scale, lane);
-  float *part = p.dkr_part + (int64_t(head) * p.Tk + tok) * 64;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const f32x4 &a = dk[NP * 4 + d];
-    *reinterpret_cast<float4 *>(part + d * 16 + 4 * (lane >> 4)) =
-        make_float4(a[0] * p.scale, a[1] * p.scale, a[2] * p.scale, a[3] * p.scale);
-  }
+  if (second)
+    run(std::true_type());
+  else
+    run(std::false_type());
 }
 
 // The shared key part's gradient: the heads' shares added in order.  One thread for four

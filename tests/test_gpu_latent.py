@@ -115,6 +115,32 @@ def test_many_sequences():
         qa, ka = qa + n, ka + m
 
 
+@pytest.mark.parametrize("count", [7, 64, 65])
+def test_ragged_sequences_of_several_tiles(count):
+    """The order in which workgroups take the sequences' tiles (longest first up to 64 sequences)
+    reaches each of them once: packed, bit for bit what a call for each sequence gives."""
+    g = torch.Generator().manual_seed(count)
+    nk = torch.randint(0, 700, (count,), generator=g).tolist()
+    nk[1], nk[-1] = 0, 1000
+    nq = [n if i % 3 else n // 4 for i, n in enumerate(nk)]
+    q, k, kr, v, grad = inputs(nq, nk, 3, 64, BF16, count)
+    where = dict(query_offsets=offsets(nq), key_offsets=offsets(nk))
+    out = torch.full((sum(nq), 3, 64), float("nan"), dtype=BF16, device=DEV)
+    out, lse = ra.rope_latent_attention(q, k, kr, v, 0.1, out=out, **where)
+    grads = ra.rope_latent_attention_backward(grad, q, k, kr, v, out, lse, 0.1, **where)
+    qa = ka = 0
+    for n, m in zip(nq, nk):
+        if n:
+            one = [x.contiguous() for x in (q[qa:qa + n], k[ka:ka + m], kr[ka:ka + m], v[ka:ka + m])]
+            o, l = ra.rope_latent_attention(*one, 0.1)
+            gr = ra.rope_latent_attention_backward(grad[qa:qa + n], *one, o, l, 0.1)
+            assert torch.equal(o, out[qa:qa + n]) and torch.equal(l, lse[qa:qa + n])
+            for i, b in enumerate(grads):
+                at = slice(qa, qa + n) if i == 0 else slice(ka, ka + m)
+                assert torch.equal(gr[i], b[at]), (n, m, i)
+        qa, ka = qa + n, ka + m
+
+
 def test_equal_sequences_without_offsets():
     check([130] * 3, [200] * 3, 4, 128, BF16, True, seed=5, spare=0, use_offsets=False)
     check([1] * 5, [77] * 5, 4, 64, F16, False, seed=6, spare=0, use_offsets=False)
