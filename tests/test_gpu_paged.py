@@ -212,6 +212,21 @@ def test_paged_many_ragged_sequences():
             assert torch.equal(first, check_paged(lens, counts, heads, latent, F16, 16, seed=9))
 
 
+def test_paged_more_sequences_than_threads():
+    """More sequences than a workgroup has threads, many of them without rows or queries, and
+    offsets that descend behind the first 512."""
+    g = torch.Generator().manual_seed(9)
+    lens = torch.randint(0, 60, (1100,), generator=g).tolist()
+    counts = torch.randint(0, 3, (1100,), generator=g).tolist()
+    check_paged(lens, counts, 16, 128, F16, 16, seed=9)
+    q, cache, table, sl, _ = paged_inputs(lens, counts, 16, 128, F16, 16, 9)
+    off = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), device=DEV)
+    off[900] += 5
+    out = torch.full((q.shape[0], 16, 128), 3.0, dtype=F16, device=DEV)
+    ra.rope_latent_attention_paged(q, cache, table, sl, 128, 0.1, query_offsets=off, out=out)
+    assert (out == 3).all()
+
+
 @pytest.mark.parametrize("heads", [16, 128])
 def test_paged_long_context(heads):
     """One sequence shared out over every compute unit, in pages of one token (whose numbers
