@@ -14,10 +14,10 @@
 //
 // An LDS tile is cut into panels of 64 elements (128 bytes) a row: two rows are one pass over the
 // 64 banks.  The eight 16-byte chunks of a row are permuted by a key so that no access meets
-// itself in a bank (SQ_LDS_BANK_CONFLICT 0): it takes all eight values over 16 rows, which keeps
-// 32 rows' reads of one chunk apart; it moves rows 0 and 2 (1 and 3) of four to different halves
-// of a row, for the transposed reads; and it differs by 1 only between rows 12 apart, for 16 rows'
-// reads of two neighbouring chunks.
+// itself in a bank (conflicts: none, or below 1% of the cycles): it takes all eight values over 16
+// rows, which keeps 32 rows' reads of one chunk apart; it moves rows 0 and 2 (1 and 3) of four to
+// different halves of a row, for the transposed reads; and it differs by 1 only between rows 12
+// apart, for 16 rows' reads of two neighbouring chunks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -58,10 +58,6 @@ struct Mfma<__bf16> {
   }
   __device__ static float low(uint32_t w) { return __uint_as_float(w << 16); }
   __device__ static float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-  // all exponent bits set in either half of a word: an infinity or a NaN
-  __device__ static bool non_finite(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-  }
 };
 
 template <>
@@ -83,9 +79,6 @@ struct Mfma<_Float16> {
   }
   __device__ static float high(uint32_t w) {
     return static_cast<float>(__builtin_bit_cast(f16x2_t, w).y);
-  }
-  __device__ static bool non_finite(uint32_t w) {
-    return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
   }
 };
 
