@@ -64,7 +64,8 @@ bool touches(const void *p, int64_t bytes, const rope_tensor *t) {
 // Rows that fill half a block and more, in short contexts, are the one loss: 24 sequences of 1200
 // tokens with 48 rows take 27.4 us with 32, 28.8 with 64 (of 5000 tokens: 58.0 and 48.9).
 int64_t paged_rows(int64_t tokens, int64_t heads, int64_t sequences) {
-  const int64_t rows = heads * ((tokens + sequences - 1) / std::max<int64_t>(sequences, 1));
+  const int64_t n = std::max<int64_t>(sequences, 1);
+  const int64_t rows = heads * (tokens / n + (tokens % n != 0));
   return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
@@ -80,7 +81,9 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 }  // namespace
 
 int64_t paged_workspace(int64_t tokens, int64_t heads, int64_t latent, int64_t sequences) {
+  // sizes that the call has no work for, or refuses
   if (tokens <= 0 || heads <= 0 || latent <= 0 || sequences <= 0) return 0;
+  if (tokens >= kIndexLimit || heads >= kIndexLimit || latent > 512) return 0;
   const int64_t rows = std::min<int64_t>(64, paged_rows(tokens, heads, sequences));
   return up(kPagedGroups * 2 * kJoinWords * 4, 256) + up(2 * kPagedGroups * rows * 8, 256) +
          2 * kPagedGroups * rows * latent * 4;
@@ -221,7 +224,11 @@ int64_t tiles_bound(int64_t tokens, int64_t sequences, int64_t each, bool offset
 }  // namespace
 
 int64_t expanded_workspace(int64_t query_tokens, int64_t key_tokens, int64_t heads) {
+  // sizes that the call has no sums for, or refuses
   if (query_tokens < 0 || key_tokens < 0 || heads <= 0) return 0;
+  if (query_tokens >= kIndexLimit || key_tokens >= kIndexLimit || heads >= kIndexLimit ||
+      std::max(query_tokens, key_tokens) * heads >= int64_t(1) << 40)
+    return 0;
   return up(query_tokens * heads * 4, 256) + key_tokens * heads * kLatentRope * 4;
 }
 

@@ -247,6 +247,10 @@ def test_workspace_sizes():
         assert paged(*args) == 0
     assert back(0, 0, 4) == 0 and back(-1, 3, 4) == 0 and back(3, 5, 0) == 0
     assert back(3, 5, 4) >= (3 * 4 + 5 * 4 * 64) * 4
+    big = 2 ** 62  # what the calls refuse needs none
+    assert paged(big, 4, 512, 1) == paged(4, big, 512, 1) == paged(4, 4, big, 1) == 0
+    assert paged(4, 4, 512, big) == paged(4, 4, 512, 2 ** 63 - 1) > 0
+    assert back(big, 4, 4) == back(4, big, 4) == back(4, 4, big) == back(2 ** 29, 4, 2 ** 29) == 0
     assert paged(1, 1, 512, 1) <= paged(1, 64, 512, 1) == paged(10 ** 6, 128, 512, 3)
 
 
