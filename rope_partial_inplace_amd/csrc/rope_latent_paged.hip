@@ -324,13 +324,18 @@ latent_paged_kernel(PagedPlan p) {
   }
   int32_t incl = wave_scan(n);
   const int32_t rest = p.B > kPagedBlock ? wave_scan(mine) : 0;
-  if (lane == 63) wave_total[wave] = incl + rest;
   // Offsets that descend could let the sequences' rows add up to more than the plan's 31 bits
-  // hold: then there is no work.
-  descends = __syncthreads_or(descends);
+  // hold: then there is no work.  (The flag goes with the sums: a barrier that combines one brings
+  // an LDS variable of its own, and the steps wait for their loads again.)
+  descends = __any(descends);
+  if (lane == 63) wave_total[wave] = descends ? -1 : incl + rest;
+  __syncthreads();
   int32_t total = 0;
 #pragma unroll
-  for (int v = 0; v < kPagedWaves; ++v) total += wave_total[v];
+  for (int v = 0; v < kPagedWaves; ++v) {
+    descends |= wave_total[v] < 0;
+    total += wave_total[v];
+  }
   auto uniform = [](int32_t x) { return __builtin_amdgcn_readfirstlane(x); };
   total = uniform(total);
   const int32_t per = uniform(int32_t((uint32_t(total) + p.clusters - 1) / uint32_t(p.clusters)));
