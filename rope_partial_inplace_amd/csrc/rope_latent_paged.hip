@@ -20,9 +20,9 @@
 // storage type: a relative error of at most half a step on each weight, as on the output itself.
 //
 // Measured, bfloat16, latent_dim 512, this kernel and the joining one: 64 sequences of 200 to 9000
-// tokens, 32 heads, 46 + 8 us (213 MB: 4.6 TB/s in the first, where a dense copy of 1 GiB reaches
+// tokens, 32 heads, 44 + 8 us (213 MB: 4.9 TB/s in the first, where a dense copy of 1 GiB reaches
 // 6.8: each workgroup's first tile and its last part's way out are not covered); 6 of 60000 to
-// 131072 tokens, 128 heads, 155 - 190 + 13 us (0.63 - 0.78 PF/s: LDS reads of the tile, once for S
+// 131072 tokens, 128 heads, 155 - 180 + 13 us (0.67 - 0.78 PF/s: LDS reads of the tile, once for S
 // and once for O, and the exponentials between, at 1.9 GHz); one of 1001 tokens, 16 heads, 11.5 +
 // 4.3 us (dependent reads: lengths, page, tile, part).
 #include <hip/hip_runtime.h>

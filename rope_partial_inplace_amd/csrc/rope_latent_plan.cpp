@@ -57,12 +57,12 @@ bool touches(const void *p, int64_t bytes, const rope_tensor *t) {
 // Rows of an item: as many as a sequence's (token, head) rows fill, 32, 64 or 128.  More rows read
 // the cache fewer times and spread a tile's LDS reads over more products; fewer leave smaller parts
 // to join.  Microseconds, bfloat16, latent_dim 512, for items of 32 | 64 | 128 rows:
-//   6 sequences of 60000 to 131072 tokens, 128 heads   350 | 244 | 222
-//   4 sequences of 16000 / 4000 tokens, 128 heads      65 / 33 | 52 / 32 | 47 / 30
-//   8 sequences of 16000 / 4000 tokens, 64 heads       65 / 32 | 53 / 32 | -
-//   64 sequences of 200 to 9000 tokens, 32 heads       54 | 62 | -
-// Rows that fill half a block and more, in short contexts, are the one loss: 24 sequences of 1200
-// tokens with 48 rows take 27.4 us with 32, 28.8 with 64 (of 5000 tokens: 58.0 and 48.9).
+//   6 sequences of 60000 to 131072 tokens, 128 heads   295 | 210 | 190
+//   4 sequences of 16000 / 4000 tokens, 128 heads      59 / 29 | 47 / 31 | 45 / 30
+//   8 sequences of 16000 / 4000 tokens, 64 heads       59 / 29 | 48 / 31 | -
+//   64 sequences of 200 to 9000 tokens, 32 heads       52 | 54 | -
+// Short contexts lose a little by it (24 sequences of 1200 tokens with 48 rows take 26.0 us with
+// 32, 28.3 with 64; of 5000 tokens 53.1 and 45.9), but their lengths are not known here.
 int64_t paged_rows(int64_t tokens, int64_t heads, int64_t sequences) {
   const int64_t n = std::max<int64_t>(sequences, 1);
   const int64_t rows = heads * (tokens / n + (tokens % n != 0));
