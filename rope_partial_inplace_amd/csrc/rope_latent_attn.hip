@@ -4,7 +4,7 @@
 // its own and a rotated part shared by all heads:
 //   s_ij = scale (<qn_ih, k_jh> + <qr_ih, r_j>),  p = softmax_j(s),  o_ih = sum_j p_ij v_jh
 // causal: the last query sees every key and each earlier one a key less.  With g the gradient of
-// o and D_ih = <g_ih, o_ih>:
+// o and D_ih = sum_j p_ij <g_ih, v_jh>:
 //   dv_jh = sum_i p_ij g_ih,   ds_ij = p_ij (<g_ih, v_jh> - D_ih)
 //   dq_ih = scale sum_j ds_ij [k_jh | r_j],  dk_jh = scale sum_i ds_ij qn_ih,
 //   dr_j  = scale sum_h sum_i ds_ij qr_ih
@@ -16,14 +16,15 @@
 //
 // Forward, and dq: a workgroup is four wavefronts of 32 query rows of one head; 64 keys and
 // values at a time pass through LDS in two buffers.  dk and dv: four pairs of wavefronts for 32
-// keys each, over 64 query rows at a time.  dq and dk/dv are two kernels that both compute p again:
-// seven products where atomics on dq would need five, for sums in a fixed order.  Probabilities and
-// ds are rounded to the storage type between the products, as P is in the absorbed form: a relative
+// keys each, over 64 query rows at a time.  dq and dk/dv are two kernels that both compute p again,
+// the first of them twice (D needs all of a row before its first ds): nine products where atomics on
+// dq would need seven, for sums in a fixed order.  Probabilities and ds are rounded to the storage type between the products, as P is in the absorbed form: a relative
 // error of at most half a step on each.
 //
 // Measured, bfloat16, causal, 32 heads of 128: 7 prompts of 300 to 6000 tokens forward 870 - 1010
 // us, 0.79 - 0.91 PF/s (a large library product on this card: 1.2 - 1.35); 4 x 2048 tokens, forward
-// 217 - 239 us, dq 313 - 340, dk and dv 493 - 556, dr 12: 0.7 - 0.76 PF/s of all nine products.
+// 213 - 239 us, D and dq 465 - 515, dk and dv 487 - 556, dr 12: 0.74 - 0.83 PF/s of all eleven
+// products.
 // The range is the clock's, which falls to 1.7 - 2.1 GHz under such kernels.  What the products
 // wait for: LDS reads, and the exponentials of a tile, which only the SIMD's other wavefront covers.
 #include <hip/hip_runtime.h>
@@ -236,6 +237,29 @@ __device__ __forceinline__ f32x16 row_product(const char *lds, int row0, int lan
   return c;
 }
 
+// x[i] += 32 LDS rows of panels 0 .. PANELS - 1 (from row 32 i) times register operands, for both
+// halves of a tile at once, a panel's operands read ahead.
+template <typename T, int PANELS>
+__device__ __forceinline__ void panel_products(const char *lds, int lane, const s16x8 *b,
+                                               f32x16 (&x)[2]) {
+  s16x8 f[2][2][4];
+  load_panel(lds, 0, 0, lane, f[0][0]);
+  load_panel(lds, 32, 0, lane, f[0][1]);
+#pragma unroll
+  for (int n = 0; n < PANELS; ++n) {
+    if (n + 1 < PANELS) {
+      load_panel(lds, 0, n + 1, lane, f[(n + 1) % 2][0]);
+      load_panel(lds, 32, n + 1, lane, f[(n + 1) % 2][1]);
+    }
+    hold_order();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[i] = Mfma<T>::mul(f[n % 2][i][k], b[n * 4 + k], x[i]);
+    hold_order();
+  }
+}
+
 // 16-byte pieces of a row as register operands: 8 (lane / 32) elements into every 16.
 template <int STEPS>
 __device__ __forceinline__ void load_operands(const char *row, bool live, int lane, s16x8 *f) {
@@ -308,26 +332,9 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
 
   auto step = [&](const char *__restrict__ cur, char *__restrict__ other, int32_t j0) {
     if (j0 + kTile < most) fetch(j0 + kTile, other);
-    // S^T of the tile's two halves, a panel's operands read ahead
+    // S^T of the tile's two halves
     f32x16 s[2] = {};
-    {
-      s16x8 f[2][2][4];
-      load_panel(cur, 0, 0, lane, f[0][0]);
-      load_panel(cur, 32, 0, lane, f[0][1]);
-#pragma unroll
-      for (int n = 0; n < NP + 1; ++n) {
-        if (n < NP) {
-          load_panel(cur, 0, n + 1, lane, f[(n + 1) % 2][0]);
-          load_panel(cur, 32, n + 1, lane, f[(n + 1) % 2][1]);
-        }
-        hold_order();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) s[i] = Mfma<T>::mul(f[n % 2][i][k], qf[n * 4 + k], s[i]);
-        hold_order();
-      }
-    }
+    panel_products<T, NP + 1>(cur, lane, qf, s);
     if (j0 + kTile > min(least, k.count)) {  // some row does not see all of it
       asm volatile("");  // a branch: most tiles need no masks
 #pragma unroll
@@ -381,11 +388,12 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
 
 // ---- backward: D and dq -------------------------------------------------------------------
 
-// D = <g, o> takes the output as it was rounded.  Its error grows with |o|, which many keys average
-// out and few do not, so where a workgroup's rows see at most two tiles of keys, D comes from
-// sum_j p_j dP_j instead, in a pass of its own over the tiles, which then both lie in LDS.  (Short
-// texts of 40 tokens: gradients off by 0.0023 in place of 0.0026 of their norm in bfloat16, where
-// the last rounding alone makes 0.0017.)
+// D = sum_j p_j dP_j takes a pass of its own over the keys.  <g, o> would be the same sum, but for
+// the rounding of o: its error dD goes into dq as scale dD sum_j p_j [k_j | r_j], which keys with a
+// common offset do not average out (2048 keys, keys and values with an offset of one deviation in
+// every channel, bfloat16: dq off by 3.9% of its norm in place of 0.27%).
+// Its two products run at 1.0 PF/s: 4 x 2048 tokens of 32 heads take this
+// kernel 465 - 515 us in place of 310 - 337, five texts of 17 to 333 tokens 21 in place of 16.
 template <typename T, int DIM>
 __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(ExpandedPlan p) {
   constexpr int NP = DIM / 64;
@@ -409,22 +417,6 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
       static_cast<const char *>(p.q) + (tok * p.q_tok + head * p.q_head) * es, live, lane, qf);
   load_operands<NP * 4>(
       static_cast<const char *>(p.grad) + (tok * p.g_tok + head * p.g_head) * es, live, lane, gf);
-  float delta = 0.0f;
-  {
-    s16x8 of[NP * 4];
-    load_operands<NP * 4>(static_cast<const char *>(p.fwd_out) + out_row * DIM * es, live, lane, of);
-#pragma unroll
-    for (int i = 0; i < NP * 4; ++i) {
-      const uint4 a = __builtin_bit_cast(uint4, gf[i]), b = __builtin_bit_cast(uint4, of[i]);
-      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        delta += Mfma<T>::low(x[c]) * Mfma<T>::low(y[c]);
-        delta += Mfma<T>::high(x[c]) * Mfma<T>::high(y[c]);
-      }
-    }
-    delta = sum_halves(delta);
-  }
   float lse2 = __builtin_huge_valf();  // rows that see nothing, or do not exist: p = 0
   if (live) {
     const float l = p.lse[out_row];
@@ -445,52 +437,63 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
     fetch_rows<NP>(vb, p.v_tok * es, j0, k.count - 1, wave, lane, to + (NP + 1) * 8192);
   };
   const float scale2 = p.negative ? -p.scale_log2 : p.scale_log2;
-  f32x16 acc[NP * 2 + 2];
-  // p (w) and dP of the 32 keys from j0 on, in the tile's half i
-  auto pairs = [&](const char *__restrict__ cur, int i, int32_t j0, float (&w)[16]) {
-    const f32x16 s = row_product<T, NP + 1, 2>(cur, i * 32, lane, qf, f32x16{});
-    const f32x16 dp = row_product<T, NP, 2>(cur + (NP + 1) * 8192, i * 32, lane, gf, f32x16{});
-    const bool whole = j0 - i * 32 + kTile <= min(least, k.count);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale2, -lse2));
-      if (!whole) w[r] = j0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < limit ? w[r] : 0.0f;
-    }
-    return dp;
+  // p_j of score s of key j; whole: every row sees all of the tile
+  auto weight = [&](float s, bool whole, int32_t j) {
+    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s, scale2, -lse2));
+    return whole || j < limit ? w : 0.0f;
   };
-  const bool few = most <= 2 * kTile;  // both tiles lie in LDS, and D comes from them
+
+  const int32_t count = most > 0 ? (most + kTile - 1) / kTile : 0;  // tiles
+  const bool few = count <= 2;  // they stay in LDS for the second pass
+  float delta = 0.0f;
+  auto sum_step = [&](const char *__restrict__ cur, char *__restrict__ other, int32_t j0) {
+    if (j0 + kTile < most)
+      fetch(j0 + kTile, other);
+    else if (!few)
+      fetch(0, other);
+    f32x16 s[2] = {}, dp[2] = {};
+    panel_products<T, NP + 1>(cur, lane, qf, s);
+    panel_products<T, NP>(cur + (NP + 1) * 8192, lane, gf, dp);
+    const bool whole = j0 + kTile <= min(least, k.count);
+    float part = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+      part += weight(s[r / 16][r % 16], whole, j0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4) *
+              dp[r / 16][r % 16];
+    delta += part;
+  };
+  f32x16 acc[NP * 2 + 2];
   auto step = [&](const char *__restrict__ cur, char *__restrict__ other, int32_t j0) {
     if (!few && j0 + kTile < most) fetch(j0 + kTile, other);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const f32x16 s = row_product<T, NP + 1, 2>(cur, i * 32, lane, qf, f32x16{});
+      const f32x16 dp =
+          row_product<T, NP, 2>(cur + (NP + 1) * 8192, i * 32, lane, gf, f32x16{});
+      const bool whole = j0 + kTile <= min(least, k.count);
       float e[16];
-      const f32x16 dp = pairs(cur, i, j0 + i * 32, e);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) e[r] *= dp[r] - delta;
+      for (int r = 0; r < 16; ++r)
+        e[r] = weight(s[r], whole, j0 + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4) *
+               (dp[r] - delta);
       column_product<T, NP * 2 + 2>(cur, i * 32, lane, round8<T>(e), round8<T>(e + 8), acc);
     }
   };
-  if (most > 0) fetch(0, tiles);
-  if (few && most > 0) {
-    if (kTile < most) fetch(kTile, tiles + TILE);
+  if (count > 0) fetch(0, tiles);
+  for (int32_t n = 0; n < count; ++n) {
     wait_loads_all();
     lds_barrier();
-    delta = 0.0f;
-    for (int32_t j0 = 0; j0 < most; j0 += 32) {
-      float w[16];
-      const f32x16 dp = pairs(tiles + j0 / kTile * TILE, j0 / 32 % 2, j0, w);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) delta += w[r] * dp[r];
-    }
-    delta = sum_halves(delta);
+    sum_step(tiles + (n & 1) * TILE, tiles + (~n & 1) * TILE, n * kTile);
   }
+  delta = sum_halves(delta);
   if (live && lane < 32) p.delta[out_row] = delta;
 #pragma unroll
   for (int d = 0; d < NP * 2 + 2; ++d) acc[d] = f32x16{};
-  for (int32_t n = 0; n * kTile < most; ++n) {
+  const int32_t first = few ? 0 : count & 1;  // the buffer that holds tile 0
+  for (int32_t n = 0; n < count; ++n) {
     wait_loads_all();
     lds_barrier();
-    step(tiles + (n & 1) * TILE, tiles + (~n & 1) * TILE, n * kTile);
+    step(tiles + ((n + first) & 1) * TILE, tiles + (~(n + first) & 1) * TILE, n * kTile);
   }
   if (live)
     store_columns<T, NP * 2 + 2>(static_cast<char *>(p.dq) + out_row * (DIM + 64) * es, acc,
@@ -589,26 +592,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
       if (i0 + kTile < q.count) fetch(i0 + kTile, other);
       const bool whole = !p.causal || last_key < i0 + shift;
       x[0] = x[1] = f32x16{};
-      {
-        constexpr int N = SECOND ? NP : NP + 1;
-        const char *from = cur + (SECOND ? (NP + 1) * 8192 : 0);
-        s16x8 g[2][2][4];
-        load_panel(from, 0, 0, lane, g[0][0]);
-        load_panel(from, 32, 0, lane, g[0][1]);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (n + 1 < N) {
-            load_panel(from, 0, n + 1, lane, g[(n + 1) % 2][0]);
-            load_panel(from, 32, n + 1, lane, g[(n + 1) % 2][1]);
-          }
-          hold_order();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) x[i] = Mfma<T>::mul(g[n % 2][i][k], f[n * 4 + k], x[i]);
-          hold_order();
-        }
-      }
+      panel_products<T, SECOND ? NP : NP + 1>(cur + (SECOND ? (NP + 1) * 8192 : 0), lane, f, x);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if constexpr (!SECOND) {

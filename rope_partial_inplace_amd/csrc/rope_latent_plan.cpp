@@ -392,7 +392,6 @@ int plan_expanded_backward(const rope_tensor *grad, const rope_tensor *query,
   p.grad = grad->data;
   p.g_tok = grad->stride[0];
   p.g_head = grad->stride[1];
-  p.fwd_out = out->data;
   p.dq = dquery->data;
   p.dk = dkey->data;
   p.dkr = dkey_rope->data;

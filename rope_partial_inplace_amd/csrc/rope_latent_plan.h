@@ -73,7 +73,7 @@ struct ExpandedPlan {
   void *out = nullptr;
   float *lse = nullptr;
   // backward
-  const void *grad = nullptr, *fwd_out = nullptr;
+  const void *grad = nullptr;
   int64_t g_tok = 0, g_head = 0;
   void *dq = nullptr, *dk = nullptr, *dkr = nullptr, *dv = nullptr;
   float *delta = nullptr;   // workspace [Tq][heads]

@@ -1,0 +1,113 @@
+"""GPU: precision of latent attention where ordinary random data does not show it: keys and values
+with a common offset.
+
+Bounds.  u is half a step of the storage type relative to a value (bf16 2^-8, f16 2^-11), e = 2^-24
+half a step of float32.  A sum of n terms each of which was rounded on its own, by at most u
+relative, is off by sum_j r_j x_j with |r_j| <= u.  Taken as independent with mean zero, Hoeffding's
+inequality bounds that by T u sqrt(sum_j x_j^2) but for a probability of 2 exp(-T^2 / 2), 3e-8 with
+T = 6 (elements: below 10^6 a call).  Errors of float32 are bounded at their worst:
+  scores   (dim + 68) e scale sum |q||k|                                              =: a
+  weights  p = exp(s - lse), relative: 2 a + (m + 16) e + 4 e |lse|                   =: r
+  dP       (dim + 4) e sum |g||v|                                                     =: b
+  D        sum_j p (r |dP| + b) + (m + 8) e sum_j p |dP|, D = sum_j p dP in float32   =: c
+  ds       p (r (|dP| + |D|) + b + c + 4 e (|dP| + |D|)) before its rounding           =: f
+A gradient then is off by
+  T u sqrt(sum (ds k)^2) + sum f |k| + (n + 4) e sum |ds||k|, times scale, and its own rounding.
+In float16 a value far below the largest of its sum may be off by 2^-24 besides."""
+import math
+
+import pytest
+import torch
+
+import rope_partial_inplace_amd as ra
+from attention_ref import ROPE, U, assert_within
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F16 = torch.bfloat16, torch.float16
+E, T = 2.0 ** -24, 6.0
+NAMES = ("dq", "dk", "dkr", "dv")
+
+
+def randn(gen, *shape):
+    return torch.randn(shape, generator=gen, device=DEV)
+
+
+def gen_of(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def gradients_reference(q, k, kr, v, g, scale, causal, dtype):
+    """(value, bound) of dq, dk, dkr and dv of one sequence, in float64."""
+    u = U[dtype]
+    step = 2.0 ** -25 if dtype == F16 else 0.0  # half a step of the smallest results
+    n, m, h, dim = q.shape[0], k.shape[0], k.shape[1], k.shape[2]
+    q, v, g = (x.double().transpose(0, 1) for x in (q, v, g))
+    kr = kr.double()[:, None, :].expand(m, h, ROPE)
+    k = torch.cat([k.double(), kr], dim=-1).transpose(0, 1).contiguous()
+    s = torch.matmul(q, k.transpose(1, 2).contiguous()) * scale
+    if causal:
+        i, j = torch.arange(n, device=DEV), torch.arange(m, device=DEV)
+        s = s.masked_fill(j[None, :] > i[:, None] + (m - n), -math.inf)
+    lse = torch.logsumexp(s, -1, keepdim=True)
+    p = torch.exp(s - lse)
+    vt = v.transpose(1, 2).contiguous()
+    dP = torch.matmul(g, vt)
+    D = (p * dP).sum(-1, keepdim=True)
+    dS = p * (dP - D)
+    a = (dim + 68) * E * abs(scale) * torch.matmul(q.abs(), k.abs().transpose(1, 2).contiguous())
+    r = 2 * a.amax(-1, keepdim=True) + (m + 16) * E + 4 * E * lse.abs()
+    b = (dim + 4) * E * torch.matmul(g.abs(), vt.abs())
+    c = (p * (r * dP.abs() + b)).sum(-1, keepdim=True) + (m + 8) * E * (p * dP.abs()).sum(-1, keepdim=True)
+    f = p * (r * (dP.abs() + D.abs()) + b + c + 4 * E * (dP.abs() + D.abs()))
+    low = 2.0 ** -25 if dtype == F16 else 0.0
+
+    def product(x, err, y, length):
+        """x y and its bound: x [h, a, length] rounded to the type, y [h, length, b]."""
+        least = low * torch.sqrt((y * y).sum(-2, keepdim=True)) * T
+        bound = (T * u * torch.sqrt(torch.matmul(x * x, y * y)) + torch.matmul(err, y.abs()) +
+                 (length + 4) * E * torch.matmul(x.abs(), y.abs()) + least)
+        return torch.matmul(x, y), bound
+
+    def final(x, e):
+        return x, e + torch.clamp(u * (x.abs() + e), min=step) + 2.0 ** -130
+
+    turned = lambda x: x.transpose(1, 2).contiguous()
+    back = lambda x: x.transpose(0, 1)
+    dq, eq = product(dS, f, k, m)
+    dk, ek = product(turned(dS), turned(f), q, n)
+    dv, ev = product(turned(p), turned(r * p), g, n)
+    dq, eq, dk, ek = dq * scale, eq * abs(scale), dk * scale, ek * abs(scale)
+    dkr, ekr = dk[..., dim:].sum(0), ek[..., dim:].sum(0) + h * E * dk[..., dim:].abs().sum(0)
+    return {"dq": final(back(dq), back(eq)), "dk": final(back(dk[..., :dim]), back(ek[..., :dim])),
+            "dkr": final(dkr, ekr), "dv": final(back(dv), back(ev))}
+
+
+def check_gradients(q, k, kr, v, g, scale, causal, dtype):
+    out, lse = ra.rope_latent_attention(q, k, kr, v, scale, causal)
+    got = dict(zip(NAMES, ra.rope_latent_attention_backward(g, q, k, kr, v, out, lse, scale, causal)))
+    torch.cuda.synchronize()
+    for name, (want, bound) in gradients_reference(q, k, kr, v, g, scale, causal, dtype).items():
+        assert_within(got[name], want, bound, name)
+
+
+def data(gen, n, m, heads, dim, dtype, wide=1.0, small=1.0):
+    """Inputs with keys `wide` times as large and queries that much smaller, gradients `small`
+    times as large."""
+    q, k, v = randn(gen, n, heads, dim + ROPE) / wide, randn(gen, m, heads, dim) * wide, randn(gen, m, heads, dim)
+    kr, g = randn(gen, m, ROPE) * wide, randn(gen, n, heads, dim) * small
+    return [x.to(dtype) for x in (q, k, kr, v, g)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n,m,dim,causal", [(200, 2048, 128, False), (300, 1000, 64, True),
+                                            (1100, 1100, 128, True), (70, 129, 64, False)])
+@pytest.mark.parametrize("offset", [1.0, 3.0])
+def test_gradients_of_keys_and_values_with_a_common_offset(offset, n, m, dim, causal, dtype):
+    """Biased projections: every channel of keys, shared key parts and values has an offset of its
+    own.  An error of D = sum_j p_j dP_j then reaches dq through sum_j p_j k_j, which no longer
+    averages out (D from the rounded output: dq off by 3.9% of its norm)."""
+    g = gen_of(31)
+    q, k, kr, v, grad = data(g, n, m, 2, dim, torch.float32)
+    k, kr, v = k + offset * randn(g, 2, dim), kr + offset * randn(g, ROPE), v + offset * randn(g, 2, dim)
+    check_gradients(*(x.to(dtype) for x in (q, k, kr, v, grad)), (dim + ROPE) ** -0.5, causal, dtype)
