@@ -18,8 +18,13 @@
 // values at a time pass through LDS in two buffers.  dk and dv: four pairs of wavefronts for 32
 // keys each, over 64 query rows at a time.  dq and dk/dv are two kernels that both compute p again,
 // the first of them twice (D needs all of a row before its first ds): nine products where atomics on
-// dq would need seven, for sums in a fixed order.  Probabilities and ds are rounded to the storage type between the products, as P is in the absorbed form: a relative
-// error of at most half a step on each.
+// dq would need seven, for sums in a fixed order.
+//
+// Probabilities and ds are rounded to the storage type between the products, as P is in the absorbed
+// form: a relative error of at most half a step on each.  float16 ends at 65504 and has 14 exponents
+// below 1, while ds is as small as the incoming gradient over the row's length and may be larger
+// than any result: backward, both are lifted or lowered by powers of two, constant for p, taken for
+// each row of dq and each key of dk from what is summed there.
 //
 // Measured, bfloat16, causal, 32 heads of 128: 7 prompts of 300 to 6000 tokens forward 870 - 1010
 // us, 0.79 - 0.91 PF/s (a large library product on this card: 1.2 - 1.35); 4 x 2048 tokens, forward
@@ -445,7 +450,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
 
   const int32_t count = most > 0 ? (most + kTile - 1) / kTile : 0;  // tiles
   const bool few = count <= 2;  // they stay in LDS for the second pass
-  float delta = 0.0f;
+  float delta = 0.0f, most_w = 0.0f, most_x = 0.0f;
   auto sum_step = [&](const char *__restrict__ cur, char *__restrict__ other, int32_t j0) {
     if (j0 + kTile < most)
       fetch(j0 + kTile, other);
@@ -457,9 +462,15 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
     const bool whole = j0 + kTile <= min(least, k.count);
     float part = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r)
-      part += weight(s[r / 16][r % 16], whole, j0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4) *
-              dp[r / 16][r % 16];
+    for (int r = 0; r < 32; ++r) {
+      const float w = weight(s[r / 16][r % 16], whole, j0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4);
+      const float x = w * dp[r / 16][r % 16];
+      part += x;
+      if constexpr (Mfma<T>::kNarrow) {
+        most_w = fmaxf(most_w, w);
+        most_x = fmaxf(most_x, __builtin_fabsf(x));
+      }
+    }
     delta += part;
   };
   f32x16 acc[NP * 2 + 2];
@@ -487,6 +498,15 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
   }
   delta = sum_halves(delta);
   if (live && lane < 32) p.delta[out_row] = delta;
+  float store = p.scale;
+  if constexpr (Mfma<T>::kNarrow) {
+    // |ds_j| <= max p |dP| + max p |D|: the row's ds are lifted so that this comes to 2^14 .. 2^15
+    // (the maxima's cost: below 4% of the kernel)
+    const float bound = max_halves(most_x) + max_halves(most_w) * __builtin_fabsf(delta);
+    const int up = min(15 - __builtin_amdgcn_frexp_expf(bound), 60);
+    lse2 -= float(up);
+    store = __builtin_ldexpf(store, -up);
+  }
 #pragma unroll
   for (int d = 0; d < NP * 2 + 2; ++d) acc[d] = f32x16{};
   const int32_t first = few ? 0 : count & 1;  // the buffer that holds tile 0
@@ -497,7 +517,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
   }
   if (live)
     store_columns<T, NP * 2 + 2>(static_cast<char *>(p.dq) + out_row * (DIM + 64) * es, acc,
-                                 p.scale, lane);
+                                 store, lane);
 }
 
 // ---- backward: dk, dv and each head's share of the shared key part's gradient ---------------
@@ -551,6 +571,9 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
   // The statistics of a tile's rows, one row a lane, read a tile ahead by every wavefront (under a
   // condition the compiler would wait for them at its end) and put into LDS by the first.
   float next_lse = 0.0f, next_delta = 0.0f;
+  // p, at most 1 (and a rounding of lse), goes to narrow types times 2^kLift
+  constexpr float kLift = Mfma<T>::kNarrow ? 14.0f : 0.0f;
+  constexpr float kLower = Mfma<T>::kNarrow ? 0x1p-14f : 1.0f;
   auto fetch = [&](int32_t i0, char *__restrict__ to) {
     fetch_rows<NP + 1, WAVES>(qb, p.q_tok * es, i0, q.count - 1, wave, lane, to);
     fetch_rows<NP, WAVES>(gb, p.g_tok * es, i0, q.count - 1, wave, lane, to + (NP + 1) * 8192);
@@ -564,7 +587,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
     if (wave == 0) {  // rows that see nothing, or do not exist: p = exp2(s - infinity) = 0
       const bool real = i0 + lane < q.count;
       stats[slot][0][lane] =
-          real && next_lse != kNegInf ? next_lse * kLog2eF : __builtin_huge_valf();
+          real && next_lse != kNegInf ? next_lse * kLog2eF - kLift : __builtin_huge_valf();
       stats[slot][1][lane] = real ? next_delta : 0.0f;
     }
   };
@@ -586,6 +609,10 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
 #pragma unroll
     for (int d = 0; d < BLOCKS; ++d) acc[d] = f32x16{};
     f32x16 x[2];  // dP of the tile's two halves, then ds; p
+    // Narrow types: ds times `lift`, and so acc.  The rows that see a key are as different as their
+    // gradients, so the key's factor is lowered, and what was summed with it, when one passes it.
+    // (540 - 590 us in place of 515 - 565 for 4 x 2048 tokens of 32 heads in float16.)
+    float lift = 0x1p26f;
 
     auto first_half = [&](const char *__restrict__ cur, char *__restrict__ other,
                           char *__restrict__ to, const float *__restrict__ st, int32_t i0) {
@@ -628,6 +655,24 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
           for (int r = 0; r < 4; ++r)
             e[4 * c + r] = SECOND ? w[r] * (x[i][4 * c + r] - d[r]) : x[i][4 * c + r];
         }
+        if constexpr (SECOND && Mfma<T>::kNarrow) {
+          float high = 0.0f;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) high = fmaxf(high, __builtin_fabsf(e[r]));
+          high = max_halves(high);
+          if (__any(high * lift > 65000.0f)) {
+            float f = 1.0f;
+            if (high * lift > 65000.0f) {  // 2^11 .. 2^12 from here on
+              const float now = __builtin_ldexpf(1.0f, 12 - __builtin_amdgcn_frexp_expf(high));
+              f = now / lift;
+              lift = now;
+            }
+#pragma unroll
+            for (int d = 0; d < BLOCKS; ++d) acc[d] *= f;
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) e[r] *= lift;
+        }
         column_product<T, BLOCKS>(cur + (SECOND ? 0 : (NP + 1) * 8192), i * 32, lane,
                                   round8<T>(e), round8<T>(e + 8), acc);
       }
@@ -648,9 +693,10 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
     if (!live) return;
     const int64_t out_row = tok * p.heads + head;
     if constexpr (!SECOND) {
-      store_columns<T, BLOCKS>(static_cast<char *>(p.dv) + out_row * DIM * es, acc, 1.0f, lane);
+      store_columns<T, BLOCKS>(static_cast<char *>(p.dv) + out_row * DIM * es, acc, kLower, lane);
     } else {
-      store_columns<T, NP * 2>(static_cast<char *>(p.dk) + out_row * DIM * es, acc, p.scale, lane);
+      const float f = Mfma<T>::kNarrow ? p.scale * (kLower / lift) : p.scale;
+      store_columns<T, NP * 2>(static_cast<char *>(p.dk) + out_row * DIM * es, acc, f, lane);
       float *part = p.dkr_part + (int64_t(head) * p.Tk + tok) * 64;
 #pragma unroll
       for (int d = 0; d < 2; ++d)
@@ -658,8 +704,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
         for (int c = 0; c < 4; ++c) {
           const f32x16 &a = acc[NP * 2 + d];
           *reinterpret_cast<float4 *>(part + d * 32 + c * 8 + 4 * (lane >> 5)) =
-              make_float4(a[4 * c] * p.scale, a[4 * c + 1] * p.scale, a[4 * c + 2] * p.scale,
-                          a[4 * c + 3] * p.scale);
+              make_float4(a[4 * c] * f, a[4 * c + 1] * f, a[4 * c + 2] * f, a[4 * c + 3] * f);
         }
     }
   };

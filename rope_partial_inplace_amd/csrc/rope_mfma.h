@@ -39,11 +39,15 @@ typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
+// kNarrow: the type's exponents end far inside float32's.  What is rounded to it between two products
+// is multiplied by a power of two first, which a sum's store takes off again: exact, and neither
+// small values become subnormal nor large ones infinite.
 template <typename T>
 struct Mfma;
 
 template <>
 struct Mfma<__bf16> {
+  static constexpr bool kNarrow = false;
   __device__ static f32x16 mul(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -62,6 +66,7 @@ struct Mfma<__bf16> {
 
 template <>
 struct Mfma<_Float16> {
+  static constexpr bool kNarrow = true;
   __device__ static f32x16 mul(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);

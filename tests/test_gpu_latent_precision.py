@@ -1,5 +1,5 @@
 """GPU: precision of latent attention where ordinary random data does not show it: keys and values
-with a common offset.
+with a common offset, small and large gradients.
 
 Bounds.  u is half a step of the storage type relative to a value (bf16 2^-8, f16 2^-11), e = 2^-24
 half a step of float32.  A sum of n terms each of which was rounded on its own, by at most u
@@ -13,7 +13,8 @@ T = 6 (elements: below 10^6 a call).  Errors of float32 are bounded at their wor
   ds       p (r (|dP| + |D|) + b + c + 4 e (|dP| + |D|)) before its rounding           =: f
 A gradient then is off by
   T u sqrt(sum (ds k)^2) + sum f |k| + (n + 4) e sum |ds||k|, times scale, and its own rounding.
-In float16 a value far below the largest of its sum may be off by 2^-24 besides."""
+What is rounded to float16 is scaled by a power of two first, so that a value down to 2^-20 of the
+largest of its sum keeps its bits; smaller ones are off by at most 2^-32 of that."""
 import math
 
 import pytest
@@ -60,11 +61,11 @@ def gradients_reference(q, k, kr, v, g, scale, causal, dtype):
     b = (dim + 4) * E * torch.matmul(g.abs(), vt.abs())
     c = (p * (r * dP.abs() + b)).sum(-1, keepdim=True) + (m + 8) * E * (p * dP.abs()).sum(-1, keepdim=True)
     f = p * (r * (dP.abs() + D.abs()) + b + c + 4 * E * (dP.abs() + D.abs()))
-    low = 2.0 ** -25 if dtype == F16 else 0.0
+    low = 2.0 ** -32 if dtype == F16 else 0.0
 
     def product(x, err, y, length):
         """x y and its bound: x [h, a, length] rounded to the type, y [h, length, b]."""
-        least = low * torch.sqrt((y * y).sum(-2, keepdim=True)) * T
+        least = low * x.abs().amax(-1, keepdim=True) * y.abs().sum(-2, keepdim=True)
         bound = (T * u * torch.sqrt(torch.matmul(x * x, y * y)) + torch.matmul(err, y.abs()) +
                  (length + 4) * E * torch.matmul(x.abs(), y.abs()) + least)
         return torch.matmul(x, y), bound
@@ -111,3 +112,55 @@ def test_gradients_of_keys_and_values_with_a_common_offset(offset, n, m, dim, ca
     q, k, kr, v, grad = data(g, n, m, 2, dim, torch.float32)
     k, kr, v = k + offset * randn(g, 2, dim), kr + offset * randn(g, ROPE), v + offset * randn(g, 2, dim)
     check_gradients(*(x.to(dtype) for x in (q, k, kr, v, grad)), (dim + ROPE) ** -0.5, causal, dtype)
+
+
+@pytest.mark.parametrize("small", [1e-1, 1e-3, 1e-4])
+@pytest.mark.parametrize("wide", [8.0, 1 / 8])
+@pytest.mark.parametrize("n,m,dim,causal", [(150, 2048, 128, False), (2048, 150, 64, False),
+                                            (900, 900, 64, True)])
+def test_float16_gradients_of_any_size(n, m, dim, causal, wide, small):
+    """Small incoming gradients over long rows: p (dP - D) lies far below float16's normal range
+    while the gradients do not."""
+    check_gradients(*data(gen_of(32), n, m, 1, dim, F16, wide, small), (dim + ROPE) ** -0.5, causal, F16)
+
+
+def test_float16_gradients_of_very_different_rows():
+    """One row's gradient is 10^5 times the others'; keys that only the others see keep theirs."""
+    q, k, kr, v, g = data(gen_of(33), 400, 400, 2, 128, torch.float32, 1.0, 1e-3)
+    g[5] *= 1e5
+    g[300:] *= 1e-1
+    check_gradients(*(x.to(F16) for x in (q, k, kr, v, g)), 192 ** -0.5, True, F16)
+
+
+def test_float16_gradients_whose_inner_values_pass_the_type():
+    """|p (dP - D)| beyond 65504 with finite gradients."""
+    gen = torch.Generator().manual_seed(LARGE_SEED)
+    q, k, kr, v, g = large_data(gen)
+    assert inner_and_results(q, k, kr, v, g)[0] > 66000
+    check_gradients(*(x.to(DEV) for x in (q, k, kr, v, g)), 192 ** -0.5, True, F16)
+
+
+LARGE_SEED = 45
+
+
+def large_data(gen):
+    r = lambda *shape: torch.randn(shape, generator=gen)
+    return [x.to(F16) for x in (r(8, 1, 192), r(8, 1, 128), r(8, ROPE), r(8, 1, 128), r(8, 1, 128) * 8000)]
+
+
+def inner_and_results(q, k, kr, v, g):
+    """Largest |p (dP - D)|, and the largest gradient (float64, on the CPU)."""
+    q, k, kr, v, g = (x.double() for x in (q[:, 0], k[:, 0], kr, v[:, 0], g[:, 0]))
+    kk = torch.cat([k, kr], 1)
+    s = (q @ kk.T * 192 ** -0.5).masked_fill(torch.ones(8, 8, dtype=torch.bool).triu(1), -math.inf)
+    p = s.softmax(1)
+    dP = g @ v.T
+    dS = p * (dP - (p * dP).sum(1, keepdim=True))
+    return (float(dS.abs().max()),
+            max(float(x.abs().max()) for x in (dS @ kk * 192 ** -0.5, dS.T @ q * 192 ** -0.5, p.T @ g)))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_float16_value_gradients_of_long_rows(dim):
+    """Weights of 2^-19: dv is a sum of p g."""
+    check_gradients(*data(gen_of(34), 8, 1 << 19, 1, dim, F16, 1.0, 100.0), (dim + ROPE) ** -0.5, False, F16)
