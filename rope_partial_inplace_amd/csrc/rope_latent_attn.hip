@@ -23,8 +23,8 @@
 // Probabilities and ds are rounded to the storage type between the products, as P is in the absorbed
 // form: a relative error of at most half a step on each.  float16 ends at 65504 and has 14 exponents
 // below 1, while ds is as small as the incoming gradient over the row's length and may be larger
-// than any result: backward, both are lifted or lowered by powers of two, constant for p, taken for
-// each row of dq and each key of dk from what is summed there.
+// than any result: both are lifted or lowered by powers of two: constant ones for p, forward too, and for ds taken
+// for each row of dq and each key of dk from what is summed there.
 //
 // Measured, bfloat16, causal, 32 heads of 128: 7 prompts of 300 to 6000 tokens forward 870 - 1010
 // us, 0.79 - 0.91 PF/s (a large library product on this card: 1.2 - 1.35); 4 x 2048 tokens, forward
@@ -50,7 +50,7 @@ constexpr int kBlockThreads = 256;
 constexpr int kKeyThreads = 512;  // of the kernel of dk and dv
 constexpr int kRows = 128;        // query rows (or keys) of a workgroup
 constexpr int kTile = 64;         // keys (or query rows) in LDS at a time
-constexpr float kLog2eF = 1.44269504f, kLn2F = 0.693147180f;
+constexpr float kLog2eF = 1.44269504f;
 
 struct Span {
   int32_t first, count;
@@ -350,10 +350,10 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
 #pragma unroll
     for (int r = 0; r < 32; ++r) best = fmaxf(best, s[r / 16][r % 16]);
     best = max_halves(best) * p.scale_log2;  // the scale is not negative: see the operands
-    // rescale only when the maximum rises by more than 8 (weights of up to 2^8 are carried)
-    if (__any(best > top + 8.0f)) {
+    // rescale only when the maximum rises by more than kSlack: until then larger weights are carried
+    if (__any(best > top + Mfma<T>::kSlack)) {
       float f = 1.0f;
-      if (best > top + 8.0f) {
+      if (best > top + Mfma<T>::kSlack) {
         f = __builtin_amdgcn_exp2f(top - best);
         top = best;
       }
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
 #pragma unroll
       for (int d = 0; d < NP * 2; ++d) acc[d] *= f;
     }
-    const float ref = top == kNegInf ? 0.0f : top;
+    const float ref = top == kNegInf ? 0.0f : top - Mfma<T>::kLift;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float e[16], part = 0.0f;
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
   const int64_t out_row = int64_t(q.first + row) * p.heads + head;
   store_columns<T, NP * 2>(static_cast<char *>(p.out) + out_row * DIM * es, acc,
                            some ? 1.0f / sum : 0.0f, lane);
-  if (lane < 32) p.lse[out_row] = some ? top * kLn2F + logf(sum) : kNegInf;
+  if (lane < 32) p.lse[out_row] = some ? natural<T>(top, sum) : kNegInf;
 }
 
 // ---- backward: D and dq -------------------------------------------------------------------
@@ -571,9 +571,9 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
   // The statistics of a tile's rows, one row a lane, read a tile ahead by every wavefront (under a
   // condition the compiler would wait for them at its end) and put into LDS by the first.
   float next_lse = 0.0f, next_delta = 0.0f;
-  // p, at most 1 (and a rounding of lse), goes to narrow types times 2^kLift
-  constexpr float kLift = Mfma<T>::kNarrow ? 14.0f : 0.0f;
-  constexpr float kLower = Mfma<T>::kNarrow ? 0x1p-14f : 1.0f;
+  // p, at most 1 (and a rounding of lse), goes to narrow types times 2^kUp
+  constexpr float kUp = Mfma<T>::kNarrow ? 14.0f : 0.0f;
+  constexpr float kDown = Mfma<T>::kNarrow ? 0x1p-14f : 1.0f;
   auto fetch = [&](int32_t i0, char *__restrict__ to) {
     fetch_rows<NP + 1, WAVES>(qb, p.q_tok * es, i0, q.count - 1, wave, lane, to);
     fetch_rows<NP, WAVES>(gb, p.g_tok * es, i0, q.count - 1, wave, lane, to + (NP + 1) * 8192);
@@ -587,7 +587,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
     if (wave == 0) {  // rows that see nothing, or do not exist: p = exp2(s - infinity) = 0
       const bool real = i0 + lane < q.count;
       stats[slot][0][lane] =
-          real && next_lse != kNegInf ? next_lse * kLog2eF - kLift : __builtin_huge_valf();
+          real && next_lse != kNegInf ? next_lse * kLog2eF - kUp : __builtin_huge_valf();
       stats[slot][1][lane] = real ? next_delta : 0.0f;
     }
   };
@@ -693,9 +693,9 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
     if (!live) return;
     const int64_t out_row = tok * p.heads + head;
     if constexpr (!SECOND) {
-      store_columns<T, BLOCKS>(static_cast<char *>(p.dv) + out_row * DIM * es, acc, kLower, lane);
+      store_columns<T, BLOCKS>(static_cast<char *>(p.dv) + out_row * DIM * es, acc, kDown, lane);
     } else {
-      const float f = Mfma<T>::kNarrow ? p.scale * (kLower / lift) : p.scale;
+      const float f = Mfma<T>::kNarrow ? p.scale * (kDown / lift) : p.scale;
       store_columns<T, NP * 2>(static_cast<char *>(p.dk) + out_row * DIM * es, acc, f, lane);
       float *part = p.dkr_part + (int64_t(head) * p.Tk + tok) * 64;
 #pragma unroll

@@ -42,12 +42,17 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // kNarrow: the type's exponents end far inside float32's.  What is rounded to it between two products
 // is multiplied by a power of two first, which a sum's store takes off again: exact, and neither
 // small values become subnormal nor large ones infinite.
+//
+// kSlack, kLift: the weights of a row's softmax are 2^(s - top + kLift), and top, a maximum of
+// earlier scores, is raised when one passes it by more than kSlack.  With 4 and 11 float16 (2^15 at
+// most) keeps half a step down to 2^-25 of the largest weight.
 template <typename T>
 struct Mfma;
 
 template <>
 struct Mfma<__bf16> {
   static constexpr bool kNarrow = false;
+  static constexpr float kSlack = 8.0f, kLift = 0.0f;
   __device__ static f32x16 mul(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -67,6 +72,7 @@ struct Mfma<__bf16> {
 template <>
 struct Mfma<_Float16> {
   static constexpr bool kNarrow = true;
+  static constexpr float kSlack = 4.0f, kLift = 11.0f;
   __device__ static f32x16 mul(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -86,6 +92,12 @@ struct Mfma<_Float16> {
     return static_cast<float>(__builtin_bit_cast(f16x2_t, w).y);
   }
 };
+
+// Natural logarithm of the sum of a row's weights 2^(s - top + kLift).
+template <typename T>
+__device__ inline float natural(float top, float sum) {
+  return (top - Mfma<T>::kLift) * 0.693147180559945f + logf(sum);
+}
 
 __device__ inline s16x8 as_operand(uint4 v) { return __builtin_bit_cast(s16x8, v); }
 

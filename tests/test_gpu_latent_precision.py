@@ -1,5 +1,5 @@
 """GPU: precision of latent attention where ordinary random data does not show it: keys and values
-with a common offset, small and large gradients.
+with a common offset, small and large gradients, weights far below the largest. weights far below the largest.
 
 Bounds.  u is half a step of the storage type relative to a value (bf16 2^-8, f16 2^-11), e = 2^-24
 half a step of float32.  A sum of n terms each of which was rounded on its own, by at most u
@@ -164,3 +164,49 @@ def inner_and_results(q, k, kr, v, g):
 def test_float16_value_gradients_of_long_rows(dim):
     """Weights of 2^-19: dv is a sum of p g."""
     check_gradients(*data(gen_of(34), 8, 1 << 19, 1, dim, F16, 1.0, 100.0), (dim + ROPE) ** -0.5, False, F16)
+
+
+def tail_scores(gen, m):
+    """Scores (in powers of two) of one key at 0 and of the others near -23.5."""
+    s = -23.5 + 0.4 * randn(gen, m)
+    s[m // 3] = 0.0
+    return s
+
+
+def check_tail(out, lse, s, v):
+    """One head: scores s [m] (natural), values v [m, d] of which the leading key's are zero.  Each
+    weight keeps a relative error of half a step."""
+    p = torch.exp(s - torch.logsumexp(s, 0))
+    want = p @ v
+    assert_within(lse.reshape(1), torch.logsumexp(s, 0).reshape(1), torch.full((1,), 2e-5, device=DEV, dtype=torch.float64), "lse")
+    bound = (2 * U[F16] + 1e-3 * U[F16] + len(s) * E) * (p @ v.abs()) + 2.0 ** -25
+    assert_within(out.reshape(-1), want, bound, "out")
+
+
+def test_float16_weights_far_below_the_largest():
+    """One key leads with weight near 1 and a value of zero; the result is the sum of many weights
+    of 2^-23.5, which float16 holds with two bits at most."""
+    g = gen_of(35)
+    m, scale = 40000, 1.0
+    goal = tail_scores(g, m) * math.log(2)
+    v = (1 + 0.1 * randn(g, m, 128)) * 8
+    v[m // 3] = 0
+    # scores from two elements of the shared part, the second holding what the first rounds away
+    kr = torch.zeros(m, ROPE, device=DEV)
+    kr[:, 0] = goal.to(F16)
+    kr[:, 1] = (goal - kr[:, 0]) * 1024
+    q = torch.zeros(1, 1, 128 + ROPE, device=DEV)
+    q[..., 128], q[..., 129] = 1, 1 / 1024
+    q, kr, v = q.to(F16), kr.to(F16), v.to(F16)
+    s = kr[:, 0].double() + kr[:, 1].double() / 1024
+    out, lse = ra.rope_latent_attention(q, torch.zeros(m, 1, 128, dtype=F16, device=DEV), kr,
+                                        v[:, None], scale)
+    check_tail(out, lse, s, v.double())
+    cache = torch.cat([v, kr], dim=1).reshape(-1, 64, 192)
+    q[..., :128] = 0
+    for heads in (1, 40):  # 32 and 64 rows a workgroup
+        out, lse = ra.rope_latent_attention_paged(q.expand(1, heads, -1).contiguous(), cache,
+                                                  torch.arange(m // 64, device=DEV)[None],
+                                                  torch.tensor([m], device=DEV), 128, scale)
+        for h in (0, heads - 1):
+            check_tail(out[0, h], lse[0, h], s, v.double())
