@@ -264,7 +264,7 @@ int rope_append_paged_cache(const rope_tensor *positions, const rope_tensor *slo
  *                offsets[b+1] of query and out; rows outside all of them are left as they are.
  *                Out-of-range values are clamped; where they descend, the call writes no result.
  *                NULL: T / B queries each (T % B == 0).
- * latent_dim     128, 256 or 512.     scale   finite.
+ * latent_dim     128, 256 or 512.     scale   finite, |scale| < 2^127.
  * out            [T, heads, latent_dim] contiguous, 16-byte aligned; lse F32 [T, heads]
  *                contiguous, or NULL.  Outputs may not overlap anything else.
  * workspace      device memory of at least rope_latent_attention_paged_workspace() bytes, 16-byte

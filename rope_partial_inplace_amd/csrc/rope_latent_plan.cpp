@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <limits>
 
 #include "rope_check.h"
 
@@ -70,10 +71,12 @@ int64_t paged_rows(int64_t tokens, int64_t heads, int64_t sequences) {
 }
 
 // |scale| * log2(e), and whether the scale is negative.  Not 0, which would turn a masked score of
-// -infinity into a NaN; no score is large enough for 1e-30 to differ from it.
-void set_scale(double scale, float *scale_log2, bool *negative) {
-  *scale_log2 = float(std::max(std::fabs(scale) * kLog2e, 1e-30));
+// -infinity into a NaN: the smallest positive number makes no difference beside scores of any size.
+// False where the product is beyond float32.
+bool set_scale(double scale, float *scale_log2, bool *negative) {
+  *scale_log2 = std::max(float(std::fabs(scale) * kLog2e), std::numeric_limits<float>::denorm_min());
   *negative = scale < 0;
+  return std::isfinite(*scale_log2);
 }
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
@@ -126,7 +129,8 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
   if (query_offsets != nullptr ? query_offsets->shape[0] != B + 1 : (B == 0 ? T != 0 : T % B != 0))
     return reject(err, ROPE_ERR_PARAM_INVALID,
                   "query_offsets must be [B + 1]; without it every sequence has T / B queries");
-  if (!std::isfinite(scale)) return reject(err, ROPE_ERR_PARAM_INVALID, "scale must be finite");
+  if (!set_scale(scale, &plan->scale_log2, &plan->negative))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "scale must be finite, and below 2^127 in size");
   if (T >= kIndexLimit || H >= kIndexLimit || T * H >= kIndexLimit || B >= kIndexLimit)
     return reject(err, ROPE_ERR_PARAM_INVALID, "too many query rows");
   if (page_table->shape[1] >= kIndexLimit || cache->shape[1] >= kIndexLimit ||
@@ -180,7 +184,6 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
   p.queries = query_offsets != nullptr ? 0 : T / B;
   p.heads = int32_t(H);
   p.latent = int32_t(latent_dim);
-  set_scale(scale, &p.scale_log2, &p.negative);
   p.out = out->data;
   p.lse = lse != nullptr ? static_cast<float *>(lse->data) : nullptr;
   const int64_t item_rows = paged_rows(T, H, B);
@@ -283,7 +286,8 @@ int plan_expanded(const rope_tensor *query, const rope_tensor *key, const rope_t
     return reject(err, ROPE_ERR_PARAM_INVALID,
                   "without offsets num_sequences must divide both token counts");
   }
-  if (!std::isfinite(scale)) return reject(err, ROPE_ERR_PARAM_INVALID, "scale must be finite");
+  if (!set_scale(scale, &plan->scale_log2, &plan->negative))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "scale must be finite, and below 2^127 in size");
   if (Tq >= kIndexLimit || Tk >= kIndexLimit || H >= kIndexLimit || B >= kIndexLimit)
     return reject(err, ROPE_ERR_PARAM_INVALID, "too many tokens, heads or sequences");
   for (const rope_tensor *t : {query, key, key_rope, value})
@@ -333,7 +337,6 @@ int plan_expanded(const rope_tensor *query, const rope_tensor *key, const rope_t
   p.heads = int32_t(H);
   p.dim = int32_t(dim);
   p.scale = float(scale);
-  set_scale(scale, &p.scale_log2, &p.negative);
   p.out = out->data;
   p.lse = static_cast<float *>(lse->data);
   return ROPE_OK;

@@ -34,7 +34,7 @@ struct PagedPlan {
   FastDiv div_page, div_heads;
   int64_t T = 0, B = 0, queries = 0;  // queries: tokens of every sequence without offsets
   int32_t heads = 0, latent = 0;
-  float scale_log2 = 0;   // |scale| * log2(e), at least 1e-30: the softmax runs in powers of two
+  float scale_log2 = 0;   // |scale| * log2(e), above 0: the softmax runs in powers of two
   bool negative = false;  // scale < 0: the kernel turns the queries' signs
   void *out = nullptr;
   float *lse = nullptr;
@@ -68,7 +68,7 @@ struct ExpandedPlan {
   int64_t Tq = 0, Tk = 0, B = 0, q_each = 0, k_each = 0;  // *_each: tokens without offsets
   int32_t heads = 0, dim = 0;
   float scale = 0;
-  float scale_log2 = 0;   // |scale| * log2(e), at least 1e-30
+  float scale_log2 = 0;   // |scale| * log2(e), above 0
   bool negative = false;  // scale < 0: the forward kernel turns the queries' signs
   void *out = nullptr;
   float *lse = nullptr;

@@ -1,5 +1,5 @@
 """GPU: precision of latent attention where ordinary random data does not show it: keys and values
-with a common offset, small and large gradients, weights far below the largest. weights far below the largest.
+with a common offset, small and large gradients, weights far below the largest.
 
 Bounds.  u is half a step of the storage type relative to a value (bf16 2^-8, f16 2^-11), e = 2^-24
 half a step of float32.  A sum of n terms each of which was rounded on its own, by at most u
@@ -210,3 +210,27 @@ def test_float16_weights_far_below_the_largest():
                                                   torch.tensor([m], device=DEV), 128, scale)
         for h in (0, heads - 1):
             check_tail(out[0, h], lse[0, h], s, v.double())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_scale_zero_with_large_scores(causal):
+    """Scale 0: every visible key has the same weight, whatever the products."""
+    g = gen_of(36)
+    q, k, kr, v, grad = data(g, 40, 40, 1, 128, BF16)
+    q, k, kr = ((x.float() * 1e17).to(BF16) for x in (q, k, kr))
+    out, lse = ra.rope_latent_attention(q, k, kr, v, 0.0, causal)
+    seen = torch.arange(1, 41, device=DEV) if causal else torch.full((40,), 40, device=DEV)
+    mean = v[:, 0].double().cumsum(0) / seen[:, None] if causal else v[:, 0].double().mean(0).expand(40, -1)
+    size = v[:, 0].double().abs().mean() * 8
+    assert_within(lse[:, 0], seen.double().log(), torch.full((40,), 1e-5, device=DEV), "lse")
+    assert ((out[:, 0].double() - mean).abs() <= 2.0 ** -7 * size).all()
+    dq, dk, dkr, dv = ra.rope_latent_attention_backward(grad, q, k, kr, v, out, lse, 0.0, causal)
+    assert (dq == 0).all() and (dk == 0).all() and (dkr == 0).all()
+    share = grad[:, 0].double() / seen[:, None]
+    want = share.flip(0).cumsum(0).flip(0) if causal else share.sum(0).expand(40, -1)
+    assert ((dv[:, 0].double() - want).abs() <= 2.0 ** -7 * share.abs().sum(0)).all()
+    cache = torch.cat([(v[:, 0].float() * 1e17).to(BF16), kr], dim=1).reshape(1, 40, 192)
+    out, lse = ra.rope_latent_attention_paged(q[-1:], cache, torch.zeros(1, 1, dtype=torch.int64, device=DEV),
+                                              torch.tensor([40], device=DEV), 128, 0.0)
+    assert abs(float(lse) - math.log(40)) < 1e-5
+    assert ((out[0, 0].double() / 1e17 - cache[0, :, :128].double().mean(0) / 1e17).abs() <= 2.0 ** -7 * size).all()
