@@ -301,6 +301,9 @@ int rope_latent_attention_paged(const rope_tensor *query, const rope_tensor *lat
  *            sequences of Tq / B and Tk / B tokens.
  * num_sequences   B; may be 0 when there are offsets.
  * out        [Tq, heads, dim] contiguous, 16-byte aligned; lse F32 [Tq, heads] contiguous.
+ * A call whose kernels would need 2^32 threads is refused: with t = Tq / 128 + B tiles (B times the
+ * tiles of a sequence without offsets), heads * t * 256 has to stay below; of the backward call also
+ * heads * t * 512 with Tk in the place of Tq, and (Tq + Tk) * 16.
  */
 int rope_latent_attention(const rope_tensor *query, const rope_tensor *key,
                           const rope_tensor *key_rope, const rope_tensor *value,

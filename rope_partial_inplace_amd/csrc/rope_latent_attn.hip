@@ -46,9 +46,8 @@
 namespace ropeamd {
 namespace {
 
-constexpr int kBlockThreads = 256;
-constexpr int kKeyThreads = 512;  // of the kernel of dk and dv
-constexpr int kRows = 128;        // query rows (or keys) of a workgroup
+constexpr int kBlockThreads = kExpandedThreads;
+constexpr int kRows = int(kExpandedRows);
 constexpr int kTile = 64;         // keys (or query rows) in LDS at a time
 constexpr float kLog2eF = 1.44269504f;
 

@@ -212,7 +212,10 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
 
 namespace {
 
-constexpr int64_t kExpandedRows = 128;  // query rows (or keys) of a workgroup
+// Whether a launch of whole rounds of the XCDs can have `groups` workgroups of `threads`.
+bool launch_fits(int64_t groups, int64_t threads) {
+  return up(groups, kXcds) * threads < kLaunchThreads;
+}
 
 // The rows of a tile of 64 tokens are addressed by 32-bit byte offsets from its first.
 bool token_stride_fits(const rope_tensor *t) {
@@ -304,7 +307,8 @@ int plan_expanded(const rope_tensor *query, const rope_tensor *key, const rope_t
                           query_offsets != nullptr);
   p.k_tiles = tiles_bound(Tk, B, query_offsets != nullptr ? 0 : Tk / std::max<int64_t>(B, 1),
                           query_offsets != nullptr);
-  if (H * std::max(p.q_tiles, p.k_tiles) > 0x7fffff00)
+  if (H * std::max(p.q_tiles, p.k_tiles) > 0x7fffff00 ||
+      !launch_fits(H * p.q_tiles, kExpandedThreads))
     return reject(err, ROPE_ERR_PARAM_INVALID, "too many tokens and heads for one launch");
   if (!outputs_apart({out, lse}, {query, key, key_rope, value, query_offsets, key_offsets}))
     return reject(err, ROPE_ERR_PARAM_INVALID, "an output overlaps another tensor");
@@ -384,6 +388,10 @@ int plan_expanded_backward(const rope_tensor *grad, const rope_tensor *query,
   // without heads or sequences there are still zero gradients to write
   p.noop = p.Tq == 0 && p.Tk == 0;
   if (p.noop) return ROPE_OK;
+  // the kernels of dk and dv, and of dkey_rope: refused before the first of them is enqueued
+  if (!launch_fits(p.heads * p.k_tiles, kKeyThreads) ||
+      !launch_fits((p.Tk + p.Tq) * 16 / kExpandedThreads + 1, kExpandedThreads))
+    return reject(err, ROPE_ERR_PARAM_INVALID, "too many tokens and heads for one launch");
   const int64_t need = expanded_workspace(p.Tq, p.Tk, p.heads);
   if (need > 0 && workspace == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "workspace is NULL");
   if (workspace_bytes < need || !aligned16(workspace))

@@ -58,6 +58,11 @@ int plan_paged(const rope_tensor *query, const rope_tensor *cache, const rope_te
 int64_t paged_workspace(int64_t tokens, int64_t heads, int64_t latent, int64_t sequences);
 
 // ---- expanded form --------------------------------------------------------------------------
+constexpr int64_t kExpandedRows = 128;  // query rows (or keys) of a workgroup
+constexpr int kExpandedThreads = 256;   // of a workgroup
+constexpr int kKeyThreads = 512;        // of one of dk and dv
+constexpr int64_t kLaunchThreads = int64_t(1) << 32;  // a launch has fewer
+
 struct ExpandedPlan {
   rope_dtype dt = ROPE_BF16;
   bool noop = false, causal = true;
