@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kBlockThreads = kExpandedThreads;
 constexpr int kRows = int(kExpandedRows);
-constexpr int kTile = 64;         // keys (or query rows) in LDS at a time
+constexpr int kTile = 64;  // keys (or query rows) in LDS at a time
 constexpr float kLog2eF = 1.44269504f;
 
 struct Span {
@@ -81,10 +81,18 @@ __device__ inline int32_t wave_sum(int32_t x) {
 // in place of 1013.)
 //
 // Up to 64 sequences, one a lane: with n_b tiles in sequence b, sum_b max(0, n_b - j) of them have
-// an index (counted from the short end) of at least j, so a bisection over j finds the t-th.  With
-// more sequences they come in their own order.  `scratch`: ten words of LDS, free again on return.
-template <bool QUERY, int THREADS>
-__device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scratch) {
+// an index (counted from the short end) of at least j, so a bisection over j finds the t-th.
+//
+// With more they come in their own order, and nothing is added up over them: a call has
+// total / 128 + B tile numbers, and from off_b / 128 + b on there are enough for sequence b's tiles
+// (some stay empty).  A search finds b, each of its steps a read of 64 offsets.  Adding up would cost
+// each of more than B workgroups a time that grows with B: forward and gradients of 4096 sequences
+// of 16 tokens and 16 heads 4.75 ms in place of 3.05, of 65536 of one token and 2 heads 90 in place
+// of 5.2; 65 of 640 and 100 of 500 tokens 1.03 and 1.38 in place of 1.06 and 1.25.  Every 64 numbers
+// are taken in bit-reversed order, or the empty ones, often every second, would leave every second
+// compute unit idle (65 sequences of 128 tokens: 226 us in place of 175).
+template <bool QUERY>
+__device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t) {
   const int64_t *off = QUERY ? p.q_off : p.k_off;
   const int64_t each = QUERY ? p.q_each : p.k_each;
   const int32_t bound = int32_t(QUERY ? p.q_tiles : p.k_tiles);
@@ -93,14 +101,10 @@ __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scrat
     if (t >= per * count) return {-1, 0};
     return {t % count, QUERY ? per - 1 - t / count : t / count};
   }
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-  auto tiles = [&](int32_t b) {
-    if (b >= p.B) return 0;
-    const Span s = span(off, QUERY ? p.q_off_stride : p.k_off_stride, QUERY ? p.Tq : p.Tk, 0, b);
-    return (s.count + kRows - 1) / kRows;
-  };
+  const int64_t stride = QUERY ? p.q_off_stride : p.k_off_stride, total = QUERY ? p.Tq : p.Tk;
+  const int lane = int(threadIdx.x) & 63;
   if (p.B <= 64) {
-    const int32_t n = tiles(lane);
+    const int32_t n = lane < p.B ? (span(off, stride, total, 0, lane).count + kRows - 1) / kRows : 0;
     if (t >= wave_sum(n)) return {-1, 0};
     int32_t j = 0, above = bound;  // more than t tiles from j on, and none from `above` on
     while (above - j > 1) {
@@ -118,30 +122,24 @@ __device__ inline TileAt find_tile(const ExpandedPlan &p, int32_t t, void *scrat
     return {seq, QUERY ? j : __builtin_amdgcn_readlane(n, seq) - 1 - j};
   }
   if (QUERY) t = bound - 1 - t;  // the last tiles first, at least
-  int32_t *sums = static_cast<int32_t *>(scratch), *found = sums + THREADS / 64;
-  if (tid == 0) found[0] = -1;
-  int32_t before = 0;
-  for (int32_t b0 = 0; b0 < p.B; b0 += THREADS) {
-    const int32_t n = tiles(b0 + tid);
-    const int32_t incl = wave_scan(n);
-    if (lane == 63) sums[wave] = incl;
-    __syncthreads();
-    int32_t base = before;
-    for (int w = 0; w < THREADS / 64; ++w) {
-      if (w < wave) base += sums[w];
-      before += sums[w];
+  if ((t | 63) < bound) t = (t & ~63) | int32_t(__brev(uint32_t(t)) >> 26);
+  // the last sequence that begins at t or before is among the `left` from seq on
+  for (int32_t seq = 0, left = int32_t(p.B);;) {  // ends: at most a 64th is left, rounded up
+    const int32_t step = (left + 63) / 64, at = lane * step;
+    const int64_t o = min(max(off[min(seq + at, int32_t(p.B)) * stride], int64_t(0)), total);
+    const int32_t begin = int32_t(o / kRows) + seq + at;
+    const uint64_t behind = __ballot(at >= left || begin > t);
+    const int32_t n = behind == 0 ? 64 : __builtin_ctzll(behind);
+    if (n == 0) return {-1, 0};
+    if (step == 1) {
+      seq += n - 1;
+      const int32_t tile = t - __builtin_amdgcn_readlane(begin, n - 1);
+      const Span s = span(off, stride, total, 0, seq);
+      return {tile * int64_t(kRows) < s.count ? seq : -1, tile};
     }
-    if (base + incl - n <= t && t < base + incl) {
-      found[0] = b0 + tid;
-      found[1] = t - (base + incl - n);
-    }
-    __syncthreads();
-    if (t < before) break;  // the same for all threads
+    seq += (n - 1) * step;
+    left = min(step, left - (n - 1) * step);
   }
-  const TileAt at = {__builtin_amdgcn_readfirstlane(found[0]),
-                     __builtin_amdgcn_readfirstlane(found[1])};
-  __syncthreads();
-  return at;
 }
 
 // Workgroup number -> (head, tile number): the workgroups of a head, which share its keys and
@@ -294,7 +292,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_forward_kernel(Expand
   __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
   int32_t head, tile;
   if (!head_and_tile(p, p.q_tiles, head, tile)) return;
-  const TileAt at = find_tile<true, kBlockThreads>(p, tile, tiles);
+  const TileAt at = find_tile<true>(p, tile);
   if (at.seq < 0) return;
   const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
   const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
@@ -405,7 +403,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void latent_dquery_kernel(Expande
   __shared__ __attribute__((aligned(16))) char tiles[2 * TILE];
   int32_t head, tile;
   if (!head_and_tile(p, p.q_tiles, head, tile)) return;
-  const TileAt at = find_tile<true, kBlockThreads>(p, tile, tiles);
+  const TileAt at = find_tile<true>(p, tile);
   if (at.seq < 0) return;
   const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
   const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
@@ -544,7 +542,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void latent_dkey_kernel(ExpandedPla
   auto &stats = lds.stats;
   int32_t head, tile;
   if (!head_and_tile(p, p.k_tiles, head, tile)) return;
-  const TileAt at = find_tile<false, kKeyThreads>(p, tile, tiles);
+  const TileAt at = find_tile<false>(p, tile);
   if (at.seq < 0) return;
   const Span q = span(p.q_off, p.q_off_stride, p.Tq, p.q_each, at.seq);
   const Span k = span(p.k_off, p.k_off_stride, p.Tk, p.k_each, at.seq);
