@@ -297,8 +297,10 @@ int rope_latent_attention_paged(const rope_tensor *query, const rope_tensor *lat
  *            parts of one projection's rows), a token's below 32 MiB.
  * query_offsets, key_offsets   INT64 [B + 1] each, ascending: sequence b is query rows
  *            query_offsets[b] to [b+1] and key rows key_offsets[b] to [b+1]; rows outside are
- *            left as they are; out-of-range values are clamped.  Both NULL: num_sequences
- *            sequences of Tq / B and Tk / B tokens.
+ *            left as they are; out-of-range values are clamped.  Where they descend, the call's results
+ *            are not defined (sequences may then share rows, which are written in no fixed order),
+ *            but no access leaves the tensors, and rows outside the first and the largest offset
+ *            are left as they are.  Both NULL: num_sequences sequences of Tq / B and Tk / B tokens.
  * num_sequences   B; may be 0 when there are offsets.
  * out        [Tq, heads, dim] contiguous, 16-byte aligned; lse F32 [Tq, heads] contiguous.
  * A call whose kernels would need 2^32 threads is refused: with t = Tq / 128 + B tiles (B times the

@@ -40,3 +40,37 @@ def test_many_sequences_as_in_calls_of_64(causal, count):
             assert torch.equal(x[at], y[at]), (b, i)
     for x in got:
         assert (x[:spare] == 0).all() and (x[-spare:] == 0).all()
+
+
+@pytest.mark.parametrize("count", [3, 70])
+def test_offsets_out_of_range_are_clamped(count):
+    """As with the clamped values, bit for bit; gradients of every token come out."""
+    n = [5] * count
+    q, k, kr, v, grad = inputs(n, n, 2, 64, BF16, count)
+    fixed = offsets(n)
+    bad = fixed.clone()
+    bad[0], bad[-1] = -(2 ** 62), 2 ** 62
+    got = []
+    for off in (fixed, bad):
+        where = dict(query_offsets=off, key_offsets=off)
+        out, lse = ra.rope_latent_attention(q, k, kr, v, 0.1, **where)
+        got.append((out, lse, *ra.rope_latent_attention_backward(grad, q, k, kr, v, out, lse, 0.1, **where)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("count", [6, 80])
+def test_descending_offsets_write_no_rows_outside(count):
+    """Results are not defined where offsets descend; rows of no sequence stay as they are."""
+    n = [9] * count
+    q, k, kr, v, grad = inputs(n, n, 2, 64, BF16, count, spare=4)
+    for place, by in ((-2, 14), (2, 9), (count // 2, -200), (3, 1 << 40)):
+        off = offsets(n, 4)
+        off[place] -= by
+        off.clamp_(4, 4 + 9 * count)
+        out = torch.full((q.shape[0], 2, 64), 7.0, dtype=BF16, device=DEV)
+        lse = torch.full((q.shape[0], 2), 7.0, device=DEV)
+        ra.rope_latent_attention(q, k, kr, v, 0.1, out=out, lse=lse, query_offsets=off, key_offsets=off)
+        for x in (out, lse):
+            assert (x[:4] == 7).all() and (x[-4:] == 7).all()
+        ra.rope_latent_attention_backward(grad, q, k, kr, v, out, lse, 0.1, query_offsets=off,
+                                          key_offsets=off)
