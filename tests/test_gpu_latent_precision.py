@@ -234,3 +234,27 @@ def test_scale_zero_with_large_scores(causal):
                                               torch.tensor([40], device=DEV), 128, 0.0)
     assert abs(float(lse) - math.log(40)) < 1e-5
     assert ((out[0, 0].double() / 1e17 - cache[0, :, :128].double().mean(0) / 1e17).abs() <= 2.0 ** -7 * size).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_float16_non_finite_values_stay_in_their_sequence(value):
+    """The factors that float16's p and ds are held with are a row's or a key's own.  A gradient that
+    is not finite (a loss scaled too far) makes gradients of its sequence that are not."""
+    from test_gpu_latent import inputs, offsets
+    nq = nk = [70, 130, 65]
+    q, k, kr, v, grad = inputs(nq, nk, 2, 64, F16, 9)
+    where = dict(query_offsets=offsets(nq), key_offsets=offsets(nk))
+
+    def both(q, k, kr, v, g):
+        o, l = ra.rope_latent_attention(q, k, kr, v, 0.1, **where)
+        return (o, l, *ra.rope_latent_attention_backward(g, q, k, kr, v, o, l, 0.1, **where))
+
+    clean = both(q, k, kr, v, grad)
+    for i in range(5):
+        x = [t.clone() for t in (q, k, kr, v, grad)]
+        x[i][70 + 129].view(-1)[0] = value  # the middle sequence's last token
+        got = both(*x)
+        for a, b in zip(got, clean):
+            assert torch.equal(a[:70], b[:70]) and torch.equal(a[200:], b[200:])
+        if i == 4:
+            assert all(not torch.isfinite(t).all() for t in got[2:])
