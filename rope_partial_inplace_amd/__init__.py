@@ -71,6 +71,7 @@ def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
             f"{LIB_PATH} is missing: build it with `python __graft_entry__.py` at the repository root")
+    import torch  # noqa: F401  its HIP runtime first: the library then uses it, not a second one
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER
     lib.rope_partial_inplace.argtypes = [P(RopeTensor), P(RopeTensor), P(RopeTensor),
@@ -229,7 +230,7 @@ def _autograd_function():
     return InplacePartialRotaryMul
 
 
-def __getattr__(name):  # autograd functions are made on first use (torch is imported then)
+def __getattr__(name):  # autograd functions are made on first use
     make = {"InplacePartialRotaryMul": _autograd_function,
             "LatentAttention": _latent_autograd_function}.get(name)
     if make is not None:
