@@ -495,7 +495,8 @@ def rope_latent_attention_backward(grad, query, key, key_rope, value, out, lse, 
                                    causal: bool = True, num_sequences: int | None = None,
                                    query_offsets=None, key_offsets=None, stream=None):
     """Gradients of rope_latent_attention's out with respect to (query, key, key_rope, value), for
-    the gradient ``grad`` of out; out and lse are the forward call's."""
+    the gradient ``grad`` of out; out and lse are the forward call's.  Rows outside all sequences get
+    zeros."""
     import torch
     dev = _device_index((grad, query, key, key_rope, value, out, lse, query_offsets, key_offsets))
     if query.dim() != 3:
@@ -548,7 +549,9 @@ def _latent_autograd_function():
 def latent_attention(query, key, key_rope, value, scale: float, causal: bool = True,
                      num_sequences: int | None = None, query_offsets=None, key_offsets=None):
     """rope_latent_attention with autograd: returns out [Tq, heads, dim]; query, key, key_rope and
-    value get gradients from the backward kernels."""
+    value get gradients from the backward kernels.  Forward and backward may be captured into a graph,
+    both in one capture and after a warm-up on a side stream; as for every torch function, no eager
+    graph of the same leaves may be alive then."""
     fn = globals().get("LatentAttention") or __getattr__("LatentAttention")
     return fn.apply(query, key, key_rope, value, scale, causal, num_sequences, query_offsets,
                     key_offsets)

@@ -12,14 +12,19 @@
 // of a token's groups go into one launch because a decoding step's batch is bound by launch
 // latency (64 tokens of 32 + 8 + 8 heads: one launch in place of two or three).
 //
-// Measured: 8192 tokens of 32 + 8 + 8 heads of 128, float16, half of each head rotated (203 MB):
-// 34.3 us, 5.9 TB/s; 32768 latent rows of 576 with 16 query tails of 64 (212 MB): 38.6 us,
-// 5.5 TB/s; a dense copy of 1 GiB reaches 6.8 TB/s.  64 tokens: 3.9 us, its launch and three
-// dependent reads (position, table row, slot).
+// Measured, from HBM (seven sets of inputs in turn): 8192 tokens of 32 + 8 + 8 heads of 128, float16,
+// half of each head rotated (203 MB): 46 us, 4.4 TB/s; the same in float32 (405 MB): 82 us, 4.9 TB/s;
+// 32768 latent rows of 576 with 16 query tails of 64 (211 MB): 50 us, 4.2 TB/s; a dense copy of 1 GiB
+// reaches 6.8 TB/s, so a third of the time is still the kernel's.  64 tokens: 4.0 us, its launch and
+// three dependent reads (position, table row, slot).
 //
-// Rows that are not made of whole 16-byte vectors go an element (or GPT-J pair) at a time: 142 us
-// in place of 34, 131 in place of 39.  A slot's page and row come from a 64-bit division: a 32-bit
-// one by a multiplication, or a test for caches without gaps, was no faster (34.2 us each).
+// Rows that are not made of whole 16-byte vectors go an element (or GPT-J pair) at a time: 180 us in
+// place of 46 (heads of 126), 170 in place of 50 (rows of 578).
+//
+// Below, times of alternatives are of calls back to back on the same inputs, which the Infinity Cache
+// of 256 MB holds in part (34 us for the first of the above, 39 for the third).  A slot's page and
+// row come from a 64-bit division: a 32-bit one by a multiplication, or a test for caches without
+// gaps, was no faster (34.2 us each).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

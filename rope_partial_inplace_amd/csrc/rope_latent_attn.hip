@@ -26,10 +26,10 @@
 // than any result: both are lifted or lowered by powers of two: constant ones for p, forward too, and for ds taken
 // for each row of dq and each key of dk from what is summed there.
 //
-// Measured, bfloat16, causal, 32 heads of 128: 7 prompts of 300 to 6000 tokens forward 870 - 1010
-// us, 0.79 - 0.91 PF/s (a large library product on this card: 1.2 - 1.35); 4 x 2048 tokens, forward
-// 213 - 239 us, D and dq 465 - 515, dk and dv 487 - 556, dr 12: 0.74 - 0.83 PF/s of all eleven
-// products.
+// Measured, bfloat16, causal, 32 heads of 128: 7 prompts of 300 to 6000 tokens forward 880 - 1080
+// us, 0.74 - 0.91 PF/s (a large library product on this card: 1.2 - 1.35), with heads of 64 610 - 750
+// us; 4 x 2048 tokens, forward 206 - 256 us, D and dq 453 - 570, dk and dv 462 - 597, dr 12.5, on
+// average 0.79 PF/s of all eleven products (not causal, forward alone, 359 - 429 us).
 // The range is the clock's, which falls to 1.7 - 2.1 GHz under such kernels.  What the products
 // wait for: LDS reads, and the exponentials of a tile, which only the SIMD's other wavefront covers.
 #include <hip/hip_runtime.h>

@@ -23,12 +23,13 @@
 // small ones beside a large one would be lost; 24 sequences of 100 to 5000 tokens with 1 to 5 queries
 // of 16 heads take 21.7 us for it in place of 20.9.)
 //
-// Measured, bfloat16, latent_dim 512, this kernel and the joining one: 64 sequences of 200 to 9000
-// tokens, 32 heads, 44 + 8 us (213 MB: 4.9 TB/s in the first, where a dense copy of 1 GiB reaches
-// 6.8: each workgroup's first tile and its last part's way out are not covered); 6 of 60000 to
-// 131072 tokens, 128 heads, 155 - 180 + 13 us (0.67 - 0.78 PF/s: LDS reads of the tile, once for S
-// and once for O, and the exponentials between, at 1.9 GHz); one of 1001 tokens, 16 heads, 11.5 +
-// 4.3 us (dependent reads: lengths, page, tile, part).
+// Measured, bfloat16, latent_dim 512, this kernel and the joining one, caches from HBM: 64 sequences
+// of 200 to 9000 tokens, 32 heads, 53 + 8 us (213 MB: 4.0 TB/s in the first, where a dense copy of
+// 1 GiB reaches 6.8: each workgroup's first tile and its last part's way out are not covered; back to
+// back on one cache, which the Infinity Cache holds in part, 44 + 8), with latent_dim 256 34 + 6, with
+// 128 24 + 6; 6 of 60000 to 131072 tokens, 128 heads, 161 - 205 + 13 us (0.55 - 0.69 PF/s: LDS reads
+// of the tile, once for S and once for O, and the exponentials between, at 1.9 GHz); one of 1001
+// tokens, 16 heads, 11.6 + 4.0 us (dependent reads: lengths, page, tile, part).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
