@@ -320,9 +320,11 @@ int rope_latent_attention(const rope_tensor *query, const rope_tensor *key,
  * its rounding into the gradients, so it is computed again, in float32).  Gradients are contiguous,
  * 16-byte aligned, of their input's shape and dtype, each summed in float32 in a fixed order and
  * rounded once (the probabilities and their gradients are rounded to the dtype between the products,
- * in F16 after an exact scaling that keeps them in its range, whatever the size of grad).  Rows
- * outside all sequences get zero gradients.  workspace: at least
- * rope_latent_attention_backward_workspace() bytes, under the rules of rope_latent_attention_paged's.
+ * in F16 after an exact scaling that keeps them in its range, whatever the size of grad).  The
+ * probabilities are taken again from lse, so their relative error grows with it, by some
+ * 2^-22 |lse|: below a bfloat16 step for |lse| up to 10^4.  Rows outside all sequences get zero
+ * gradients.  workspace: at least rope_latent_attention_backward_workspace() bytes, under the rules
+ * of rope_latent_attention_paged's.
  */
 int64_t rope_latent_attention_backward_workspace(int64_t query_tokens, int64_t key_tokens,
                                                  int64_t num_heads);

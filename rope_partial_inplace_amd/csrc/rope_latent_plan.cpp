@@ -74,9 +74,11 @@ int64_t paged_rows(int64_t tokens, int64_t heads, int64_t sequences) {
 // -infinity into a NaN: the smallest positive number makes no difference beside scores of any size.
 // False where the product is beyond float32.
 bool set_scale(double scale, float *scale_log2, bool *negative) {
-  *scale_log2 = std::max(float(std::fabs(scale) * kLog2e), std::numeric_limits<float>::denorm_min());
+  const double x = std::fabs(scale) * kLog2e;
+  if (!(x <= std::numeric_limits<float>::max())) return false;  // infinite and NaN too
+  *scale_log2 = std::max(float(x), std::numeric_limits<float>::denorm_min());
   *negative = scale < 0;
-  return std::isfinite(*scale_log2);
+  return true;
 }
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }

@@ -107,7 +107,7 @@ def data(gen, n, m, heads, dim, dtype, wide=1.0, small=1.0):
 def test_gradients_of_keys_and_values_with_a_common_offset(offset, n, m, dim, causal, dtype):
     """Biased projections: every channel of keys, shared key parts and values has an offset of its
     own.  An error of D = sum_j p_j dP_j then reaches dq through sum_j p_j k_j, which no longer
-    averages out (D from the rounded output: dq off by 3.9% of its norm)."""
+    averages out (D from the rounded output: dq off by 5% of its norm at an offset of 1, by 45% at 3)."""
     g = gen_of(31)
     q, k, kr, v, grad = data(g, n, m, 2, dim, torch.float32)
     k, kr, v = k + offset * randn(g, 2, dim), kr + offset * randn(g, ROPE), v + offset * randn(g, 2, dim)
