@@ -18,6 +18,9 @@
  *                                  of every head and one rotated key part shared by the heads
  *   rope_latent_attention_backward
  *                                  its gradients
+ *   rope_append_paged_cache_q8     rotates a batch's new keys (and queries) by position and writes
+ *                                  keys and values to a paged cache of 8-bit codes with a scale
+ *                                  for each block of tokens and head
  *
  * Pages defining the operations:
  *   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码
@@ -63,7 +66,9 @@ typedef enum {
   ROPE_F32 = 0,  /* IEEE binary32 */
   ROPE_F16 = 1,  /* IEEE binary16 */
   ROPE_BF16 = 2, /* bfloat16 */
-  ROPE_I64 = 3   /* int64 (positions) */
+  ROPE_I64 = 3,  /* int64 (positions) */
+  ROPE_I8 = 4,   /* int8 codes of a cache in 8 bits */
+  ROPE_E4M3 = 5  /* 8-bit floating point codes, 4 exponent and 3 mantissa bits, no infinities */
 } rope_dtype;
 
 /* Status codes.  The two parameter codes are the ones of [IPRM §返回值与错误码];
@@ -335,6 +340,56 @@ int rope_latent_attention_backward(
     int64_t num_sequences, double scale, int causal, const rope_tensor *dquery,
     const rope_tensor *dkey, const rope_tensor *dkey_rope, const rope_tensor *dvalue,
     void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rope_append_paged_cache_q8 -- rotate by position, append to a paged cache in 8 bits.
+ *
+ * A cached key (or value) element is code * scale: the codes lie in a cache [pages, pageSize, Nk, D]
+ * of I8 or E4M3, and every block of pageSize / blocks tokens of a page and every head has one
+ * float32 scale in [pages, blocks, Nk].  Sequence b's new tokens are rows token_offsets[b] to
+ * token_offsets[b+1] of key, value and query; they are the last ones of its seq_lens[b] tokens, so
+ * the i-th of n goes to place p = seq_lens[b] - n + i: row p % pageSize of page
+ * page_table[b, p / pageSize].  Rotation is that of rope_append_paged_cache, in float32, and keys are
+ * coded from its unrounded results.
+ *
+ * For each block and head that takes new tokens, with top = the largest |x| of the new elements:
+ *       need = max(top / 127, 2^-120)                                      I8
+ *       need = the smallest power of two >= max(top / 448, 2^-120)         E4M3
+ *       scale = need, or the larger of need and the present scale where the block holds earlier
+ *               tokens of the sequence; their codes are then round(code * (old scale / scale))
+ *       code = round(x * (1 / scale))       (to nearest even; every step is one float32 operation,
+ *                                            top / 127 a product with the float32 nearest 1/127)
+ * Powers of two keep E4M3 codes exact when a scale grows, down to the type's subnormal numbers;
+ * I8 codes of the block's earlier tokens lose up to half a step each time.  Scales outlive tokens
+ * that are taken back (a smaller seq_lens): only a block's first token starts a scale anew.
+ * Non-finite elements: E4M3 codes them as NaN and leaves them out of top; I8, which has no NaN, sets
+ * the scale of the block and head to NaN, and so all its tokens.  Rows behind the last token are
+ * left as they are.
+ *
+ * positions      INT64 [T], as in rope_append_paged_cache.
+ * query          [T, Nq, Dq] or NULL, with query_out [T, Nq, Dq] (NULL exactly if query is; it may
+ *                be the query itself).  All tokens' queries are rotated.
+ * key            [T, Nk, D]; value [T, Nk, Dv]; cos_sin_cache [maxSeqLen, rotaryDim].  One dtype,
+ *                F32, F16 or BF16.
+ * key_cache, value_cache    [pages, pageSize, Nk, D] and [.., Dv], I8 or E4M3, one of the two.
+ * key_scales, value_scales  F32 [pages, blocks, Nk]; blocks divides pageSize.
+ * page_table     INT64 [B, maxPages]; seq_lens INT64 [B], clamped to [0, maxPages * pageSize].
+ *                Tokens before place 0, and tokens whose page is not in [0, pages) (padding), are
+ *                skipped.  A page that takes tokens belongs to one sequence only -- a precondition
+ *                that is not checked (rope_fork_pages keeps it).
+ * token_offsets  INT64 [B + 1], ascending (else nothing is appended), clamped to [0, T]; rows outside
+ *                all sequences are not appended.  NULL: T / B tokens each (T % B == 0).
+ * Any non-negative strides with unit inner stride (scales: any non-negative strides).  Outputs whose
+ * strides reach an element twice, and any other overlap with an output, are refused.  T = 0 is a no-op.
+ */
+int rope_append_paged_cache_q8(const rope_tensor *positions, const rope_tensor *query,
+                               const rope_tensor *key, const rope_tensor *value,
+                               const rope_tensor *cos_sin_cache, const rope_tensor *page_table,
+                               const rope_tensor *seq_lens, const rope_tensor *token_offsets,
+                               int64_t query_rot_start, int64_t key_rot_start, int is_neox_style,
+                               const rope_tensor *query_out, const rope_tensor *key_cache,
+                               const rope_tensor *value_cache, const rope_tensor *key_scales,
+                               const rope_tensor *value_scales, void *stream);
 
 /* Text describing the last failing call on the calling thread ("" if none).  The pointer
  * stays valid until the next call on this thread. */

@@ -46,7 +46,7 @@ ROPE_ERR_PARAM_NULLPTR = 161001
 ROPE_ERR_PARAM_INVALID = 161002
 ROPE_ERR_RUNTIME = 361001
 
-ROPE_F32, ROPE_F16, ROPE_BF16, ROPE_I64 = 0, 1, 2, 3
+ROPE_F32, ROPE_F16, ROPE_BF16, ROPE_I64, ROPE_I8, ROPE_E4M3 = 0, 1, 2, 3, 4, 5
 
 
 class RopeTensor(ctypes.Structure):
@@ -108,6 +108,9 @@ def _load() -> ctypes.CDLL:
     lib.rope_latent_attention_backward.argtypes = [T] * 7 + where + [T] * 4 + [
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
     lib.rope_latent_attention_backward.restype = ctypes.c_int
+    lib.rope_append_paged_cache_q8.argtypes = [T] * 8 + [ctypes.c_int64, ctypes.c_int64,
+                                                         ctypes.c_int] + [T] * 5 + [ctypes.c_void_p]
+    lib.rope_append_paged_cache_q8.restype = ctypes.c_int
     lib.rope_last_error.argtypes = []
     lib.rope_last_error.restype = ctypes.c_char_p
     return lib
@@ -123,7 +126,8 @@ def last_error() -> str:
 def _dtype_code(t) -> int:
     import torch
     return {torch.float32: ROPE_F32, torch.float16: ROPE_F16, torch.bfloat16: ROPE_BF16,
-            torch.int64: ROPE_I64}.get(t.dtype, 99)
+            torch.int64: ROPE_I64, torch.int8: ROPE_I8,
+            torch.float8_e4m3fn: ROPE_E4M3}.get(t.dtype, 99)
 
 
 def describe(t) -> RopeTensor:
@@ -555,6 +559,35 @@ def latent_attention(query, key, key_rope, value, scale: float, causal: bool = T
     fn = globals().get("LatentAttention") or __getattr__("LatentAttention")
     return fn.apply(query, key, key_rope, value, scale, causal, num_sequences, query_offsets,
                     key_offsets)
+
+
+# ---- paged cache in 8 bits ----------------------------------------------------------------------
+
+def rope_append_paged_cache_q8(positions, key, value, key_cache, value_cache, key_scales,
+                               value_scales, page_table, seq_lens, cos_sin_cache,
+                               query_offsets=None, query=None, query_out=None,
+                               query_rot_start: int = 0, key_rot_start: int = 0,
+                               is_neox_style: bool = True, stream=None):
+    """Rotate a batch's keys (and queries) by position and append keys and values to a paged cache of
+    8-bit codes: key [T, Nk, D] and value [T, Nk, Dv] go to the last places of their sequences in
+    key_cache [pages, pageSize, Nk, D] and value_cache [pages, pageSize, Nk, Dv] (int8 or
+    float8_e4m3fn), with float32 scales [pages, blocks, Nk] for each block of pageSize / blocks tokens
+    and head.  page_table [B, maxPages], seq_lens [B] (the new tokens included) and query_offsets
+    [B + 1] (the packed batch's) are int64; without offsets every sequence has T / B new tokens.
+    Where a block's scale has to grow, the codes of the sequence's earlier tokens in it are rounded
+    anew.  Rotation as in rope_append_paged_cache.  Returns query_out [T, Nq, Dq] (allocated when not
+    given; it may be query itself), or None without a query."""
+    dev = _device_index((positions, query, key, value, cos_sin_cache, page_table, seq_lens,
+                         query_offsets, query_out, key_cache, value_cache, key_scales,
+                         value_scales))
+    if query is not None and query_out is None:
+        query_out, = _new(stream, dev, (query.shape, query.dtype, query.device))
+    _run_on(dev, LIB.rope_append_paged_cache_q8, _pack(positions), _pack(query), _pack(key),
+            _pack(value), _pack(cos_sin_cache), _pack(page_table), _pack(seq_lens),
+            _pack(query_offsets), query_rot_start, key_rot_start, bool(is_neox_style),
+            _pack(query_out), _pack(key_cache), _pack(value_cache), _pack(key_scales),
+            _pack(value_scales), _raw_stream(stream, dev))
+    return query_out
 
 
 class PreparedCall:

@@ -22,13 +22,13 @@ LIB_PATH = os.path.join(HERE, "librope_amd.so")
 ARCH = "gfx950"
 
 HOST_SOURCES = [os.path.join(CSRC, n) for n in
-                ("rope_plan.cpp", "rope_append_plan.cpp", "rope_latent_plan.cpp")]
+                ("rope_plan.cpp", "rope_append_plan.cpp", "rope_latent_plan.cpp", "rope_q8_plan.cpp")]
 KERNEL_SOURCES = [os.path.join(CSRC, n) for n in
                   ("rope_kernels.hip", "rope_append.hip", "rope_latent_paged.hip",
-                   "rope_latent_attn.hip")]
+                   "rope_latent_attn.hip", "rope_q8_append.hip")]
 HEADERS = [os.path.join(CSRC, n) for n in
            ("rope_plan.h", "rope_append_plan.h", "rope_latent_plan.h", "rope_check.h", "rope_io.h",
-            "rope_launch.h", "rope_mfma.h")]
+            "rope_launch.h", "rope_mfma.h", "rope_q8_plan.h", "rope_q8.h")]
 SOURCES = HOST_SOURCES + KERNEL_SOURCES
 # Everything the library is built from; its digest is written beside the library (STAMP_PATH)
 # so that a library older than its sources is noticed before it is tested.
@@ -114,7 +114,7 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     commands = [["g++", *HOST_FLAGS, *inc, "-c", src, "-o", obj(src)] for src in HOST_SOURCES]
     commands += [[hipcc(), *HIPCC_FLAGS, *MFMA_FLAGS, *(extra_flags or []), *inc, "-c", src, "-o", obj(src)]
                  for src in KERNEL_SOURCES]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=8) as pool:
         list(pool.map(lambda cmd: _run(cmd, verbose), commands))
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *map(obj, SOURCES), "-o", tmp],
          verbose)

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <string>
 
 #include "rope.h"
@@ -16,6 +17,8 @@ inline int bytes_of(rope_dtype dt) {
     case ROPE_F16: return 2;
     case ROPE_BF16: return 2;
     case ROPE_I64: return 8;
+    case ROPE_I8: return 1;
+    case ROPE_E4M3: return 1;
   }
   return 0;
 }
@@ -164,6 +167,44 @@ inline bool rows_aligned16(const rope_tensor *t) {
   for (int d = 0; d + 1 < t->ndim; ++d)
     if (t->shape[d] > 1 && (t->stride[d] * bytes_of(t->dtype)) % 16 != 0) return false;
   return true;
+}
+
+// Checks that the operators on caches make of all their tensors (NULL entries are absent ones).
+inline int common_checks(std::initializer_list<const rope_tensor *> all, std::string *err) {
+  for (const rope_tensor *t : all)
+    if (t != nullptr && valid_rank(t) && count(t) > 0 && t->data == nullptr)
+      return reject(err, ROPE_ERR_PARAM_NULLPTR, "a non-empty tensor has NULL data");
+  for (const rope_tensor *t : all)
+    if (t != nullptr && (!valid_rank(t) || !addressable(t)))
+      return reject(err, ROPE_ERR_PARAM_INVALID, "bad shape or extent");
+  for (const rope_tensor *t : all)
+    if (t != nullptr && !non_negative_strides(t))
+      return reject(err, ROPE_ERR_PARAM_INVALID, "negative strides are not supported");
+  return ROPE_OK;
+}
+
+inline bool is_i64_vector(const rope_tensor *t) { return t->dtype == ROPE_I64 && t->ndim == 1; }
+
+// Outputs share no element with each other or with an input.
+inline bool outputs_apart(std::initializer_list<const rope_tensor *> outs,
+                          std::initializer_list<const rope_tensor *> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    if (*o == nullptr || count(*o) == 0) continue;
+    for (auto q = o + 1; q != outs.end(); ++q)
+      if (*q != nullptr && count(*q) > 0 && !disjoint(*o, *q)) return false;
+    for (const rope_tensor *i : ins)
+      if (i != nullptr && count(i) > 0 && !disjoint(*o, i)) return false;
+  }
+  return true;
+}
+
+// Whether [p, p + bytes) shares memory with t's extent.
+inline bool touches(const void *p, int64_t bytes, const rope_tensor *t) {
+  if (t == nullptr || count(t) == 0 || bytes <= 0) return false;
+  uintptr_t a, b;
+  extent(t, &a, &b);
+  const uintptr_t w = reinterpret_cast<uintptr_t>(p);
+  return a < w + uintptr_t(bytes) && w < b;
 }
 
 }  // namespace ropeamd

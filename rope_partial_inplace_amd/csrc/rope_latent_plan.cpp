@@ -17,44 +17,6 @@ constexpr int64_t kIndexLimit = int64_t(1) << 30;  // token and row numbers stay
 
 bool half_precision(rope_dtype dt) { return dt == ROPE_F16 || dt == ROPE_BF16; }
 
-// Checks that every operator here makes of its tensors (NULL entries are absent ones).
-int common_checks(std::initializer_list<const rope_tensor *> all, std::string *err) {
-  for (const rope_tensor *t : all)
-    if (t != nullptr && valid_rank(t) && count(t) > 0 && t->data == nullptr)
-      return reject(err, ROPE_ERR_PARAM_NULLPTR, "a non-empty tensor has NULL data");
-  for (const rope_tensor *t : all)
-    if (t != nullptr && (!valid_rank(t) || !addressable(t)))
-      return reject(err, ROPE_ERR_PARAM_INVALID, "bad shape or extent");
-  for (const rope_tensor *t : all)
-    if (t != nullptr && !non_negative_strides(t))
-      return reject(err, ROPE_ERR_PARAM_INVALID, "negative strides are not supported");
-  return ROPE_OK;
-}
-
-bool is_i64_vector(const rope_tensor *t) { return t->dtype == ROPE_I64 && t->ndim == 1; }
-
-// Outputs share no element with each other or with an input.
-bool outputs_apart(std::initializer_list<const rope_tensor *> outs,
-                   std::initializer_list<const rope_tensor *> ins) {
-  for (auto o = outs.begin(); o != outs.end(); ++o) {
-    if (*o == nullptr || count(*o) == 0) continue;
-    for (auto q = o + 1; q != outs.end(); ++q)
-      if (*q != nullptr && count(*q) > 0 && !disjoint(*o, *q)) return false;
-    for (const rope_tensor *i : ins)
-      if (i != nullptr && count(i) > 0 && !disjoint(*o, i)) return false;
-  }
-  return true;
-}
-
-// Whether [p, p + bytes) shares memory with t's extent.
-bool touches(const void *p, int64_t bytes, const rope_tensor *t) {
-  if (t == nullptr || count(t) == 0 || bytes <= 0) return false;
-  uintptr_t a, b;
-  extent(t, &a, &b);
-  const uintptr_t w = reinterpret_cast<uintptr_t>(p);
-  return a < w + uintptr_t(bytes) && w < b;
-}
-
 // Rows of an item: as many as a sequence's (token, head) rows fill, 32, 64 or 128.  More rows read
 // the cache fewer times and spread a tile's LDS reads over more products; fewer leave smaller parts
 // to join.  Microseconds, bfloat16, latent_dim 512, for items of 32 | 64 | 128 rows:

@@ -1,0 +1,104 @@
+// rope_q8.h -- 8-bit codes and their scales in device code (library-internal, gfx950).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "rope_plan.h"
+
+namespace ropeamd {
+namespace {
+
+__device__ inline uint32_t div_by(const FastDiv &f, uint32_t n) {
+  const uint32_t t = __umulhi(f.m, n);
+  return (t + ((n - t) >> f.s1)) >> f.s2;
+}
+
+__device__ inline bool finite(float x) {
+  return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
+}
+
+// The larger of `top` and |x|; a non-finite x sets the flag instead.
+__device__ inline float larger(float top, float x, bool *bad) {
+  const bool good = finite(x);
+  *bad |= !good;
+  return good ? fmaxf(top, fabsf(x)) : top;
+}
+
+// The scale that elements of size `top` need.  e4m3: the power of two 2^k with top <= 448 * 2^k, read off
+// top's exponent and whether its fraction passes that of 448 = 1.75 * 2^8.
+template <bool E4M3>
+__device__ inline float needed_scale(float top) {
+  if constexpr (E4M3) {
+    const uint32_t u = __float_as_uint(top);
+    const int32_t k = int32_t(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float(uint32_t(max(k, -120) + 127) << 23);
+  } else {
+    return fmaxf(top * (1.0f / 127), 0x1p-120f);
+  }
+}
+
+// Four floats to codes, to nearest even.  They lie within the codes' range but for NaN and infinity:
+// e4m3 NaN, int8 the ends of its range (under a NaN scale: any code).
+template <bool E4M3>
+__device__ inline uint32_t encode4(float a, float b, float c, float d) {
+  if constexpr (E4M3) {
+    const float nan = __builtin_nanf("");
+    a = finite(a) ? a : nan;
+    b = finite(b) ? b : nan;
+    c = finite(c) ? c : nan;
+    d = finite(d) ? d : nan;
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+  } else {
+    auto one = [](float x) {
+      return uint32_t(int32_t(rintf(fminf(fmaxf(x, -127.0f), 127.0f)))) & 0xffu;
+    };
+    return one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+  }
+}
+
+template <bool E4M3>
+__device__ inline void decode4(uint32_t w, float *f) {
+  if constexpr (E4M3) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
+    f[0] = lo[0];
+    f[1] = lo[1];
+    f[2] = hi[0];
+    f[3] = hi[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = float(int8_t(w >> (8 * i)));
+  }
+}
+
+// Four codes under a scale that is 1 / ratio times the old one.
+template <bool E4M3>
+__device__ inline uint32_t recode(uint32_t w, float ratio) {
+  float f[4];
+  decode4<E4M3>(w, f);
+  return encode4<E4M3>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+}
+
+// V = 1, 4 or 8 codes of f * inv.
+template <bool E4M3, int V>
+__device__ inline void store_codes(uint8_t *to, const float *f, float inv) {
+  if constexpr (V == 1) {
+    *to = uint8_t(encode4<E4M3>(f[0] * inv, 0.0f, 0.0f, 0.0f));
+  } else {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      w[i] = encode4<E4M3>(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv,
+                           f[4 * i + 3] * inv);
+    if constexpr (V == 4)
+      *reinterpret_cast<uint32_t *>(to) = w[0];
+    else
+      *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+  }
+}
+
+}  // namespace
+}  // namespace ropeamd

@@ -1,0 +1,125 @@
+// rope_q8_plan.h -- launch plans of the append to and the attention over a paged cache in 8 bits
+// (library-internal).
+#pragma once
+
+#include <cstdint>
+#include <string>
+
+#include "rope.h"
+#include "rope_append_plan.h"
+#include "rope_plan.h"
+
+namespace ropeamd {
+
+// Where sequences lie: lengths, pages and the rows of a packed batch (offsets NULL: `each` rows).
+struct Sequences {
+  const int64_t *table = nullptr, *lens = nullptr, *offsets = nullptr;
+  int64_t table_seq = 0, table_page = 0, len_stride = 0, off_stride = 0;
+  int64_t num_pages = 0, max_pages = 0, page_size = 1;
+  int64_t T = 0, B = 0, each = 0;
+  FastDiv div_page;
+};
+
+// ---- append -----------------------------------------------------------------------------------
+// Keys or values: where their rows, codes and scales lie.
+struct Q8Rows {
+  const void *in = nullptr;
+  int64_t in_tok = 0, in_head = 0;  // elements
+  uint8_t *codes = nullptr;
+  int64_t page = 0, row = 0, head = 0;  // strides of the codes (bytes)
+  float *scales = nullptr;
+  int64_t s_page = 0, s_block = 0, s_head = 0;
+  int32_t dim = 0;
+  int32_t rot_start = 0;
+  uint32_t rot_items = 0;  // rotated items of a row, in the order of AppendRows
+  uint32_t items = 0;
+  bool wide_rows = false;  // code rows split into aligned 16-byte pieces
+  FastDiv div_items;
+};
+
+struct AppendQ8Plan {
+  rope_dtype dt = ROPE_F32;
+  bool neox = true, vector_io = false, noop = false, e4m3 = false;
+  bool idx32 = true;  // query items and wavefronts are numbered in 32 bits
+  // A wavefront takes one place of tokens (one block of a sequence) and several of its heads.
+  // Places are numbered so that their sequence can be found from the offsets alone: by token, where
+  // all but a block's first new token have nothing to do, or, fewer for long appends, from
+  // offsets[b] / block + 2 b on, which is enough for the blocks a sequence's tokens can touch.
+  bool by_token = true;
+  int32_t lanes = 64;      // lanes of a head's block: a power of two
+  int32_t lanes_log2 = 6;
+  int64_t places = 0, kv_blocks = 0, query_blocks = 0;
+  int32_t head_groups = 1;  // wavefronts of a place
+  int32_t heads = 0;
+  int32_t block = 1;  // tokens of a scale
+  int32_t half = 0;   // rotaryDim / 2
+  const int64_t *positions = nullptr;
+  int64_t pos_stride = 0;
+  const void *table = nullptr;  // cos and sin
+  int64_t table_stride = 0, max_seq = 0;
+  Sequences seq;
+  FastDiv div_groups, div_block;
+  Q8Rows kv[2];
+  AppendRows query;
+};
+
+constexpr int kQ8Block = 256;
+
+int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const rope_tensor *key,
+                   const rope_tensor *value, const rope_tensor *cos_sin_cache,
+                   const rope_tensor *page_table, const rope_tensor *seq_lens,
+                   const rope_tensor *token_offsets, int64_t query_rot_start,
+                   int64_t key_rot_start, int is_neox_style, const rope_tensor *query_out,
+                   const rope_tensor *key_cache, const rope_tensor *value_cache,
+                   const rope_tensor *key_scales, const rope_tensor *value_scales,
+                   AppendQ8Plan *plan, std::string *err);
+
+// ---- attention --------------------------------------------------------------------------------
+constexpr int64_t kQ8Step = 128;    // cached tokens a workgroup takes at a time
+constexpr int64_t kQ8Groups = 1024; // workgroups, at most
+constexpr int kQ8JoinWords = 8;
+
+// Keys or values of the cache.
+struct Q8Cache {
+  const uint8_t *codes = nullptr;
+  int64_t page = 0, head = 0;  // bytes
+  int32_t row = 0;
+  const float *scales = nullptr;
+  int64_t s_page = 0, s_block = 0, s_head = 0;
+};
+
+struct AttnQ8Plan {
+  rope_dtype dt = ROPE_BF16;
+  bool e4m3 = false, noop = false;
+  // pages of whole runs of 16 tokens and scales of whole runs of 4: a half tile lies in one page
+  // and a lane's four neighbouring tokens under one scale
+  bool runs = false;
+  const void *q = nullptr;
+  int64_t q_tok = 0, q_head = 0;
+  Q8Cache k, v;
+  Sequences seq;
+  int32_t heads = 0, kv_heads = 0, group = 1, head_size = 0, block = 1;
+  FastDiv div_group, div_block;
+  float scale_log2 = 0;
+  int32_t tiles = 1;   // 16-row tiles of a workgroup (1 or 2)
+  int32_t groups = 0;  // workgroups
+  void *out = nullptr;
+  float *lse = nullptr;
+  // workspace: for a workgroup's first and last part the record of the item it is part of, its
+  // rows' maxima and sums, and its unnormalised outputs
+  int64_t *joins = nullptr;  // [groups][2][kQ8JoinWords]
+  float *stats = nullptr;    // [groups][2][rows][2]
+  float *parts = nullptr;    // [groups][2][rows][head_size]
+};
+
+int64_t attention_q8_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_size,
+                               int64_t sequences);
+
+int plan_attention_q8(const rope_tensor *query, const rope_tensor *key_cache,
+                      const rope_tensor *value_cache, const rope_tensor *key_scales,
+                      const rope_tensor *value_scales, const rope_tensor *page_table,
+                      const rope_tensor *seq_lens, const rope_tensor *query_offsets, double scale,
+                      const rope_tensor *out, const rope_tensor *lse, void *workspace,
+                      int64_t workspace_bytes, AttnQ8Plan *plan, std::string *err);
+
+}  // namespace ropeamd
