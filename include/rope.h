@@ -21,6 +21,7 @@
  *   rope_append_paged_cache_q8     rotates a batch's new keys (and queries) by position and writes
  *                                  keys and values to a paged cache of 8-bit codes with a scale
  *                                  for each block of tokens and head
+ *   rope_attention_paged_q8        grouped-query attention over that cache
  *
  * Pages defining the operations:
  *   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码
@@ -390,6 +391,40 @@ int rope_append_paged_cache_q8(const rope_tensor *positions, const rope_tensor *
                                const rope_tensor *query_out, const rope_tensor *key_cache,
                                const rope_tensor *value_cache, const rope_tensor *key_scales,
                                const rope_tensor *value_scales, void *stream);
+
+/*
+ * rope_attention_paged_q8 -- grouped-query attention over a paged cache in 8 bits.
+ *
+ * Head h of query token i (of n, in a sequence of len cached tokens, its own n among them) attends to
+ * the tokens j < len - n + 1 + i of key head h / (heads / Nk):
+ *       s_j = scale * key_scale_j * <query[i, h], key_code_j>,   p = softmax_j(s)
+ *       out[i, h] = sum_j p_j value_scale_j value_code_j,        lse[i, h] = log sum_j exp(s_j)
+ * Codes are exact in the query's dtype; products accumulate in float32; maxima, sums and outputs are
+ * float32 until one rounding to the output's dtype; the weights p_j value_scale_j are rounded to the
+ * dtype for the second product.  A query that sees no token gets zeros and lse = -infinity.  Rows past
+ * len may hold anything: they reach no result.  A token that a sequence's last query sees and an
+ * earlier one does not has weight 0 for the earlier one, so a NaN among its value codes makes that
+ * query's output NaN too (its scales do not reach it).
+ *
+ * query          [T, heads, D], F16 or BF16, D 64, 128 or 256, heads a multiple of Nk, unit inner
+ *                stride, rows on 16-byte boundaries, any non-negative strides.
+ * key_cache, value_cache    [pages, pageSize, Nk, D], I8 or E4M3, one of the two; unit inner stride,
+ *                rows on 16-byte boundaries, a token's stride below 2^24; any pageSize.
+ * key_scales, value_scales  F32 [pages, blocks, Nk], any non-negative strides; blocks divides pageSize.
+ * page_table, seq_lens, query_offsets, out [T, heads, D], lse, scale and workspace: as in
+ *                rope_latent_attention_paged (pages out of range are clamped), the workspace of at
+ *                least rope_attention_paged_q8_workspace() bytes.
+ * Results do not depend on timing: every sum is taken in a fixed order.
+ */
+int64_t rope_attention_paged_q8_workspace(int64_t num_tokens, int64_t num_heads,
+                                          int64_t num_key_heads, int64_t head_size,
+                                          int64_t num_sequences);
+int rope_attention_paged_q8(const rope_tensor *query, const rope_tensor *key_cache,
+                            const rope_tensor *value_cache, const rope_tensor *key_scales,
+                            const rope_tensor *value_scales, const rope_tensor *page_table,
+                            const rope_tensor *seq_lens, const rope_tensor *query_offsets,
+                            double scale, const rope_tensor *out, const rope_tensor *lse,
+                            void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Text describing the last failing call on the calling thread ("" if none).  The pointer
  * stays valid until the next call on this thread. */

@@ -111,6 +111,11 @@ def _load() -> ctypes.CDLL:
     lib.rope_append_paged_cache_q8.argtypes = [T] * 8 + [ctypes.c_int64, ctypes.c_int64,
                                                          ctypes.c_int] + [T] * 5 + [ctypes.c_void_p]
     lib.rope_append_paged_cache_q8.restype = ctypes.c_int
+    lib.rope_attention_paged_q8_workspace.argtypes = [ctypes.c_int64] * 5
+    lib.rope_attention_paged_q8_workspace.restype = ctypes.c_int64
+    lib.rope_attention_paged_q8.argtypes = [T] * 8 + [ctypes.c_double, T, T, ctypes.c_void_p,
+                                                      ctypes.c_int64, ctypes.c_void_p]
+    lib.rope_attention_paged_q8.restype = ctypes.c_int
     lib.rope_last_error.argtypes = []
     lib.rope_last_error.restype = ctypes.c_char_p
     return lib
@@ -588,6 +593,38 @@ def rope_append_paged_cache_q8(positions, key, value, key_cache, value_cache, ke
             _pack(query_out), _pack(key_cache), _pack(value_cache), _pack(key_scales),
             _pack(value_scales), _raw_stream(stream, dev))
     return query_out
+
+
+def rope_attention_paged_q8(query, key_cache, value_cache, key_scales, value_scales, page_table,
+                            seq_lens, scale: float, query_offsets=None, out=None, lse=None,
+                            stream=None):
+    """Grouped-query attention over a paged cache of 8-bit codes: query [T, heads, D] (float16 or
+    bfloat16, D 64, 128 or 256) against key_cache and value_cache [pages, pageSize, Nk, D] (int8 or
+    float8_e4m3fn) with float32 scales [pages, blocks, Nk]; query head h reads key head
+    h // (heads // Nk).  page_table [B, maxPages], seq_lens [B] (the queries' own tokens included) and
+    query_offsets [B + 1] are int64; without offsets every sequence has T / B queries.  Query i of n
+    sees the cached tokens below seq_len - n + 1 + i.  Returns (out [T, heads, D], lse [T, heads]
+    float32); rows outside all sequences are not written, so pass out and lse where they are to be
+    defined."""
+    import torch
+    dev = _device_index((query, key_cache, value_cache, key_scales, value_scales, page_table,
+                         seq_lens, query_offsets, out, lse))
+    if query.dim() != 3 or key_cache.dim() != 4 or seq_lens.dim() != 1:
+        raise RopeError(ROPE_ERR_PARAM_INVALID,
+                        "query must be 3-D, key_cache 4-D and seq_lens 1-D")
+    T, heads, width = query.shape
+    need = LIB.rope_attention_paged_q8_workspace(T, heads, key_cache.shape[2], width,
+                                                 seq_lens.shape[0])
+    d = query.device
+    new_out, new_lse, workspace = _new(
+        stream, dev, ((T, heads, width), query.dtype, d) if out is None else None,
+        ((T, heads), torch.float32, d) if lse is None else None, (need, torch.uint8, d))
+    out, lse = out if new_out is None else new_out, lse if new_lse is None else new_lse
+    _run_on(dev, LIB.rope_attention_paged_q8, _pack(query), _pack(key_cache), _pack(value_cache),
+            _pack(key_scales), _pack(value_scales), _pack(page_table), _pack(seq_lens),
+            _pack(query_offsets), scale, _pack(out), _pack(lse), workspace.data_ptr(), need,
+            _raw_stream(stream, dev))
+    return out, lse
 
 
 class PreparedCall:
