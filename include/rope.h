@@ -22,6 +22,10 @@
  *                                  keys and values to a paged cache of 8-bit codes with a scale
  *                                  for each block of tokens and head
  *   rope_attention_paged_q8        grouped-query attention over that cache
+ *   rope_copy_pages                copies listed pages of any number of caches
+ *   rope_fork_pages                the page tables, holds and copies of a batch whose sequences
+ *                                  continue those of another (beams, samples, sequences that end)
+ *   rope_compact_pages             moves the pages in use to the lowest numbers
  *
  * Pages defining the operations:
  *   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码
@@ -425,6 +429,84 @@ int rope_attention_paged_q8(const rope_tensor *query, const rope_tensor *key_cac
                             const rope_tensor *seq_lens, const rope_tensor *query_offsets,
                             double scale, const rope_tensor *out, const rope_tensor *lse,
                             void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rope_copy_pages -- page targets[i] of every cache becomes a copy of its page sources[i].
+ *
+ * caches         num_caches descriptions [pages, ...] of 1 to 4 dims and any of the dtypes, all of the
+ *                same number of pages: the keys, values and scales of all layers.  A page has to be
+ *                one dense block of memory, its dimensions in any order, pages any stride apart.
+ * sources, targets   INT64 [N], any non-negative stride.  A pair with a number outside [0, pages) is
+ *                skipped (padding).  Targets in range have to be distinct, and no target the source
+ *                of another pair -- preconditions that are not checked: such pages end up with parts
+ *                of either.
+ */
+int rope_copy_pages(const rope_tensor *sources, const rope_tensor *targets,
+                    const rope_tensor *caches, int64_t num_caches, void *stream);
+
+/*
+ * rope_fork_pages -- the next step's sequences continue this step's.
+ *
+ * New row i continues sequence p = parents[i] with all its seq_lens[p] tokens, and is to take grow[i]
+ * tokens more.  Sequences that no row continues end.  ref_counts[page] is the number of holds on a
+ * page: the rows of page_table that list it, and any others (a cache of shared beginnings may hold
+ * pages too); pages without holds are free.
+ *   - Full pages are shared.  A last page that is not full goes to the first row that continues its
+ *     sequence if it has no other hold (ref_counts 1 or less); every other such row gets a copy of
+ *     its tokens in a new page, in all caches.
+ *   - New pages are taken for grow[i] tokens.
+ *   - New pages are the lowest numbers with ref_counts 0, dealt to the rows in order, to a row its
+ *     copied page first.  Pages that this call frees are free for the next one.
+ *   - page_table_out[i] lists the row's pages, then -1; seq_lens_out[i] = seq_lens[p] + grow[i];
+ *     ref_counts_out are the holds afterwards.  All of a row's tokens have to fit page_table_out:
+ *     grow is cut there.
+ *   - shortage[0] is the number of pages that were wanted and not there; -1 stands for them in
+ *     page_table_out, and where it is not 0, rows with such an entry cannot go on.
+ * The sequences of one batch may be freed, forked, reordered and extended by one call, without the
+ * host's knowing their lengths.
+ *
+ * page_table     INT64 [B, maxPages]; seq_lens INT64 [B], clamped to [0, maxPages * pageSize].
+ *                Entries in use outside [0, pages) stay and count nowhere.
+ * parents        INT64 [R]; outside [0, B): an empty row of length 0.     grow  INT64 [R] or NULL (0);
+ *                below 0: 0.
+ * ref_counts     INT64 [pages];  page_size: tokens of a page.
+ * caches         as in rope_copy_pages, num_caches may be 0.  Of a cache [pages, n, ...] whose second
+ *                dimension is the outermost of a page and n divides page_size or the reverse (rows, or
+ *                blocks of rows), only the part that holds the copied tokens is written; of others the
+ *                whole page.
+ * page_table_out INT64 [R, any], seq_lens_out INT64 [R], shortage INT64 [1]: apart from all inputs.
+ * ref_counts_out INT64 [pages], may be ref_counts itself.
+ * workspace      at least rope_fork_pages_workspace() bytes, under the rules of
+ *                rope_latent_attention_paged's.
+ */
+int64_t rope_fork_pages_workspace(int64_t num_sequences, int64_t num_rows, int64_t num_pages);
+int rope_fork_pages(const rope_tensor *page_table, const rope_tensor *seq_lens,
+                    const rope_tensor *parents, const rope_tensor *grow,
+                    const rope_tensor *ref_counts, int64_t page_size, const rope_tensor *caches,
+                    int64_t num_caches, const rope_tensor *page_table_out,
+                    const rope_tensor *seq_lens_out, const rope_tensor *ref_counts_out,
+                    const rope_tensor *shortage, void *workspace, int64_t workspace_bytes,
+                    void *stream);
+
+/*
+ * rope_compact_pages -- the pages in use (ref_counts above 0) become pages 0 to live - 1.
+ *
+ * The k-th page in use from number `live` on moves, in all caches, to the k-th free page below it.
+ * page_map[page] is the new number of a page in use and -1 of a free one; page_table_out[b, j] is
+ * page_map of the entry (entries outside [0, pages) stay); ref_counts_out are the holds under the new
+ * numbers; live[0] the number of pages in use.  What the moved pages held before stays in their old
+ * places, now free.
+ *
+ * page_table     INT64 [B, maxPages], page_table_out the same shape; it may be page_table itself.
+ * ref_counts, ref_counts_out INT64 [pages], the latter may be ref_counts itself; page_map INT64
+ * [pages], live INT64 [1].  caches as in rope_copy_pages, num_caches may be 0.
+ */
+int64_t rope_compact_pages_workspace(int64_t num_pages);
+int rope_compact_pages(const rope_tensor *page_table, const rope_tensor *ref_counts,
+                       const rope_tensor *caches, int64_t num_caches,
+                       const rope_tensor *page_table_out, const rope_tensor *ref_counts_out,
+                       const rope_tensor *page_map, const rope_tensor *live, void *workspace,
+                       int64_t workspace_bytes, void *stream);
 
 /* Text describing the last failing call on the calling thread ("" if none).  The pointer
  * stays valid until the next call on this thread. */

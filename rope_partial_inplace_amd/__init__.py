@@ -116,6 +116,18 @@ def _load() -> ctypes.CDLL:
     lib.rope_attention_paged_q8.argtypes = [T] * 8 + [ctypes.c_double, T, T, ctypes.c_void_p,
                                                       ctypes.c_int64, ctypes.c_void_p]
     lib.rope_attention_paged_q8.restype = ctypes.c_int
+    lists = [T, ctypes.c_int64]  # caches, their number
+    memory = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]  # workspace, bytes, stream
+    lib.rope_copy_pages.argtypes = [T, T, *lists, ctypes.c_void_p]
+    lib.rope_copy_pages.restype = ctypes.c_int
+    lib.rope_fork_pages_workspace.argtypes = [ctypes.c_int64] * 3
+    lib.rope_fork_pages_workspace.restype = ctypes.c_int64
+    lib.rope_fork_pages.argtypes = [T] * 5 + [ctypes.c_int64, *lists] + [T] * 4 + memory
+    lib.rope_fork_pages.restype = ctypes.c_int
+    lib.rope_compact_pages_workspace.argtypes = [ctypes.c_int64]
+    lib.rope_compact_pages_workspace.restype = ctypes.c_int64
+    lib.rope_compact_pages.argtypes = [T, T, *lists] + [T] * 4 + memory
+    lib.rope_compact_pages.restype = ctypes.c_int
     lib.rope_last_error.argtypes = []
     lib.rope_last_error.restype = ctypes.c_char_p
     return lib
@@ -625,6 +637,96 @@ def rope_attention_paged_q8(query, key_cache, value_cache, key_scales, value_sca
             _pack(query_offsets), scale, _pack(out), _pack(lse), workspace.data_ptr(), need,
             _raw_stream(stream, dev))
     return out, lse
+
+
+# ---- pages of a cache ------------------------------------------------------------------------------
+
+class PageCaches:
+    """The caches of all layers, described once: a program that copies, forks or compacts pages at
+    every step makes one of its list (keys, values and scales, [pages, ...] each) and passes it in the
+    list's place.  The tensors must keep their storage while the object is used."""
+
+    def __init__(self, caches):
+        self.tensors = list(caches)
+        self.device = _device_index(self.tensors)
+        self.packed = b"".join(map(_pack, self.tensors)) or None
+
+
+def _page_caches(caches, dev: int):
+    """(PageCaches, device): the list described, on the device of the other tensors."""
+    if not isinstance(caches, PageCaches):
+        caches = PageCaches(caches)
+    if dev >= 0 and caches.device >= 0 and dev != caches.device:
+        raise RopeError(ROPE_ERR_PARAM_INVALID, "tensors are on different devices")
+    return caches, max(dev, caches.device)
+
+
+def rope_copy_pages(sources, targets, caches, stream=None):
+    """Copy pages: page targets[i] of every cache becomes a copy of page sources[i] (int64 [N]); a pair
+    with a number out of range is skipped.  Targets have to be distinct, and none the source of another
+    pair.  caches: tensors [pages, ...] whose pages are dense blocks, or a PageCaches of them."""
+    caches, dev = _page_caches(caches, _device_index((sources, targets)))
+    _run_on(dev, LIB.rope_copy_pages, _pack(sources), _pack(targets), caches.packed,
+            len(caches.tensors), _raw_stream(stream, dev))
+
+
+def rope_fork_pages(page_table, seq_lens, parents, ref_counts, page_size: int, caches=(),
+                    grow=None, page_table_out=None, seq_lens_out=None, ref_counts_out=None,
+                    shortage=None, stream=None):
+    """The next step's sequences continue this step's: new row i has all seq_lens[parents[i]] tokens of
+    sequence parents[i] (an empty row where that is out of range) and room for grow[i] more.  Full pages
+    are shared, a last page that is not full is copied in all caches for every row but the first that
+    continues its sequence (for that one, too, if something else holds the page), and new pages are the
+    lowest with ref_counts 0.  Sequences without a row end.  All index tensors are int64: page_table
+    [B, maxPages], seq_lens [B], parents and grow [R], ref_counts [pages] (holds on each page).  Returns
+    (page_table_out [R, maxPages], seq_lens_out [R], ref_counts_out [pages], shortage [1]), allocated
+    where not given; ref_counts_out may be ref_counts itself, page_table_out may be wider.  shortage is
+    the number of pages that were wanted and not free; -1 stands for them in page_table_out."""
+    import torch
+    caches, dev = _page_caches(caches, _device_index((page_table, seq_lens, parents, ref_counts, grow,
+                                                      page_table_out, seq_lens_out, ref_counts_out,
+                                                      shortage)))
+    if page_table.dim() != 2 or parents.dim() != 1 or ref_counts.dim() != 1:
+        raise RopeError(ROPE_ERR_PARAM_INVALID,
+                        "page_table must be 2-D, parents and ref_counts 1-D")
+    rows, pages, d, i64 = parents.shape[0], ref_counts.shape[0], page_table.device, torch.int64
+    need = LIB.rope_fork_pages_workspace(page_table.shape[0], rows, pages)
+    given = (page_table_out, seq_lens_out, ref_counts_out, shortage)
+    shapes = ((rows, page_table.shape[1]), (rows,), (pages,), (1,))
+    *new, workspace = _new(stream, dev, *((s, i64, d) if g is None else None
+                                          for g, s in zip(given, shapes)),
+                           (need, torch.uint8, d))
+    outs = tuple(g if n is None else n for g, n in zip(given, new))
+    _run_on(dev, LIB.rope_fork_pages, _pack(page_table), _pack(seq_lens), _pack(parents),
+            _pack(grow), _pack(ref_counts), page_size, caches.packed, len(caches.tensors),
+            *map(_pack, outs), workspace.data_ptr(), need, _raw_stream(stream, dev))
+    return outs
+
+
+def rope_compact_pages(page_table, ref_counts, caches=(), page_table_out=None, ref_counts_out=None,
+                       page_map=None, live=None, stream=None):
+    """The pages in use (ref_counts above 0) move, in all caches, to the lowest numbers: the k-th one
+    from number `live` on to the k-th free page below.  Returns (page_table_out, ref_counts_out,
+    page_map, live): the table and the holds under the new numbers, page_map [pages] with the new
+    number of every page in use and -1 for the others, live [1] the number of pages in use; all int64,
+    allocated where not given.  page_table_out may be page_table and ref_counts_out ref_counts."""
+    import torch
+    caches, dev = _page_caches(caches, _device_index((page_table, ref_counts, page_table_out,
+                                                      ref_counts_out, page_map, live)))
+    if ref_counts.dim() != 1:
+        raise RopeError(ROPE_ERR_PARAM_INVALID, "ref_counts must be 1-D")
+    pages, d, i64 = ref_counts.shape[0], ref_counts.device, torch.int64
+    need = LIB.rope_compact_pages_workspace(pages)
+    given = (page_table_out, ref_counts_out, page_map, live)
+    shapes = (page_table.shape, (pages,), (pages,), (1,))
+    *new, workspace = _new(stream, dev, *((s, i64, d) if g is None else None
+                                          for g, s in zip(given, shapes)),
+                           (need, torch.uint8, d))
+    outs = tuple(g if n is None else n for g, n in zip(given, new))
+    _run_on(dev, LIB.rope_compact_pages, _pack(page_table), _pack(ref_counts), caches.packed,
+            len(caches.tensors), *map(_pack, outs), workspace.data_ptr(), need,
+            _raw_stream(stream, dev))
+    return outs
 
 
 class PreparedCall:

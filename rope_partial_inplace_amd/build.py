@@ -22,15 +22,16 @@ LIB_PATH = os.path.join(HERE, "librope_amd.so")
 ARCH = "gfx950"
 
 HOST_SOURCES = [os.path.join(CSRC, n) for n in
-                ("rope_plan.cpp", "rope_append_plan.cpp", "rope_latent_plan.cpp", "rope_q8_plan.cpp")]
+                ("rope_plan.cpp", "rope_append_plan.cpp", "rope_latent_plan.cpp", "rope_q8_plan.cpp",
+                 "rope_pages_plan.cpp")]
 KERNEL_SOURCES = [os.path.join(CSRC, n) for n in
                   ("rope_kernels.hip", "rope_append.hip", "rope_latent_paged.hip",
                    "rope_latent_attn.hip", "rope_q8_append.hip",
-                   "rope_q8_attn_bf16.hip", "rope_q8_attn_f16.hip")]
+                   "rope_q8_attn_bf16.hip", "rope_q8_attn_f16.hip", "rope_pages.hip")]
 HEADERS = [os.path.join(CSRC, n) for n in
            ("rope_plan.h", "rope_append_plan.h", "rope_latent_plan.h", "rope_check.h", "rope_io.h",
             "rope_launch.h", "rope_mfma.h", "rope_q8_plan.h", "rope_q8.h",
-            "rope_q8_attn.h")]
+            "rope_q8_attn.h", "rope_pages_plan.h")]
 SOURCES = HOST_SOURCES + KERNEL_SOURCES
 # Everything the library is built from; its digest is written beside the library (STAMP_PATH)
 # so that a library older than its sources is noticed before it is tested.

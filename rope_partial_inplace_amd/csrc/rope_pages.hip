@@ -1,0 +1,527 @@
+// rope_pages.hip -- copying, forking and compacting the pages of a cache (gfx950).
+//
+// Copy: page targets[i] of every cache becomes a copy of page sources[i].
+//
+// Fork: new row i continues sequence parents[i].  Full pages are shared; the last page, if it is not
+// full, goes to the first row that continues the sequence when nothing else holds it, and is copied
+// to a new page for the others; new pages are taken for the tokens to come.  New pages are the lowest
+// free ones, dealt in the order of the rows, so the result does not depend on timing: ranks are sums
+// over the rows and over the pages before.  Pages that this call frees are not handed out by it: none
+// of them can then be read by one copy and written by another.
+//   1. one workgroup: which row continues a sequence first, what each row wants, and the sums of
+//      that; the others count the free pages of 4096 each
+//   2. the free pages' numbers, as many as are wanted; the holds as they were
+//   3. tables, holds and copies
+//
+// Compact: with n pages in use, the k-th one at or behind place n goes to the k-th free place before.
+//   1. pages in use of 4096 each; 2. the map and the list of moves; 3. tables, holds and copies
+//
+// All of it moves bytes.  A copy's words of all caches and pages are numbered through, 1024 of them a
+// workgroup, so that small caches (scales) and large ones fill the card alike.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <string>
+#include <vector>
+
+#include "rope.h"
+#include "rope_launch.h"
+#include "rope_pages_plan.h"
+#include "rope_q8.h"
+
+namespace ropeamd {
+namespace {
+
+constexpr int64_t kUnit = int64_t(kPageBlock) * kPageWords;  // words of a workgroup at a time
+constexpr int64_t kCopyGroups = 2048;  // workgroups where the host does not know the copies
+
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+typedef uint32_t words2 __attribute__((ext_vector_type(2)));
+
+// What to copy: pages `from` to `to`, the first `tokens` of page_size tokens (0: whole pages).
+struct Move {
+  int64_t from, to, tokens;
+};
+
+__device__ inline int64_t wave_sum_before(int64_t x, int64_t *total) {
+  const int lane = int(threadIdx.x) & 63;
+  int64_t incl = x;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t y = __shfl_up(incl, d);
+    if (lane >= d) incl += y;
+  }
+  *total = __shfl(incl, 63);
+  return incl - x;
+}
+
+// Words v, v + kPageBlock, .. of a cache's moves, W bytes each.
+template <typename W, typename Moves>
+__device__ inline void copy_words(const PageCache &c, int64_t v, int64_t all, bool small,
+                                  int64_t num_pages, int64_t page_size, Moves moves) {
+  W word[kPageWords];
+  W *to[kPageWords];
+#pragma unroll
+  for (int k = 0; k < kPageWords; ++k) {
+    to[k] = nullptr;
+    const int64_t at = v + int64_t(k) * kPageBlock;
+    if (at >= all) continue;
+    const int64_t i = small ? int64_t(div_by(c.div_vecs, uint32_t(at))) : at / c.vecs;
+    const uint32_t word_of = uint32_t(at - i * c.vecs);
+    const Move m = moves(i);
+    bool wanted = m.from >= 0 && m.from < num_pages && m.to >= 0 && m.to < num_pages;
+    if (m.tokens > 0 && c.parts != 0) {  // the parts that hold them, the last one whole
+      const int64_t parts = (m.tokens * c.parts + page_size - 1) / page_size;
+      wanted &= word_of < uint64_t(parts) * c.part_words;
+    }
+    if (!wanted) continue;
+    const int64_t off = int64_t(word_of) * int64_t(sizeof(W));
+    word[k] = __builtin_nontemporal_load(reinterpret_cast<const W *>(c.base + m.from * c.page + off));
+    to[k] = reinterpret_cast<W *>(c.base + m.to * c.page + off);
+  }
+#pragma unroll
+  for (int k = 0; k < kPageWords; ++k)
+    if (to[k] != nullptr) __builtin_nontemporal_store(word[k], to[k]);
+}
+
+// All words of `count` moves in all caches, shared by `groups` workgroups, of which this is `group`.
+template <typename Moves>
+__device__ inline void copy_pages(const PageCaches &p, int64_t count, int64_t group, int64_t groups,
+                                  int64_t num_pages, int64_t page_size, Moves moves) {
+  const int lane = int(threadIdx.x) & 63;
+  const int64_t words = lane < p.count ? count * p.cache[lane].vecs : 0;
+  int64_t total;
+  const int64_t before = wave_sum_before((words + kUnit - 1) / kUnit, &total);
+  for (int64_t u = group; u < total; u += groups) {
+    // the last cache whose units begin at or before u
+    const int t = 63 - __builtin_clzll(__ballot(lane < p.count && before <= u) | 1ull);
+    const int64_t begin = __shfl(before, t);
+    const PageCache &c = p.cache[__builtin_amdgcn_readfirstlane(t)];
+    const int64_t all = count * c.vecs, v = (u - begin) * kUnit + threadIdx.x;
+    const bool small = all + kUnit < (int64_t(1) << 32);
+    switch (c.width) {
+      case 4: copy_words<words4>(c, v, all, small, num_pages, page_size, moves); break;
+      case 3: copy_words<words2>(c, v, all, small, num_pages, page_size, moves); break;
+      case 2: copy_words<uint32_t>(c, v, all, small, num_pages, page_size, moves); break;
+      case 1: copy_words<uint16_t>(c, v, all, small, num_pages, page_size, moves); break;
+      default: copy_words<uint8_t>(c, v, all, small, num_pages, page_size, moves); break;
+    }
+  }
+}
+
+__global__ __launch_bounds__(kPageBlock) void copy_pages_kernel(CopyPagesPlan p) {
+  copy_pages(p.caches, p.moves, blockIdx.x, gridDim.x, p.num_pages, 1, [&](int64_t i) {
+    return Move{p.sources[i * p.source_stride], p.targets[i * p.target_stride], 0};
+  });
+}
+
+// ---- counting over a workgroup of 1024 -------------------------------------------------------------
+// Sum of x over the threads before this one, and over all.
+__device__ inline int64_t scan_block(int64_t x, int64_t *lds, int64_t *total) {
+  const int wave = int(threadIdx.x) >> 6, lane = int(threadIdx.x) & 63;
+  int64_t sum;
+  const int64_t before = wave_sum_before(x, &sum);
+  __syncthreads();
+  if (lane == 0) lds[wave] = sum;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int v = 0; v < kCountBlock / 64; ++v) {
+    if (v < wave) base += lds[v];
+    all += lds[v];
+  }
+  *total = all;
+  return base + before;
+}
+
+constexpr int kPerThread = int(kPageChunk) / kCountBlock;
+
+// How many of this thread's pages of a chunk (kPerThread neighbours) below `end` have (USED) or
+// have no (!USED) holds; bit k of the flags: page k.
+template <bool USED>
+__device__ inline int32_t chunk_flags(const int64_t *refs, int64_t stride, int64_t chunk,
+                                      int64_t end, uint32_t *flags) {
+  *flags = 0;
+  const int64_t first = chunk * kPageChunk + int64_t(threadIdx.x) * kPerThread;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k)
+    if (first + k < end && (refs[(first + k) * stride] > 0) == USED) *flags |= 1u << k;
+  return __popc(*flags);
+}
+
+// Sum of the chunks' counts before `chunk`, and of all.
+__device__ inline int64_t chunks_before(const int32_t *counts, int64_t chunks, int64_t chunk,
+                                        int64_t *lds, int64_t *total) {
+  int64_t before = 0, all = 0, sum;
+  for (int64_t i = threadIdx.x; i < chunks; i += kCountBlock) {
+    all += counts[i];
+    if (i < chunk) before += counts[i];
+  }
+  scan_block(before, lds, &sum);
+  scan_block(all, lds, total);
+  return sum;
+}
+
+// ---- fork ------------------------------------------------------------------------------------------
+__device__ inline int64_t clamped_len(const ForkPlan &p, int64_t b) {
+  return min(max(p.lens[b * p.len_stride], int64_t(0)), p.table.width * p.page_size);
+}
+
+__device__ inline int64_t pages_of(const ForkPlan &p, int64_t tokens) {
+  return int64_t((uint32_t(tokens) + uint32_t(p.page_size) - 1) / uint32_t(p.page_size));
+}
+
+// What row i continues and how long it gets.
+struct Row {
+  int64_t parent, len, grown;  // parent -1: an empty row
+};
+
+__device__ inline Row row_of(const ForkPlan &p, int64_t i) {
+  Row r = {p.parents[i * p.parent_stride], 0, 0};
+  if (r.parent < 0 || r.parent >= p.table.rows) return {-1, 0, 0};
+  r.len = clamped_len(p, r.parent);
+  const int64_t g = p.grow != nullptr ? max(p.grow[i * p.grow_stride], int64_t(0)) : 0;
+  r.grown = r.len + min(g, p.out.width * p.page_size - r.len);
+  return r;
+}
+
+template <typename X>
+__device__ inline X fresh(const X *p) {  // as the other threads' atomics left it
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__global__ __launch_bounds__(kCountBlock) void fork_count_kernel(ForkPlan p) {
+  __shared__ int64_t lds[kCountBlock / 64];
+  const int64_t B = p.table.rows, R = p.out.rows;
+  int64_t sum;
+  if (blockIdx.x > 0) {
+    const int64_t chunk = int64_t(blockIdx.x) - 1;
+    uint32_t flags;
+    const int32_t n = chunk_flags<false>(p.refs, p.ref_stride, chunk, p.num_pages, &flags);
+    scan_block(n, lds, &sum);
+    if (threadIdx.x == 0) p.counts[chunk] = int32_t(sum);
+    return;
+  }
+  for (int64_t b = threadIdx.x; b < B; b += kCountBlock) {
+    __hip_atomic_store(&p.first[b], 0x7fffffff, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(&p.children[b], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    p.kept[b] = 0;
+  }
+  __threadfence();
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < R; i += kCountBlock) {
+    const int64_t b = p.parents[i * p.parent_stride];
+    if (b < 0 || b >= B) continue;
+    atomicMin(&p.first[b], int32_t(i));
+    atomicAdd(&p.children[b], 1);
+  }
+  __threadfence();
+  __syncthreads();
+  int64_t wanted = 0, copies = 0;
+  for (int64_t i0 = 0; i0 < R; i0 += kCountBlock) {
+    const int64_t i = i0 + threadIdx.x;
+    int64_t need = 0, last = -1;
+    Row r = {-1, 0, 0};
+    bool copy = false;
+    if (i < R) r = row_of(p, i);
+    if (r.parent >= 0) {
+      const int64_t used = pages_of(p, r.len);
+      need = pages_of(p, r.grown) - used;
+      if (r.len % p.page_size != 0) {
+        last = p.table.data[r.parent * p.table.row + (used - 1) * p.table.col];
+        if (last >= 0 && last < p.num_pages) {
+          const bool keep = fresh(&p.first[r.parent]) == i && p.refs[last * p.ref_stride] <= 1;
+          if (keep) p.kept[r.parent] = 1;
+          copy = !keep;
+          need += copy;
+        }
+      }
+    }
+    int64_t all;
+    const int64_t base = wanted + scan_block(need, lds, &all);
+    wanted += all;
+    const int64_t k = copies + scan_block(copy, lds, &all);
+    copies += all;
+    if (i < R) p.base[i] = base;
+    if (copy) {
+      p.copies[3 * k] = last;
+      p.copies[3 * k + 1] = base;
+      p.copies[3 * k + 2] = r.len % p.page_size;
+    }
+  }
+  if (threadIdx.x == 0) {
+    p.totals[0] = wanted;
+    p.totals[1] = copies;
+  }
+}
+
+__global__ __launch_bounds__(kCountBlock) void fork_free_kernel(ForkPlan p) {
+  __shared__ int64_t lds[kCountBlock / 64];
+  const int64_t chunk = blockIdx.x, wanted = p.totals[0];
+  int64_t total, sum;
+  int64_t rank = chunks_before(p.counts, p.chunks, chunk, lds, &total);
+  if (chunk == 0 && threadIdx.x == 0) {
+    p.totals[2] = total;
+    p.shortage[0] = max(wanted - total, int64_t(0));
+  }
+  if (chunk >= p.chunks) return;  // no pages at all
+  uint32_t flags;
+  const int32_t n = chunk_flags<false>(p.refs, p.ref_stride, chunk, p.num_pages, &flags);
+  rank += scan_block(n, lds, &sum);
+  const int64_t first = chunk * kPageChunk + int64_t(threadIdx.x) * kPerThread;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    if (first + k >= p.num_pages) break;
+    if (flags >> k & 1u) {
+      if (rank < wanted) p.free[rank] = int32_t(first + k);
+      ++rank;
+    }
+    p.refs_out[(first + k) * p.ref_out_stride] = p.refs[(first + k) * p.ref_stride];
+  }
+}
+
+__device__ inline int64_t new_page(const ForkPlan &p, int64_t rank) {
+  return rank < p.totals[2] ? int64_t(p.free[rank]) : -1;
+}
+
+__device__ inline void add_holds(const ForkPlan &p, int64_t page, int64_t n) {
+  if (n != 0 && page >= 0 && page < p.num_pages)
+    atomicAdd(reinterpret_cast<unsigned long long *>(p.refs_out + page * p.ref_out_stride),
+              static_cast<unsigned long long>(n));  // modulo 2^64: n may be negative
+}
+
+__device__ inline void fork_tables(const ForkPlan &p, int64_t at, int64_t step) {
+  const int64_t wide = max(p.out.width, int64_t(1));
+  for (int64_t e = at; e < p.out.rows * wide; e += step) {
+    const int64_t i = e / wide, j = e - i * wide;
+    const Row r = row_of(p, i);
+    if (j == 0) p.lens_out[i * p.len_out_stride] = r.grown;
+    if (j >= p.out.width) continue;
+    int64_t page = -1;
+    const int64_t used = pages_of(p, r.len);
+    if (j < pages_of(p, r.grown)) {
+      const int64_t *from = p.table.data + r.parent * p.table.row;
+      int64_t own = used;  // the row's first new page
+      if (r.len % p.page_size != 0) {
+        const int64_t last = from[(used - 1) * p.table.col];
+        if (last >= 0 && last < p.num_pages &&
+            !(p.first[r.parent] == i && p.kept[r.parent] != 0))
+          own = used - 1;
+      }
+      if (j < own) {
+        page = from[j * p.table.col];
+      } else {
+        page = new_page(p, p.base[i] + (j - own));
+        add_holds(p, page, 1);
+      }
+    }
+    p.out.data[i * p.out.row + j * p.out.col] = page;
+  }
+  // holds of the sequences: full pages go on once for every row, the last one if a row keeps it
+  for (int64_t e = at; e < p.table.rows * p.table.width; e += step) {
+    const int64_t b = e / p.table.width, j = e - b * p.table.width;
+    const int64_t len = clamped_len(p, b), held = pages_of(p, len);
+    if (j >= held) continue;
+    const int64_t page = p.table.data[b * p.table.row + j * p.table.col];
+    const bool tail = j == held - 1 && len % p.page_size != 0;
+    add_holds(p, page, (tail ? p.kept[b] : p.children[b]) - 1);
+  }
+}
+
+__global__ __launch_bounds__(kPageBlock) void fork_write_kernel(ForkPlan p) {
+  const int64_t block = blockIdx.x;
+  if (block < p.table_blocks) {
+    fork_tables(p, block * kPageBlock + threadIdx.x, p.table_blocks * kPageBlock);
+    return;
+  }
+  copy_pages(p.caches, p.totals[1], block - p.table_blocks, gridDim.x - p.table_blocks, p.num_pages,
+             p.page_size, [&](int64_t i) {
+               const int64_t *c = p.copies + 3 * i;
+               return Move{c[0], new_page(p, c[1]), c[2]};
+             });
+}
+
+// ---- compact ---------------------------------------------------------------------------------------
+__global__ __launch_bounds__(kCountBlock) void compact_count_kernel(CompactPlan p) {
+  __shared__ int64_t lds[kCountBlock / 64];
+  uint32_t flags;
+  int64_t sum;
+  scan_block(chunk_flags<true>(p.refs, p.ref_stride, blockIdx.x, p.num_pages, &flags), lds, &sum);
+  if (threadIdx.x == 0) p.counts[blockIdx.x] = int32_t(sum);
+}
+
+__global__ __launch_bounds__(kCountBlock) void compact_map_kernel(CompactPlan p) {
+  __shared__ int64_t lds[kCountBlock / 64];
+  const int64_t chunk = blockIdx.x;
+  int64_t n, sum, below;
+  uint32_t flags;
+  int64_t rank = chunks_before(p.counts, p.chunks, chunk, lds, &n);
+  // pages in use before place n: of the whole chunks before it, and of its own
+  const int64_t border = n / kPageChunk;
+  const int64_t whole = chunks_before(p.counts, p.chunks, border, lds, &sum);
+  scan_block(chunk_flags<true>(p.refs, p.ref_stride, border, min(n, p.num_pages), &flags), lds, &below);
+  const int64_t moves = n - whole - below;
+  if (chunk == 0 && threadIdx.x == 0) {
+    p.totals[0] = moves;
+    p.live[0] = n;
+  }
+  if (chunk >= p.chunks) return;  // no pages at all
+  rank += scan_block(chunk_flags<true>(p.refs, p.ref_stride, chunk, p.num_pages, &flags), lds, &sum);
+  const int64_t first = chunk * kPageChunk + int64_t(threadIdx.x) * kPerThread;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int64_t page = first + k;
+    if (page >= p.num_pages) break;
+    const bool used = flags >> k & 1u;
+    if (used && page >= n) p.moves[2 * (rank - (n - moves))] = page;
+    if (!used && page < n) p.moves[2 * (page - rank) + 1] = page;
+    // a moved page's entry: the number of its move, until the next launch has its place
+    p.map[page * p.map_stride] = !used ? -1 : page < n ? page : -2 - (rank - (n - moves));
+    p.refs_out[page * p.ref_out_stride] = p.refs[page * p.ref_stride];
+    rank += used;
+  }
+}
+
+// A page's new number from its map entry: below -1 the number of its move (launch 2), or the new number
+// already (another thread of launch 3 may have written it).
+__device__ inline int64_t moved_to(const CompactPlan &p, int64_t entry) {
+  return entry < -1 ? p.moves[2 * (-2 - entry) + 1] : entry;
+}
+
+__device__ inline void compact_tables(const CompactPlan &p, int64_t at, int64_t step) {
+  const int64_t moves = p.totals[0];
+  for (int64_t k = at; k < moves; k += step) {
+    const int64_t from = p.moves[2 * k], to = p.moves[2 * k + 1];
+    __hip_atomic_store(&p.map[from * p.map_stride], to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    p.refs_out[to * p.ref_out_stride] = p.refs_out[from * p.ref_out_stride];
+    p.refs_out[from * p.ref_out_stride] = 0;
+  }
+  for (int64_t e = at; e < p.table.rows * p.table.width; e += step) {
+    const int64_t b = e / p.table.width, j = e - b * p.table.width;
+    int64_t page = p.table.data[b * p.table.row + j * p.table.col];
+    if (page >= 0 && page < p.num_pages) page = moved_to(p, fresh(&p.map[page * p.map_stride]));
+    p.out.data[b * p.out.row + j * p.out.col] = page;
+  }
+}
+
+__global__ __launch_bounds__(kPageBlock) void compact_write_kernel(CompactPlan p) {
+  const int64_t block = blockIdx.x;
+  if (block < p.table_blocks) {
+    compact_tables(p, block * kPageBlock + threadIdx.x, p.table_blocks * kPageBlock);
+    return;
+  }
+  copy_pages(p.caches, p.totals[0], block - p.table_blocks, gridDim.x - p.table_blocks, p.num_pages,
+             1, [&](int64_t i) { return Move{p.moves[2 * i], p.moves[2 * i + 1], 0}; });
+}
+
+// The last launch of a plan: tables, and the copies in the first caches; then the other caches' copies,
+// as many at a time as a launch holds.  `copies`: workgroups for a launch's copies.
+template <typename Plan, typename Groups>
+int run_writes(const void *fn, Plan &p, const std::vector<PageCache> &list, Groups copies,
+               void *stream) {
+  size_t at = 0;
+  do {
+    p.caches.count = int32_t(std::min<size_t>(kPageCaches, list.size() - at));
+    std::copy_n(list.begin() + std::ptrdiff_t(at), p.caches.count, p.caches.cache);
+    at += size_t(p.caches.count);
+    const int64_t blocks = p.table_blocks + (p.caches.count > 0 ? copies(p) : 0);
+    if (blocks > 0) {
+      const int st = launch_kernel(fn, dim3(uint32_t(blocks)), kPageBlock, 0, stream, &p);
+      if (st != ROPE_OK) return st;
+    }
+    p.table_blocks = 0;
+  } while (at < list.size());
+  return ROPE_OK;
+}
+
+}  // namespace
+}  // namespace ropeamd
+
+using namespace ropeamd;
+
+ROPE_API int rope_copy_pages(const rope_tensor *sources, const rope_tensor *targets,
+                             const rope_tensor *caches, int64_t num_caches, void *stream) {
+  CopyPagesPlan p;
+  std::vector<PageCache> list;
+  std::string err;
+  const int st = plan_copy_pages(sources, targets, caches, num_caches, &p, &list, &err);
+  if (st != ROPE_OK) {
+    g_last_error = err;
+    return st;
+  }
+  g_last_error.clear();
+  return run_writes(reinterpret_cast<const void *>(&copy_pages_kernel), p, list,
+                    [](const CopyPagesPlan &q) {
+                      int64_t units = 0;
+                      for (int i = 0; i < q.caches.count; ++i)
+                        units += (q.moves * q.caches.cache[i].vecs + kUnit - 1) / kUnit;
+                      return std::min(units, int64_t(1) << 22);
+                    }, stream);
+}
+
+ROPE_API int64_t rope_fork_pages_workspace(int64_t num_sequences, int64_t num_rows,
+                                           int64_t num_pages) {
+  return fork_workspace(num_sequences, num_rows, num_pages);
+}
+
+ROPE_API int rope_fork_pages(const rope_tensor *page_table, const rope_tensor *seq_lens,
+                             const rope_tensor *parents, const rope_tensor *grow,
+                             const rope_tensor *ref_counts, int64_t page_size,
+                             const rope_tensor *caches, int64_t num_caches,
+                             const rope_tensor *page_table_out, const rope_tensor *seq_lens_out,
+                             const rope_tensor *ref_counts_out, const rope_tensor *shortage,
+                             void *workspace, int64_t workspace_bytes, void *stream) {
+  ForkPlan p;
+  std::vector<PageCache> list;
+  std::string err;
+  int st = plan_fork_pages(page_table, seq_lens, parents, grow, ref_counts, page_size, caches,
+                           num_caches, page_table_out, seq_lens_out, ref_counts_out, shortage,
+                           workspace, workspace_bytes, &p, &list, &err);
+  if (st != ROPE_OK) {
+    g_last_error = err;
+    return st;
+  }
+  g_last_error.clear();
+  st = launch_kernel(reinterpret_cast<const void *>(&fork_count_kernel),
+                     dim3(uint32_t(1 + p.chunks)), kCountBlock, 0, stream, &p);
+  if (st != ROPE_OK) return st;
+  st = launch_kernel(reinterpret_cast<const void *>(&fork_free_kernel),
+                     dim3(uint32_t(std::max<int64_t>(1, p.chunks))), kCountBlock, 0, stream, &p);
+  if (st != ROPE_OK) return st;
+  return run_writes(reinterpret_cast<const void *>(&fork_write_kernel), p, list,
+                    [](const ForkPlan &) { return kCopyGroups; }, stream);
+}
+
+ROPE_API int64_t rope_compact_pages_workspace(int64_t num_pages) {
+  return compact_workspace(num_pages);
+}
+
+ROPE_API int rope_compact_pages(const rope_tensor *page_table, const rope_tensor *ref_counts,
+                                const rope_tensor *caches, int64_t num_caches,
+                                const rope_tensor *page_table_out,
+                                const rope_tensor *ref_counts_out, const rope_tensor *page_map,
+                                const rope_tensor *live, void *workspace, int64_t workspace_bytes,
+                                void *stream) {
+  CompactPlan p;
+  std::vector<PageCache> list;
+  std::string err;
+  int st = plan_compact_pages(page_table, ref_counts, caches, num_caches, page_table_out,
+                              ref_counts_out, page_map, live, workspace, workspace_bytes, &p, &list,
+                              &err);
+  if (st != ROPE_OK) {
+    g_last_error = err;
+    return st;
+  }
+  g_last_error.clear();
+  if (p.chunks > 0) {
+    st = launch_kernel(reinterpret_cast<const void *>(&compact_count_kernel),
+                       dim3(uint32_t(p.chunks)), kCountBlock, 0, stream, &p);
+    if (st != ROPE_OK) return st;
+  }
+  st = launch_kernel(reinterpret_cast<const void *>(&compact_map_kernel),
+                     dim3(uint32_t(std::max<int64_t>(1, p.chunks))), kCountBlock, 0, stream, &p);
+  if (st != ROPE_OK) return st;
+  return run_writes(reinterpret_cast<const void *>(&compact_write_kernel), p, list,
+                    [](const CompactPlan &) { return kCopyGroups; }, stream);
+}
