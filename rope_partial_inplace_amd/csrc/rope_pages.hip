@@ -16,8 +16,7 @@
 // Compact: with n pages in use, the k-th one at or behind place n goes to the k-th free place before.
 //   1. pages in use of 4096 each; 2. the map and the list of moves; 3. tables, holds and copies
 //
-// All of it moves bytes.  A copy's words of all caches and pages are numbered through, 1024 of them a
-// workgroup, so that small caches (scales) and large ones fill the card alike.
+// All of it moves bytes.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -33,11 +32,18 @@
 namespace ropeamd {
 namespace {
 
-constexpr int64_t kUnit = int64_t(kPageBlock) * kPageWords;  // words of a workgroup at a time
-constexpr int64_t kCopyGroups = 2048;  // workgroups where the host does not know the copies
+// Wavefronts at most where the host does not know the copies.
+constexpr int64_t kForkGroups = 8192, kCompactGroups = 65536;
 
 typedef uint32_t words4 __attribute__((ext_vector_type(4)));
 typedef uint32_t words2 __attribute__((ext_vector_type(2)));
+
+// 16 bytes past the caches, from a base that is the same for all lanes: buffer stores with the
+// device-scope and streaming bits.
+__device__ inline void store_streamed(char *base, int offset, words4 v) {
+  const auto buffer = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(0xffffffff), 0x00020000);
+  __builtin_amdgcn_raw_buffer_store_b128(v, buffer, offset, 0, 16 | 2);
+}
 
 // What to copy: pages `from` to `to`, the first `tokens` of page_size tokens (0: whole pages).
 struct Move {
@@ -56,62 +62,92 @@ __device__ inline int64_t wave_sum_before(int64_t x, int64_t *total) {
   return incl - x;
 }
 
-// Words v, v + kPageBlock, .. of a cache's moves, W bytes each.
-template <typename W, typename Moves>
-__device__ inline void copy_words(const PageCache &c, int64_t v, int64_t all, bool small,
-                                  int64_t num_pages, int64_t page_size, Moves moves) {
-  W word[kPageWords];
-  W *to[kPageWords];
-#pragma unroll
-  for (int k = 0; k < kPageWords; ++k) {
-    to[k] = nullptr;
-    const int64_t at = v + int64_t(k) * kPageBlock;
-    if (at >= all) continue;
-    const int64_t i = small ? int64_t(div_by(c.div_vecs, uint32_t(at))) : at / c.vecs;
-    const uint32_t word_of = uint32_t(at - i * c.vecs);
-    const Move m = moves(i);
-    bool wanted = m.from >= 0 && m.from < num_pages && m.to >= 0 && m.to < num_pages;
-    if (m.tokens > 0 && c.parts != 0) {  // the parts that hold them, the last one whole
-      const int64_t parts = (m.tokens * c.parts + page_size - 1) / page_size;
-      wanted &= word_of < uint64_t(parts) * c.part_words;
-    }
-    if (!wanted) continue;
-    const int64_t off = int64_t(word_of) * int64_t(sizeof(W));
-    word[k] = __builtin_nontemporal_load(reinterpret_cast<const W *>(c.base + m.from * c.page + off));
-    to[k] = reinterpret_cast<W *>(c.base + m.to * c.page + off);
-  }
-#pragma unroll
-  for (int k = 0; k < kPageWords; ++k)
-    if (to[k] != nullptr) __builtin_nontemporal_store(word[k], to[k]);
+// How many of a page's words a move takes.
+__device__ inline uint32_t words_of(const PageRun &r, const Move &m, int64_t num_pages,
+                                    int64_t page_size) {
+  if (m.from < 0 || m.from >= num_pages || m.to < 0 || m.to >= num_pages) return 0;
+  if (m.tokens <= 0 || r.parts == 0) return r.vecs;
+  // the parts that hold the tokens, the last one whole
+  return uint32_t((m.tokens * r.parts + page_size - 1) / page_size) * r.part_words;
 }
 
-// All words of `count` moves in all caches, shared by `groups` workgroups, of which this is `group`.
-template <typename Moves>
+// Unit `u` of a run: words of 2^width bytes as type W.
+template <int WORDS, typename W, typename Moves>
+__device__ inline void copy_unit(const PageCaches &p, const PageRun &r, int64_t u, int64_t count,
+                                 int64_t num_pages, int64_t page_size, Moves moves) {
+  const int lane = int(threadIdx.x) & 63;
+  const bool small = count * r.count * r.pieces < (int64_t(1) << 31);
+  if (r.lanes_log2 == 6) {
+    const int64_t mc = small ? int64_t(div_by(r.div_pieces, uint32_t(u))) : u / r.pieces;
+    const uint32_t piece = uint32_t(u - mc * r.pieces);
+    const int64_t k = small ? int64_t(uint32_t(mc) / uint32_t(count)) : mc / count;
+    const int64_t i = mc - k * count;
+    const int c = r.first + int(k);
+    const Move m = moves(i);
+    const uint32_t all = words_of(r, m, num_pages, page_size), w0 = piece * (64 * WORDS);
+    const char *from = p.base[c] + m.from * p.page[c] + int64_t(w0) * int64_t(sizeof(W));
+    char *to = p.base[c] + m.to * p.page[c] + int64_t(w0) * int64_t(sizeof(W));
+    W word[WORDS];
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k)
+      if (w0 + 64 * k + lane < all)
+        word[k] = __builtin_nontemporal_load(reinterpret_cast<const W *>(from) + (64 * k + lane));
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k)
+      if (w0 + 64 * k + lane < all) {
+        if constexpr (sizeof(W) == 16) store_streamed(to, 16 * (64 * k + lane), word[k]);
+        else __builtin_nontemporal_store(word[k], reinterpret_cast<W *>(to) + (64 * k + lane));
+      }
+  } else {
+    const int64_t mc = u * (64 >> r.lanes_log2) + (lane >> r.lanes_log2);
+    const int64_t k = small ? int64_t(uint32_t(mc) / uint32_t(count)) : mc / count;
+    if (k >= r.count) return;
+    const int64_t i = mc - k * count;
+    const int c = r.first + int(k);
+    const uint32_t w = uint32_t(lane) & ((1u << r.lanes_log2) - 1);
+    const Move m = moves(i);
+    if (w >= words_of(r, m, num_pages, page_size)) return;
+    const W word = reinterpret_cast<const W *>(p.base[c] + m.from * p.page[c])[w];
+    reinterpret_cast<W *>(p.base[c] + m.to * p.page[c])[w] = word;
+  }
+}
+
+// All words of `count` moves in all caches, shared by `groups` wavefronts, of which this is `group`.
+template <int WORDS, typename Moves>
 __device__ inline void copy_pages(const PageCaches &p, int64_t count, int64_t group, int64_t groups,
                                   int64_t num_pages, int64_t page_size, Moves moves) {
-  const int lane = int(threadIdx.x) & 63;
-  const int64_t words = lane < p.count ? count * p.cache[lane].vecs : 0;
-  int64_t total;
-  const int64_t before = wave_sum_before((words + kUnit - 1) / kUnit, &total);
+  int64_t end[kPageRuns], total = 0;
+#pragma unroll
+  for (int r = 0; r < kPageRuns; ++r) {
+    if (r < p.runs) {
+      const int per = 64 >> p.run[r].lanes_log2;
+      total += (count * p.run[r].count * p.run[r].pieces + per - 1) / per;
+    }
+    end[r] = total;
+  }
   for (int64_t u = group; u < total; u += groups) {
-    // the last cache whose units begin at or before u
-    const int t = 63 - __builtin_clzll(__ballot(lane < p.count && before <= u) | 1ull);
-    const int64_t begin = __shfl(before, t);
-    const PageCache &c = p.cache[__builtin_amdgcn_readfirstlane(t)];
-    const int64_t all = count * c.vecs, v = (u - begin) * kUnit + threadIdx.x;
-    const bool small = all + kUnit < (int64_t(1) << 32);
-    switch (c.width) {
-      case 4: copy_words<words4>(c, v, all, small, num_pages, page_size, moves); break;
-      case 3: copy_words<words2>(c, v, all, small, num_pages, page_size, moves); break;
-      case 2: copy_words<uint32_t>(c, v, all, small, num_pages, page_size, moves); break;
-      case 1: copy_words<uint16_t>(c, v, all, small, num_pages, page_size, moves); break;
-      default: copy_words<uint8_t>(c, v, all, small, num_pages, page_size, moves); break;
+    int r = 0;
+    int64_t begin = 0;
+#pragma unroll
+    for (int k = 0; k + 1 < kPageRuns; ++k)
+      if (u >= end[k]) {
+        r = k + 1;
+        begin = end[k];
+      }
+    const PageRun &run = p.run[r];
+    const int64_t at = u - begin;
+    switch (run.width) {
+      case 4: copy_unit<WORDS, words4>(p, run, at, count, num_pages, page_size, moves); break;
+      case 3: copy_unit<WORDS, words2>(p, run, at, count, num_pages, page_size, moves); break;
+      case 2: copy_unit<WORDS, uint32_t>(p, run, at, count, num_pages, page_size, moves); break;
+      case 1: copy_unit<WORDS, uint16_t>(p, run, at, count, num_pages, page_size, moves); break;
+      default: copy_unit<WORDS, uint8_t>(p, run, at, count, num_pages, page_size, moves); break;
     }
   }
 }
 
 __global__ __launch_bounds__(kPageBlock) void copy_pages_kernel(CopyPagesPlan p) {
-  copy_pages(p.caches, p.moves, blockIdx.x, gridDim.x, p.num_pages, 1, [&](int64_t i) {
+  copy_pages<kPageWords>(p.caches, p.moves, blockIdx.x, gridDim.x, p.num_pages, 1, [&](int64_t i) {
     return Move{p.sources[i * p.source_stride], p.targets[i * p.target_stride], 0};
   });
 }
@@ -150,17 +186,15 @@ __device__ inline int32_t chunk_flags(const int64_t *refs, int64_t stride, int64
   return __popc(*flags);
 }
 
-// Sum of the chunks' counts before `chunk`, and of all.
+// Sum of the chunks' counts before `chunk`, and of all.  At most 2^30 pages: both fit one scan.
 __device__ inline int64_t chunks_before(const int32_t *counts, int64_t chunks, int64_t chunk,
                                         int64_t *lds, int64_t *total) {
-  int64_t before = 0, all = 0, sum;
-  for (int64_t i = threadIdx.x; i < chunks; i += kCountBlock) {
-    all += counts[i];
-    if (i < chunk) before += counts[i];
-  }
-  scan_block(before, lds, &sum);
-  scan_block(all, lds, total);
-  return sum;
+  int64_t mine = 0, sum;
+  for (int64_t i = threadIdx.x; i < chunks; i += kCountBlock)
+    mine += int64_t(counts[i]) << 32 | int64_t(i < chunk ? counts[i] : 0);
+  scan_block(mine, lds, &sum);
+  *total = sum >> 32;
+  return sum & 0xffffffff;
 }
 
 // ---- fork ------------------------------------------------------------------------------------------
@@ -191,8 +225,14 @@ __device__ inline X fresh(const X *p) {  // as the other threads' atomics left i
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// LOCAL: what the rows' threads tell each other about the sequences goes through LDS, which holds
+// kLocalRows of them; else through global memory.
+constexpr int64_t kLocalRows = 4096;
+
+template <bool LOCAL>
 __global__ __launch_bounds__(kCountBlock) void fork_count_kernel(ForkPlan p) {
   __shared__ int64_t lds[kCountBlock / 64];
+  __shared__ int32_t local[LOCAL ? 2 * kLocalRows : 1];
   const int64_t B = p.table.rows, R = p.out.rows;
   int64_t sum;
   if (blockIdx.x > 0) {
@@ -203,21 +243,28 @@ __global__ __launch_bounds__(kCountBlock) void fork_count_kernel(ForkPlan p) {
     if (threadIdx.x == 0) p.counts[chunk] = int32_t(sum);
     return;
   }
+  int32_t *first = LOCAL ? local : p.first, *children = LOCAL ? local + kLocalRows : p.children;
+  constexpr int kScope = LOCAL ? __HIP_MEMORY_SCOPE_WORKGROUP : __HIP_MEMORY_SCOPE_AGENT;
   for (int64_t b = threadIdx.x; b < B; b += kCountBlock) {
-    __hip_atomic_store(&p.first[b], 0x7fffffff, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(&p.children[b], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(&first[b], 0x7fffffff, __ATOMIC_RELAXED, kScope);
+    __hip_atomic_store(&children[b], 0, __ATOMIC_RELAXED, kScope);
     p.kept[b] = 0;
   }
-  __threadfence();
+  if (!LOCAL) __threadfence();
   __syncthreads();
   for (int64_t i = threadIdx.x; i < R; i += kCountBlock) {
     const int64_t b = p.parents[i * p.parent_stride];
     if (b < 0 || b >= B) continue;
-    atomicMin(&p.first[b], int32_t(i));
-    atomicAdd(&p.children[b], 1);
+    __hip_atomic_fetch_min(&first[b], int32_t(i), __ATOMIC_RELAXED, kScope);
+    __hip_atomic_fetch_add(&children[b], 1, __ATOMIC_RELAXED, kScope);
   }
-  __threadfence();
+  if (!LOCAL) __threadfence();
   __syncthreads();
+  if (LOCAL)
+    for (int64_t b = threadIdx.x; b < B; b += kCountBlock) {
+      p.first[b] = first[b];
+      p.children[b] = children[b];
+    }
   int64_t wanted = 0, copies = 0;
   for (int64_t i0 = 0; i0 < R; i0 += kCountBlock) {
     const int64_t i = i0 + threadIdx.x;
@@ -231,18 +278,20 @@ __global__ __launch_bounds__(kCountBlock) void fork_count_kernel(ForkPlan p) {
       if (r.len % p.page_size != 0) {
         last = p.table.data[r.parent * p.table.row + (used - 1) * p.table.col];
         if (last >= 0 && last < p.num_pages) {
-          const bool keep = fresh(&p.first[r.parent]) == i && p.refs[last * p.ref_stride] <= 1;
+          const bool keep = __hip_atomic_load(&first[r.parent], __ATOMIC_RELAXED, kScope) == i &&
+                            p.refs[last * p.ref_stride] <= 1;
           if (keep) p.kept[r.parent] = 1;
           copy = !keep;
           need += copy;
         }
       }
     }
+    // both sums in one scan: at most 2^30 new pages a row's table holds, and 1024 rows' at a time
     int64_t all;
-    const int64_t base = wanted + scan_block(need, lds, &all);
-    wanted += all;
-    const int64_t k = copies + scan_block(copy, lds, &all);
-    copies += all;
+    const int64_t before = scan_block(need << 11 | int64_t(copy), lds, &all);
+    const int64_t base = wanted + (before >> 11), k = copies + (before & 2047);
+    wanted += all >> 11;
+    copies += all & 2047;
     if (i < R) p.base[i] = base;
     if (copy) {
       p.copies[3 * k] = last;
@@ -335,7 +384,7 @@ __global__ __launch_bounds__(kPageBlock) void fork_write_kernel(ForkPlan p) {
     fork_tables(p, block * kPageBlock + threadIdx.x, p.table_blocks * kPageBlock);
     return;
   }
-  copy_pages(p.caches, p.totals[1], block - p.table_blocks, gridDim.x - p.table_blocks, p.num_pages,
+  copy_pages<kForkWords>(p.caches, p.totals[1], block - p.table_blocks, gridDim.x - p.table_blocks, p.num_pages,
              p.page_size, [&](int64_t i) {
                const int64_t *c = p.copies + 3 * i;
                return Move{c[0], new_page(p, c[1]), c[2]};
@@ -411,20 +460,18 @@ __global__ __launch_bounds__(kPageBlock) void compact_write_kernel(CompactPlan p
     compact_tables(p, block * kPageBlock + threadIdx.x, p.table_blocks * kPageBlock);
     return;
   }
-  copy_pages(p.caches, p.totals[0], block - p.table_blocks, gridDim.x - p.table_blocks, p.num_pages,
+  copy_pages<kPageWords>(p.caches, p.totals[0], block - p.table_blocks, gridDim.x - p.table_blocks, p.num_pages,
              1, [&](int64_t i) { return Move{p.moves[2 * i], p.moves[2 * i + 1], 0}; });
 }
 
 // The last launch of a plan: tables, and the copies in the first caches; then the other caches' copies,
 // as many at a time as a launch holds.  `copies`: workgroups for a launch's copies.
 template <typename Plan, typename Groups>
-int run_writes(const void *fn, Plan &p, const std::vector<PageCache> &list, Groups copies,
-               void *stream) {
+int run_writes(const void *fn, Plan &p, const std::vector<PageCache> &list, int words,
+               Groups copies, void *stream) {
   size_t at = 0;
   do {
-    p.caches.count = int32_t(std::min<size_t>(kPageCaches, list.size() - at));
-    std::copy_n(list.begin() + std::ptrdiff_t(at), p.caches.count, p.caches.cache);
-    at += size_t(p.caches.count);
+    at = take_caches(list, at, words, &p.caches);
     const int64_t blocks = p.table_blocks + (p.caches.count > 0 ? copies(p) : 0);
     if (blocks > 0) {
       const int st = launch_kernel(fn, dim3(uint32_t(blocks)), kPageBlock, 0, stream, &p);
@@ -451,12 +498,9 @@ ROPE_API int rope_copy_pages(const rope_tensor *sources, const rope_tensor *targ
     return st;
   }
   g_last_error.clear();
-  return run_writes(reinterpret_cast<const void *>(&copy_pages_kernel), p, list,
+  return run_writes(reinterpret_cast<const void *>(&copy_pages_kernel), p, list, kPageWords,
                     [](const CopyPagesPlan &q) {
-                      int64_t units = 0;
-                      for (int i = 0; i < q.caches.count; ++i)
-                        units += (q.moves * q.caches.cache[i].vecs + kUnit - 1) / kUnit;
-                      return std::min(units, int64_t(1) << 22);
+                      return std::min(q.caches.units(q.moves), int64_t(1) << 25);
                     }, stream);
 }
 
@@ -483,14 +527,18 @@ ROPE_API int rope_fork_pages(const rope_tensor *page_table, const rope_tensor *s
     return st;
   }
   g_last_error.clear();
-  st = launch_kernel(reinterpret_cast<const void *>(&fork_count_kernel),
+  st = launch_kernel(p.table.rows <= kLocalRows
+                         ? reinterpret_cast<const void *>(&fork_count_kernel<true>)
+                         : reinterpret_cast<const void *>(&fork_count_kernel<false>),
                      dim3(uint32_t(1 + p.chunks)), kCountBlock, 0, stream, &p);
   if (st != ROPE_OK) return st;
   st = launch_kernel(reinterpret_cast<const void *>(&fork_free_kernel),
                      dim3(uint32_t(std::max<int64_t>(1, p.chunks))), kCountBlock, 0, stream, &p);
   if (st != ROPE_OK) return st;
-  return run_writes(reinterpret_cast<const void *>(&fork_write_kernel), p, list,
-                    [](const ForkPlan &) { return kCopyGroups; }, stream);
+  return run_writes(reinterpret_cast<const void *>(&fork_write_kernel), p, list, kForkWords,
+                    [](const ForkPlan &q) {
+                      return std::min(q.caches.units(q.out.rows), kForkGroups);
+                    }, stream);
 }
 
 ROPE_API int64_t rope_compact_pages_workspace(int64_t num_pages) {
@@ -522,6 +570,8 @@ ROPE_API int rope_compact_pages(const rope_tensor *page_table, const rope_tensor
   st = launch_kernel(reinterpret_cast<const void *>(&compact_map_kernel),
                      dim3(uint32_t(std::max<int64_t>(1, p.chunks))), kCountBlock, 0, stream, &p);
   if (st != ROPE_OK) return st;
-  return run_writes(reinterpret_cast<const void *>(&compact_write_kernel), p, list,
-                    [](const CompactPlan &) { return kCopyGroups; }, stream);
+  return run_writes(reinterpret_cast<const void *>(&compact_write_kernel), p, list, kPageWords,
+                    [](const CompactPlan &q) {
+                      return std::min(q.caches.units(q.num_pages / 2), kCompactGroups);
+                    }, stream);
 }

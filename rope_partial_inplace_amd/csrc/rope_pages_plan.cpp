@@ -3,6 +3,7 @@
 #include "rope_pages_plan.h"
 
 #include <algorithm>
+#include <tuple>
 
 #include "rope_check.h"
 
@@ -38,15 +39,20 @@ bool page_block(const rope_tensor *t, int64_t page_size, PageCache *c) {
     part = bytes / t->shape[1];
   uint64_t all = reinterpret_cast<uintptr_t>(t->data) | uint64_t(c->page) | uint64_t(bytes) |
                  uint64_t(part);
-  c->width = 0;
-  while (c->width < 4 && (all >> c->width & 1) == 0) ++c->width;
-  if (bytes >> c->width >= kMaxPageWords) return false;
-  c->vecs = uint32_t(bytes >> c->width);
-  c->parts = part > 0 ? uint32_t(t->shape[1]) : 0;
-  c->part_words = uint32_t(part >> c->width);
-  c->div_vecs = make_fastdiv(std::max(1u, c->vecs));
+  PageRun &r = c->run;
+  while (r.width < 4 && (all >> r.width & 1) == 0) ++r.width;
+  if (bytes >> r.width >= kMaxPageWords) return false;
+  r.vecs = uint32_t(bytes >> r.width);
+  r.parts = part > 0 ? uint32_t(t->shape[1]) : 0;
+  r.part_words = uint32_t(part >> r.width);
+  if (r.vecs < 64) {
+    r.lanes_log2 = 0;
+    while ((1u << r.lanes_log2) < r.vecs) ++r.lanes_log2;
+  }
   return true;
 }
+
+auto order_of(const PageRun &r) { return std::tie(r.vecs, r.width, r.parts, r.part_words); }
 
 // The caches of a call: checked, and without those that hold nothing.
 int check_caches(const rope_tensor *caches, int64_t num_caches, int64_t *pages, int64_t page_size,
@@ -89,6 +95,10 @@ int check_caches(const rope_tensor *caches, int64_t num_caches, int64_t *pages, 
       if (!disjoint(by_start[i].second, by_start[k].second))
         return reject(err, ROPE_ERR_PARAM_INVALID, "caches overlap");
   }
+  // pages that are alike side by side
+  std::stable_sort(list->begin(), list->end(), [](const PageCache &x, const PageCache &y) {
+    return order_of(x.run) < order_of(y.run);
+  });
   return ROPE_OK;
 }
 
@@ -114,6 +124,28 @@ const int64_t *i64(const rope_tensor *t) { return static_cast<const int64_t *>(t
 int64_t *i64_out(const rope_tensor *t) { return static_cast<int64_t *>(t->data); }
 
 }  // namespace
+
+size_t take_caches(const std::vector<PageCache> &list, size_t at, int words, PageCaches *to) {
+  to->runs = to->count = 0;
+  for (; at < list.size() && to->count < kPageCaches; ++at) {
+    const PageCache &c = list[at];
+    if (to->runs == 0 || order_of(to->run[to->runs - 1]) != order_of(c.run)) {
+      if (to->runs == kPageRuns) break;
+      to->run[to->runs] = c.run;
+      to->run[to->runs++].first = to->count;
+    }
+    ++to->run[to->runs - 1].count;
+    to->base[to->count] = c.base;
+    to->page[to->count++] = c.page;
+  }
+  for (int r = 0; r < to->runs; ++r) {
+    PageRun &run = to->run[r];
+    if (run.lanes_log2 == 6)
+      run.pieces = (run.vecs + 64 * uint32_t(words) - 1) / (64 * uint32_t(words));
+    run.div_pieces = make_fastdiv(run.pieces);
+  }
+  return at;
+}
 
 int plan_copy_pages(const rope_tensor *sources, const rope_tensor *targets,
                     const rope_tensor *caches, int64_t num_caches, CopyPagesPlan *plan,

@@ -10,27 +10,62 @@
 
 namespace ropeamd {
 
-// One cache: pages of `vecs` words of 2^width bytes each, `page` bytes apart.  Where a page's outermost
-// dimension is its rows (or blocks of rows), the first tokens of a page are its first words:
-// part_words of them for each of `parts` equal parts of a page's tokens.
-struct PageCache {
-  char *base = nullptr;
-  int64_t page = 0;
-  uint32_t vecs = 0, part_words = 0, parts = 0;
-  int32_t width = 0;
-  FastDiv div_vecs;
+// Caches whose pages are alike: `vecs` words of 2^width bytes each.  Where a page's outermost dimension
+// is its rows (or blocks of rows), the first tokens of a page are its first words: part_words of them
+// for each of `parts` equal parts of a page's tokens.
+//
+// A run's work is numbered cache by cache, in it move by move, in that piece by piece (move by move and
+// then cache by cache, 500 pages of 16 KiB in 64 caches took 207 us in place of 175).  Pages of at least
+// 64 words are cut into pieces that a wavefront copies, so that its page numbers are scalars; of
+// smaller ones a wavefront takes several, 2^lanes_log2 lanes each.
+struct PageRun {
+  int32_t first = 0, count = 0;  // caches
+  uint32_t vecs = 0, pieces = 1, part_words = 0, parts = 0;
+  int32_t width = 0, lanes_log2 = 6;
+  FastDiv div_pieces;
 };
 
-constexpr int kPageCaches = 64;    // of a launch: one a lane when a launch finds its way
-constexpr int kPageBlock = 256;    // threads of a copying workgroup
-constexpr int kPageWords = 4;      // words that a thread copies at a time
+constexpr int kPageBlock = 64;  // threads of a copying workgroup
+#ifndef PW
+#define PW 2
+#endif
+#ifndef FW
+#define FW 8
+#endif
+constexpr int kPageWords = PW;  // words of a lane
+constexpr int kForkWords = FW;  // the same where the way to a word is longer
 constexpr int64_t kPageChunk = 4096;  // pages that a workgroup counts
 constexpr int kCountBlock = 1024;
 
+// What a launch copies between.
+constexpr int kPageCaches = 160;
+constexpr int kPageRuns = 4;
 struct PageCaches {
-  int32_t count = 0;
-  PageCache cache[kPageCaches];
+  int32_t runs = 0, count = 0;
+  PageRun run[kPageRuns];
+  char *base[kPageCaches];
+  int64_t page[kPageCaches];  // bytes from one page to the next
+  // wavefronts that `moves` moves take
+  int64_t units(int64_t moves) const {
+    int64_t n = 0;
+    for (int r = 0; r < runs; ++r) {
+      const int64_t per = int64_t(1) << (6 - run[r].lanes_log2);
+      n += (moves * run[r].count * run[r].pieces + per - 1) / per;
+    }
+    return n;
+  }
 };
+
+// A cache as the checks leave it.
+struct PageCache {
+  PageRun run;
+  char *base = nullptr;
+  int64_t page = 0;
+};
+
+// As many of the caches from `at` on as a launch takes, in pieces of `words` words a lane; returns where
+// the next launch's begin.
+size_t take_caches(const std::vector<PageCache> &list, size_t at, int words, PageCaches *to);
 
 // ---- copy ------------------------------------------------------------------------------------------
 struct CopyPagesPlan {
