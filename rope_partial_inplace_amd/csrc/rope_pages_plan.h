@@ -26,14 +26,8 @@ struct PageRun {
 };
 
 constexpr int kPageBlock = 64;  // threads of a copying workgroup
-#ifndef PW
-#define PW 2
-#endif
-#ifndef FW
-#define FW 8
-#endif
-constexpr int kPageWords = PW;  // words of a lane
-constexpr int kForkWords = FW;  // the same where the way to a word is longer
+constexpr int kPageWords = 2;  // words of a lane
+constexpr int kForkWords = 8;  // the same where the way to a word is longer
 constexpr int64_t kPageChunk = 4096;  // pages that a workgroup counts
 constexpr int kCountBlock = 1024;
 

@@ -15,16 +15,9 @@ __device__ inline uint32_t div_by(const FastDiv &f, uint32_t n) {
   return (t + ((n - t) >> f.s1)) >> f.s2;
 }
 
-__device__ inline bool finite(float x) {
-  return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
-}
-
-// The larger of `top` and |x|; a non-finite x sets the flag instead.
-__device__ inline float larger(float top, float x, bool *bad) {
-  const bool good = finite(x);
-  *bad |= !good;
-  return good ? fmaxf(top, fabsf(x)) : top;
-}
+// Size of x as a number that orders floats by it; infinities and NaN are the largest.
+__device__ inline uint32_t size_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr uint32_t kNonFinite = 0x7f800000u;
 
 // The scale that elements of size `top` need.  e4m3: the power of two 2^k with top <= 448 * 2^k, read off
 // top's exponent and whether its fraction passes that of 448 = 1.75 * 2^8.
@@ -39,23 +32,24 @@ __device__ inline float needed_scale(float top) {
   }
 }
 
-// Four floats to codes, to nearest even.  They lie within the codes' range but for NaN and infinity:
-// e4m3 NaN, int8 the ends of its range (under a NaN scale: any code).
-template <bool E4M3>
+// Four floats within the codes' range to codes, to nearest even.  A NaN or infinity (CHECK: there may be
+// some) becomes NaN in e4m3 and any code in int8, whose scale is then NaN.
+//
+// int8: added to 1.5 * 2^23 a float is rounded to an integer, whose low byte is the code.
+template <bool E4M3, bool CHECK>
 __device__ inline uint32_t encode4(float a, float b, float c, float d) {
   if constexpr (E4M3) {
-    const float nan = __builtin_nanf("");
-    a = finite(a) ? a : nan;
-    b = finite(b) ? b : nan;
-    c = finite(c) ? c : nan;
-    d = finite(d) ? d : nan;
+    if constexpr (CHECK) {
+      auto one = [](float x) { return size_bits(x) < kNonFinite ? x : __builtin_nanf(""); };
+      a = one(a), b = one(b), c = one(c), d = one(d);
+    }
     const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
   } else {
-    auto one = [](float x) {
-      return uint32_t(int32_t(rintf(fminf(fmaxf(x, -127.0f), 127.0f)))) & 0xffu;
-    };
-    return one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+    auto one = [](float x) { return __float_as_uint(x + 0x1.8p23f); };
+    const uint32_t lo = __builtin_amdgcn_perm(one(b), one(a), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(one(d), one(c), 0x04000c0cu);
+    return lo | hi;
   }
 }
 
@@ -79,20 +73,20 @@ template <bool E4M3>
 __device__ inline uint32_t recode(uint32_t w, float ratio) {
   float f[4];
   decode4<E4M3>(w, f);
-  return encode4<E4M3>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+  return encode4<E4M3, true>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
 }
 
 // V = 1, 4 or 8 codes of f * inv.
-template <bool E4M3, int V>
+template <bool E4M3, bool CHECK, int V>
 __device__ inline void store_codes(uint8_t *to, const float *f, float inv) {
   if constexpr (V == 1) {
-    *to = uint8_t(encode4<E4M3>(f[0] * inv, 0.0f, 0.0f, 0.0f));
+    *to = uint8_t(encode4<E4M3, CHECK>(f[0] * inv, 0.0f, 0.0f, 0.0f));
   } else {
     uint32_t w[V / 4];
 #pragma unroll
     for (int i = 0; i < V / 4; ++i)
-      w[i] = encode4<E4M3>(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv,
-                           f[4 * i + 3] * inv);
+      w[i] = encode4<E4M3, CHECK>(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv,
+                                  f[4 * i + 3] * inv);
     if constexpr (V == 4)
       *reinterpret_cast<uint32_t *>(to) = w[0];
     else

@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "rope.h"
 #include "rope_io.h"
@@ -28,20 +29,24 @@
 namespace ropeamd {
 namespace {
 
-// V elements of a row from `e` on, and (pairs) V more a partner's distance on, in float32.
-template <int V, bool PAIR>
-struct Elements {
-  float a[V], b[PAIR ? V : 1];
-  int32_t e;
-  bool two;  // b holds elements
-};
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-template <typename T, int V>
+// 16 bytes that are used once.
+__device__ inline uint4 load_once(const void *p) {
+  const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4 *>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ inline void store_once(void *p, const uint4 &v) {
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, static_cast<u32x4 *>(p));
+}
+
+// V elements; ONCE: no other item reads them.
+template <typename T, int V, bool ONCE>
 __device__ inline void load_floats(const T *p, float *f) {
   if constexpr (V == 1)
     f[0] = Io<T>::from_raw(*reinterpret_cast<const typename Io<T>::raw *>(p));
   else
-    Io<T>::unpack(*reinterpret_cast<const uint4 *>(p), f);
+    Io<T>::unpack(ONCE ? load_once(p) : *reinterpret_cast<const uint4 *>(p), f);
 }
 
 // The V / 2 cos (or sin) values of a GPT-J vector: 8 bytes.
@@ -52,44 +57,70 @@ __device__ inline void load_half_floats(const T *p, float *f) {
   Io<T>::word_to_floats(w.y, f + Io<T>::kPerWord);
 }
 
-// Item `unit` of a row, rotated where it lies in the slice (cs: the token's cosines and sines).
+// Where an item of a row lies: V elements from `e` on, and if it is rotated and made of pairs V more
+// from e + partner on.
+struct Spot {
+  int32_t e;
+  bool turned;
+};
+
+template <int V, bool NEOX>
+__device__ inline Spot spot_of(uint32_t unit, uint32_t rot_items, int32_t rot_start, int32_t half) {
+  Spot s;
+  s.turned = unit < rot_items;
+  int32_t e = int32_t(unit - rot_items) * V;  // outside the slice
+  if (e >= rot_start && rot_items != 0) e += 2 * half;
+  s.e = s.turned ? rot_start + int32_t(unit) * (V == 1 && !NEOX ? 2 : V) : e;
+  return s;
+}
+
+template <bool NEOX>
+__device__ inline int32_t partner(int32_t half) {
+  return NEOX ? half : 1;
+}
+
+// The cosines and sines of an item (cs: its token's).  An item outside the slice takes some others: there
+// are no branches, so that several items' loads are under way at once.
 template <typename T, int V, bool NEOX>
-__device__ inline Elements<V, NEOX || V == 1> item_of(const T *in, const T *cs, uint32_t unit,
-                                                      uint32_t rot_items, int32_t rot_start,
-                                                      int32_t half) {
-  constexpr bool PAIR = NEOX || V == 1;
-  Elements<V, PAIR> x;
-  x.two = false;
-  if (unit >= rot_items) {  // outside the slice
-    x.e = int32_t(unit - rot_items) * V;
-    if (x.e >= rot_start && rot_items != 0) x.e += 2 * half;
-    load_floats<T, V>(in + x.e, x.a);
-    return x;
+struct Turn {
+  static constexpr int N = NEOX || V == 1 ? V : V / 2;
+  float c[N], s[N];
+  __device__ void load(const T *cs, const Spot &at, uint32_t unit, int32_t half) {
+    const int32_t u = at.turned ? int32_t(unit) : 0;
+    if constexpr (NEOX || V == 1) {
+      load_floats<T, V, false>(cs + u * V, c);
+      load_floats<T, V, false>(cs + half + u * V, s);
+    } else {
+      load_half_floats<T>(cs + u * (V / 2), c);
+      load_half_floats<T>(cs + half + u * (V / 2), s);
+    }
   }
-  x.e = rot_start + int32_t(unit) * (V == 1 && !NEOX ? 2 : V);
-  float p[V], c[V], s[V];
-  load_floats<T, V>(in + x.e, p);
-  if constexpr (PAIR) {
+};
+
+// An item in float32, rotated where it lies in the slice.
+template <typename T, int V, bool NEOX>
+__device__ inline void rotated(const T *in, const Turn<T, V, NEOX> &r, const Spot &at, int32_t half,
+                               float *a, float *b) {
+  float p[V];
+  load_floats<T, V, true>(in + at.e, p);
+  if constexpr (NEOX || V == 1) {
     float q[V];
-    load_floats<T, V>(in + x.e + (NEOX ? half : 1), q);
-    load_floats<T, V>(cs + int32_t(unit) * V, c);
-    load_floats<T, V>(cs + half + int32_t(unit) * V, s);
+    load_floats<T, V, true>(in + at.e + (at.turned ? partner<NEOX>(half) : 0), q);
 #pragma unroll
     for (int m = 0; m < V; ++m) {
-      x.a[m] = p[m] * c[m] - q[m] * s[m];
-      x.b[m] = q[m] * c[m] + p[m] * s[m];
+      const float x = p[m] * r.c[m] - q[m] * r.s[m];
+      b[m] = q[m] * r.c[m] + p[m] * r.s[m];
+      a[m] = at.turned ? x : p[m];
     }
-    x.two = true;
   } else {
-    load_half_floats<T>(cs + int32_t(unit) * (V / 2), c);
-    load_half_floats<T>(cs + half + int32_t(unit) * (V / 2), s);
 #pragma unroll
     for (int m = 0; m < V / 2; ++m) {
-      x.a[2 * m] = p[2 * m] * c[m] - p[2 * m + 1] * s[m];
-      x.a[2 * m + 1] = p[2 * m + 1] * c[m] + p[2 * m] * s[m];
+      const float x = p[2 * m] * r.c[m] - p[2 * m + 1] * r.s[m];
+      const float y = p[2 * m + 1] * r.c[m] + p[2 * m] * r.s[m];
+      a[2 * m] = at.turned ? x : p[2 * m];
+      a[2 * m + 1] = at.turned ? y : p[2 * m + 1];
     }
   }
-  return x;
 }
 
 template <typename T>
@@ -98,7 +129,10 @@ __device__ inline const T *angles(const AppendQ8Plan &p, int64_t token) {
   return static_cast<const T *>(p.table) + min(max(pos, int64_t(0)), p.max_seq - 1) * p.table_stride;
 }
 
-// ---- queries: an item a lane, as in the append to a cache without codes -------------------------
+// ---- queries ------------------------------------------------------------------------------------
+// A thread takes one item of kQueryHeads neighbouring heads, which share its cosines and sines.  (One head
+// a thread is bound by its address arithmetic: 11167 tokens of 32 heads of 128, half of each rotated
+// in pairs, 40 us.)
 template <typename T, int V, bool NEOX>
 __device__ inline void rotate_queries(const AppendQ8Plan &p, int64_t block) {
   const AppendRows &r = p.query;
@@ -114,29 +148,40 @@ __device__ inline void rotate_queries(const AppendQ8Plan &p, int64_t block) {
     t = it / r.total;
     i = uint32_t(it - t * r.total);
   }
-  const uint32_t h = div_by(r.div_items, i), unit = i - h * r.items;
-  const T *in = static_cast<const T *>(r.in) + t * r.in_tok + int64_t(h) * r.in_head;
-  T *out = static_cast<T *>(r.out) + t * r.out_tok + int64_t(h) * r.out_head;
-  if (unit >= r.rot_items) {  // copied bit for bit
-    int64_t e = int64_t(unit - r.rot_items) * V;
-    if (e >= r.rot_start) e += 2 * p.half;
-    if constexpr (V == 1)
-      *reinterpret_cast<typename Io<T>::raw *>(out + e) =
-          *reinterpret_cast<const typename Io<T>::raw *>(in + e);
-    else
-      *reinterpret_cast<uint4 *>(out + e) = *reinterpret_cast<const uint4 *>(in + e);
-    return;
-  }
-  const auto x = item_of<T, V, NEOX>(in, angles<T>(p, t), unit, r.rot_items, r.rot_start, p.half);
-  auto store = [&](T *to, const float *f) {
-    if constexpr (V == 1)
-      Io<T>::store1(to, 0, f[0]);
-    else
-      *reinterpret_cast<uint4 *>(to) = Io<T>::pack(f);
+  const uint32_t hg = div_by(r.div_items, i), unit = i - hg * r.items;
+  const int64_t h = int64_t(hg) * kQueryHeads;
+  const T *in = static_cast<const T *>(r.in) + t * r.in_tok + h * r.in_head;
+  T *out = static_cast<T *>(r.out) + t * r.out_tok + h * r.out_head;
+  const Spot at = spot_of<V, NEOX>(unit, r.rot_items, r.rot_start, p.half);
+  Turn<T, V, NEOX> turn;
+  turn.load(angles<T>(p, t), at, unit, p.half);
+  const int heads = int(min(p.query_heads - h, int64_t(kQueryHeads)));
+  auto one = [&](int k) {
+    const T *x = in + k * r.in_head;
+    T *y = out + k * r.out_head;
+    float a[V], b[V];
+    rotated<T, V, NEOX>(x, turn, at, p.half, a, b);
+    // what lies outside the slice is copied bit for bit (raised to float32 and rounded again, all but a
+    // NaN's payload would be)
+    if constexpr (V == 1) {
+      T v;
+      Io<T>::store1(&v, 0, a[0]);
+      *(y + at.e) = at.turned ? v : x[at.e];
+      if (at.turned) Io<T>::store1(y + at.e + partner<NEOX>(p.half), 0, b[0]);
+    } else {
+      const uint4 w = load_once(x + at.e), z = Io<T>::pack(a);
+      store_once(y + at.e, make_uint4(at.turned ? z.x : w.x, at.turned ? z.y : w.y,
+                                      at.turned ? z.z : w.z, at.turned ? z.w : w.w));
+      if constexpr (NEOX)
+        if (at.turned) store_once(y + at.e + p.half, Io<T>::pack(b));
+    }
   };
-  store(out + x.e, x.a);
-  if constexpr (NEOX || V == 1)
-    if (x.two) store(out + x.e + (NEOX ? p.half : 1), x.b);
+  if (heads == kQueryHeads) {
+#pragma unroll
+    for (int k = 0; k < kQueryHeads; ++k) one(k);
+  } else {
+    for (int k = 0; k < heads; ++k) one(k);
+  }
 }
 
 // ---- keys and values -----------------------------------------------------------------------------
@@ -148,16 +193,16 @@ struct Place {
   int32_t row0 = 0, block = 0;  // the block's first row in its page, and its number there
 };
 
-// Place `u` of the plan's numbering, the same for all lanes; false: it has no tokens.
+// Place `u` of the plan's numbering, the same for all lanes; false: it has no tokens.  The page's number
+// is read last and not looked at here, so that the tokens' elements can be on their way first.
 __device__ inline bool find_place(const AppendQ8Plan &p, int64_t u, Place *out) {
   const Sequences &s = p.seq;
   auto first_place = [&](int64_t offset, int64_t i) {
     return p.by_token ? offset : int64_t(div_by(p.div_block, uint32_t(offset))) + 2 * i;
   };
-  auto offset = [&](int64_t i) {
-    return min(max(s.offsets[i * s.off_stride], int64_t(0)), s.T);
-  };
-  int64_t b = 0, o0, o1;
+  const int lane = int(threadIdx.x) & 63;
+  const int64_t limit = s.max_pages * s.page_size;
+  int64_t b = 0, o0, o1, len;
   if (s.offsets == nullptr) {
     int64_t n = s.B;  // the last b with first_place(b) <= u, in [b, b + n)
     while (n > 1) {   // ends: halved every time
@@ -171,22 +216,31 @@ __device__ inline bool find_place(const AppendQ8Plan &p, int64_t u, Place *out) 
     }
     o0 = b * s.each;
     o1 = o0 + s.each;
+    len = s.lens[b * s.len_stride];
   } else {
-    // the same, 64 offsets at a time: ascending, they make the lanes below a run from lane 0 on
-    const int lane = int(threadIdx.x) & 63;
+    // the same, 64 offsets at a time: ascending, they make the lanes below a run from lane 0 on; the
+    // last time with the lengths
     int64_t n = s.B;
-    while (n > 1) {  // ends: n becomes n / 64 rounded up, or less
+    while (true) {  // ends: n becomes n / 64 rounded up, or less
       const int64_t step = (n + 63) >> 6, i = lane * step;
-      const bool below = i < n && first_place(offset(b + i), b + i) <= u;
-      const int64_t run = (63 - __builtin_clzll(__ballot(below) | 1ull)) * step;
-      b += run;
-      n = min(step, n - run);
+      int64_t o = 0, l = 0;
+      if (i <= n && b + i <= s.B) o = min(max(s.offsets[(b + i) * s.off_stride], int64_t(0)), s.T);
+      if (step == 1 && i < n) l = s.lens[(b + i) * s.len_stride];
+      const bool below = i < n && first_place(o, b + i) <= u;
+      const int run = 63 - __builtin_clzll(__ballot(below) | 1ull);
+      b += run * step;
+      if (step == 1) {
+        o0 = __shfl(o, run);
+        o1 = __shfl(o, (run + 1) & 63);
+        len = __shfl(l, run);
+        if (run == 63) o1 = min(max(s.offsets[(b + 1) * s.off_stride], int64_t(0)), s.T);
+        break;
+      }
+      n = min(step, n - run * step);
     }
-    o0 = offset(b);
-    o1 = offset(b + 1);
   }
+  len = min(max(len, int64_t(0)), limit);
   const int64_t n = o1 - o0;
-  const int64_t len = min(max(s.lens[b * s.len_stride], int64_t(0)), s.max_pages * s.page_size);
   const int64_t start = len - n;  // place of the sequence's first new token (below 0: cut off)
   const int64_t first = max(start, int64_t(0));
   const int64_t k0 = u - first_place(o0, b);
@@ -205,7 +259,6 @@ __device__ inline bool find_place(const AppendQ8Plan &p, int64_t u, Place *out) 
   const int64_t begin = int64_t(div_by(p.div_block, uint32_t(lo))) * p.block;
   const int64_t page = div_by(s.div_page, uint32_t(begin));
   out->page = s.table[b * s.table_seq + page * s.table_page];
-  if (out->page < 0 || out->page >= s.num_pages) return false;
   out->first = o0 + (lo - start);
   out->count = int32_t(min(len, begin + p.block) - lo);
   out->before = int32_t(lo - begin);
@@ -214,46 +267,103 @@ __device__ inline bool find_place(const AppendQ8Plan &p, int64_t u, Place *out) 
   return true;
 }
 
-template <typename T, int V, bool NEOX, bool E4M3>
-__device__ inline void append_block(const AppendQ8Plan &p, const Place &at, int32_t head2) {
-  const int lane = int(threadIdx.x) & 63;
-  const bool mine = head2 < 2 * p.heads;
-  const int64_t h = (mine ? head2 : 0) >> 1;
-  const Q8Rows &r = p.kv[head2 & 1];
-  const uint32_t lanes = uint32_t(p.lanes), l = uint32_t(lane) & (lanes - 1);
-  const uint32_t n = mine ? uint32_t(at.count) * r.items : 0;
-  auto read = [&](uint32_t i, uint32_t *row) {
-    const uint32_t t = div_by(r.div_items, i);
-    *row = t;
-    const T *in = static_cast<const T *>(r.in) + (at.first + t) * r.in_tok + h * r.in_head;
-    const T *cs = r.rot_items != 0 ? angles<T>(p, at.first + t) : nullptr;
-    return item_of<T, V, NEOX>(in, cs, i - t * r.items, r.rot_items, r.rot_start, p.half);
-  };
-  float *scale_at = r.scales + at.page * r.s_page + at.block * r.s_block + h * r.s_head;
-  const float old = mine && at.before > 0 ? *scale_at : 0.0f;
+// New tokens of one block and head by `lanes` neighbouring threads (head below 0: threads without one).
+// ROT: rows with rotated items.  Blocks of up to kQ8Held elements a thread stay in registers between
+// the maximum and the codes; longer ones are read again (the second time from the caches beside the
+// compute unit).
 
-  float top = 0.0f;
-  bool bad = false;
-  for (uint32_t i = l; i < n; i += lanes) {
-    uint32_t row;
-    const auto x = read(i, &row);
+template <typename T, int V, bool NEOX, bool E4M3, bool ROT>
+__device__ inline void append_block(const AppendQ8Plan &p, const Q8Rows &r, const Place &at,
+                                    int32_t head) {
+  constexpr bool PAIR = ROT && (NEOX || V == 1);
+  constexpr int ITEM = PAIR ? 2 * V : V, HELD = V == 1 ? 1 : kQ8Held / ITEM;
+  const uint32_t lane = threadIdx.x & 63, lanes = uint32_t(p.lanes), l = threadIdx.x & (lanes - 1);
+  const bool mine = head >= 0;
+  const int64_t h = mine ? head : 0;
+  const uint32_t n = mine ? uint32_t(at.count) * r.items : 0;
+  const T *in = static_cast<const T *>(r.in) + at.first * r.in_tok + h * r.in_head;
+  // Rows of at most `lanes` items lie side by side, 2^row_log2 threads each: a thread has item `unit` of
+  // every rows-th row.  Item i of the block: V or (rotated pairs) 2 V floats.
+  const uint32_t unit = l & ((1u << r.row_log2) - 1), row0 = l >> r.row_log2;
+  const uint32_t rows_at_once = lanes >> r.row_log2, count = uint32_t(at.count);
+  const Spot spot = spot_of<V, NEOX>(unit, r.rot_items, r.rot_start, p.half);
+  auto read = [&](uint32_t row, const Spot &s, uint32_t item, float *f) {
+    const T *from = in + int64_t(row) * r.in_tok;
+    if constexpr (ROT) {
+      Turn<T, V, NEOX> turn;
+      turn.load(angles<T>(p, at.first + row), s, item, p.half);
+      rotated<T, V, NEOX>(from, turn, s, p.half, f, f + V);
+    } else {
+      load_floats<T, V, true>(from + s.e, f);
+    }
+  };
+  const bool held = r.side_by_side && count <= rows_at_once * HELD;
+  const bool mine_too = mine && unit < r.items;
+  float x[HELD][ITEM];
+  if (held) {
+    const Spot s = unit < r.items ? spot : spot_of<V, NEOX>(0, r.rot_items, r.rot_start, p.half);
 #pragma unroll
-    for (int m = 0; m < V; ++m) top = larger(top, x.a[m], &bad);
-    if constexpr (NEOX || V == 1)
-      if (x.two) {
+    for (int k = 0; k < HELD; ++k)
+      if (k * rows_at_once < count)
+        read(min(row0 + k * rows_at_once, count - 1), s, unit < r.items ? unit : 0, x[k]);
+  }
+  // the elements are on their way: now the page
+  const bool kept = at.page >= 0 && at.page < p.seq.num_pages;  // else padding; the same for all lanes
+  const int64_t page = kept ? at.page : 0;
+  uint8_t *rows = r.codes + page * r.page + int64_t(at.row0) * r.row + h * r.head;
+  float *scale_at = r.scales + page * r.s_page + at.block * r.s_block + h * r.s_head;
+  const float old = kept && mine && at.before > 0 ? *scale_at : 0.0f;
+  // the largest size, over all elements or the finite ones
+  auto largest = [&](auto only_finite) {
+    constexpr bool FINITE = decltype(only_finite)::value;
+    uint32_t high = 0;
+    auto measure = [&](bool turned, const float *f) {
+      auto take = [&](float y) {
+        const uint32_t u = size_bits(y);
+        high = max(high, FINITE && u >= kNonFinite ? 0u : u);
+      };
 #pragma unroll
-        for (int m = 0; m < V; ++m) top = larger(top, x.b[m], &bad);
+      for (int m = 0; m < V; ++m) take(f[m]);
+      if constexpr (PAIR)
+        if (turned) {
+#pragma unroll
+          for (int m = 0; m < V; ++m) take(f[V + m]);
+        }
+    };
+    if (held) {  // a row or an item read twice changes no maximum
+#pragma unroll
+      for (int k = 0; k < HELD; ++k)
+        if (k * rows_at_once < count) measure(spot.turned, x[k]);
+      if (!mine) high = 0;
+    } else {
+      for (uint32_t i = l; i < n; i += lanes) {
+        const uint32_t row = div_by(r.div_items, i), item = i - row * r.items;
+        const Spot s = spot_of<V, NEOX>(item, r.rot_items, r.rot_start, p.half);
+        read(row, s, item, x[0]);
+        measure(s.turned, x[0]);
       }
-  }
-  for (uint32_t d = 1; d < lanes; d *= 2) top = fmaxf(top, __shfl_xor(top, int(d)));
-  float now = needed_scale<E4M3>(top);
-  if (!E4M3) {  // int8 has no NaN: the scale says it
-    const uint64_t group = (lanes == 64 ? ~0ull : (1ull << lanes) - 1) << (uint32_t(lane) - l);
-    if ((__ballot(bad) & group) != 0) now = __builtin_nanf("");
-  }
+    }
+    for (uint32_t d = 1; d < lanes && d < 64; d *= 2)
+      high = max(high, uint32_t(__shfl_xor(int(high), int(d))));
+    if (lanes > 64) {  // the workgroup's four wavefronts
+      __shared__ uint32_t highs[kQ8Block / 64];
+      __syncthreads();
+      if (lane == 0) highs[threadIdx.x >> 6] = high;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kQ8Block / 64; ++k) high = max(high, highs[k]);
+    }
+    return high;
+  };
+  uint32_t high = largest(std::false_type());
+  const bool bad = high >= kNonFinite;
+  const bool check = __any(bad);  // of a long block the same for the workgroup
+  if (check && E4M3) high = largest(std::true_type());
+  if (!kept) return;
+  float now = needed_scale<E4M3>(__uint_as_float(high));
+  if (!E4M3 && bad) now = __builtin_nanf("");  // int8 has no NaN: the scale says it
   if (at.before > 0 && now == now && !(old <= now)) now = old;  // the larger; a NaN stays
 
-  uint8_t *rows = r.codes + at.page * r.page + int64_t(at.row0) * r.row + h * r.head;
   if (mine && at.before > 0 && now != old) {  // the earlier tokens' codes under the new scale
     const float ratio = old / now;
     const int32_t width = r.wide_rows ? 16 : 1, pieces = r.dim / width;
@@ -270,34 +380,60 @@ __device__ inline void append_block(const AppendQ8Plan &p, const Place &at, int3
     }
   }
   const float inv = 1.0f / now;
-  for (uint32_t i = l; i < n; i += lanes) {
-    uint32_t row;
-    const auto x = read(i, &row);
-    uint8_t *to = rows + int64_t(at.before + int32_t(row)) * r.row + x.e;
-    store_codes<E4M3, V>(to, x.a, inv);
-    if constexpr (NEOX || V == 1)
-      if (x.two) store_codes<E4M3, V>(to + (NEOX ? p.half : 1), x.b, inv);
-  }
+  auto encode = [&](auto checked) {
+    constexpr bool CHECK = decltype(checked)::value;
+    auto write = [&](uint32_t row, const Spot &s, const float *f) {
+      uint8_t *to = rows + int64_t(at.before + int32_t(row)) * r.row + s.e;
+      store_codes<E4M3, CHECK, V>(to, f, inv);
+      if constexpr (PAIR)
+        if (s.turned) store_codes<E4M3, CHECK, V>(to + partner<NEOX>(p.half), f + V, inv);
+    };
+    if (held) {
+#pragma unroll
+      for (int k = 0; k < HELD; ++k)
+        if (mine_too && row0 + k * rows_at_once < count) write(row0 + k * rows_at_once, spot, x[k]);
+    } else {
+      for (uint32_t i = l; i < n; i += lanes) {
+        const uint32_t row = div_by(r.div_items, i), item = i - row * r.items;
+        const Spot s = spot_of<V, NEOX>(item, r.rot_items, r.rot_start, p.half);
+        read(row, s, item, x[0]);
+        write(row, s, x[0]);
+      }
+    }
+  };
+  if (E4M3 && check)
+    encode(std::true_type());
+  else
+    encode(std::false_type());
   if (mine && l == 0 && (at.before == 0 || now != old)) *scale_at = now;
 }
 
 template <typename T, int V, bool NEOX, bool E4M3>
-__global__ __launch_bounds__(kQ8Block) void append_q8_kernel(AppendQ8Plan p) {
-  const int64_t all = p.kv_blocks + p.query_blocks;
-  for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
-    if (block >= p.kv_blocks) {
-      rotate_queries<T, V, NEOX>(p, block - p.kv_blocks);
-      continue;
-    }
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int64_t w = block * (kQ8Block / 64) + wave;
-    const int64_t u = p.idx32 ? int64_t(div_by(p.div_groups, uint32_t(w))) : w / p.head_groups;
-    Place at;
-    if (u >= p.places || !find_place(p, u, &at)) continue;
-    const int32_t head2 = int32_t(w - u * p.head_groups) * (64 >> p.lanes_log2) +
-                          ((int32_t(threadIdx.x) & 63) >> p.lanes_log2);
-    append_block<T, V, NEOX, E4M3>(p, at, head2);
+__global__ __launch_bounds__(kQ8Block) __attribute__((amdgpu_waves_per_eu(6))) void
+append_q8_kernel(AppendQ8Plan p) {
+  const int64_t block = p.first_block + blockIdx.x;
+  if (block >= p.kv_blocks) {
+    rotate_queries<T, V, NEOX>(p, block - p.kv_blocks);
+    return;
   }
+  int64_t w = block;  // a workgroup's part of a place, or a wavefront's
+  if (p.lanes <= 64)
+    w = block * (kQ8Block / 64) + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int64_t u = p.idx32 ? int64_t(div_by(p.div_groups, uint32_t(w))) : w / p.head_groups;
+  Place at;
+  if (u >= p.places || !find_place(p, u, &at)) return;
+  // the first half of a place's wavefronts takes keys, the second values
+  int32_t group = int32_t(w - u * p.head_groups);
+  const bool keys = group < p.head_groups / 2;
+  if (!keys) group -= p.head_groups / 2;
+  int32_t head = group;
+  if (p.lanes < 64)
+    head = group * (64 >> p.lanes_log2) + ((int32_t(threadIdx.x) & 63) >> p.lanes_log2);
+  if (head >= p.heads) head = -1;
+  if (keys)
+    append_block<T, V, NEOX, E4M3, true>(p, p.kv[0], at, head);
+  else
+    append_block<T, V, NEOX, E4M3, false>(p, p.kv[1], at, head);
 }
 
 template <typename T, bool E4M3>
@@ -341,7 +477,12 @@ ROPE_API int rope_append_paged_cache_q8(
   const void *fn = plan.dt == ROPE_F32   ? pick_append_q8_codes<float>(plan)
                    : plan.dt == ROPE_F16 ? pick_append_q8_codes<_Float16>(plan)
                                          : pick_append_q8_codes<__bf16>(plan);
-  // a launch has fewer than 2^32 threads: more blocks than that are taken in turns
-  const int64_t blocks = std::min(plan.kv_blocks + plan.query_blocks, int64_t(1) << 23);
-  return launch_kernel(fn, dim3(uint32_t(blocks)), kQ8Block, 0, stream, &plan);
+  // a launch has fewer than 2^32 threads
+  const int64_t blocks = plan.kv_blocks + plan.query_blocks, most = int64_t(1) << 23;
+  for (; plan.first_block < blocks; plan.first_block += most) {
+    const int64_t n = std::min(blocks - plan.first_block, most);
+    const int rc = launch_kernel(fn, dim3(uint32_t(n)), kQ8Block, 0, stream, &plan);
+    if (rc != ROPE_OK) return rc;
+  }
+  return ROPE_OK;
 }

@@ -205,7 +205,8 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
     r.rot_start = int32_t(query_rot_start);
     r.rot_items = uint32_t(p.neox ? rd / 2 / step : rd / run);
     r.items = r.rot_items + (in_place ? 0u : uint32_t((query->shape[2] - rd) / step));
-    r.total = uint32_t(query->shape[1]) * r.items;
+    p.query_heads = query->shape[1];
+    r.total = uint32_t((query->shape[1] + kQueryHeads - 1) / kQueryHeads) * r.items;
     r.all = T * int64_t(r.total);  // below 2^30 * 2^24
     r.div_items = make_fastdiv(std::max(1u, r.items));
     r.div_total = make_fastdiv(std::max(1u, r.total));
@@ -219,7 +220,11 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
     p.block = int32_t(key_cache->shape[1] / key_scales->shape[1]);
     p.div_block = make_fastdiv(uint32_t(p.block));
     const rope_tensor *caches[2] = {key_cache, value_cache}, *scales[2] = {key_scales, value_scales};
-    int64_t most = 1;
+    const int64_t spread = T / p.block + 2 * p.seq.B;
+    p.by_token = T <= spread;
+    p.places = p.by_token ? T : spread;
+    const int64_t tokens = p.by_token ? 1 : p.block;  // of a place; numbered by token, mostly one
+    int64_t lanes = 4;  // that hold them
     for (int g = 0; g < 2; ++g) {
       Q8Rows &r = p.kv[g];
       const rope_tensor *in = ins[g + 1], *c = caches[g], *s = scales[g];
@@ -241,19 +246,24 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
       r.rot_items = uint32_t(p.neox ? turned / 2 / step : turned / run);
       r.items = r.rot_items + uint32_t((in->shape[2] - turned) / step);
       r.div_items = make_fastdiv(std::max(1u, r.items));
-      most = std::max<int64_t>(most, std::min<int64_t>(p.block, T) * r.items);
+      while ((uint32_t(1) << r.row_log2) < r.items) ++r.row_log2;
+      const int64_t item = g == 0 && (p.neox || step == 1) ? 2 * step : step;  // elements held for one
+      lanes = std::max({lanes, (tokens << r.row_log2) * item / kQ8Held,
+                        std::min(int64_t(64), int64_t(1) << r.row_log2)});
     }
-    // lanes of a head's block: as its items need, up to the wavefront
     p.lanes = 4;
-    p.lanes_log2 = 2;
-    while (p.lanes < 64 && p.lanes < most) p.lanes *= 2, ++p.lanes_log2;
-    p.head_groups = int32_t((2 * int64_t(p.heads) + 64 / p.lanes - 1) / (64 / p.lanes));
-    const int64_t spread = T / p.block + 2 * p.seq.B;
-    p.by_token = T <= spread;
-    p.places = p.by_token ? T : spread;
+    while (p.lanes < 64 && p.lanes < lanes) p.lanes *= 2;
+    if (p.lanes < lanes) p.lanes = kQ8Block;
+    while ((1 << p.lanes_log2) != p.lanes) ++p.lanes_log2;
+    for (Q8Rows &r : p.kv) {  // a row's items of one wavefront
+      r.side_by_side = (1 << r.row_log2) <= std::min(p.lanes, 64);
+      if (!r.side_by_side) r.row_log2 = 0;
+    }
+    const int64_t heads_each = std::max(1, 64 / p.lanes), units = p.lanes > 64 ? 1 : kQ8Block / 64;
+    p.head_groups = 2 * int32_t((p.heads + heads_each - 1) / heads_each);
     p.div_groups = make_fastdiv(uint32_t(p.head_groups));
-    p.kv_blocks = (p.places * p.head_groups + kQ8Block / 64 - 1) / (kQ8Block / 64);
-    p.idx32 = p.idx32 && p.kv_blocks * (kQ8Block / 64) < (int64_t(1) << 31);
+    p.kv_blocks = (p.places * p.head_groups + units - 1) / units;
+    p.idx32 = p.idx32 && p.kv_blocks * units < (int64_t(1) << 31);
   }
   if (p.kv_blocks + p.query_blocks == 0) p.noop = true;
   return ROPE_OK;

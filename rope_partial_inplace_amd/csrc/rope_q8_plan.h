@@ -34,6 +34,8 @@ struct Q8Rows {
   uint32_t rot_items = 0;  // rotated items of a row, in the order of AppendRows
   uint32_t items = 0;
   bool wide_rows = false;  // code rows split into aligned 16-byte pieces
+  bool side_by_side = false;  // a row's items fit the threads of a block, 2^row_log2 of them
+  int32_t row_log2 = 0;
   FastDiv div_items;
 };
 
@@ -41,15 +43,17 @@ struct AppendQ8Plan {
   rope_dtype dt = ROPE_F32;
   bool neox = true, vector_io = false, noop = false, e4m3 = false;
   bool idx32 = true;  // query items and wavefronts are numbered in 32 bits
-  // A wavefront takes one place of tokens (one block of a sequence) and several of its heads.
+  // A wavefront (for long blocks a workgroup) takes one place of tokens (one block of a sequence) and several of its heads.
   // Places are numbered so that their sequence can be found from the offsets alone: by token, where
   // all but a block's first new token have nothing to do, or, fewer for long appends, from
   // offsets[b] / block + 2 b on, which is enough for the blocks a sequence's tokens can touch.
   bool by_token = true;
-  int32_t lanes = 64;      // lanes of a head's block: a power of two
-  int32_t lanes_log2 = 6;
+  int32_t lanes = 64;      // threads of a head's block: a power of two up to 64, or 256
+  int32_t lanes_log2 = 0;
   int64_t places = 0, kv_blocks = 0, query_blocks = 0;
-  int32_t head_groups = 1;  // wavefronts of a place
+  int64_t first_block = 0;  // of a launch
+  int64_t query_heads = 0;
+  int32_t head_groups = 2;  // wavefronts of a place: half of them for keys, half for values
   int32_t heads = 0;
   int32_t block = 1;  // tokens of a scale
   int32_t half = 0;   // rotaryDim / 2
@@ -64,6 +68,8 @@ struct AppendQ8Plan {
 };
 
 constexpr int kQ8Block = 256;
+constexpr int kQueryHeads = 4;
+constexpr int kQ8Held = 32;  // elements that a thread holds
 
 int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const rope_tensor *key,
                    const rope_tensor *value, const rope_tensor *cos_sin_cache,
