@@ -31,7 +31,7 @@ KERNEL_SOURCES = [os.path.join(CSRC, n) for n in
 HEADERS = [os.path.join(CSRC, n) for n in
            ("rope_plan.h", "rope_append_plan.h", "rope_latent_plan.h", "rope_check.h", "rope_io.h",
             "rope_launch.h", "rope_mfma.h", "rope_q8_plan.h", "rope_q8.h",
-            "rope_q8_attn.h", "rope_pages_plan.h")]
+            "rope_q8_attn.h", "rope_q8_rows.h", "rope_pages_plan.h")]
 SOURCES = HOST_SOURCES + KERNEL_SOURCES
 # Everything the library is built from; its digest is written beside the library (STAMP_PATH)
 # so that a library older than its sources is noticed before it is tested.

@@ -14,8 +14,8 @@
 // wavefronts of a workgroup, which take every fourth 32 tokens each, join their sums at the end.
 //
 // Layout (16x16x32 products, lane l = 16 g + c):
-//   S^T = K Q^T: A[key c][8 d], lane's d = 64 i + 16 g + 8 e + 0..7 for product (i, e): 16 bytes a load
-//   and two products; register r of S^T: key 4 g + r of query row c.
+//   S^T = K Q^T: A[key c][8 d], lane's d = g D / 4 + 16 i + 8 e + 0..7 for product (i, e): 16 bytes a load
+//   and two products, and each load touches whole 128-byte lines; register r of S^T: key 4 g + r of query row c.
 //   O^T = V^T P^T: the lane's eight keys are those of its two S^T registers sets, 4 g + r and
 //   16 + 4 g + r, so P stays where it was computed; it loads D / 16 neighbouring bytes of each of the
 //   eight tokens (16 lanes: a whole row) and turns them: column t of the eight is the A operand of
@@ -106,55 +106,90 @@ struct Operand<T, false> {
   }
 };
 
-// What a sequence asks for.
+// What a sequence asks for: its query rows (token by token, the heads of a group one after the other) in
+// tiles.  A tile's steps end with the last token that one of its rows sees, so of causal rows a later
+// tile has more steps; the k-th tile from the end and the k-th from the front make a pair, and all
+// pairs, of every key head, cost alike.
 struct SequenceQ8 {
   int32_t len, first, count;  // cached tokens; first query token, query tokens (below 0: descending)
-  int32_t items, steps;       // items of a key head; steps of an item
-  __device__ int64_t cost(int kv_heads) const {
-    return int64_t(items) * kv_heads * (steps + kQ8ItemCost);
+  int32_t tiles;
+  int32_t cost;               // of a pair
+  __device__ int32_t pairs() const { return (tiles + 1) / 2; }
+};
+
+template <int ROWS, int STEP>
+struct WorkQ8 {
+  const AttnQ8Plan &p;
+
+  // Tokens that the last row of a tile sees, and its steps.
+  __device__ int32_t visible(const SequenceQ8 &s, int32_t tile) const {
+    const int32_t rows = s.count * p.group;
+    const int32_t tok = int32_t(div_by(p.div_group, uint32_t(min((tile + 1) * ROWS, rows) - 1)));
+    return max(0, s.len - s.count + 1 + tok);
+  }
+  __device__ int32_t steps(const SequenceQ8 &s, int32_t tile) const {
+    return max(1, (visible(s, tile) + STEP - 1) / STEP);
+  }
+  // Lengths and offsets are device data: values outside their ranges are clamped.
+  __device__ SequenceQ8 sequence(int32_t b) const {
+    const Sequences &q = p.seq;
+    SequenceQ8 s;
+    s.len = int32_t(min(max(q.lens[b * q.len_stride], int64_t(0)), q.max_pages * q.page_size));
+    if (q.offsets != nullptr) {
+      const int64_t o0 = min(max(q.offsets[b * q.off_stride], int64_t(0)), q.T);
+      const int64_t o1 = min(max(q.offsets[(b + 1) * q.off_stride], int64_t(0)), q.T);
+      s.first = int32_t(o0);
+      s.count = int32_t(o1 - o0);
+    } else {
+      s.first = int32_t(b * q.each);
+      s.count = int32_t(q.each);
+    }
+    s.tiles = (max(s.count, 0) * p.group + ROWS - 1) / ROWS;
+    s.cost = 0;
+    if (s.tiles > 0) {
+      s.cost = steps(s, s.tiles - 1) + kQ8ItemCost;
+      // the first tile beside the last; other pairs see up to ROWS rows' tokens more than this one
+      if (s.tiles > 1) s.cost += steps(s, 0) + kQ8ItemCost + ROWS / STEP + 2;
+    }
+    return s;
+  }
+  __device__ int64_t cost(const SequenceQ8 &s) const {
+    return int64_t(s.pairs()) * p.kv_heads * s.cost;
   }
 };
 
-// Lengths and offsets are device data: values outside their ranges are clamped.
-__device__ inline SequenceQ8 sequence_q8(const AttnQ8Plan &p, int32_t b, int rows) {
-  const Sequences &q = p.seq;
-  SequenceQ8 s;
-  s.len = int32_t(min(max(q.lens[b * q.len_stride], int64_t(0)), q.max_pages * q.page_size));
-  if (q.offsets != nullptr) {
-    const int64_t o0 = min(max(q.offsets[b * q.off_stride], int64_t(0)), q.T);
-    const int64_t o1 = min(max(q.offsets[(b + 1) * q.off_stride], int64_t(0)), q.T);
-    s.first = int32_t(o0);
-    s.count = int32_t(o1 - o0);
-  } else {
-    s.first = int32_t(b * q.each);
-    s.count = int32_t(q.each);
-  }
-  s.items = (max(s.count, 0) * p.group + rows - 1) / rows;
-  s.steps = max(1, (s.len + int32_t(kQ8Step) - 1) / int32_t(kQ8Step));
-  return s;
+// How a tile's tokens are found.  kCoarse: pages of whole runs of 16 tokens and scales of whole runs of 4: a
+// half tile lies in one page, whose number is the same for all lanes, and a lane's four neighbouring
+// tokens under one scale.  kFine: such pages, any scales: a lane reads those of one token, and the others'
+// come from its neighbours.  kAny: pages of any size, too.
+enum { kAny = 0, kFine = 1, kCoarse = 2 };
+
+// Keys, or values, of 32 tokens: a lane's codes, and its tokens' scales.
+template <int D, int MODE>
+struct KeysQ8 {
+  uint4 code[2][D / 64];
+  float scale[MODE == kCoarse ? 2 : 1];
+};
+template <int D, int MODE>
+struct ValuesQ8 {
+  uint32_t code[8][D / 64];
+  float scale[MODE == kCoarse ? 2 : 1];
+};
+
+// Scale of the lane's token j of eight: 16 (j / 4) + 4 g + j % 4 of the tile.
+template <int MODE>
+__device__ __forceinline__ float scale_of(const float *s, int j, int lane) {
+  if constexpr (MODE == kCoarse) return s[j / 4];
+  return __shfl(s[0], 16 * (j / 4) + 4 * (lane >> 4) + j % 4);
 }
 
-// 32 tokens of a key head: codes, and the scales of the lane's keys in S^T.
-template <int D, bool RUNS>
-struct TileQ8 {
-  static constexpr int W = D / 64;
-  static constexpr int SC = RUNS ? 2 : 8;
-  uint4 k[2][W];
-  uint32_t v[8][W];
-  float ks[SC], vs[SC];
-  __device__ float key_scale(int j) const { return ks[RUNS ? j / 4 : j]; }
-  __device__ float value_scale(int j) const { return vs[RUNS ? j / 4 : j]; }
-};
-
-// Where a tile lies: runs of 16 tokens in one page each, the same for all lanes; or a token a lane.
-template <bool RUNS>
-struct WhereQ8;
-template <>
-struct WhereQ8<true> {
+// Where a tile lies: the pages of its halves, or the page and row of a token a lane.
+template <int MODE>
+struct WhereQ8 {
   int64_t page[2];
 };
 template <>
-struct WhereQ8<false> {
+struct WhereQ8<kAny> {
   int32_t page, row;
 };
 
@@ -164,11 +199,11 @@ __device__ inline int64_t page_of(const Sequences &s, int32_t b, int32_t index) 
 }
 
 // Tokens past the last one (`last`) repeat it.
-template <bool RUNS>
-__device__ __forceinline__ WhereQ8<RUNS> locate(const Sequences &s, int32_t b, int32_t t0,
+template <int MODE>
+__device__ __forceinline__ WhereQ8<MODE> locate(const Sequences &s, int32_t b, int32_t t0,
                                                 int32_t last, int lane) {
-  WhereQ8<RUNS> w;
-  if constexpr (RUNS) {
+  WhereQ8<MODE> w;
+  if constexpr (MODE != kAny) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       w.page[h] = page_of(s, b, int32_t(div_by(s.div_page, uint32_t(min(t0 + 16 * h, last)))));
@@ -198,52 +233,97 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&v)[W]) {
   }
 }
 
-template <int D, bool RUNS>
-__device__ __forceinline__ void load_tile(const AttnQ8Plan &p, const WhereQ8<RUNS> &w, int32_t t0,
-                                          int32_t last, int64_t head, int lane,
-                                          TileQ8<D, RUNS> &t) {
-  constexpr int W = D / 64;
-  const int c = lane & 15, g = lane >> 4;
-  if constexpr (RUNS) {
+// Half h of a tile in one page: its first row there, and how many tokens follow that row's.
+struct HalfQ8 {
+  int32_t row, more;
+};
+__device__ __forceinline__ HalfQ8 half_of(const Sequences &s, int32_t t0, int h, int32_t last) {
+  const int32_t begin = min(t0 + 16 * h, last);
+  return {begin - int32_t(div_by(s.div_page, uint32_t(begin)) * uint32_t(s.page_size)), last - begin};
+}
+
+// The scales of a tile whose halves lie in one page each.
+template <int MODE>
+__device__ __forceinline__ void load_scales(const AttnQ8Plan &p, const Q8Cache &c,
+                                            const WhereQ8<MODE> &w, int32_t t0, int32_t last,
+                                            int64_t head, int lane, float *scale) {
+  if constexpr (MODE == kCoarse) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int32_t begin = min(t0 + 16 * h, last), more = last - begin;
-      const int32_t row = begin - int32_t(div_by(p.seq.div_page, uint32_t(begin)) *
-                                          uint32_t(p.seq.page_size));
-      const uint8_t *k = p.k.codes + w.page[h] * p.k.page + head * p.k.head + int64_t(row) * p.k.row;
-      const uint32_t at = uint32_t(min(c, more) * p.k.row + 16 * g);
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        t.k[h][i] = *reinterpret_cast<const uint4 *>(k + (at + 64 * i));
-      const uint8_t *v = p.v.codes + w.page[h] * p.v.page + head * p.v.head + int64_t(row) * p.v.row;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        load_words<W>(v + uint32_t(min(4 * g + j, more) * p.v.row + c * (D / 16)), t.v[4 * h + j]);
-      const int64_t block = div_by(p.div_block, uint32_t(row + min(4 * g, more)));
-      t.ks[h] = p.k.scales[w.page[h] * p.k.s_page + head * p.k.s_head + block * p.k.s_block];
-      t.vs[h] = p.v.scales[w.page[h] * p.v.s_page + head * p.v.s_head + block * p.v.s_block];
+      const HalfQ8 x = half_of(p.seq, t0, h, last);
+      const int64_t block = div_by(p.div_block, uint32_t(x.row + min(4 * (lane >> 4), x.more)));
+      scale[h] = c.scales[w.page[h] * c.s_page + head * c.s_head + block * c.s_block];
     }
+  } else if constexpr (MODE == kFine) {
+    const HalfQ8 a = half_of(p.seq, t0, 0, last), b = half_of(p.seq, t0, 1, last);
+    const bool up = (lane & 16) != 0;
+    const int32_t row = (up ? b.row : a.row) + min(lane & 15, up ? b.more : a.more);
+    const int64_t block = div_by(p.div_block, uint32_t(row));
+    scale[0] = c.scales[(up ? w.page[1] : w.page[0]) * c.s_page + head * c.s_head + block * c.s_block];
   } else {
     const int64_t block = div_by(p.div_block, uint32_t(w.row));
-    const float ks = p.k.scales[w.page * p.k.s_page + head * p.k.s_head + block * p.k.s_block];
-    const float vs = p.v.scales[w.page * p.v.s_page + head * p.v.s_head + block * p.v.s_block];
+    scale[0] = c.scales[w.page * c.s_page + head * c.s_head + block * c.s_block];
+  }
+}
+
+template <int D, int MODE>
+__device__ __forceinline__ void load_keys(const AttnQ8Plan &p, const WhereQ8<MODE> &w, int32_t t0,
+                                          int32_t last, int64_t head, int lane,
+                                          KeysQ8<D, MODE> &k) {
+  const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t *from;
+    uint32_t at = 0;
+    if constexpr (MODE != kAny) {
+      const HalfQ8 x = half_of(p.seq, t0, h, last);
+      from = p.k.codes + w.page[h] * p.k.page + head * p.k.head + int64_t(x.row) * p.k.row;
+      at = uint32_t(min(c, x.more) * p.k.row + D / 4 * g);
+    } else {
+      const int64_t page = __shfl(w.page, 16 * h + c), row = __shfl(w.row, 16 * h + c);
+      from = p.k.codes + page * p.k.page + head * p.k.head + row * p.k.row + D / 4 * g;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+      k.code[h][i] = *reinterpret_cast<const uint4 *>(from + (at + 16 * i));
+  }
+  load_scales<MODE>(p, p.k, w, t0, last, head, lane, k.scale);
+}
+
+template <int D, int MODE>
+__device__ __forceinline__ void load_values(const AttnQ8Plan &p, const WhereQ8<MODE> &w, int32_t t0,
+                                            int32_t last, int64_t head, int lane,
+                                            ValuesQ8<D, MODE> &v) {
+  const int c = lane & 15, g = lane >> 4;
+  if constexpr (MODE != kAny) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t page = __shfl(w.page, 16 * h + c), row = __shfl(w.row, 16 * h + c);
-      const uint8_t *k = p.k.codes + page * p.k.page + head * p.k.head + row * p.k.row + 16 * g;
+      const HalfQ8 x = half_of(p.seq, t0, h, last);
+      const uint8_t *from =
+          p.v.codes + w.page[h] * p.v.page + head * p.v.head + int64_t(x.row) * p.v.row;
 #pragma unroll
-      for (int i = 0; i < W; ++i) t.k[h][i] = *reinterpret_cast<const uint4 *>(k + 64 * i);
+      for (int j = 0; j < 4; ++j)
+        load_words(from + uint32_t(min(4 * g + j, x.more) * p.v.row + c * (D / 16)),
+                   v.code[4 * h + j]);
     }
+  } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int key = 16 * (j / 4) + 4 * g + j % 4;
       const int64_t page = __shfl(w.page, key), row = __shfl(w.row, key);
-      load_words<W>(p.v.codes + page * p.v.page + head * p.v.head + row * p.v.row + c * (D / 16),
-                    t.v[j]);
-      t.ks[j] = __shfl(ks, key);
-      t.vs[j] = __shfl(vs, key);
+      load_words(p.v.codes + page * p.v.page + head * p.v.head + row * p.v.row + c * (D / 16),
+                 v.code[j]);
     }
   }
+  load_scales<MODE>(p, p.v, w, t0, last, head, lane, v.scale);
+}
+
+// The power of two above x >= 0, within those whose reciprocal is one, too; and that of such a power.
+__device__ inline float reach_above(float x) {
+  return __uint_as_float((min(max(__float_as_uint(x) >> 23, 1u), 252u) + 1u) << 23);
+}
+__device__ inline float inverse_power(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
 }
 
 // A wavefront's running state for R tiles of 16 query rows; the lane's row of a tile is row c.
@@ -258,33 +338,35 @@ struct StateQ8 {
   float reach, by_reach;
 };
 
-template <typename T, int D, int R, bool E4M3, bool RUNS>
-__device__ __forceinline__ void attend_tile(const TileQ8<D, RUNS> &t, StateQ8<T, D, R> &s,
-                                            int32_t t0, int32_t floor, float scale_log2, int lane) {
-  constexpr int W = D / 64;
+// Scores of a tile in powers of two, masked where not every row sees all of it (t0 + 32 above `floor`).
+template <typename T, int D, int R, bool E4M3, int MODE>
+__device__ __forceinline__ void score_tile(const KeysQ8<D, MODE> &k, const StateQ8<T, D, R> &s,
+                                           int32_t t0, int32_t floor, float scale_log2, int lane,
+                                           f32x4 (&x)[R][2]) {
   const int g = lane >> 4;
   using Op = Operand<T, E4M3>;
-  f32x4 x[R][2];
 #pragma unroll
   for (int r = 0; r < R; ++r) x[r][0] = x[r][1] = f32x4{};
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const s16x8 a = Op::row(t.k[h][i].x, t.k[h][i].y), b = Op::row(t.k[h][i].z, t.k[h][i].w);
+    for (int i = 0; i < D / 64; ++i) {
+      const uint4 w = k.code[h][i];
+      const s16x8 a = Op::row(w.x, w.y), b = Op::row(w.z, w.w);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         x[r][h] = Mfma<T>::mul16(a, s.q[r][2 * i], x[r][h]);
         x[r][h] = Mfma<T>::mul16(b, s.q[r][2 * i + 1], x[r][h]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
-  // scores in powers of two
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int j = 0; j < 8; ++j) {
+    const float f = scale_of<MODE>(k.scale, j, lane) * scale_log2;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[r][j / 4][j % 4] *= t.key_scale(j) * scale_log2;
-  const bool masked = t0 + kTile > floor;
-  if (masked) {
+    for (int r = 0; r < R; ++r) x[r][j / 4][j % 4] *= f;
+  }
+  if (t0 + kTile > floor) {
     asm volatile("");  // a branch: most tiles need no masks
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -292,8 +374,16 @@ __device__ __forceinline__ void attend_tile(const TileQ8<D, RUNS> &t, StateQ8<T,
       for (int j = 0; j < 8; ++j)
         if (t0 + 16 * (j / 4) + 4 * g + j % 4 >= s.limit[r]) x[r][j / 4][j % 4] = kNegInf;
   }
-  // A row's maximum is raised only when a tile passes it by more than kSlack; until then larger weights
-  // are carried, which changes no result beyond its rounding.
+}
+
+// The weights of a tile, at maxima that are raised where a score passes one by more than kSlack (until
+// then larger weights are carried, which changes no result beyond its rounding), and
+// O^T += V^T P^T.
+template <typename T, int D, int R, bool E4M3, int MODE>
+__device__ __forceinline__ void weigh_tile(const ValuesQ8<D, MODE> &v, StateQ8<T, D, R> &s,
+                                           int32_t t0, int32_t floor, int lane,
+                                           const f32x4 (&x)[R][2]) {
+  const int g = lane >> 4;
   float best[R];
   bool raise = false;
 #pragma unroll
@@ -304,22 +394,19 @@ __device__ __forceinline__ void attend_tile(const TileQ8<D, RUNS> &t, StateQ8<T,
     best[r] = max_quarters(m);
     raise |= best[r] > s.top[r] + Mfma<T>::kSlack;
   }
-  float vs[RUNS ? 2 : 8];
+  constexpr int SC = MODE == kCoarse ? 2 : 1;
+  if constexpr (Mfma<T>::kNarrow) {
 #pragma unroll
-  for (int j = 0; j < (RUNS ? 2 : 8); ++j) {
-    vs[j] = t.vs[j];
-    if constexpr (Mfma<T>::kNarrow) raise |= fabsf(vs[j]) > s.reach;
+    for (int j = 0; j < SC; ++j) raise |= fabsf(v.scale[j]) > s.reach;
   }
   if (__any(raise)) {
     float reach = s.reach;
     if constexpr (Mfma<T>::kNarrow) {
       float most = 0.0f;
 #pragma unroll
-      for (int j = 0; j < (RUNS ? 2 : 8); ++j) most = fmaxf(most, fabsf(vs[j]));
+      for (int j = 0; j < SC; ++j) most = fmaxf(most, fabsf(v.scale[j]));
       for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-      // the power of two above it, within those whose reciprocal is one, too
-      const uint32_t e = min(max(__float_as_uint(most) >> 23, 1u), 252u) + 1u;
-      if (most > reach) reach = __uint_as_float(e << 23);
+      if (most > reach) reach = reach_above(most);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -329,63 +416,76 @@ __device__ __forceinline__ void attend_tile(const TileQ8<D, RUNS> &t, StateQ8<T,
         s.top[r] = best[r];
       }
       s.sum[r] *= f;
-      if constexpr (Mfma<T>::kNarrow) f *= s.reach * __uint_as_float((254u << 23) - __float_as_uint(reach));
+      if constexpr (Mfma<T>::kNarrow) f *= s.reach * inverse_power(reach);
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) s.o[r][n] *= f;
     }
     if constexpr (Mfma<T>::kNarrow) {
       s.reach = reach;
-      s.by_reach = __uint_as_float((254u << 23) - __float_as_uint(reach));
+      s.by_reach = inverse_power(reach);
     }
   }
-  if constexpr (Mfma<T>::kNarrow) {
+  float scale[SC];
 #pragma unroll
-    for (int j = 0; j < (RUNS ? 2 : 8); ++j) vs[j] *= s.by_reach;
+  for (int j = 0; j < SC; ++j) scale[j] = Mfma<T>::kNarrow ? v.scale[j] * s.by_reach : v.scale[j];
+  float e[R][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float vs = scale_of<MODE>(scale, j, lane);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float ref = s.top[r] == kNegInf ? 0.0f : s.top[r] - Mfma<T>::kLift;
+      const float y = __builtin_amdgcn_exp2f(x[r][j / 4][j % 4] - ref);
+      s.sum[r] += y;
+      e[r][j] = y * vs;
+    }
+  }
+  if (t0 + kTile > floor) {
+    asm volatile("");
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // whatever the scale of a token that the row does not see
+        if (t0 + 16 * (j / 4) + 4 * g + j % 4 >= s.limit[r]) e[r][j] = 0.0f;
   }
   s16x8 w[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float ref = s.top[r] == kNegInf ? 0.0f : s.top[r] - Mfma<T>::kLift;
-    float e[8];
+  for (int r = 0; r < R; ++r) w[r] = round8<T>(e[r]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float y = __builtin_amdgcn_exp2f(x[r][j / 4][j % 4] - ref);
-      s.sum[r] += y;
-      e[j] = y * vs[RUNS ? j / 4 : j];
-    }
-    if (masked) {
-      asm volatile("");
+  for (int i = 0; i < D / 64; ++i) {
+    uint32_t c[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // whatever the scale of a token that the row does not see
-        if (t0 + 16 * (j / 4) + 4 * g + j % 4 >= s.limit[r]) e[j] = 0.0f;
-    }
-    w[r] = round8<T>(e);
-  }
+    for (int j = 0; j < 8; ++j) c[j] = v.code[j][i];
+    auto multiply = [&](int n, const s16x8 &a, const s16x8 &b) {
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    uint32_t v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = t.v[j][i];
-    s16x8 a[4];
-    Op::template columns<false>(v, &a[0], &a[1]);
-    Op::template columns<true>(v, &a[2], &a[3]);
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int r = 0; r < R; ++r) s.o[r][4 * i + n] = Mfma<T>::mul16(a[n], w[r], s.o[r][4 * i + n]);
+      for (int r = 0; r < R; ++r) {
+        s.o[r][n] = Mfma<T>::mul16(a, w[r], s.o[r][n]);
+        s.o[r][n + 1] = Mfma<T>::mul16(b, w[r], s.o[r][n + 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // or the compiler converts everything first, and spills
+    };
+    s16x8 a, b;
+    Operand<T, E4M3>::template columns<false>(c, &a, &b);
+    multiply(4 * i, a, b);
+    Operand<T, E4M3>::template columns<true>(c, &a, &b);
+    multiply(4 * i + 2, a, b);
   }
 }
 
-// Sum over the workgroup's threads before this one, and of all (in `total`).
+// Sum over the workgroup's threads before this one, and of all (in `total`).  SMALL: sums fit 31 bits.
+template <bool SMALL>
 __device__ inline int64_t block_scan(int64_t x, int64_t *lds, int64_t *total) {
   const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
   int64_t incl = x;
+  if constexpr (SMALL) {
+    incl = wave_scan(int32_t(x));
+  } else {
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int64_t y = __shfl_up(incl, d);
-    if (lane >= d) incl += y;
+    for (int d = 1; d < 64; d *= 2) {
+      const int64_t y = __shfl_up(incl, d);
+      if (lane >= d) incl += y;
+    }
   }
-  __syncthreads();
   if (lane == 63) lds[wave] = incl;
   __syncthreads();
   int64_t base = 0, all = 0;
@@ -403,217 +503,314 @@ __device__ inline int64_t uniform64(int64_t x) {
                  uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(uint64_t(x))))));
 }
 
-template <typename T, int D, int R, bool E4M3, bool RUNS>
-__global__ __launch_bounds__(kAttnBlock) void attention_q8_kernel(AttnQ8Plan p) {
+// A piece of a workgroup's share: steps [st0, st1) of one tile of rows of one key head.
+struct SegmentQ8 {
+  int32_t head, row0, live;   // the tile's first row, and rows in it
+  int32_t steps, st0, st1;
+  int32_t hidden;             // + a row's token: cached tokens that the row sees
+  int32_t most;               // tokens that the last row sees
+  int64_t begin;              // where the tile's cost begins
+  int32_t part;               // 0: the first piece of the share
+  __device__ bool whole() const { return st0 == 0 && st1 == steps; }
+};
+
+struct ShareLds {
+  int64_t scan[2][kAttnWaves];
+  int64_t place;
+  SequenceQ8 found;
+  int32_t b, descends[kAttnWaves];
+};
+
+// A workgroup's share of the cost of all pairs, which it goes through piece by piece.  All members are the
+// same for all lanes.
+template <int ROWS, int STEP>
+struct ShareQ8 {
+  WorkQ8<ROWS, STEP> work;
+  int64_t per, w0, w1, w;   // the share [w0, w1), and where in it
+  int64_t *rec;
+  int32_t b, item, x;       // sequence, pair and key head, place in their cost
+  SequenceQ8 sq;
+  uint32_t partial = 0;     // bit s: part s of this workgroup is one of a tile's several
+
+  __device__ static int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+  // Finds the share; false where there is none.
+  __device__ bool begin(ShareLds &lds) {
+    const AttnQ8Plan &p = work.p;
+    const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+    const int32_t B = int32_t(p.seq.B);
+    const int64_t me = blockIdx.x;
+    // The first 256 sequences' sums say which one the share begins in, if it is one of them; later ones
+    // are gone through again.
+    SequenceQ8 s = {};
+    int64_t rest = 0, total, n = 0;
+    bool down = false;
+    if (tid < B) {
+      s = work.sequence(tid);
+      n = work.cost(s);
+      down = s.count < 0;
+    }
+    for (int32_t i = tid + kAttnBlock; i < B; i += kAttnBlock) {
+      const SequenceQ8 y = work.sequence(i);
+      rest += work.cost(y);
+      down |= y.count < 0;
+    }
+    down = __any(down);
+    if (lane == 0) lds.descends[wave] = down;
+    int64_t place = p.small ? block_scan<true>(n, lds.scan[0], &total)
+                            : block_scan<false>(n, lds.scan[0], &total);
+    int64_t before = total;  // of the sequences so far
+    if (B > kAttnBlock) {
+      int64_t all;
+      block_scan<false>(rest, lds.scan[1], &all);
+      total += all;
+    }
+#pragma unroll
+    for (int v = 0; v < kAttnWaves; ++v) down |= lds.descends[v] != 0;
+    total = uniform64(total);
+    per = p.small ? int64_t((uint32_t(total) + uint32_t(p.groups) - 1) / uint32_t(p.groups))
+                  : (total + p.groups - 1) / p.groups;
+    w = w0 = me * per;
+    w1 = min(total, w0 + per);
+    rec = p.joins + me * 2 * kQ8JoinWords;
+    if (down || w0 >= total) {
+      if (tid < 2) rec[tid * kQ8JoinWords] = 0;
+      return false;
+    }
+    for (int32_t b0 = 0;; b0 += kAttnBlock) {  // ends: w0 < total
+      if (b0 > 0) {
+        n = 0;
+        if (b0 + tid < B) {
+          s = work.sequence(b0 + tid);
+          n = work.cost(s);
+        }
+        int64_t all;
+        __syncthreads();  // the last round's sums have been read
+        place = before + block_scan<false>(n, lds.scan[0], &all);
+        before += all;
+      }
+      if (place <= w0 && w0 < place + n) {
+        lds.b = b0 + tid;
+        lds.place = place;
+        lds.found = s;
+      }
+      if (w0 < before) break;
+    }
+    __syncthreads();
+    b = uniform(lds.b);
+    sq = {uniform(lds.found.len), uniform(lds.found.first), uniform(lds.found.count),
+          uniform(lds.found.tiles), uniform(lds.found.cost)};
+    const int64_t into = w0 - uniform64(lds.place);
+    item = int32_t(p.small ? int64_t(uint32_t(into) / uint32_t(sq.cost)) : into / sq.cost);
+    x = int32_t(into - int64_t(item) * sq.cost);
+    return true;
+  }
+
+  // The piece that begins at w.
+  __device__ SegmentQ8 segment() {
+    const AttnQ8Plan &p = work.p;
+    const int32_t pair = int32_t(uint32_t(item) / uint32_t(p.kv_heads));
+    SegmentQ8 g;
+    g.head = item - pair * p.kv_heads;
+    int32_t tile = sq.tiles - 1 - pair, at = 0, end = sq.cost;
+    if (tile != pair) {  // two tiles: the longer one first
+      const int32_t border = work.steps(sq, tile) + kQ8ItemCost;
+      if (x < border) {
+        end = border;
+      } else {
+        at = border;
+        tile = pair;
+      }
+    }
+    g.row0 = tile * ROWS;
+    g.live = min(ROWS, sq.count * p.group - g.row0);
+    g.steps = work.steps(sq, tile);
+    g.most = work.visible(sq, tile);
+    g.hidden = sq.len - sq.count + 1;
+    g.begin = w - (x - at);
+    const int32_t x1 = int32_t(min(int64_t(end), x + (w1 - w)));
+    g.st0 = min(max(0, x - at - kQ8ItemCost), g.steps);
+    g.st1 = min(max(0, x1 - at - kQ8ItemCost), g.steps);
+    g.part = w == w0 ? 0 : 1;
+    w += x1 - x;
+    x = x1;
+    return g;
+  }
+
+  // Notes a piece that is not a whole tile, for the joining kernel: the tile's parts are those of n
+  // workgroups from `first` on.
+  __device__ void note(const SegmentQ8 &g) {
+    if (g.whole()) return;
+    partial |= 1u << g.part;
+    if (threadIdx.x == 0) {
+      const int64_t from = g.begin + kQ8ItemCost, first = from / per;
+      int64_t *to = rec + g.part * kQ8JoinWords;
+      to[0] = (from + g.steps - 1) / per - first + 1;
+      to[1] = first;
+      to[2] = g.begin <= first * per ? 0 : 1;
+      to[3] = sq.first;
+      to[4] = g.head;
+      to[5] = g.row0;
+      to[6] = g.live;
+    }
+  }
+
+  // On to the next piece; false at the end of the share.
+  __device__ bool next() {
+    if (w >= w1) {
+      if (threadIdx.x < 2 && (partial >> threadIdx.x & 1u) == 0) rec[threadIdx.x * kQ8JoinWords] = 0;
+      return false;
+    }
+    if (x >= sq.cost) {
+      x = 0;
+      if (++item >= sq.pairs() * work.p.kv_heads) {
+        item = 0;
+        do {  // ends: w < w1 <= total, so a later sequence has tiles
+          sq = work.sequence(++b);
+        } while (sq.tiles == 0);
+      }
+    }
+    return true;
+  }
+};
+
+// Where row `m` of a tile lies in the output, in rows of D.
+__device__ inline int64_t output_row(const AttnQ8Plan &p, const SegmentQ8 &g, int32_t first, int32_t m) {
+  const int32_t r = g.row0 + m, tok = int32_t(div_by(p.div_group, uint32_t(r)));
+  return int64_t(first + tok) * p.heads + g.head * p.group + r - tok * p.group;
+}
+
+template <typename T, int D, int R, bool E4M3, int MODE>
+__global__ __launch_bounds__(kAttnBlock) __attribute__((amdgpu_waves_per_eu(q8_waves(D, R)))) void
+attention_q8_kernel(AttnQ8Plan p) {
   constexpr int ROWS = 16 * R, N = D / 16;
   constexpr int LANE = 4 * N + 4;  // floats of a lane's outputs, kept apart by a chunk of 16 bytes
   __shared__ __attribute__((aligned(16))) float join_o[kAttnWaves][64 * LANE];
   __shared__ float join_top[kAttnWaves][16], join_sum[kAttnWaves][16];
-  __shared__ int64_t scan[kAttnWaves];
-  __shared__ int64_t found_at;
-  __shared__ int32_t found_b, descends;
+  __shared__ ShareLds share_lds;
 
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  auto uniform = [](int32_t x) { return __builtin_amdgcn_readfirstlane(x); };
-  const int32_t B = int32_t(p.seq.B);
-  const int64_t me = blockIdx.x;
+  ShareQ8<ROWS, int(kQ8Step)> share = {{p}};
+  if (!share.begin(share_lds)) return;
+  do {
+    const SegmentQ8 g = share.segment();
+    if (g.st0 >= g.st1) continue;
+    const SequenceQ8 &sq = share.sq;
+    // fewest tokens that a row sees
+    const int32_t floor = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0)));
 
-  // ---- this workgroup's share [w0, w1) of all items' cost ----
-  if (tid == 0) descends = 0;
-  __syncthreads();
-  int64_t mine = 0, total;
-  for (int32_t b = tid; b < B; b += kAttnBlock) {
-    const SequenceQ8 s = sequence_q8(p, b, ROWS);
-    mine += s.cost(p.kv_heads);
-    if (s.count < 0) descends = 1;
-  }
-  block_scan(mine, scan, &total);
-  const int64_t per = (total + p.groups - 1) / p.groups;
-  const int64_t w0 = me * per, w1 = min(total, w0 + per);
-  int64_t *rec = p.joins + me * 2 * kQ8JoinWords;
-  if (descends || w0 >= total) {
-    if (tid < 2) rec[tid * kQ8JoinWords] = 0;
-    return;
-  }
-  int64_t before = 0;
-  for (int32_t b0 = 0;; b0 += kAttnBlock) {  // ends: w0 < total
-    int64_t n = 0, all;
-    if (b0 + tid < B) n = sequence_q8(p, b0 + tid, ROWS).cost(p.kv_heads);
-    const int64_t at = before + block_scan(n, scan, &all);
-    if (at <= w0 && w0 < at + n) {
-      found_b = b0 + tid;
-      found_at = at;
+    StateQ8<T, D, R> s;
+    s.reach = 0x1p-120f;
+    s.by_reach = 0x1p120f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int32_t m = r * 16 + (lane & 15);
+      const bool some = m < g.live;
+      const int32_t tok = int32_t(div_by(p.div_group, uint32_t(g.row0 + (some ? m : 0))));
+      const int32_t h = g.head * p.group + g.row0 + (some ? m : 0) - tok * p.group;
+      s.limit[r] = some ? g.hidden + tok : 0;
+      s.top[r] = kNegInf;
+      s.sum[r] = 0.0f;
+      const T *q = static_cast<const T *>(p.q) + int64_t(sq.first + tok) * p.q_tok +
+                   int64_t(h) * p.q_head + D / 4 * (lane >> 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        s.q[r][i] = some ? as_operand(*reinterpret_cast<const uint4 *>(q + 8 * i)) : s16x8{};
+#pragma unroll
+      for (int n = 0; n < N; ++n) s.o[r][n] = f32x4{};
     }
-    before += all;
-    if (w0 < before) break;
-  }
-  __syncthreads();
-  int32_t b = uniform(found_b);
-  SequenceQ8 sq = sequence_q8(p, b, ROWS);
-  int64_t w = w0;
-  int32_t item, x0;
-  {
-    const int64_t into = w0 - uniform64(found_at);
-    const int64_t cost = sq.steps + kQ8ItemCost;
-    item = int32_t(into / cost);
-    x0 = int32_t(into - item * cost);
-  }
-  uint32_t partial = 0;  // bit s: part s of this workgroup is one of an item's several
-
-  while (true) {
-    const int32_t cost = sq.steps + kQ8ItemCost;
-    const int32_t x1 = int32_t(min(int64_t(cost), x0 + (w1 - w)));
-    const int32_t st0 = max(0, x0 - kQ8ItemCost), st1 = max(0, x1 - kQ8ItemCost);
-    if (st0 < st1) {
-      const int32_t head = int32_t(uint32_t(item) % uint32_t(p.kv_heads));
-      const int32_t row0 = int32_t(uint32_t(item) / uint32_t(p.kv_heads)) * ROWS;
-      const int32_t rows = sq.count * p.group, live = min(ROWS, rows - row0);
-      const int32_t hidden = sq.len - sq.count + 1;  // + token: tokens that it sees
-      // fewest and most tokens that a row sees
-      const int32_t floor = hidden + int32_t(div_by(p.div_group, uint32_t(row0)));
-      const int32_t most = min(sq.len, hidden + int32_t(div_by(p.div_group, uint32_t(row0 + live - 1))));
-
-      StateQ8<T, D, R> s;
-      s.reach = 0x1p-120f;
-      s.by_reach = 0x1p120f;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int32_t m = r * 16 + (lane & 15);
-        const bool some = m < live;
-        const int32_t tok = int32_t(div_by(p.div_group, uint32_t(row0 + (some ? m : 0))));
-        const int32_t h = head * p.group + row0 + (some ? m : 0) - tok * p.group;
-        s.limit[r] = some ? hidden + tok : 0;
-        s.top[r] = kNegInf;
-        s.sum[r] = 0.0f;
-        const T *q = static_cast<const T *>(p.q) + int64_t(sq.first + tok) * p.q_tok +
-                     int64_t(h) * p.q_head + 16 * (lane >> 4);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          s.q[r][i] = some ? as_operand(*reinterpret_cast<const uint4 *>(q + 64 * (i / 2) + 8 * (i % 2)))
-                           : s16x8{};
-#pragma unroll
-        for (int n = 0; n < N; ++n) s.o[r][n] = f32x4{};
-      }
-      {
-        const int32_t last = sq.len - 1;
-        int32_t t0 = st0 * int32_t(kQ8Step) + wave * kTile;
-        const int32_t end = min(st1 * int32_t(kQ8Step), most);
-        auto at = [&](int32_t t) { return locate<RUNS>(p.seq, b, t, last, lane); };
-        if (t0 < end) {
-          TileQ8<D, RUNS> a, c;
-          load_tile<D, RUNS>(p, at(t0), t0, last, head, lane, a);
-          WhereQ8<RUNS> next = at(t0 + int32_t(kQ8Step));
-          while (true) {  // ends: t0 grows
-            int32_t t1 = t0 + int32_t(kQ8Step);
-            if (t1 < end) {
-              load_tile<D, RUNS>(p, next, t1, last, head, lane, c);
-              next = at(t1 + int32_t(kQ8Step));
-            }
-            attend_tile<T, D, R, E4M3, RUNS>(a, s, t0, floor, p.scale_log2, lane);
-            if (t1 >= end) break;
-            t0 = t1 + int32_t(kQ8Step);
-            if (t0 < end) {
-              load_tile<D, RUNS>(p, next, t0, last, head, lane, a);
-              next = at(t0 + int32_t(kQ8Step));
-            }
-            attend_tile<T, D, R, E4M3, RUNS>(c, s, t1, floor, p.scale_log2, lane);
-            if (t0 >= end) break;
-          }
-        }
-      }
-
-      // ---- the wavefronts' sums, joined 16 rows at a time; 16 threads a row ----
-      const bool whole = st0 == 0 && st1 == sq.steps;
-      const int part = w == w0 ? 0 : 1;
-      const int64_t slot = me * 2 + part;
-      const int m = tid >> 4, gr = tid & 15;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float sum = sum_quarters(s.sum[r]);
-        const float unit = Mfma<T>::kNarrow ? s.reach : 1.0f;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int n = 0; n < N; n += 4)
-            *reinterpret_cast<f32x4 *>(&join_o[wave][lane * LANE + k * N + n]) =
-                f32x4{s.o[r][n][k], s.o[r][n + 1][k], s.o[r][n + 2][k], s.o[r][n + 3][k]} * unit;
-        if (lane < 16) {
-          join_top[wave][lane] = s.top[r];
-          join_sum[wave][lane] = sum;
-        }
-        __syncthreads();
-        const int row = r * 16 + m;
-        if (row >= live) continue;
-        float top = join_top[0][m];
-#pragma unroll
-        for (int v = 1; v < kAttnWaves; ++v) top = fmaxf(top, join_top[v][m]);
-        float l = 0.0f, o[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) o[n] = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kAttnWaves; ++v) {
-          const float f = __builtin_amdgcn_exp2f(join_top[v][m] - (top == kNegInf ? 0.0f : top));
-          l += f * join_sum[v][m];
-          const float *from = &join_o[v][((gr >> 2) * 16 + m) * LANE + (gr & 3) * N];
-#pragma unroll
-          for (int n = 0; n < N; n += 4) {
-            const f32x4 y = *reinterpret_cast<const f32x4 *>(from + n);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n + e] += f * y[e];
-          }
-        }
-        if (whole) {
-          const int32_t tok = int32_t(div_by(p.div_group, uint32_t(row0 + row)));
-          const int64_t at = int64_t(sq.first + tok) * p.heads + head * p.group + row0 + row -
-                             tok * p.group;
-          const bool some = l > 0.0f || l != l;  // a row that sees nothing gets zeros
-          const float inv = some ? 1.0f / l : 0.0f;
-          uint32_t y[N / 2];
-#pragma unroll
-          for (int n = 0; n < N / 2; ++n) y[n] = Mfma<T>::pack(o[2 * n] * inv, o[2 * n + 1] * inv);
-          char *out = static_cast<char *>(p.out) + at * (2 * D) + gr * (2 * N);
-#pragma unroll
-          for (int n = 0; n < N / 2; n += 2)
-            *reinterpret_cast<uint2 *>(out + 4 * n) = make_uint2(y[n], y[n + 1]);
-          if (gr == 0 && p.lse != nullptr) p.lse[at] = some ? natural<T>(top, l) : kNegInf;
-        } else {
-          float *to = p.parts + (slot * ROWS + row) * D + gr * N;
-#pragma unroll
-          for (int n = 0; n < N; n += 4)
-            *reinterpret_cast<f32x4 *>(to + n) = f32x4{o[n], o[n + 1], o[n + 2], o[n + 3]};
-          if (gr == 0)
-            *reinterpret_cast<float2 *>(p.stats + (slot * ROWS + row) * 2) = make_float2(top, l);
-        }
-      }
-      if (!whole) {
-        partial |= 1u << part;
-        if (tid == 0) {  // the item's parts: `n` workgroups from `first` on
-          const int64_t begin = w - x0, first = (begin + kQ8ItemCost) / per;
-          int64_t *to = rec + part * kQ8JoinWords;
-          to[0] = (begin + cost - 1) / per - first + 1;
-          to[1] = first;
-          to[2] = begin <= first * per ? 0 : 1;
-          to[3] = sq.first;
-          to[4] = head;
-          to[5] = row0;
-          to[6] = live;
+    {
+      const int32_t last = sq.len - 1, step = int32_t(kQ8Step), b = share.b;
+      const int64_t head = g.head;
+      int32_t t0 = g.st0 * step + wave * kTile;
+      const int32_t end = min(g.st1 * step, g.most);
+      auto at = [&](int32_t t) { return locate<MODE>(p.seq, b, t, last, lane); };
+      if (t0 < end) {
+        // A tile's keys are asked for once the tile before is scored, its values once that is weighed.
+        // The loads are made whether or not there is another tile (the present one again, from the
+        // caches): behind a branch the compiler would wait for all loads at each use.
+        KeysQ8<D, MODE> k;
+        ValuesQ8<D, MODE> v;
+        WhereQ8<MODE> next = at(t0);
+        load_keys<D, MODE>(p, next, t0, last, head, lane, k);
+        load_values<D, MODE>(p, next, t0, last, head, lane, v);
+        while (true) {  // ends: t0 grows
+          const int32_t t1 = t0 + step < end ? t0 + step : t0;
+          next = at(t1);
+          f32x4 x[R][2];
+          score_tile<T, D, R, E4M3, MODE>(k, s, t0, floor, p.scale_log2, lane, x);
+          load_keys<D, MODE>(p, next, t1, last, head, lane, k);
+          weigh_tile<T, D, R, E4M3, MODE>(v, s, t0, floor, lane, x);
+          if (t1 == t0) break;
+          load_values<D, MODE>(p, next, t1, last, head, lane, v);
+          t0 = t1;
         }
       }
     }
-    w += x1 - x0;
-    if (w >= w1) break;
-    x0 = 0;
-    if (++item >= sq.items * p.kv_heads) {
-      item = 0;
-      do {  // ends: w < w1 <= total, so a later sequence has items
-        ++b;
-        sq = sequence_q8(p, b, ROWS);
-      } while (sq.items == 0);
+
+    // ---- the wavefronts' sums, joined 16 rows at a time; 16 threads a row ----
+    const int64_t slot = int64_t(blockIdx.x) * 2 + g.part;
+    const int m = tid >> 4, gr = tid & 15;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float sum = sum_quarters(s.sum[r]);
+      const float unit = Mfma<T>::kNarrow ? s.reach : 1.0f;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int n = 0; n < N; n += 4)
+          *reinterpret_cast<f32x4 *>(&join_o[wave][lane * LANE + k * N + n]) =
+              f32x4{s.o[r][n][k], s.o[r][n + 1][k], s.o[r][n + 2][k], s.o[r][n + 3][k]} * unit;
+      if (lane < 16) {
+        join_top[wave][lane] = s.top[r];
+        join_sum[wave][lane] = sum;
+      }
+      __syncthreads();
+      const int row = r * 16 + m;
+      if (row >= g.live) continue;
+      float top = join_top[0][m];
+#pragma unroll
+      for (int v = 1; v < kAttnWaves; ++v) top = fmaxf(top, join_top[v][m]);
+      float l = 0.0f, o[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) o[n] = 0.0f;
+#pragma unroll
+      for (int v = 0; v < kAttnWaves; ++v) {
+        const float f = __builtin_amdgcn_exp2f(join_top[v][m] - (top == kNegInf ? 0.0f : top));
+        l += f * join_sum[v][m];
+        const float *from = &join_o[v][((gr >> 2) * 16 + m) * LANE + (gr & 3) * N];
+#pragma unroll
+        for (int n = 0; n < N; n += 4) {
+          const f32x4 y = *reinterpret_cast<const f32x4 *>(from + n);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n + e] += f * y[e];
+        }
+      }
+      if (g.whole()) {
+        const int64_t at = output_row(p, g, sq.first, row);
+        const bool some = l > 0.0f || l != l;  // a row that sees nothing gets zeros
+        const float inv = some ? 1.0f / l : 0.0f;
+        uint32_t y[N / 2];
+#pragma unroll
+        for (int n = 0; n < N / 2; ++n) y[n] = Mfma<T>::pack(o[2 * n] * inv, o[2 * n + 1] * inv);
+        char *out = static_cast<char *>(p.out) + at * (2 * D) + gr * (2 * N);
+#pragma unroll
+        for (int n = 0; n < N / 2; n += 2)
+          *reinterpret_cast<uint2 *>(out + 4 * n) = make_uint2(y[n], y[n + 1]);
+        if (gr == 0 && p.lse != nullptr) p.lse[at] = some ? natural<T>(top, l) : kNegInf;
+      } else {
+        float *to = p.parts + (slot * ROWS + row) * D + gr * N;
+#pragma unroll
+        for (int n = 0; n < N; n += 4)
+          *reinterpret_cast<f32x4 *>(to + n) = f32x4{o[n], o[n + 1], o[n + 2], o[n + 3]};
+        if (gr == 0)
+          *reinterpret_cast<float2 *>(p.stats + (slot * ROWS + row) * 2) = make_float2(top, l);
+      }
     }
-  }
-  if (tid < 2 && (partial >> tid & 1u) == 0) rec[tid * kQ8JoinWords] = 0;
+    share.note(g);
+  } while (share.next());
 }
 
 // Joins the parts of items that several workgroups had a share of: with unnormalised outputs o_k at
@@ -626,7 +823,7 @@ __global__ __launch_bounds__(kAttnBlock) void attention_q8_join_kernel(AttnQ8Pla
   if (n <= 1) return;
   const int64_t g0 = rec[1], first = rec[2];
   const int32_t k0 = int32_t(int64_t(blockIdx.x >> 1) - g0);
-  const int32_t rows = 16 * p.tiles, wide = p.head_size / 4;
+  const int32_t rows = p.rows, wide = p.head_size / 4;
   const int32_t cells = int32_t(rec[6]) * wide;
   const int32_t c0 = int32_t(int64_t(cells) * k0 / n), c1 = int32_t(int64_t(cells) * (k0 + 1) / n);
   for (int32_t cell = c0 + int32_t(threadIdx.x); cell < c1; cell += kAttnBlock) {
@@ -670,30 +867,6 @@ __global__ __launch_bounds__(kAttnBlock) void attention_q8_join_kernel(AttnQ8Pla
         make_uint2(Mfma<T>::pack(o[0] * inv, o[1] * inv), Mfma<T>::pack(o[2] * inv, o[3] * inv));
     if (d == 0 && p.lse != nullptr) p.lse[at] = some ? natural<T>(top, l) : kNegInf;
   }
-}
-
-template <typename T, int D, int R>
-const void *pick_attention_q8(const AttnQ8Plan &p) {
-#define ROPE_KQ(E, RU) reinterpret_cast<const void *>(&attention_q8_kernel<T, D, R, E, RU>)
-  if (p.e4m3) return p.runs ? ROPE_KQ(true, true) : ROPE_KQ(true, false);
-  return p.runs ? ROPE_KQ(false, true) : ROPE_KQ(false, false);
-#undef ROPE_KQ
-}
-
-template <typename T, int D>
-const void *pick_attention_q8(const AttnQ8Plan &p) {
-  return p.tiles == 1 ? pick_attention_q8<T, D, 1>(p) : pick_attention_q8<T, D, 2>(p);
-}
-
-template <typename T>
-int run_attention_q8(AttnQ8Plan &p, void *stream) {
-  const void *fn = p.head_size == 64    ? pick_attention_q8<T, 64>(p)
-                   : p.head_size == 128 ? pick_attention_q8<T, 128>(p)
-                                        : pick_attention_q8<T, 256>(p);
-  const int st = launch_kernel(fn, dim3(uint32_t(p.groups)), kAttnBlock, 0, stream, &p);
-  if (st != ROPE_OK) return st;
-  return launch_kernel(reinterpret_cast<const void *>(&attention_q8_join_kernel<T>),
-                       dim3(uint32_t(p.groups) * 2), kAttnBlock, 0, stream, &p);
 }
 
 }  // namespace

@@ -2,7 +2,7 @@
 // entry points for both types.
 #include <string>
 
-#include "rope_q8_attn.h"
+#include "rope_q8_rows.h"
 
 namespace ropeamd {
 

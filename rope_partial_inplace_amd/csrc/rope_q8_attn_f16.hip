@@ -1,5 +1,5 @@
 // rope_q8_attn_f16.hip -- attention over a paged cache in 8 bits for float16 queries.
-#include "rope_q8_attn.h"
+#include "rope_q8_rows.h"
 
 namespace ropeamd {
 

@@ -271,10 +271,15 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
 
 // Rows of a workgroup: one or two tiles of 16, as many as a sequence's (token, head) rows of a key
 // head fill.
-static int64_t q8_tiles(int64_t tokens, int64_t group, int64_t sequences) {
+static int64_t q8_rows(int64_t tokens, int64_t group, int64_t sequences) {
   const int64_t n = std::max<int64_t>(sequences, 1);
   const int64_t rows = group * (tokens / n + (tokens % n != 0));
-  return rows <= 16 ? 1 : 2;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : kQ8ManyRows;
+}
+
+// Workgroups: as many as the card holds at a time.
+static int64_t q8_groups(int64_t rows, int64_t width) {
+  return 256 * (rows == kQ8ManyRows ? (width == 256 ? 1 : 2) : q8_waves(int(width), int(rows / 16)));
 }
 
 int64_t attention_q8_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_size,
@@ -283,9 +288,10 @@ int64_t attention_q8_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, 
   if (tokens <= 0 || heads <= 0 || kv_heads <= 0 || head_size <= 0 || sequences <= 0) return 0;
   if (tokens >= kIndexLimit || heads >= kIndexLimit || head_size > 256 || heads % kv_heads != 0)
     return 0;
-  const int64_t rows = 16 * q8_tiles(tokens, heads / kv_heads, sequences);
-  return up(kQ8Groups * 2 * kQ8JoinWords * 8, 256) + up(2 * kQ8Groups * rows * 8, 256) +
-         2 * kQ8Groups * rows * head_size * 4;
+  const int64_t rows = q8_rows(tokens, heads / kv_heads, sequences);
+  const int64_t groups = q8_groups(rows, head_size);
+  return up(groups * 2 * kQ8JoinWords * 8, 256) + up(2 * groups * rows * 8, 256) +
+         2 * groups * rows * head_size * 4;
 }
 
 int plan_attention_q8(const rope_tensor *query, const rope_tensor *key_cache,
@@ -377,7 +383,7 @@ int plan_attention_q8(const rope_tensor *query, const rope_tensor *key_cache,
   // a cache without pages or rows holds no tokens: every length is clamped to 0
   if (key_cache->shape[0] == 0 || key_cache->shape[1] == 0) p.seq.max_pages = 0;
   p.block = key_cache->shape[1] > 0 ? int32_t(key_cache->shape[1] / key_scales->shape[1]) : 1;
-  p.runs = p.seq.page_size % 16 == 0 && p.block % 4 == 0;
+  p.mode = p.seq.page_size % 16 != 0 ? 0 : p.block % 4 != 0 ? 1 : 2;
   p.heads = int32_t(H);
   p.kv_heads = int32_t(N);
   p.group = int32_t(H / N);
@@ -385,16 +391,20 @@ int plan_attention_q8(const rope_tensor *query, const rope_tensor *key_cache,
   p.div_group = make_fastdiv(uint32_t(p.group));
   p.div_block = make_fastdiv(uint32_t(p.block));
   p.scale_log2 = float(scaled);
-  p.tiles = int32_t(q8_tiles(T, p.group, B));
-  p.groups = int32_t(kQ8Groups);
+  p.rows = int32_t(q8_rows(T, p.group, B));
+  p.groups = int32_t(q8_groups(p.rows, D));
   p.out = out->data;
   p.lse = lse != nullptr ? static_cast<float *>(lse->data) : nullptr;
-  const int64_t rows = 16 * p.tiles;
+  const int64_t rows = p.rows;
+  // tiles: as many as the rows fill, and one begun for every sequence; steps, and what beginning costs
+  const double tiles = double(N) * (double(T) * double(p.group) / double(rows) + double(B));
+  const double steps = double(p.seq.max_pages) * double(p.seq.page_size) / 64 + 16;
+  p.small = tiles * steps < double(int64_t(1) << 30);
   char *w = static_cast<char *>(workspace);
   p.joins = reinterpret_cast<int64_t *>(w);
-  w += up(kQ8Groups * 2 * kQ8JoinWords * 8, 256);
+  w += up(p.groups * 2 * kQ8JoinWords * 8, 256);
   p.stats = reinterpret_cast<float *>(w);
-  w += up(2 * kQ8Groups * rows * 8, 256);
+  w += up(2 * p.groups * rows * 8, 256);
   p.parts = reinterpret_cast<float *>(w);
   return ROPE_OK;
 }

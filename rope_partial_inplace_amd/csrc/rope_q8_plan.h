@@ -82,7 +82,12 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
 
 // ---- attention --------------------------------------------------------------------------------
 constexpr int64_t kQ8Step = 128;    // cached tokens a workgroup takes at a time
-constexpr int64_t kQ8Groups = 1024; // workgroups, at most
+// Wavefronts of a SIMD that the registers allow, for heads of `width` and `tiles` 16-row tiles; a call has
+// as many workgroups as the card then holds, 256 compute units at a time.
+constexpr int q8_waves(int width, int tiles) {
+  return width == 256 ? (tiles == 1 ? 2 : 1) : tiles == 1 ? (width == 64 ? 4 : 3) : width == 64 ? 3 : 2;
+}
+constexpr int64_t kQ8ManyRows = 128;  // rows of a workgroup where there are many
 constexpr int kQ8JoinWords = 8;
 
 // Keys or values of the cache.
@@ -97,9 +102,7 @@ struct Q8Cache {
 struct AttnQ8Plan {
   rope_dtype dt = ROPE_BF16;
   bool e4m3 = false, noop = false;
-  // pages of whole runs of 16 tokens and scales of whole runs of 4: a half tile lies in one page
-  // and a lane's four neighbouring tokens under one scale
-  bool runs = false;
+  int32_t mode = 0;  // 2: pages of whole runs of 16 tokens and scales of whole runs of 4; 1: such pages
   const void *q = nullptr;
   int64_t q_tok = 0, q_head = 0;
   Q8Cache k, v;
@@ -107,8 +110,9 @@ struct AttnQ8Plan {
   int32_t heads = 0, kv_heads = 0, group = 1, head_size = 0, block = 1;
   FastDiv div_group, div_block;
   float scale_log2 = 0;
-  int32_t tiles = 1;   // 16-row tiles of a workgroup (1 or 2)
+  int32_t rows = 16;   // query rows of a workgroup
   int32_t groups = 0;  // workgroups
+  bool small = false;  // the items' cost (in tokens' steps) fits 31 bits, whatever the lengths
   void *out = nullptr;
   float *lse = nullptr;
   // workspace: for a workgroup's first and last part the record of the item it is part of, its

@@ -1,0 +1,321 @@
+// rope_q8_rows.h -- attention over a paged cache of 8-bit codes for many query rows of a key head: pieces of
+// prompts, drafts of many heads (gfx950; library-internal, instantiated beside rope_q8_attn.h).
+//
+// With some 40 rows and more a call is bound by its products and what lies between them, and a tile's
+// codes are worth turning into operands once for all rows: a workgroup has 128 rows, 32 of each
+// wavefront.  Codes come to registers a tile ahead, are made 16-bit operands and go to LDS, into the
+// second of two buffers, in the panels of rope_mfma.h; S^T = K Q^T and O^T = V^T P^T are 32x32x16
+// products, so that a lane owns a query row and P goes from one to the other in registers.
+// Scales wait, as in the other kernel: keys' multiply the scores, values' the weights.
+#pragma once
+
+#include "rope_q8_attn.h"
+
+namespace ropeamd {
+namespace {
+
+template <int D>
+struct RowsShape {
+  static constexpr int TILE = D == 256 ? 32 : 64;  // tokens of a step
+  static constexpr int PANELS = D / 64;
+  static constexpr int PANEL = TILE * 128;          // bytes
+  static constexpr int THREADS = kAttnBlock / TILE;  // of a token's codes
+  static constexpr int BYTES = D / THREADS;          // of one thread
+};
+
+// What a thread has of a tile: some of a token's key and value codes, and a scale (of the keys in the first
+// TILE threads, of the values in the next).
+template <int D>
+struct StageQ8 {
+  uint4 k[RowsShape<D>::BYTES / 16], v[RowsShape<D>::BYTES / 16];
+  float scale;
+};
+
+template <int D>
+struct RowsLds {
+  struct Buffer {
+    char k[RowsShape<D>::PANELS * RowsShape<D>::PANEL], v[RowsShape<D>::PANELS * RowsShape<D>::PANEL];
+    float k_scale[RowsShape<D>::TILE], v_scale[RowsShape<D>::TILE];
+  };
+  Buffer buffer[2];
+  ShareLds share;
+};
+
+// The page and row of a thread's token, tokens past the last one repeat it.
+struct TokenQ8 {
+  int32_t page, row;
+};
+__device__ __forceinline__ TokenQ8 token_at(const Sequences &s, int32_t b, int32_t t) {
+  const uint32_t i = div_by(s.div_page, uint32_t(t));
+  return {int32_t(page_of(s, b, int32_t(i))), t - int32_t(i * uint32_t(s.page_size))};
+}
+
+template <int D>
+__device__ __forceinline__ void fetch(const AttnQ8Plan &p, const TokenQ8 &codes, const TokenQ8 &scale,
+                                      int64_t head, int tid, StageQ8<D> &x) {
+  using S = RowsShape<D>;
+  const int64_t at = tid % S::THREADS * S::BYTES;
+  const uint8_t *k = p.k.codes + codes.page * p.k.page + head * p.k.head + int64_t(codes.row) * p.k.row + at;
+  const uint8_t *v = p.v.codes + codes.page * p.v.page + head * p.v.head + int64_t(codes.row) * p.v.row + at;
+#pragma unroll
+  for (int i = 0; i < S::BYTES / 16; ++i) {
+    x.k[i] = *reinterpret_cast<const uint4 *>(k + 16 * i);
+    x.v[i] = *reinterpret_cast<const uint4 *>(v + 16 * i);
+  }
+  const Q8Cache &c = tid < S::TILE ? p.k : p.v;
+  x.scale = c.scales[scale.page * c.s_page + head * c.s_head +
+                     int64_t(div_by(p.div_block, uint32_t(scale.row))) * c.s_block];
+}
+
+// Into a buffer, as operands.
+template <typename T, int D, bool E4M3>
+__device__ __forceinline__ void put(const StageQ8<D> &x, int tid, float scale_log2,
+                                    typename RowsLds<D>::Buffer &to) {
+  using S = RowsShape<D>;
+  using Op = Operand<T, E4M3>;
+  const uint32_t row = uint32_t(tid) / S::THREADS;
+  const uint32_t first = uint32_t(tid) % S::THREADS * (S::BYTES / 8);  // 16-byte chunk of the row
+#pragma unroll
+  for (int i = 0; i < S::BYTES / 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t c = first + 2 * i + e;
+      const uint32_t at = c / 8 * S::PANEL + panel_chunk(row, c % 8);
+      const s16x8 k = e == 0 ? Op::row(x.k[i].x, x.k[i].y) : Op::row(x.k[i].z, x.k[i].w);
+      const s16x8 v = e == 0 ? Op::row(x.v[i].x, x.v[i].y) : Op::row(x.v[i].z, x.v[i].w);
+      *reinterpret_cast<s16x8 *>(to.k + at) = k;
+      *reinterpret_cast<s16x8 *>(to.v + at) = v;
+    }
+  if (tid < S::TILE)
+    to.k_scale[tid] = x.scale * scale_log2;
+  else if (tid < 2 * S::TILE)
+    to.v_scale[tid - S::TILE] = x.scale;
+}
+
+template <typename T, int D, bool E4M3>
+__global__ __launch_bounds__(kAttnBlock) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2))) void
+attention_q8_rows_kernel(AttnQ8Plan p) {
+  using S = RowsShape<D>;
+  constexpr int TILE = S::TILE, KB = TILE / 32, ROWS = int(kQ8ManyRows), DB = D / 32;
+  __shared__ __attribute__((aligned(16))) RowsLds<D> lds;
+  const int tid = int(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  ShareQ8<ROWS, TILE> share = {{p}};
+  if (!share.begin(lds.share)) return;
+  do {
+    const SegmentQ8 g = share.segment();
+    if (g.st0 >= g.st1) continue;
+    const SequenceQ8 &sq = share.sq;
+    const int32_t b = share.b, last = sq.len - 1;
+    const int64_t head = g.head;
+
+    // ---- the lane's query row ----
+    const int32_t m = wave * 32 + (lane & 31);
+    const bool some = m < g.live;
+    const int32_t tok = int32_t(div_by(p.div_group, uint32_t(g.row0 + (some ? m : 0))));
+    const int32_t limit = some ? g.hidden + tok : 0;
+    const int32_t floor = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0 + min(wave * 32, g.live - 1))));
+    s16x8 q[D / 16];
+    {
+      const int32_t h = g.head * p.group + g.row0 + (some ? m : 0) - tok * p.group;
+      const T *from = static_cast<const T *>(p.q) + int64_t(sq.first + tok) * p.q_tok +
+                      int64_t(h) * p.q_head + 8 * (lane >> 5);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        q[i] = some ? as_operand(*reinterpret_cast<const uint4 *>(from + 16 * i)) : s16x8{};
+    }
+    float top = kNegInf, sum = 0.0f;
+    float reach = 0x1p-120f, by_reach = 0x1p120f;  // as in StateQ8
+    f32x16 o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+
+    // ---- the steps that a row of the tile sees ----
+    const int32_t end = min(g.st1 * TILE, g.most);
+    int32_t t0 = g.st0 * TILE;
+    if (t0 < end) {
+      auto codes_at = [&](int32_t t) { return token_at(p.seq, b, min(t + tid / S::THREADS, last)); };
+      auto scale_at = [&](int32_t t) { return token_at(p.seq, b, min(t + tid % TILE, last)); };
+      StageQ8<D> stage;
+      fetch<D>(p, codes_at(t0), scale_at(t0), head, tid, stage);
+      lds_barrier();  // what the last piece read of the buffers
+      put<T, D, E4M3>(stage, tid, p.scale_log2, lds.buffer[0]);
+      int32_t t1 = t0 + TILE < end ? t0 + TILE : t0;
+      TokenQ8 codes = codes_at(t1), scale = scale_at(t1);
+      for (int32_t n = 0;; ++n) {  // ends: t0 grows
+        lds_barrier();
+        // the next tile's codes on their way (the present one's again behind the last: no branch)
+        fetch<D>(p, codes, scale, head, tid, stage);
+        const int32_t t2 = t1 + TILE < end ? t1 + TILE : t1;
+        codes = codes_at(t2);
+        scale = scale_at(t2);
+        const typename RowsLds<D>::Buffer &at = lds.buffer[n & 1];
+
+        // S^T
+        f32x16 x[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) x[kb] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            const s16x8 a = *reinterpret_cast<const s16x8 *>(
+                at.k + i / 4 * S::PANEL +
+                panel_chunk(uint32_t(kb * 32 + (lane & 31)), uint32_t(i % 4 * 2 + (lane >> 5))));
+            x[kb] = Mfma<T>::mul(a, q[i], x[kb]);
+            if (i % 2 == 1 && kb == KB - 1) __builtin_amdgcn_sched_barrier(0);  // or it spills
+          }
+        // scores in powers of two, masked where not every row of the wavefront sees all of the tile
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const f32x4 f = *reinterpret_cast<const f32x4 *>(at.k_scale + kb * 32 + c * 8 + 4 * (lane >> 5));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[kb][4 * c + r] *= f[r];
+          }
+        const bool masked = t0 + TILE > floor;
+        if (masked) {
+          asm volatile("");
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (t0 + kb * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 >= limit) x[kb][r] = kNegInf;
+        }
+        float best = kNegInf;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) best = fmaxf(best, x[kb][r]);
+        best = max_halves(best);
+        bool raise = best > top + Mfma<T>::kSlack;
+        float most = 0.0f;
+        if constexpr (Mfma<T>::kNarrow) {
+          most = fabsf(at.v_scale[lane % TILE]);
+          raise |= most > reach;
+        }
+        if (__any(raise)) {
+          float f = 1.0f;
+          if (best > top + Mfma<T>::kSlack) {
+            f = __builtin_amdgcn_exp2f(top - best);
+            top = best;
+          }
+          sum *= f;
+          if constexpr (Mfma<T>::kNarrow) {
+            for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+            const float now = most > reach ? reach_above(most) : reach;
+            f *= reach * inverse_power(now);
+            reach = now;
+            by_reach = inverse_power(now);
+          }
+#pragma unroll
+          for (int d = 0; d < DB; ++d) o[d] *= f;
+        }
+        const float ref = top == kNegInf ? 0.0f : top - Mfma<T>::kLift;
+        s16x8 w[KB][2];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          float e[16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            f32x4 f = *reinterpret_cast<const f32x4 *>(at.v_scale + kb * 32 + c * 8 + 4 * (lane >> 5));
+            if constexpr (Mfma<T>::kNarrow) f *= by_reach;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float y = __builtin_amdgcn_exp2f(x[kb][4 * c + r] - ref);
+              sum += y;
+              e[4 * c + r] = y * f[r];
+            }
+          }
+          if (masked) {
+            asm volatile("");
+#pragma unroll
+            for (int r = 0; r < 16; ++r)  // whatever the scale of a token that the row does not see
+              if (t0 + kb * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 >= limit) e[r] = 0.0f;
+          }
+          w[kb][0] = round8<T>(e);
+          w[kb][1] = round8<T>(e + 8);
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              o[d] = Mfma<T>::mul(transposed_operand(at.v + d / 2 * S::PANEL + (kb * 2 + h) * 2048,
+                                                     uint32_t(lane), uint32_t(d % 2)),
+                                  w[kb][h], o[d]);
+              if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+        if (t1 == t0) break;
+        put<T, D, E4M3>(stage, tid, p.scale_log2, lds.buffer[~n & 1]);
+        t0 = t1;
+        t1 = t2;
+      }
+    }
+    sum = sum_halves(sum);
+
+    // ---- the piece's result ----
+    if (some) {
+      const float unit = Mfma<T>::kNarrow ? reach : 1.0f;
+      if (g.whole()) {
+        const int64_t row = output_row(p, g, sq.first, m);
+        const bool any = sum > 0.0f || sum != sum;  // a row that sees nothing gets zeros
+        const float inv = any ? unit / sum : 0.0f;
+        char *out = static_cast<char *>(p.out) + row * (2 * D) + 8 * (lane >> 5);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint2 *>(out + d * 64 + c * 16) =
+                make_uint2(Mfma<T>::pack(o[d][4 * c] * inv, o[d][4 * c + 1] * inv),
+                           Mfma<T>::pack(o[d][4 * c + 2] * inv, o[d][4 * c + 3] * inv));
+        if (lane < 32 && p.lse != nullptr) p.lse[row] = any ? natural<T>(top, sum) : kNegInf;
+      } else {
+        const int64_t row = (int64_t(blockIdx.x) * 2 + g.part) * ROWS + m;
+        float *to = p.parts + row * D + 4 * (lane >> 5);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<f32x4 *>(to + d * 32 + c * 8) =
+                f32x4{o[d][4 * c], o[d][4 * c + 1], o[d][4 * c + 2], o[d][4 * c + 3]} * unit;
+        if (lane < 32) *reinterpret_cast<float2 *>(p.stats + row * 2) = make_float2(top, sum);
+      }
+    }
+    share.note(g);
+  } while (share.next());
+}
+
+template <typename T, int D, int R>
+const void *pick_attention_q8(const AttnQ8Plan &p) {
+#define ROPE_KQ(E, MO) reinterpret_cast<const void *>(&attention_q8_kernel<T, D, R, E, MO>)
+#define ROPE_KM(E) (p.mode == kCoarse ? ROPE_KQ(E, kCoarse) : p.mode == kFine ? ROPE_KQ(E, kFine) : ROPE_KQ(E, kAny))
+  return p.e4m3 ? ROPE_KM(true) : ROPE_KM(false);
+#undef ROPE_KM
+#undef ROPE_KQ
+}
+
+template <typename T, int D>
+const void *pick_attention_q8(const AttnQ8Plan &p) {
+  if (p.rows == kQ8ManyRows)
+    return p.e4m3 ? reinterpret_cast<const void *>(&attention_q8_rows_kernel<T, D, true>)
+                  : reinterpret_cast<const void *>(&attention_q8_rows_kernel<T, D, false>);
+  return p.rows == 16 ? pick_attention_q8<T, D, 1>(p) : pick_attention_q8<T, D, 2>(p);
+}
+
+template <typename T>
+int run_attention_q8(AttnQ8Plan &p, void *stream) {
+  const void *fn = p.head_size == 64    ? pick_attention_q8<T, 64>(p)
+                   : p.head_size == 128 ? pick_attention_q8<T, 128>(p)
+                                        : pick_attention_q8<T, 256>(p);
+  const int st = launch_kernel(fn, dim3(uint32_t(p.groups)), kAttnBlock, 0, stream, &p);
+  if (st != ROPE_OK) return st;
+  return launch_kernel(reinterpret_cast<const void *>(&attention_q8_join_kernel<T>),
+                       dim3(uint32_t(p.groups) * 2), kAttnBlock, 0, stream, &p);
+}
+
+}  // namespace
+}  // namespace ropeamd
