@@ -23,8 +23,17 @@ struct RowsShape {
   static constexpr int BYTES = D / THREADS;          // of one thread
 };
 
+// Scales of a tile.  COARSE (pages and blocks of whole runs of 4 tokens): one for each 4 tokens,
+// those of the lanes below 32 first: of tokens 8 c + 4 (l / 32) and on at 8 (l / 32) + c, c up to 8; else
+// one for each token.
+template <int D, bool COARSE>
+struct ScalesOf {
+  static constexpr int RUN = COARSE ? 4 : 1, COUNT = RowsShape<D>::TILE / RUN;
+  __device__ static int place(int i) { return COARSE ? (i & 1) * (COUNT / 2) + (i >> 1) : i; }
+};
+
 // What a thread has of a tile: some of a token's key and value codes, and a scale (of the keys in the first
-// TILE threads, of the values in the next).
+// threads, of the values in the next).
 template <int D>
 struct StageQ8 {
   uint4 k[RowsShape<D>::BYTES / 16], v[RowsShape<D>::BYTES / 16];
@@ -50,7 +59,7 @@ __device__ __forceinline__ TokenQ8 token_at(const Sequences &s, int32_t b, int32
   return {int32_t(page_of(s, b, int32_t(i))), t - int32_t(i * uint32_t(s.page_size))};
 }
 
-template <int D>
+template <int D, bool COARSE>
 __device__ __forceinline__ void fetch(const AttnQ8Plan &p, const TokenQ8 &codes, const TokenQ8 &scale,
                                       int64_t head, int tid, StageQ8<D> &x) {
   using S = RowsShape<D>;
@@ -62,13 +71,13 @@ __device__ __forceinline__ void fetch(const AttnQ8Plan &p, const TokenQ8 &codes,
     x.k[i] = *reinterpret_cast<const uint4 *>(k + 16 * i);
     x.v[i] = *reinterpret_cast<const uint4 *>(v + 16 * i);
   }
-  const Q8Cache &c = tid < S::TILE ? p.k : p.v;
+  const Q8Cache &c = tid < ScalesOf<D, COARSE>::COUNT ? p.k : p.v;
   x.scale = c.scales[scale.page * c.s_page + head * c.s_head +
                      int64_t(div_by(p.div_block, uint32_t(scale.row))) * c.s_block];
 }
 
 // Into a buffer, as operands.
-template <typename T, int D, bool E4M3>
+template <typename T, int D, bool E4M3, bool COARSE>
 __device__ __forceinline__ void put(const StageQ8<D> &x, int tid, float scale_log2,
                                     typename RowsLds<D>::Buffer &to) {
   using S = RowsShape<D>;
@@ -79,20 +88,34 @@ __device__ __forceinline__ void put(const StageQ8<D> &x, int tid, float scale_lo
   for (int i = 0; i < S::BYTES / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t c = first + 2 * i + e;
-      const uint32_t at = c / 8 * S::PANEL + panel_chunk(row, c % 8);
+      const uint32_t at = first / 8 * S::PANEL + (panel_chunk(row, first % 8) ^ (uint32_t(2 * i + e) * 16u));
       const s16x8 k = e == 0 ? Op::row(x.k[i].x, x.k[i].y) : Op::row(x.k[i].z, x.k[i].w);
       const s16x8 v = e == 0 ? Op::row(x.v[i].x, x.v[i].y) : Op::row(x.v[i].z, x.v[i].w);
       *reinterpret_cast<s16x8 *>(to.k + at) = k;
       *reinterpret_cast<s16x8 *>(to.v + at) = v;
     }
-  if (tid < S::TILE)
-    to.k_scale[tid] = x.scale * scale_log2;
-  else if (tid < 2 * S::TILE)
-    to.v_scale[tid - S::TILE] = x.scale;
+  using Sc = ScalesOf<D, COARSE>;
+  if (tid < Sc::COUNT)
+    to.k_scale[Sc::place(tid)] = x.scale * scale_log2;
+  else if (tid < 2 * Sc::COUNT)
+    to.v_scale[Sc::place(tid - Sc::COUNT)] = x.scale;
 }
 
-template <typename T, int D, bool E4M3>
+// The scales of the lane's tokens of block kb of 32 in S^T: four by four.
+template <int D, bool COARSE>
+__device__ __forceinline__ void scales_at(const float *s, int kb, int lane, f32x4 (&f)[4]) {
+  if constexpr (COARSE) {
+    const f32x4 y = *reinterpret_cast<const f32x4 *>(s + (lane >> 5) * (RowsShape<D>::TILE / 8) + kb * 4);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f[c] = f32x4{y[c], y[c], y[c], y[c]};
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      f[c] = *reinterpret_cast<const f32x4 *>(s + kb * 32 + c * 8 + 4 * (lane >> 5));
+  }
+}
+
+template <typename T, int D, bool E4M3, bool COARSE>
 __global__ __launch_bounds__(kAttnBlock) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2))) void
 attention_q8_rows_kernel(AttnQ8Plan p) {
   using S = RowsShape<D>;
@@ -130,50 +153,67 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
 #pragma unroll
     for (int d = 0; d < DB; ++d) o[d] = f32x16{};
 
+    uint32_t keys_at = panel_chunk(uint32_t(lane & 31), uint32_t(lane >> 5));
+    uint32_t values_at = panel_transposed(uint32_t(lane), 0, 0);
+
     // ---- the steps that a row of the tile sees ----
     const int32_t end = min(g.st1 * TILE, g.most);
     int32_t t0 = g.st0 * TILE;
     if (t0 < end) {
       auto codes_at = [&](int32_t t) { return token_at(p.seq, b, min(t + tid / S::THREADS, last)); };
-      auto scale_at = [&](int32_t t) { return token_at(p.seq, b, min(t + tid % TILE, last)); };
+      auto scale_at = [&](int32_t t) {
+        return token_at(p.seq, b, min(t + tid % ScalesOf<D, COARSE>::COUNT * ScalesOf<D, COARSE>::RUN, last));
+      };
       StageQ8<D> stage;
-      fetch<D>(p, codes_at(t0), scale_at(t0), head, tid, stage);
+      fetch<D, COARSE>(p, codes_at(t0), scale_at(t0), head, tid, stage);
       lds_barrier();  // what the last piece read of the buffers
-      put<T, D, E4M3>(stage, tid, p.scale_log2, lds.buffer[0]);
+      put<T, D, E4M3, COARSE>(stage, tid, p.scale_log2, lds.buffer[0]);
       int32_t t1 = t0 + TILE < end ? t0 + TILE : t0;
       TokenQ8 codes = codes_at(t1), scale = scale_at(t1);
       for (int32_t n = 0;; ++n) {  // ends: t0 grows
         lds_barrier();
         // the next tile's codes on their way (the present one's again behind the last: no branch)
-        fetch<D>(p, codes, scale, head, tid, stage);
+        fetch<D, COARSE>(p, codes, scale, head, tid, stage);
         const int32_t t2 = t1 + TILE < end ? t1 + TILE : t1;
         codes = codes_at(t2);
         scale = scale_at(t2);
         const typename RowsLds<D>::Buffer &at = lds.buffer[n & 1];
 
+        // Opaque: the places that follow from these are worked out again in every step.  Kept from step to
+        // step they would take registers that the products need.
+        asm volatile("" : "+v"(keys_at), "+v"(values_at));
         // S^T
         f32x16 x[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) x[kb] = f32x16{};
+        constexpr int AHEAD = 2;  // products whose operands are read ahead
+        s16x8 kf[AHEAD + 1][KB];
+        auto load_keys = [&](int i) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+          for (int kb = 0; kb < KB; ++kb)
+            kf[i % (AHEAD + 1)][kb] = *reinterpret_cast<const s16x8 *>(
+                at.k + i / 4 * S::PANEL + kb * 4096 + (keys_at ^ (i % 4 * 32u)));
+        };
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            const s16x8 a = *reinterpret_cast<const s16x8 *>(
-                at.k + i / 4 * S::PANEL +
-                panel_chunk(uint32_t(kb * 32 + (lane & 31)), uint32_t(i % 4 * 2 + (lane >> 5))));
-            x[kb] = Mfma<T>::mul(a, q[i], x[kb]);
-            if (i % 2 == 1 && kb == KB - 1) __builtin_amdgcn_sched_barrier(0);  // or it spills
-          }
+        for (int i = 0; i < AHEAD; ++i) load_keys(i);
+        __builtin_amdgcn_s_setprio(1);  // the other wavefront's exponentials fill the pauses
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          if (i + AHEAD < D / 16) load_keys(i + AHEAD);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) x[kb] = Mfma<T>::mul(kf[i % (AHEAD + 1)][kb], q[i], x[kb]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
         // scores in powers of two, masked where not every row of the wavefront sees all of the tile
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < KB; ++kb) {
+          f32x4 f[4];
+          scales_at<D, COARSE>(at.k_scale, kb, lane, f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const f32x4 f = *reinterpret_cast<const f32x4 *>(at.k_scale + kb * 32 + c * 8 + 4 * (lane >> 5));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[kb][4 * c + r] *= f[r];
-          }
+          for (int r = 0; r < 16; ++r) x[kb][r] *= f[r / 4][r % 4];
+        }
         const bool masked = t0 + TILE > floor;
         if (masked) {
           asm volatile("");
@@ -192,7 +232,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         bool raise = best > top + Mfma<T>::kSlack;
         float most = 0.0f;
         if constexpr (Mfma<T>::kNarrow) {
-          most = fabsf(at.v_scale[lane % TILE]);
+          most = fabsf(at.v_scale[lane % ScalesOf<D, COARSE>::COUNT]);
           raise |= most > reach;
         }
         if (__any(raise)) {
@@ -217,16 +257,17 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
           float e[16];
+          f32x4 f[4];
+          scales_at<D, COARSE>(at.v_scale, kb, lane, f);
+          if constexpr (Mfma<T>::kNarrow) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            f32x4 f = *reinterpret_cast<const f32x4 *>(at.v_scale + kb * 32 + c * 8 + 4 * (lane >> 5));
-            if constexpr (Mfma<T>::kNarrow) f *= by_reach;
+            for (int c = 0; c < 4; ++c) f[c] *= by_reach;
+          }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float y = __builtin_amdgcn_exp2f(x[kb][4 * c + r] - ref);
-              sum += y;
-              e[4 * c + r] = y * f[r];
-            }
+          for (int r = 0; r < 16; ++r) {
+            const float y = __builtin_amdgcn_exp2f(x[kb][r] - ref);
+            sum += y;
+            e[r] = y * f[r / 4][r % 4];
           }
           if (masked) {
             asm volatile("");
@@ -238,19 +279,26 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
           w[kb][1] = round8<T>(e + 8);
         }
         // O^T += V^T P^T
+        constexpr int V_AHEAD = 3, PRODUCTS = KB * 2 * DB;
+        s16x8 vf[V_AHEAD + 1];
+        auto load_values = [&](int n) {  // 16 tokens n / DB, columns 32 (n % DB) and on
+          const char *from = at.v + n % DB / 2 * S::PANEL + n / DB * 2048;
+          const uint32_t v = values_at ^ (n % DB % 2 * 64u);
+          vf[n % (V_AHEAD + 1)] = join(read_transposed(from + v), read_transposed(from + (v ^ kEightRows)));
+        };
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int n = 0; n < V_AHEAD; ++n) load_values(n);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-              o[d] = Mfma<T>::mul(transposed_operand(at.v + d / 2 * S::PANEL + (kb * 2 + h) * 2048,
-                                                     uint32_t(lane), uint32_t(d % 2)),
-                                  w[kb][h], o[d]);
-              if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-            }
+        for (int n = 0; n < PRODUCTS; ++n) {
+          if (n + V_AHEAD < PRODUCTS) load_values(n + V_AHEAD);
+          __builtin_amdgcn_sched_barrier(0);
+          o[n % DB] = Mfma<T>::mul(vf[n % (V_AHEAD + 1)], w[n / DB / 2][n / DB % 2], o[n % DB]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
         if (t1 == t0) break;
-        put<T, D, E4M3>(stage, tid, p.scale_log2, lds.buffer[~n & 1]);
+        put<T, D, E4M3, COARSE>(stage, tid, p.scale_log2, lds.buffer[~n & 1]);
         t0 = t1;
         t1 = t2;
       }
@@ -300,9 +348,13 @@ const void *pick_attention_q8(const AttnQ8Plan &p) {
 
 template <typename T, int D>
 const void *pick_attention_q8(const AttnQ8Plan &p) {
-  if (p.rows == kQ8ManyRows)
-    return p.e4m3 ? reinterpret_cast<const void *>(&attention_q8_rows_kernel<T, D, true>)
-                  : reinterpret_cast<const void *>(&attention_q8_rows_kernel<T, D, false>);
+  if (p.rows == kQ8ManyRows) {
+#define ROPE_KR(E, C) reinterpret_cast<const void *>(&attention_q8_rows_kernel<T, D, E, C>)
+    const bool coarse = p.seq.page_size % 4 == 0 && p.block % 4 == 0;
+    if (p.e4m3) return coarse ? ROPE_KR(true, true) : ROPE_KR(true, false);
+    return coarse ? ROPE_KR(false, true) : ROPE_KR(false, false);
+#undef ROPE_KR
+  }
   return p.rows == 16 ? pick_attention_q8<T, D, 1>(p) : pick_attention_q8<T, D, 2>(p);
 }
 
