@@ -55,7 +55,8 @@
  *    (except ROPE_ERR_RUNTIME, which reports a failed launch).  rope_last_error() gives a
  *    text for the last failing call of the calling thread.
  *  - Determinism: every output element is written by exactly one GPU lane with no atomics,
- *    so repeated calls give bit-identical results ([IPRM §约束说明], [RSCC §约束说明]).
+ *    so repeated calls give bit-identical results ([IPRM §约束说明], [RSCC §约束说明]).  (The counts of
+ *    rope_fork_pages are sums of integers, which no order changes.)
  */
 #ifndef ROPE_AMD_H
 #define ROPE_AMD_H
@@ -382,8 +383,9 @@ int rope_latent_attention_backward(
  *                Tokens before place 0, and tokens whose page is not in [0, pages) (padding), are
  *                skipped.  A page that takes tokens belongs to one sequence only -- a precondition
  *                that is not checked (rope_fork_pages keeps it).
- * token_offsets  INT64 [B + 1], ascending (else nothing is appended), clamped to [0, T]; rows outside
- *                all sequences are not appended.  NULL: T / B tokens each (T % B == 0).
+ * token_offsets  INT64 [B + 1], ascending; out-of-range values are clamped to [0, T], and rows outside
+ *                all sequences are not appended.  Where they descend, what is appended is not defined,
+ *                but no access leaves the tensors.  NULL: T / B tokens each (T % B == 0).
  * Any non-negative strides with unit inner stride (scales: any non-negative strides).  Outputs whose
  * strides reach an element twice, and any other overlap with an output, are refused.  T = 0 is a no-op.
  */
@@ -474,7 +476,8 @@ int rope_copy_pages(const rope_tensor *sources, const rope_tensor *targets,
  *                dimension is the outermost of a page and n divides page_size or the reverse (rows, or
  *                blocks of rows), only the part that holds the copied tokens is written; of others the
  *                whole page.
- * page_table_out INT64 [R, any], seq_lens_out INT64 [R], shortage INT64 [1]: apart from all inputs.
+ * page_table_out INT64 [R, maxPages or more], seq_lens_out INT64 [R], shortage INT64 [1]: apart from
+ *                all inputs.
  * ref_counts_out INT64 [pages], may be ref_counts itself.
  * workspace      at least rope_fork_pages_workspace() bytes, under the rules of
  *                rope_latent_attention_paged's.
