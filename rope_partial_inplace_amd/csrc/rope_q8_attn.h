@@ -10,8 +10,12 @@
 // layout in which the matrix instructions take them, and are made operands there: exact in bfloat16
 // and float16 both, so the scales can wait -- ks multiplies the finished scores, vs the weights,
 // before those are rounded for the second product.  No LDS and no barrier stand between a load and its use: a
-// wavefront takes 32 tokens at a time, has the next 32 under way (8 KB at D 128), and four
-// wavefronts of a workgroup, which take every fourth 32 tokens each, join their sums at the end.
+// wavefront takes 32 tokens at a time and has the next 32 under way (8 KB at D 128).  The four wavefronts
+// of a workgroup take up to four key heads of the same tokens; those of one head, each of which
+// takes every n-th 32 tokens, join their sums at the end.
+//
+// Measured with 8 key heads of 128: 64 sequences of 200-9000 tokens 67 us (284 MB), of 9000 218 us (5.4 TB/s),
+// six of 60-131k tokens and a scale for each 276 us (5.3 TB/s).
 //
 // Layout (16x16x32 products, lane l = 16 g + c):
 //   S^T = K Q^T: A[key c][8 d], lane's d = g D / 4 + 16 i + 8 e + 0..7 for product (i, e): 16 bytes a load
@@ -38,7 +42,7 @@ namespace {
 constexpr int kAttnBlock = 256;
 constexpr int kAttnWaves = kAttnBlock / 64;
 constexpr int kTile = 32;  // tokens of a wavefront at a time
-static_assert(kTile * kAttnWaves == kQ8Step, "a step is a tile of every wavefront");
+static_assert(kTile * kAttnWaves == 1 << q8_step_log2(16, 64, 0), "a step is a tile of every wavefront");
 
 // What beginning an item costs, in steps: the shares of the workgroups are cut by steps and this.
 constexpr int32_t kQ8ItemCost = 2;
@@ -117,7 +121,7 @@ struct SequenceQ8 {
   __device__ int32_t pairs() const { return (tiles + 1) / 2; }
 };
 
-template <int ROWS, int STEP>
+template <int ROWS>
 struct WorkQ8 {
   const AttnQ8Plan &p;
 
@@ -128,7 +132,7 @@ struct WorkQ8 {
     return max(0, s.len - s.count + 1 + tok);
   }
   __device__ int32_t steps(const SequenceQ8 &s, int32_t tile) const {
-    return max(1, (visible(s, tile) + STEP - 1) / STEP);
+    return max(1, (visible(s, tile) + (1 << p.step_log2) - 1) >> p.step_log2);
   }
   // Lengths and offsets are device data: values outside their ranges are clamped.
   __device__ SequenceQ8 sequence(int32_t b) const {
@@ -149,12 +153,12 @@ struct WorkQ8 {
     if (s.tiles > 0) {
       s.cost = steps(s, s.tiles - 1) + kQ8ItemCost;
       // the first tile beside the last; other pairs see up to ROWS rows' tokens more than this one
-      if (s.tiles > 1) s.cost += steps(s, 0) + kQ8ItemCost + ROWS / STEP + 2;
+      if (s.tiles > 1) s.cost += steps(s, 0) + kQ8ItemCost + (ROWS >> p.step_log2) + 2;
     }
     return s;
   }
   __device__ int64_t cost(const SequenceQ8 &s) const {
-    return int64_t(s.pairs()) * p.kv_heads * s.cost;
+    return int64_t(s.pairs()) * p.head_sets * s.cost;
   }
 };
 
@@ -505,7 +509,7 @@ __device__ inline int64_t uniform64(int64_t x) {
 
 // A piece of a workgroup's share: steps [st0, st1) of one tile of rows of one key head.
 struct SegmentQ8 {
-  int32_t head, row0, live;   // the tile's first row, and rows in it
+  int32_t set, row0, live;    // of key heads; the tile's first row, and rows in it
   int32_t steps, st0, st1;
   int32_t hidden;             // + a row's token: cached tokens that the row sees
   int32_t most;               // tokens that the last row sees
@@ -523,9 +527,9 @@ struct ShareLds {
 
 // A workgroup's share of the cost of all pairs, which it goes through piece by piece.  All members are the
 // same for all lanes.
-template <int ROWS, int STEP>
+template <int ROWS>
 struct ShareQ8 {
-  WorkQ8<ROWS, STEP> work;
+  WorkQ8<ROWS> work;
   int64_t per, w0, w1, w;   // the share [w0, w1), and where in it
   int64_t *rec;
   int32_t b, item, x;       // sequence, pair and key head, place in their cost
@@ -609,9 +613,9 @@ struct ShareQ8 {
   // The piece that begins at w.
   __device__ SegmentQ8 segment() {
     const AttnQ8Plan &p = work.p;
-    const int32_t pair = int32_t(uint32_t(item) / uint32_t(p.kv_heads));
+    const int32_t pair = int32_t(uint32_t(item) / uint32_t(p.head_sets));
     SegmentQ8 g;
-    g.head = item - pair * p.kv_heads;
+    g.set = item - pair * p.head_sets;
     int32_t tile = sq.tiles - 1 - pair, at = 0, end = sq.cost;
     if (tile != pair) {  // two tiles: the longer one first
       const int32_t border = work.steps(sq, tile) + kQ8ItemCost;
@@ -649,7 +653,7 @@ struct ShareQ8 {
       to[1] = first;
       to[2] = g.begin <= first * per ? 0 : 1;
       to[3] = sq.first;
-      to[4] = g.head;
+      to[4] = g.set;
       to[5] = g.row0;
       to[6] = g.live;
     }
@@ -663,7 +667,7 @@ struct ShareQ8 {
     }
     if (x >= sq.cost) {
       x = 0;
-      if (++item >= sq.pairs() * work.p.kv_heads) {
+      if (++item >= sq.pairs() * work.p.head_sets) {
         item = 0;
         do {  // ends: w < w1 <= total, so a later sequence has tiles
           sq = work.sequence(++b);
@@ -674,10 +678,11 @@ struct ShareQ8 {
   }
 };
 
-// Where row `m` of a tile lies in the output, in rows of D.
-__device__ inline int64_t output_row(const AttnQ8Plan &p, const SegmentQ8 &g, int32_t first, int32_t m) {
+// Where row `m` of a tile of key head `head` lies in the output, in rows of D.
+__device__ inline int64_t output_row(const AttnQ8Plan &p, const SegmentQ8 &g, int32_t head,
+                                     int32_t first, int32_t m) {
   const int32_t r = g.row0 + m, tok = int32_t(div_by(p.div_group, uint32_t(r)));
-  return int64_t(first + tok) * p.heads + g.head * p.group + r - tok * p.group;
+  return int64_t(first + tok) * p.heads + head * p.group + r - tok * p.group;
 }
 
 template <typename T, int D, int R, bool E4M3, int MODE>
@@ -691,12 +696,15 @@ attention_q8_kernel(AttnQ8Plan p) {
 
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  ShareQ8<ROWS, int(kQ8Step)> share = {{p}};
+  // the wavefront's key head of a set, and its turn among those of the same head
+  const int32_t own = wave & (p.abreast - 1), turn = wave >> p.abreast_log2;
+  ShareQ8<ROWS> share = {{p}};
   if (!share.begin(share_lds)) return;
   do {
     const SegmentQ8 g = share.segment();
     if (g.st0 >= g.st1) continue;
     const SequenceQ8 &sq = share.sq;
+    const int32_t key_head = g.set * p.abreast + own;
     // fewest tokens that a row sees
     const int32_t floor = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0)));
 
@@ -708,7 +716,7 @@ attention_q8_kernel(AttnQ8Plan p) {
       const int32_t m = r * 16 + (lane & 15);
       const bool some = m < g.live;
       const int32_t tok = int32_t(div_by(p.div_group, uint32_t(g.row0 + (some ? m : 0))));
-      const int32_t h = g.head * p.group + g.row0 + (some ? m : 0) - tok * p.group;
+      const int32_t h = key_head * p.group + g.row0 + (some ? m : 0) - tok * p.group;
       s.limit[r] = some ? g.hidden + tok : 0;
       s.top[r] = kNegInf;
       s.sum[r] = 0.0f;
@@ -721,9 +729,9 @@ attention_q8_kernel(AttnQ8Plan p) {
       for (int n = 0; n < N; ++n) s.o[r][n] = f32x4{};
     }
     {
-      const int32_t last = sq.len - 1, step = int32_t(kQ8Step), b = share.b;
-      const int64_t head = g.head;
-      int32_t t0 = g.st0 * step + wave * kTile;
+      const int32_t last = sq.len - 1, step = 1 << p.step_log2, b = share.b;
+      const int64_t head = key_head;
+      int32_t t0 = g.st0 * step + turn * kTile;
       const int32_t end = min(g.st1 * step, g.most);
       auto at = [&](int32_t t) { return locate<MODE>(p.seq, b, t, last, lane); };
       if (t0 < end) {
@@ -749,9 +757,12 @@ attention_q8_kernel(AttnQ8Plan p) {
       }
     }
 
-    // ---- the wavefronts' sums, joined 16 rows at a time; 16 threads a row ----
-    const int64_t slot = int64_t(blockIdx.x) * 2 + g.part;
-    const int m = tid >> 4, gr = tid & 15;
+    // ---- the sums of a head's wavefronts, joined 16 rows at a time; 16 threads a row, as many threads
+    // for each head ----
+    const int heads_log2 = p.abreast_log2, gr = tid & 15;
+    const int mine = tid >> (8 - heads_log2), m0 = tid >> 4 & ((16 >> heads_log2) - 1);
+    const int64_t slot = (int64_t(blockIdx.x) * 2 + g.part) * p.abreast + mine;
+    const int32_t to_head = g.set * p.abreast + mine;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float sum = sum_quarters(s.sum[r]);
@@ -768,45 +779,44 @@ attention_q8_kernel(AttnQ8Plan p) {
         join_sum[wave][lane] = sum;
       }
       __syncthreads();
-      const int row = r * 16 + m;
-      if (row >= g.live) continue;
-      float top = join_top[0][m];
+      for (int m = m0; m < min(16, g.live - r * 16); m += 16 >> heads_log2) {
+        const int row = r * 16 + m;
+        float top = kNegInf;
+        for (int v = mine; v < kAttnWaves; v += p.abreast) top = fmaxf(top, join_top[v][m]);
+        float l = 0.0f, o[N];
 #pragma unroll
-      for (int v = 1; v < kAttnWaves; ++v) top = fmaxf(top, join_top[v][m]);
-      float l = 0.0f, o[N];
+        for (int n = 0; n < N; ++n) o[n] = 0.0f;
+        for (int v = mine; v < kAttnWaves; v += p.abreast) {
+          const float f = __builtin_amdgcn_exp2f(join_top[v][m] - (top == kNegInf ? 0.0f : top));
+          l += f * join_sum[v][m];
+          const float *from = &join_o[v][((gr >> 2) * 16 + m) * LANE + (gr & 3) * N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) o[n] = 0.0f;
+          for (int n = 0; n < N; n += 4) {
+            const f32x4 y = *reinterpret_cast<const f32x4 *>(from + n);
 #pragma unroll
-      for (int v = 0; v < kAttnWaves; ++v) {
-        const float f = __builtin_amdgcn_exp2f(join_top[v][m] - (top == kNegInf ? 0.0f : top));
-        l += f * join_sum[v][m];
-        const float *from = &join_o[v][((gr >> 2) * 16 + m) * LANE + (gr & 3) * N];
-#pragma unroll
-        for (int n = 0; n < N; n += 4) {
-          const f32x4 y = *reinterpret_cast<const f32x4 *>(from + n);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n + e] += f * y[e];
+            for (int e = 0; e < 4; ++e) o[n + e] += f * y[e];
+          }
         }
-      }
-      if (g.whole()) {
-        const int64_t at = output_row(p, g, sq.first, row);
-        const bool some = l > 0.0f || l != l;  // a row that sees nothing gets zeros
-        const float inv = some ? 1.0f / l : 0.0f;
-        uint32_t y[N / 2];
+        if (g.whole()) {
+          const int64_t at = output_row(p, g, to_head, sq.first, row);
+          const bool some = l > 0.0f || l != l;  // a row that sees nothing gets zeros
+          const float inv = some ? 1.0f / l : 0.0f;
+          uint32_t y[N / 2];
 #pragma unroll
-        for (int n = 0; n < N / 2; ++n) y[n] = Mfma<T>::pack(o[2 * n] * inv, o[2 * n + 1] * inv);
-        char *out = static_cast<char *>(p.out) + at * (2 * D) + gr * (2 * N);
+          for (int n = 0; n < N / 2; ++n) y[n] = Mfma<T>::pack(o[2 * n] * inv, o[2 * n + 1] * inv);
+          char *out = static_cast<char *>(p.out) + at * (2 * D) + gr * (2 * N);
 #pragma unroll
-        for (int n = 0; n < N / 2; n += 2)
-          *reinterpret_cast<uint2 *>(out + 4 * n) = make_uint2(y[n], y[n + 1]);
-        if (gr == 0 && p.lse != nullptr) p.lse[at] = some ? natural<T>(top, l) : kNegInf;
-      } else {
-        float *to = p.parts + (slot * ROWS + row) * D + gr * N;
+          for (int n = 0; n < N / 2; n += 2)
+            *reinterpret_cast<uint2 *>(out + 4 * n) = make_uint2(y[n], y[n + 1]);
+          if (gr == 0 && p.lse != nullptr) p.lse[at] = some ? natural<T>(top, l) : kNegInf;
+        } else {
+          float *to = p.parts + (slot * ROWS + row) * D + gr * N;
 #pragma unroll
-        for (int n = 0; n < N; n += 4)
-          *reinterpret_cast<f32x4 *>(to + n) = f32x4{o[n], o[n + 1], o[n + 2], o[n + 3]};
-        if (gr == 0)
-          *reinterpret_cast<float2 *>(p.stats + (slot * ROWS + row) * 2) = make_float2(top, l);
+          for (int n = 0; n < N; n += 4)
+            *reinterpret_cast<f32x4 *>(to + n) = f32x4{o[n], o[n + 1], o[n + 2], o[n + 3]};
+          if (gr == 0)
+            *reinterpret_cast<float2 *>(p.stats + (slot * ROWS + row) * 2) = make_float2(top, l);
+        }
       }
     }
     share.note(g);
@@ -815,31 +825,41 @@ attention_q8_kernel(AttnQ8Plan p) {
 
 // Joins the parts of items that several workgroups had a share of: with unnormalised outputs o_k at
 // maximum m_k and weight sum l_k,  out = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k,  m = max m_k.
-// One workgroup for each part takes its n-th of the item's rows and columns.
+// One workgroup for each of an item's n parts takes the n-th of its lines (rows of its key heads), several
+// lines at a time, head_size / 4 threads each.  Of more than four parts several threads share an element's,
+// so that the 43 parts of an item of long contexts take two rounds of loads, not eleven (11.8 -> 6.8 us).
 template <typename T>
 __global__ __launch_bounds__(kAttnBlock) void attention_q8_join_kernel(AttnQ8Plan p) {
+  __shared__ f32x4 join_o[kAttnBlock];
+  __shared__ float2 join_stat[kAttnBlock];
   const int64_t *rec = p.joins + int64_t(blockIdx.x) * kQ8JoinWords;
   const int32_t n = int32_t(rec[0]);
   if (n <= 1) return;
   const int64_t g0 = rec[1], first = rec[2];
   const int32_t k0 = int32_t(int64_t(blockIdx.x >> 1) - g0);
-  const int32_t rows = p.rows, wide = p.head_size / 4;
-  const int32_t cells = int32_t(rec[6]) * wide;
-  const int32_t c0 = int32_t(int64_t(cells) * k0 / n), c1 = int32_t(int64_t(cells) * (k0 + 1) / n);
-  for (int32_t cell = c0 + int32_t(threadIdx.x); cell < c1; cell += kAttnBlock) {
-    const int32_t m = cell / wide, d = cell - m * wide;
-    float top = kNegInf, l = 0.0f;
+  const int32_t live = int32_t(rec[6]), lines = live * p.abreast;
+  const int32_t l0 = int32_t(int64_t(lines) * k0 / n), l1 = int32_t(int64_t(lines) * (k0 + 1) / n);
+  const int32_t tid = int32_t(threadIdx.x), wide = p.head_size / 4;  // 16, 32 or 64
+  const int32_t d = tid & (wide - 1), turn = tid / wide, turns = kAttnBlock / wide;
+  constexpr int AHEAD = 4;  // parts that a thread reads at a time
+  int32_t ways = 1;         // threads of an element
+  while (ways < turns && ways * AHEAD < n) ways *= 2;
+  const int32_t way = turn & (ways - 1);
+  for (int32_t l = l0; l < l1; l += turns / ways) {
+    const int32_t line = l + turn / ways, own = line / live, m = line - own * live;
+    const bool some = line < l1;
+    float top = kNegInf, sum = 0.0f;
     f32x4 o = {};
-    constexpr int AHEAD = 4;
-    for (int32_t k = 0; k < n; k += AHEAD) {
+    for (int32_t k = way; k < n; k += AHEAD * ways) {
       float2 stat[AHEAD];
       f32x4 x[AHEAD];
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
+        const int32_t part = k + u * ways;
         stat[u] = make_float2(kNegInf, 0.0f);
         x[u] = f32x4{};
-        if (k + u < n) {
-          const int64_t at = ((g0 + k + u) * 2 + (k + u == 0 ? first : 0)) * rows + m;
+        if (some && part < n) {
+          const int64_t at = (((g0 + part) * 2 + (part == 0 ? first : 0)) * p.abreast + own) * p.rows + m;
           stat[u] = *reinterpret_cast<const float2 *>(p.stats + at * 2);
           x[u] = *reinterpret_cast<const f32x4 *>(p.parts + at * p.head_size + d * 4);
         }
@@ -850,22 +870,39 @@ __global__ __launch_bounds__(kAttnBlock) void attention_q8_join_kernel(AttnQ8Pla
       const float ref = next == kNegInf ? 0.0f : next;
       const float f = __builtin_amdgcn_exp2f(top - ref);
       top = next;
-      l *= f;
+      sum *= f;
       o *= f;
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
         const float y = __builtin_amdgcn_exp2f(stat[u].x - ref);
-        l += stat[u].y * y;
+        sum += stat[u].y * y;
         o += x[u] * y;
       }
     }
-    const bool some = l > 0.0f || l != l;
-    const float inv = some ? 1.0f / l : 0.0f;
-    const int32_t r = int32_t(rec[5]) + m, tok = int32_t(div_by(p.div_group, uint32_t(r)));
-    const int64_t at = (rec[3] + tok) * p.heads + rec[4] * p.group + r - tok * p.group;
+    if (ways > 1) {
+      __syncthreads();
+      join_o[tid] = o;
+      join_stat[tid] = make_float2(top, sum);
+      __syncthreads();
+      if (way != 0) continue;
+      for (int32_t v = 1; v < ways; ++v) top = fmaxf(top, join_stat[tid + v * wide].x);
+      const float ref = top == kNegInf ? 0.0f : top;
+      sum = 0.0f;
+      o = f32x4{};
+      for (int32_t v = 0; v < ways; ++v) {
+        const float y = __builtin_amdgcn_exp2f(join_stat[tid + v * wide].x - ref);
+        sum += join_stat[tid + v * wide].y * y;
+        o += join_o[tid + v * wide] * y;
+      }
+    }
+    if (!some) continue;
+    const bool any = sum > 0.0f || sum != sum;
+    const float inv = any ? 1.0f / sum : 0.0f;
+    const int32_t row = int32_t(rec[5]) + m, tok = int32_t(div_by(p.div_group, uint32_t(row)));
+    const int64_t at = (rec[3] + tok) * p.heads + (rec[4] * p.abreast + own) * p.group + row - tok * p.group;
     *reinterpret_cast<uint2 *>(static_cast<char *>(p.out) + (at * p.head_size + d * 4) * 2) =
         make_uint2(Mfma<T>::pack(o[0] * inv, o[1] * inv), Mfma<T>::pack(o[2] * inv, o[3] * inv));
-    if (d == 0 && p.lse != nullptr) p.lse[at] = some ? natural<T>(top, l) : kNegInf;
+    if (d == 0 && p.lse != nullptr) p.lse[at] = any ? natural<T>(top, sum) : kNegInf;
   }
 }
 

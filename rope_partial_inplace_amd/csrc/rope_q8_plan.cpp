@@ -282,6 +282,11 @@ static int64_t q8_groups(int64_t rows, int64_t width) {
   return 256 * (rows == kQ8ManyRows ? (width == 256 ? 1 : 2) : q8_waves(int(width), int(rows / 16)));
 }
 
+// Key heads of a workgroup, at most.
+static int64_t q8_abreast(int64_t rows, int64_t kv_heads) {
+  return rows == kQ8ManyRows ? 1 : kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1;
+}
+
 int64_t attention_q8_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_size,
                                int64_t sequences) {
   // sizes that the call has no work for, or refuses
@@ -290,8 +295,8 @@ int64_t attention_q8_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, 
     return 0;
   const int64_t rows = q8_rows(tokens, heads / kv_heads, sequences);
   const int64_t groups = q8_groups(rows, head_size);
-  return up(groups * 2 * kQ8JoinWords * 8, 256) + up(2 * groups * rows * 8, 256) +
-         2 * groups * rows * head_size * 4;
+  const int64_t lines = groups * 2 * q8_abreast(rows, kv_heads) * rows;
+  return up(groups * 2 * kQ8JoinWords * 8, 256) + up(lines * 8, 256) + lines * head_size * 4;
 }
 
 int plan_attention_q8(const rope_tensor *query, const rope_tensor *key_cache,
@@ -396,15 +401,20 @@ int plan_attention_q8(const rope_tensor *query, const rope_tensor *key_cache,
   p.out = out->data;
   p.lse = lse != nullptr ? static_cast<float *>(lse->data) : nullptr;
   const int64_t rows = p.rows;
+  const bool side_by_side = p.seq.page_size == 1 || p.k.head < p.k.row;
+  p.abreast = side_by_side ? int32_t(q8_abreast(rows, N)) : 1;
+  while ((1 << p.abreast_log2) < p.abreast) ++p.abreast_log2;
+  p.head_sets = p.kv_heads / p.abreast;
+  p.step_log2 = q8_step_log2(rows, D, p.abreast_log2);
   // tiles: as many as the rows fill, and one begun for every sequence; steps, and what beginning costs
-  const double tiles = double(N) * (double(T) * double(p.group) / double(rows) + double(B));
-  const double steps = double(p.seq.max_pages) * double(p.seq.page_size) / 64 + 16;
+  const double tiles = double(p.head_sets) * (double(T) * double(p.group) / double(rows) + double(B));
+  const double steps = double(p.seq.max_pages) * double(p.seq.page_size) / double(1 << p.step_log2) + 16;
   p.small = tiles * steps < double(int64_t(1) << 30);
   char *w = static_cast<char *>(workspace);
   p.joins = reinterpret_cast<int64_t *>(w);
   w += up(p.groups * 2 * kQ8JoinWords * 8, 256);
   p.stats = reinterpret_cast<float *>(w);
-  w += up(2 * p.groups * rows * 8, 256);
+  w += up(2 * p.groups * p.abreast * rows * 8, 256);
   p.parts = reinterpret_cast<float *>(w);
   return ROPE_OK;
 }

@@ -81,14 +81,20 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
                    AppendQ8Plan *plan, std::string *err);
 
 // ---- attention --------------------------------------------------------------------------------
-constexpr int64_t kQ8Step = 128;    // cached tokens a workgroup takes at a time
-// Wavefronts of a SIMD that the registers allow, for heads of `width` and `tiles` 16-row tiles; a call has
-// as many workgroups as the card then holds, 256 compute units at a time.
+// Wavefronts of a SIMD for heads of `width` and `tiles` 16-row tiles; a call has as many workgroups as the card
+// then holds, 256 compute units at a time.  Two, where the registers allow three (heads of 128, one tile): what is
+// under way is enough, and fewer streams at a time reach more of HBM's rate (64 decoding sequences 70.5 -> 67
+// us, six of 60-131k tokens 289 -> 281).
 constexpr int q8_waves(int width, int tiles) {
-  return width == 256 ? (tiles == 1 ? 2 : 1) : tiles == 1 ? (width == 64 ? 4 : 3) : width == 64 ? 3 : 2;
+  return width == 64 ? 3 : width == 128 || tiles == 1 ? 2 : 1;
 }
 constexpr int64_t kQ8ManyRows = 128;  // rows of a workgroup where there are many
 constexpr int kQ8JoinWords = 8;
+// Cached tokens that a workgroup takes at a time: 32 of each of the wavefronts of a head, of which there are
+// 4 >> heads_log2; 64, or 32, where there are many rows.
+constexpr int q8_step_log2(int64_t rows, int64_t width, int heads_log2) {
+  return rows == kQ8ManyRows ? (width == 256 ? 5 : 6) : 7 - heads_log2;
+}
 
 // Keys or values of the cache.
 struct Q8Cache {
@@ -112,14 +118,21 @@ struct AttnQ8Plan {
   float scale_log2 = 0;
   int32_t rows = 16;   // query rows of a workgroup
   int32_t groups = 0;  // workgroups
+  // Wavefronts of a workgroup take different key heads of the same tokens (sets of 2 or 4) where those lie
+  // side by side: 128 bytes of every token, 1 KB apart, are no good way through HBM, and with a scale for
+  // each token the lines of scales are shared, too (six sequences of 60-131k tokens of 8 heads of 128: 331 us
+  // with sets of 1, 300 with 2, 281 with 4; 64 of 9000, heads of 64: 202 -> 134).  Caches that keep a head's tokens
+  // together have sets of 1 (64 of 9000, heads of 128: 212 us, with 4: 218).
+  int32_t abreast = 1, abreast_log2 = 0, head_sets = 0;
+  int32_t step_log2 = 7;  // cached tokens of a workgroup at a time
   bool small = false;  // the items' cost (in tokens' steps) fits 31 bits, whatever the lengths
   void *out = nullptr;
   float *lse = nullptr;
   // workspace: for a workgroup's first and last part the record of the item it is part of, its
   // rows' maxima and sums, and its unnormalised outputs
   int64_t *joins = nullptr;  // [groups][2][kQ8JoinWords]
-  float *stats = nullptr;    // [groups][2][rows][2]
-  float *parts = nullptr;    // [groups][2][rows][head_size]
+  float *stats = nullptr;    // [groups][2][abreast][rows][2]
+  float *parts = nullptr;    // [groups][2][abreast][rows][head_size]
 };
 
 int64_t attention_q8_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_size,

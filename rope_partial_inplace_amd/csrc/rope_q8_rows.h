@@ -17,6 +17,7 @@ namespace {
 template <int D>
 struct RowsShape {
   static constexpr int TILE = D == 256 ? 32 : 64;  // tokens of a step
+  static_assert(TILE == 1 << q8_step_log2(kQ8ManyRows, D, 0), "a step is a tile");
   static constexpr int PANELS = D / 64;
   static constexpr int PANEL = TILE * 128;          // bytes
   static constexpr int THREADS = kAttnBlock / TILE;  // of a token's codes
@@ -123,14 +124,14 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
   __shared__ __attribute__((aligned(16))) RowsLds<D> lds;
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  ShareQ8<ROWS, TILE> share = {{p}};
+  ShareQ8<ROWS> share = {{p}};
   if (!share.begin(lds.share)) return;
   do {
     const SegmentQ8 g = share.segment();
     if (g.st0 >= g.st1) continue;
     const SequenceQ8 &sq = share.sq;
     const int32_t b = share.b, last = sq.len - 1;
-    const int64_t head = g.head;
+    const int64_t head = g.set;
 
     // ---- the lane's query row ----
     const int32_t m = wave * 32 + (lane & 31);
@@ -140,7 +141,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
     const int32_t floor = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0 + min(wave * 32, g.live - 1))));
     s16x8 q[D / 16];
     {
-      const int32_t h = g.head * p.group + g.row0 + (some ? m : 0) - tok * p.group;
+      const int32_t h = g.set * p.group + g.row0 + (some ? m : 0) - tok * p.group;
       const T *from = static_cast<const T *>(p.q) + int64_t(sq.first + tok) * p.q_tok +
                       int64_t(h) * p.q_head + 8 * (lane >> 5);
 #pragma unroll
@@ -309,7 +310,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
     if (some) {
       const float unit = Mfma<T>::kNarrow ? reach : 1.0f;
       if (g.whole()) {
-        const int64_t row = output_row(p, g, sq.first, m);
+        const int64_t row = output_row(p, g, g.set, sq.first, m);
         const bool any = sum > 0.0f || sum != sum;  // a row that sees nothing gets zeros
         const float inv = any ? unit / sum : 0.0f;
         char *out = static_cast<char *>(p.out) + row * (2 * D) + 8 * (lane >> 5);
