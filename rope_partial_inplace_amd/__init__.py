@@ -401,7 +401,7 @@ def _raw_stream(stream, dev: int):
 def _run_on(dev: int, fn, *args):
     """One C call with GPU `dev` as the current HIP device."""
     import torch
-    if dev < 0 or dev == torch.cuda.current_device():
+    if dev < 0 or dev == torch._C._cuda_getDevice():
         code = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -411,17 +411,17 @@ def _run_on(dev: int, fn, *args):
 
 
 def _new(stream, dev: int, *specs):
-    """New tensors of (shape, dtype, device), None for a spec of None.  Torch allocates them for
-    the stream that the call runs on: outputs and workspaces belong to it."""
+    """New tensors of (shape, dtype, a tensor on their device), None for a spec of None.  Torch
+    allocates them for the stream that the call runs on: outputs and workspaces belong to it."""
     import torch
     if stream is None or dev < 0:
-        return [s and torch.empty(s[0], dtype=s[1], device=s[2]) for s in specs]
+        return [s and s[2].new_empty(s[0], dtype=s[1]) for s in specs]
     if not isinstance(stream, torch.cuda.Stream):
         handle = getattr(stream, "cuda_stream", stream)
         stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
                   else torch.cuda.default_stream(dev))
     with torch.cuda.stream(stream):
-        return [s and torch.empty(s[0], dtype=s[1], device=s[2]) for s in specs]
+        return [s and s[2].new_empty(s[0], dtype=s[1]) for s in specs]
 
 
 def rope_append_paged_cache(positions, slots, key, key_cache, cos_sin_cache, value=None,
@@ -438,7 +438,7 @@ def rope_append_paged_cache(positions, slots, key, key_cache, cos_sin_cache, val
     dev = _device_index((positions, slots, query, key, value, cos_sin_cache, query_out, key_cache,
                          value_cache))
     if query is not None and query_out is None:
-        query_out, = _new(stream, dev, (query.shape, query.dtype, query.device))
+        query_out, = _new(stream, dev, (query.shape, query.dtype, query))
     _run_on(dev, LIB.rope_append_paged_cache, _pack(positions), _pack(slots), _pack(query),
             _pack(key), _pack(value), _pack(cos_sin_cache), query_rot_start, key_rot_start,
             bool(is_neox_style), _pack(query_out), _pack(key_cache), _pack(value_cache),
@@ -465,11 +465,10 @@ def rope_latent_attention_paged(query, latent_cache, page_table, seq_lens, laten
         raise RopeError(ROPE_ERR_PARAM_INVALID, "query must be 3-D and seq_lens 1-D")
     T, heads, _ = query.shape
     need = LIB.rope_latent_attention_paged_workspace(T, heads, latent_dim, seq_lens.shape[0])
-    d = query.device
     new_out, new_lse, workspace = _new(
         stream, dev,
-        ((T, heads, max(0, latent_dim)), query.dtype, d) if out is None else None,
-        ((T, heads), torch.float32, d) if lse is None else None, (need, torch.uint8, d))
+        ((T, heads, max(0, latent_dim)), query.dtype, query) if out is None else None,
+        ((T, heads), torch.float32, query) if lse is None else None, (need, torch.uint8, query))
     out, lse = out if new_out is None else new_out, lse if new_lse is None else new_lse
     _run_on(dev, LIB.rope_latent_attention_paged, _pack(query), _pack(latent_cache),
             _pack(page_table), _pack(seq_lens), _pack(query_offsets), latent_dim, scale,
@@ -499,11 +498,10 @@ def rope_latent_attention(query, key, key_rope, value, scale: float, causal: boo
     if query.dim() != 3 or value.dim() != 3:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "query and value must be 3-D")
     T, heads, _ = query.shape
-    d = query.device
     new_out, new_lse = _new(
         stream, dev,
-        ((T, heads, value.shape[2]), query.dtype, d) if out is None else None,
-        ((T, heads), torch.float32, d) if lse is None else None)
+        ((T, heads, value.shape[2]), query.dtype, query) if out is None else None,
+        ((T, heads), torch.float32, query) if lse is None else None)
     out, lse = out if new_out is None else new_out, lse if new_lse is None else new_lse
     _run_on(dev, LIB.rope_latent_attention, _pack(query), _pack(key), _pack(key_rope),
             _pack(value), _pack(query_offsets), _pack(key_offsets),
@@ -525,8 +523,8 @@ def rope_latent_attention_backward(grad, query, key, key_rope, value, out, lse, 
     need = LIB.rope_latent_attention_backward_workspace(query.shape[0], key.shape[0],
                                                         query.shape[1])
     *grads, workspace = _new(stream, dev,
-                             *((t.shape, t.dtype, t.device) for t in (query, key, key_rope, value)),
-                             (need, torch.uint8, query.device))
+                             *((t.shape, t.dtype, t) for t in (query, key, key_rope, value)),
+                             (need, torch.uint8, query))
     _run_on(dev, LIB.rope_latent_attention_backward, _pack(grad), _pack(query), _pack(key),
             _pack(key_rope), _pack(value), _pack(out), _pack(lse), _pack(query_offsets),
             _pack(key_offsets), _sequences(num_sequences, query_offsets), scale, bool(causal),
@@ -598,7 +596,7 @@ def rope_append_paged_cache_q8(positions, key, value, key_cache, value_cache, ke
                          query_offsets, query_out, key_cache, value_cache, key_scales,
                          value_scales))
     if query is not None and query_out is None:
-        query_out, = _new(stream, dev, (query.shape, query.dtype, query.device))
+        query_out, = _new(stream, dev, (query.shape, query.dtype, query))
     _run_on(dev, LIB.rope_append_paged_cache_q8, _pack(positions), _pack(query), _pack(key),
             _pack(value), _pack(cos_sin_cache), _pack(page_table), _pack(seq_lens),
             _pack(query_offsets), query_rot_start, key_rot_start, bool(is_neox_style),
@@ -627,10 +625,9 @@ def rope_attention_paged_q8(query, key_cache, value_cache, key_scales, value_sca
     T, heads, width = query.shape
     need = LIB.rope_attention_paged_q8_workspace(T, heads, key_cache.shape[2], width,
                                                  seq_lens.shape[0])
-    d = query.device
     new_out, new_lse, workspace = _new(
-        stream, dev, ((T, heads, width), query.dtype, d) if out is None else None,
-        ((T, heads), torch.float32, d) if lse is None else None, (need, torch.uint8, d))
+        stream, dev, ((T, heads, width), query.dtype, query) if out is None else None,
+        ((T, heads), torch.float32, query) if lse is None else None, (need, torch.uint8, query))
     out, lse = out if new_out is None else new_out, lse if new_lse is None else new_lse
     _run_on(dev, LIB.rope_attention_paged_q8, _pack(query), _pack(key_cache), _pack(value_cache),
             _pack(key_scales), _pack(value_scales), _pack(page_table), _pack(seq_lens),
@@ -689,13 +686,13 @@ def rope_fork_pages(page_table, seq_lens, parents, ref_counts, page_size: int, c
     if page_table.dim() != 2 or parents.dim() != 1 or ref_counts.dim() != 1:
         raise RopeError(ROPE_ERR_PARAM_INVALID,
                         "page_table must be 2-D, parents and ref_counts 1-D")
-    rows, pages, d, i64 = parents.shape[0], ref_counts.shape[0], page_table.device, torch.int64
+    rows, pages, like, i64 = parents.shape[0], ref_counts.shape[0], page_table, torch.int64
     need = LIB.rope_fork_pages_workspace(page_table.shape[0], rows, pages)
     given = (page_table_out, seq_lens_out, ref_counts_out, shortage)
     shapes = ((rows, page_table.shape[1]), (rows,), (pages,), (1,))
-    *new, workspace = _new(stream, dev, *((s, i64, d) if g is None else None
+    *new, workspace = _new(stream, dev, *((s, i64, like) if g is None else None
                                           for g, s in zip(given, shapes)),
-                           (need, torch.uint8, d))
+                           (need, torch.uint8, like))
     outs = tuple(g if n is None else n for g, n in zip(given, new))
     _run_on(dev, LIB.rope_fork_pages, _pack(page_table), _pack(seq_lens), _pack(parents),
             _pack(grow), _pack(ref_counts), page_size, caches.packed, len(caches.tensors),
@@ -715,13 +712,13 @@ def rope_compact_pages(page_table, ref_counts, caches=(), page_table_out=None, r
                                                       ref_counts_out, page_map, live)))
     if ref_counts.dim() != 1:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "ref_counts must be 1-D")
-    pages, d, i64 = ref_counts.shape[0], ref_counts.device, torch.int64
+    pages, like, i64 = ref_counts.shape[0], ref_counts, torch.int64
     need = LIB.rope_compact_pages_workspace(pages)
     given = (page_table_out, ref_counts_out, page_map, live)
     shapes = (page_table.shape, (pages,), (pages,), (1,))
-    *new, workspace = _new(stream, dev, *((s, i64, d) if g is None else None
+    *new, workspace = _new(stream, dev, *((s, i64, like) if g is None else None
                                           for g, s in zip(given, shapes)),
-                           (need, torch.uint8, d))
+                           (need, torch.uint8, like))
     outs = tuple(g if n is None else n for g, n in zip(given, new))
     _run_on(dev, LIB.rope_compact_pages, _pack(page_table), _pack(ref_counts), caches.packed,
             len(caches.tensors), *map(_pack, outs), workspace.data_ptr(), need,

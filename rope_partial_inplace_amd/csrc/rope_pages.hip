@@ -10,13 +10,15 @@
 // of them can then be read by one copy and written by another.
 //   1. one workgroup: which row continues a sequence first, what each row wants, and the sums of
 //      that; the others count the free pages of 4096 each
-//   2. the free pages' numbers, as many as are wanted; the holds as they were
+//   2. the free pages' numbers; the holds as they were
 //   3. tables, holds and copies
 //
 // Compact: with n pages in use, the k-th one at or behind place n goes to the k-th free place before.
 //   1. pages in use of 4096 each; 2. the map and the list of moves; 3. tables, holds and copies
 //
-// All of it moves bytes.
+// Of small pools launches 1 and 2 are one: each workgroup counts the pages before its own by itself.
+//
+// Copies move bytes; all else is a few sums, bound by the way from one launch to the next.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -36,6 +38,11 @@ namespace {
 // reads of page numbers, an idle wavefront its launch (355000 pieces of a compacted pool: 271 us with
 // 65536 wavefronts, 252 with 262144, 332 with one for every piece that could be).
 constexpr int64_t kForkGroups = 8192, kCompactGroups = 262144;
+
+// Chunks of pages that every workgroup counts for itself, at most.  That saves the launch that would tell it, and
+// costs it a turn for each chunk: fork 14.4 -> 11.0 us with one chunk, 14.0 -> 12.1 with four, 14.0 -> 14.4
+// with eight; compaction, which counts twice, 12.0 -> 10.3 with one, 16.3 -> 18.8 with four.
+constexpr int64_t kFewFork = 4, kFewCompact = 2;
 
 typedef uint32_t words4 __attribute__((ext_vector_type(4)));
 typedef uint32_t words2 __attribute__((ext_vector_type(2)));
@@ -199,7 +206,38 @@ __device__ inline int64_t chunks_before(const int32_t *counts, int64_t chunks, i
   return sum & 0xffffffff;
 }
 
+// The same, counted here: pages with (USED) or without holds before `chunk`, and all of them (ALL) or
+// those up to `chunk`.
+template <bool USED, bool ALL>
+__device__ inline int64_t count_before(const int64_t *refs, int64_t stride, int64_t num_pages,
+                                       int64_t chunks, int64_t chunk, int64_t *lds, int64_t *total) {
+  int64_t mine = 0, sum;
+  for (int64_t c = 0; c < (ALL ? chunks : chunk + 1); ++c) {
+    uint32_t flags;
+    const int64_t n = chunk_flags<USED>(refs, stride, c, num_pages, &flags);
+    mine += n << 32 | (c < chunk ? n : 0);
+  }
+  scan_block(mine, lds, &sum);
+  *total = sum >> 32;
+  return sum & 0xffffffff;
+}
+
 // ---- fork ------------------------------------------------------------------------------------------
+// The numbers of a chunk's free pages, `rank` of which lie before it, and the holds as they were.
+__device__ inline void list_free(const ForkPlan &p, int64_t chunk, int64_t rank, int64_t *lds) {
+  uint32_t flags;
+  int64_t sum;
+  const int32_t n = chunk_flags<false>(p.refs, p.ref_stride, chunk, p.num_pages, &flags);
+  rank += scan_block(n, lds, &sum);
+  const int64_t first = chunk * kPageChunk + int64_t(threadIdx.x) * kPerThread;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    if (first + k >= p.num_pages) break;
+    if (flags >> k & 1u) p.free[rank++] = int32_t(first + k);
+    p.refs_out[(first + k) * p.ref_out_stride] = p.refs[(first + k) * p.ref_stride];
+  }
+}
+
 __device__ inline int64_t clamped_len(const ForkPlan &p, int64_t b) {
   return min(max(p.lens[b * p.len_stride], int64_t(0)), p.table.width * p.page_size);
 }
@@ -231,7 +269,8 @@ __device__ inline X fresh(const X *p) {  // as the other threads' atomics left i
 // kLocalRows of them; else through global memory.
 constexpr int64_t kLocalRows = 4096;
 
-template <bool LOCAL>
+// FEW: the other workgroups list their chunk's free pages, too.
+template <bool LOCAL, bool FEW>
 __global__ __launch_bounds__(kCountBlock) void fork_count_kernel(ForkPlan p) {
   __shared__ int64_t lds[kCountBlock / 64];
   __shared__ int32_t local[LOCAL ? 2 * kLocalRows : 1];
@@ -239,10 +278,17 @@ __global__ __launch_bounds__(kCountBlock) void fork_count_kernel(ForkPlan p) {
   int64_t sum;
   if (blockIdx.x > 0) {
     const int64_t chunk = int64_t(blockIdx.x) - 1;
-    uint32_t flags;
-    const int32_t n = chunk_flags<false>(p.refs, p.ref_stride, chunk, p.num_pages, &flags);
-    scan_block(n, lds, &sum);
-    if (threadIdx.x == 0) p.counts[chunk] = int32_t(sum);
+    if constexpr (FEW) {
+      const int64_t rank = count_before<false, false>(p.refs, p.ref_stride, p.num_pages, p.chunks,
+                                                      chunk, lds, &sum);
+      if (chunk == p.chunks - 1 && threadIdx.x == 0) p.totals[2] = sum;
+      list_free(p, chunk, rank, lds);
+    } else {
+      uint32_t flags;
+      const int32_t n = chunk_flags<false>(p.refs, p.ref_stride, chunk, p.num_pages, &flags);
+      scan_block(n, lds, &sum);
+      if (threadIdx.x == 0) p.counts[chunk] = int32_t(sum);
+    }
     return;
   }
   int32_t *first = LOCAL ? local : p.first, *children = LOCAL ? local + kLocalRows : p.children;
@@ -304,32 +350,16 @@ __global__ __launch_bounds__(kCountBlock) void fork_count_kernel(ForkPlan p) {
   if (threadIdx.x == 0) {
     p.totals[0] = wanted;
     p.totals[1] = copies;
+    if (p.chunks == 0) p.totals[2] = 0;
   }
 }
 
 __global__ __launch_bounds__(kCountBlock) void fork_free_kernel(ForkPlan p) {
   __shared__ int64_t lds[kCountBlock / 64];
-  const int64_t chunk = blockIdx.x, wanted = p.totals[0];
-  int64_t total, sum;
-  int64_t rank = chunks_before(p.counts, p.chunks, chunk, lds, &total);
-  if (chunk == 0 && threadIdx.x == 0) {
-    p.totals[2] = total;
-    p.shortage[0] = max(wanted - total, int64_t(0));
-  }
-  if (chunk >= p.chunks) return;  // no pages at all
-  uint32_t flags;
-  const int32_t n = chunk_flags<false>(p.refs, p.ref_stride, chunk, p.num_pages, &flags);
-  rank += scan_block(n, lds, &sum);
-  const int64_t first = chunk * kPageChunk + int64_t(threadIdx.x) * kPerThread;
-#pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
-    if (first + k >= p.num_pages) break;
-    if (flags >> k & 1u) {
-      if (rank < wanted) p.free[rank] = int32_t(first + k);
-      ++rank;
-    }
-    p.refs_out[(first + k) * p.ref_out_stride] = p.refs[(first + k) * p.ref_stride];
-  }
+  int64_t total;
+  const int64_t rank = chunks_before(p.counts, p.chunks, blockIdx.x, lds, &total);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.totals[2] = total;
+  list_free(p, blockIdx.x, rank, lds);
 }
 
 __device__ inline int64_t new_page(const ForkPlan &p, int64_t rank) {
@@ -343,6 +373,7 @@ __device__ inline void add_holds(const ForkPlan &p, int64_t page, int64_t n) {
 }
 
 __device__ inline void fork_tables(const ForkPlan &p, int64_t at, int64_t step) {
+  if (at == 0) p.shortage[0] = max(p.totals[0] - p.totals[2], int64_t(0));
   const int64_t wide = max(p.out.width, int64_t(1));
   for (int64_t e = at; e < p.out.rows * wide; e += step) {
     const int64_t i = e / wide, j = e - i * wide;
@@ -402,15 +433,22 @@ __global__ __launch_bounds__(kCountBlock) void compact_count_kernel(CompactPlan 
   if (threadIdx.x == 0) p.counts[blockIdx.x] = int32_t(sum);
 }
 
+template <bool FEW>
 __global__ __launch_bounds__(kCountBlock) void compact_map_kernel(CompactPlan p) {
   __shared__ int64_t lds[kCountBlock / 64];
   const int64_t chunk = blockIdx.x;
   int64_t n, sum, below;
   uint32_t flags;
-  int64_t rank = chunks_before(p.counts, p.chunks, chunk, lds, &n);
+  auto before = [&](int64_t c, int64_t *all) {
+    if constexpr (FEW)
+      return count_before<true, true>(p.refs, p.ref_stride, p.num_pages, p.chunks, c, lds, all);
+    else
+      return chunks_before(p.counts, p.chunks, c, lds, all);
+  };
+  int64_t rank = before(chunk, &n);
   // pages in use before place n: of the whole chunks before it, and of its own
   const int64_t border = n / kPageChunk;
-  const int64_t whole = chunks_before(p.counts, p.chunks, border, lds, &sum);
+  const int64_t whole = before(border, &sum);
   scan_block(chunk_flags<true>(p.refs, p.ref_stride, border, min(n, p.num_pages), &flags), lds, &below);
   const int64_t moves = n - whole - below;
   if (chunk == 0 && threadIdx.x == 0) {
@@ -529,14 +567,18 @@ ROPE_API int rope_fork_pages(const rope_tensor *page_table, const rope_tensor *s
     return st;
   }
   g_last_error.clear();
-  st = launch_kernel(p.table.rows <= kLocalRows
-                         ? reinterpret_cast<const void *>(&fork_count_kernel<true>)
-                         : reinterpret_cast<const void *>(&fork_count_kernel<false>),
-                     dim3(uint32_t(1 + p.chunks)), kCountBlock, 0, stream, &p);
+#define ROPE_FC(L, F) reinterpret_cast<const void *>(&fork_count_kernel<L, F>)
+  const bool few = p.chunks <= kFewFork;
+  const void *count = p.table.rows <= kLocalRows ? (few ? ROPE_FC(true, true) : ROPE_FC(true, false))
+                                                 : (few ? ROPE_FC(false, true) : ROPE_FC(false, false));
+#undef ROPE_FC
+  st = launch_kernel(count, dim3(uint32_t(1 + p.chunks)), kCountBlock, 0, stream, &p);
   if (st != ROPE_OK) return st;
-  st = launch_kernel(reinterpret_cast<const void *>(&fork_free_kernel),
-                     dim3(uint32_t(std::max<int64_t>(1, p.chunks))), kCountBlock, 0, stream, &p);
-  if (st != ROPE_OK) return st;
+  if (!few) {
+    st = launch_kernel(reinterpret_cast<const void *>(&fork_free_kernel), dim3(uint32_t(p.chunks)),
+                       kCountBlock, 0, stream, &p);
+    if (st != ROPE_OK) return st;
+  }
   return run_writes(reinterpret_cast<const void *>(&fork_write_kernel), p, list, kForkWords,
                     [](const ForkPlan &q) {
                       return std::min(q.caches.units(q.out.rows), kForkGroups);
@@ -564,12 +606,14 @@ ROPE_API int rope_compact_pages(const rope_tensor *page_table, const rope_tensor
     return st;
   }
   g_last_error.clear();
-  if (p.chunks > 0) {
+  const bool few = p.chunks <= kFewCompact;
+  if (!few) {
     st = launch_kernel(reinterpret_cast<const void *>(&compact_count_kernel),
                        dim3(uint32_t(p.chunks)), kCountBlock, 0, stream, &p);
     if (st != ROPE_OK) return st;
   }
-  st = launch_kernel(reinterpret_cast<const void *>(&compact_map_kernel),
+  st = launch_kernel(few ? reinterpret_cast<const void *>(&compact_map_kernel<true>)
+                         : reinterpret_cast<const void *>(&compact_map_kernel<false>),
                      dim3(uint32_t(std::max<int64_t>(1, p.chunks))), kCountBlock, 0, stream, &p);
   if (st != ROPE_OK) return st;
   return run_writes(reinterpret_cast<const void *>(&compact_write_kernel), p, list, kPageWords,

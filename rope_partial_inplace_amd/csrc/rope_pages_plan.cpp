@@ -275,7 +275,8 @@ int plan_fork_pages(const rope_tensor *page_table, const rope_tensor *seq_lens,
   p.num_pages = pages;
   p.page_size = page_size;
   p.chunks = (pages + kPageChunk - 1) / kPageChunk;
-  const int64_t entries = std::max(R * std::max<int64_t>(p.out.width, 1), B * p.table.width);
+  const int64_t entries =  // the first one's thread writes the shortage, too
+      std::max({int64_t(1), R * std::max<int64_t>(p.out.width, 1), B * p.table.width});
   p.table_blocks = std::min<int64_t>(1 << 16, (entries + kPageBlock - 1) / kPageBlock);
   char *w = static_cast<char *>(workspace);
   auto take = [&w](int64_t bytes) {

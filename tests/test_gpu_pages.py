@@ -225,6 +225,13 @@ def test_compact_sizes(pages, share):
                 share)
 
 
+@pytest.mark.parametrize("pages", [8 * 4096, 8 * 4096 + 1, 70000, 300001])
+def test_large_pools(pages):
+    """Pools whose free pages are counted chunk by chunk first."""
+    run_compact(random.Random(pages), 7, 5, pages, ["vector"], 0.4, in_place=pages % 2 == 1)
+    run_fork(random.Random(pages), 40, 70, 4, 6, pages, ["vector"], in_place=pages % 2 == 0)
+
+
 def test_pages_beyond_4_gib():
     pages, words = 70, 1 << 26  # 64 MiB each
     x = torch.zeros(pages, words, dtype=torch.int8, device=DEV)
