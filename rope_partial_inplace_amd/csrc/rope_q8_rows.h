@@ -7,6 +7,10 @@
 // second of two buffers, in the panels of rope_mfma.h; S^T = K Q^T and O^T = V^T P^T are 32x32x16
 // products, so that a lane owns a query row and P goes from one to the other in registers.
 // Scales wait, as in the other kernel: keys' multiply the scores, values' the weights.
+//
+// 4 x 4096 prompt tokens of 32 heads of 128, 8 key heads: 685 us, 0.80 PFLOP/s.  The vector units work 0.61 of the
+// cycles (of 327 instructions a step 96 turn codes into operands, 161 are the softmax's), the matrix units 0.33:
+// the two wavefronts of a SIMD rarely need them at the same time, and what is left is not idle.
 #pragma once
 
 #include "rope_q8_attn.h"
@@ -21,20 +25,34 @@ struct RowsShape {
   static constexpr int PANELS = D / 64;
   static constexpr int PANEL = TILE * 128;          // bytes
   static constexpr int THREADS = kAttnBlock / TILE;  // of a token's codes
-  static constexpr int BYTES = D / THREADS;          // of one thread
+  static constexpr int BYTES = D / THREADS;          // of one thread: pieces of 16
+  // A wavefront takes tokens of 16 from run(wave) on (8 where a tile has 32); a lane one of them, and
+  // every THREADS-th 16 codes from 16 piece() on.  Eight lanes write operands to LDS at a time: two tokens 8
+  // apart, whose chunks of half a row of a panel lie in different banks.  (With neighbouring tokens, and a lane's
+  // codes side by side, four met in a bank: 0.22 of the cycles were such conflicts, 4 x 4096 tokens of 32
+  // heads took 742 us, not 685.)
+  __device__ static int run(int wave) { return D == 256 ? wave / 2 * 16 : wave * 16; }
+  __device__ static int token(int wave, int lane) {
+    const int x = lane >> 2;
+    return D == 256 ? (x & 1) << 3 | wave % 2 * 4 | lane >> 4
+                    : (x & 1) << 3 | (x & 2) >> 1 | (x & 12) >> 1;
+  }
+  __device__ static int piece(int lane) { return D == 256 ? (lane & 3) | (lane >> 1 & 4) : lane & 3; }
 };
 
-// Scales of a tile.  COARSE (pages and blocks of whole runs of 4 tokens): one for each 4 tokens,
-// those of the lanes below 32 first: of tokens 8 c + 4 (l / 32) and on at 8 (l / 32) + c, c up to 8; else
-// one for each token.
-template <int D, bool COARSE>
+// Scales of a tile.  kCoarse: one for each 4 tokens, those of the lanes below 32 first: of tokens
+// 8 c + 4 (l / 32) and on at 8 (l / 32) + c, c up to 8; else one for each token.
+template <int D, int MODE>
 struct ScalesOf {
-  static constexpr int RUN = COARSE ? 4 : 1, COUNT = RowsShape<D>::TILE / RUN;
-  __device__ static int place(int i) { return COARSE ? (i & 1) * (COUNT / 2) + (i >> 1) : i; }
+  static constexpr int RUN = MODE == kCoarse ? 4 : 1, COUNT = RowsShape<D>::TILE / RUN;
+  static constexpr int EACH = COUNT / kAttnWaves;  // of a wavefront's own tokens
+  // the token of a wavefront's run of 16 whose scale a lane loads
+  __device__ static int token(int wave, int lane) { return (wave * EACH % (16 / RUN) + lane % EACH) * RUN; }
+  __device__ static int place(int i) { return MODE == kCoarse ? (i & 1) * (COUNT / 2) + (i >> 1) : i; }
 };
 
-// What a thread has of a tile: some of a token's key and value codes, and a scale (of the keys in the first
-// threads, of the values in the next).
+// What a thread has of a tile: some of a token's key and value codes, and a scale (of its wavefront's keys in
+// the first lanes, of their values in the next).
 template <int D>
 struct StageQ8 {
   uint4 k[RowsShape<D>::BYTES / 16], v[RowsShape<D>::BYTES / 16];
@@ -51,61 +69,110 @@ struct RowsLds {
   ShareLds share;
 };
 
-// The page and row of a thread's token, tokens past the last one repeat it.
-struct TokenQ8 {
-  int32_t page, row;
+// Where a wavefront's tokens of a tile lie; tokens past the last one repeat it.  Pages of whole runs of 16
+// tokens: all in one page, whose number and first row are the same for all lanes.
+template <int MODE>
+struct TokensQ8 {
+  int64_t page;
+  int32_t row, more;  // the first token's row; tokens that follow it in the sequence
 };
-__device__ __forceinline__ TokenQ8 token_at(const Sequences &s, int32_t b, int32_t t) {
-  const uint32_t i = div_by(s.div_page, uint32_t(t));
-  return {int32_t(page_of(s, b, int32_t(i))), t - int32_t(i * uint32_t(s.page_size))};
+template <>
+struct TokensQ8<kAny> {
+  int32_t page, row;  // of the thread's token, and of the one whose scale it loads
+  int32_t scale_page, scale_row;
+};
+
+template <int D, int MODE>
+__device__ __forceinline__ TokensQ8<MODE> tokens_at(const Sequences &s, int32_t b, int32_t t, int32_t last,
+                                                    int wave, int lane) {
+  using S = RowsShape<D>;
+  const int32_t t0 = t + S::run(wave);
+  TokensQ8<MODE> x;
+  if constexpr (MODE != kAny) {
+    const int32_t begin = min(t0, last);
+    const uint32_t i = div_by(s.div_page, uint32_t(begin));
+    x.page = page_of(s, b, int32_t(i));
+    x.row = begin - int32_t(i * uint32_t(s.page_size));
+    x.more = last - begin;
+  } else {
+    auto one = [&](int32_t token, int32_t &page, int32_t &row) {
+      const uint32_t i = div_by(s.div_page, uint32_t(token));
+      page = int32_t(page_of(s, b, int32_t(i)));
+      row = token - int32_t(i * uint32_t(s.page_size));
+    };
+    one(min(t0 + S::token(wave, lane), last), x.page, x.row);
+    one(min(t0 + ScalesOf<D, MODE>::token(wave, lane), last), x.scale_page, x.scale_row);
+  }
+  return x;
 }
 
-template <int D, bool COARSE>
-__device__ __forceinline__ void fetch(const AttnQ8Plan &p, const TokenQ8 &codes, const TokenQ8 &scale,
-                                      int64_t head, int tid, StageQ8<D> &x) {
+template <int D, int MODE>
+__device__ __forceinline__ void fetch(const AttnQ8Plan &p, const TokensQ8<MODE> &x, int64_t head, int wave,
+                                      int lane, StageQ8<D> &stage) {
   using S = RowsShape<D>;
-  const int64_t at = tid % S::THREADS * S::BYTES;
-  const uint8_t *k = p.k.codes + codes.page * p.k.page + head * p.k.head + int64_t(codes.row) * p.k.row + at;
-  const uint8_t *v = p.v.codes + codes.page * p.v.page + head * p.v.head + int64_t(codes.row) * p.v.row + at;
+  using Sc = ScalesOf<D, MODE>;
+  const uint8_t *k, *v;
+  uint32_t k_at, v_at;
+  const float *scale;
+  const bool keys = lane < Sc::EACH;
+  if constexpr (MODE != kAny) {
+    const int64_t page = uniform64(x.page), row = x.row;
+    k = p.k.codes + page * p.k.page + head * p.k.head + row * p.k.row;
+    v = p.v.codes + page * p.v.page + head * p.v.head + row * p.v.row;
+    const int32_t token = min(S::token(wave, lane), x.more);
+    k_at = uint32_t(token * p.k.row + S::piece(lane) * 16);
+    v_at = uint32_t(token * p.v.row + S::piece(lane) * 16);
+    const float *ks = p.k.scales + page * p.k.s_page + head * p.k.s_head;
+    const float *vs = p.v.scales + page * p.v.s_page + head * p.v.s_head;
+    const int32_t at = x.row + min(Sc::token(wave, lane), x.more);
+    scale = (keys ? ks : vs) +
+            int64_t(div_by(p.div_block, uint32_t(at))) * (keys ? p.k.s_block : p.v.s_block);
+  } else {
+    k = p.k.codes + x.page * p.k.page + head * p.k.head + int64_t(x.row) * p.k.row;
+    v = p.v.codes + x.page * p.v.page + head * p.v.head + int64_t(x.row) * p.v.row;
+    k_at = v_at = uint32_t(S::piece(lane) * 16);
+    const Q8Cache &c = keys ? p.k : p.v;
+    scale = c.scales + x.scale_page * c.s_page + head * c.s_head +
+            int64_t(div_by(p.div_block, uint32_t(x.scale_row))) * c.s_block;
+  }
 #pragma unroll
   for (int i = 0; i < S::BYTES / 16; ++i) {
-    x.k[i] = *reinterpret_cast<const uint4 *>(k + 16 * i);
-    x.v[i] = *reinterpret_cast<const uint4 *>(v + 16 * i);
+    stage.k[i] = *reinterpret_cast<const uint4 *>(k + (k_at + 16 * S::THREADS * i));
+    stage.v[i] = *reinterpret_cast<const uint4 *>(v + (v_at + 16 * S::THREADS * i));
   }
-  const Q8Cache &c = tid < ScalesOf<D, COARSE>::COUNT ? p.k : p.v;
-  x.scale = c.scales[scale.page * c.s_page + head * c.s_head +
-                     int64_t(div_by(p.div_block, uint32_t(scale.row))) * c.s_block];
+  stage.scale = *scale;
 }
 
 // Into a buffer, as operands.
-template <typename T, int D, bool E4M3, bool COARSE>
+template <typename T, int D, bool E4M3, int MODE>
 __device__ __forceinline__ void put(const StageQ8<D> &x, int tid, float scale_log2,
                                     typename RowsLds<D>::Buffer &to) {
   using S = RowsShape<D>;
   using Op = Operand<T, E4M3>;
-  const uint32_t row = uint32_t(tid) / S::THREADS;
-  const uint32_t first = uint32_t(tid) % S::THREADS * (S::BYTES / 8);  // 16-byte chunk of the row
+  const int wave = tid / 64, lane = tid & 63;
+  const uint32_t row = uint32_t(S::run(wave) + S::token(wave, lane));
+  const uint32_t piece = uint32_t(S::piece(lane));  // four to a panel's row, two chunks each
 #pragma unroll
   for (int i = 0; i < S::BYTES / 16; ++i)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t at = first / 8 * S::PANEL + (panel_chunk(row, first % 8) ^ (uint32_t(2 * i + e) * 16u));
+      const uint32_t at = (piece / 4 + uint32_t(S::THREADS / 4 * i)) * S::PANEL +
+                          (panel_chunk(row, piece % 4 * 2) ^ uint32_t(16 * e));
       const s16x8 k = e == 0 ? Op::row(x.k[i].x, x.k[i].y) : Op::row(x.k[i].z, x.k[i].w);
       const s16x8 v = e == 0 ? Op::row(x.v[i].x, x.v[i].y) : Op::row(x.v[i].z, x.v[i].w);
       *reinterpret_cast<s16x8 *>(to.k + at) = k;
       *reinterpret_cast<s16x8 *>(to.v + at) = v;
     }
-  using Sc = ScalesOf<D, COARSE>;
-  if (tid < Sc::COUNT)
-    to.k_scale[Sc::place(tid)] = x.scale * scale_log2;
-  else if (tid < 2 * Sc::COUNT)
-    to.v_scale[Sc::place(tid - Sc::COUNT)] = x.scale;
+  using Sc = ScalesOf<D, MODE>;
+  const int at = Sc::place(wave * Sc::EACH + lane % Sc::EACH);
+  if (lane < 2 * Sc::EACH)
+    (lane < Sc::EACH ? to.k_scale : to.v_scale)[at] = lane < Sc::EACH ? x.scale * scale_log2 : x.scale;
 }
 
 // The scales of the lane's tokens of block kb of 32 in S^T: four by four.
-template <int D, bool COARSE>
+template <int D, int MODE>
 __device__ __forceinline__ void scales_at(const float *s, int kb, int lane, f32x4 (&f)[4]) {
-  if constexpr (COARSE) {
+  if constexpr (MODE == kCoarse) {
     const f32x4 y = *reinterpret_cast<const f32x4 *>(s + (lane >> 5) * (RowsShape<D>::TILE / 8) + kb * 4);
 #pragma unroll
     for (int c = 0; c < 4; ++c) f[c] = f32x4{y[c], y[c], y[c], y[c]};
@@ -116,7 +183,7 @@ __device__ __forceinline__ void scales_at(const float *s, int kb, int lane, f32x
   }
 }
 
-template <typename T, int D, bool E4M3, bool COARSE>
+template <typename T, int D, bool E4M3, int MODE>
 __global__ __launch_bounds__(kAttnBlock) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2))) void
 attention_q8_rows_kernel(AttnQ8Plan p) {
   using S = RowsShape<D>;
@@ -161,23 +228,19 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
     const int32_t end = min(g.st1 * TILE, g.most);
     int32_t t0 = g.st0 * TILE;
     if (t0 < end) {
-      auto codes_at = [&](int32_t t) { return token_at(p.seq, b, min(t + tid / S::THREADS, last)); };
-      auto scale_at = [&](int32_t t) {
-        return token_at(p.seq, b, min(t + tid % ScalesOf<D, COARSE>::COUNT * ScalesOf<D, COARSE>::RUN, last));
-      };
+      auto at_tile = [&](int32_t t) { return tokens_at<D, MODE>(p.seq, b, t, last, wave, lane); };
       StageQ8<D> stage;
-      fetch<D, COARSE>(p, codes_at(t0), scale_at(t0), head, tid, stage);
+      fetch<D, MODE>(p, at_tile(t0), head, wave, lane, stage);
       lds_barrier();  // what the last piece read of the buffers
-      put<T, D, E4M3, COARSE>(stage, tid, p.scale_log2, lds.buffer[0]);
+      put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, lds.buffer[0]);
       int32_t t1 = t0 + TILE < end ? t0 + TILE : t0;
-      TokenQ8 codes = codes_at(t1), scale = scale_at(t1);
+      TokensQ8<MODE> tokens = at_tile(t1);
       for (int32_t n = 0;; ++n) {  // ends: t0 grows
         lds_barrier();
         // the next tile's codes on their way (the present one's again behind the last: no branch)
-        fetch<D, COARSE>(p, codes, scale, head, tid, stage);
+        fetch<D, MODE>(p, tokens, head, wave, lane, stage);
         const int32_t t2 = t1 + TILE < end ? t1 + TILE : t1;
-        codes = codes_at(t2);
-        scale = scale_at(t2);
+        tokens = at_tile(t2);
         const typename RowsLds<D>::Buffer &at = lds.buffer[n & 1];
 
         // Opaque: the places that follow from these are worked out again in every step.  Kept from step to
@@ -211,7 +274,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
           f32x4 f[4];
-          scales_at<D, COARSE>(at.k_scale, kb, lane, f);
+          scales_at<D, MODE>(at.k_scale, kb, lane, f);
 #pragma unroll
           for (int r = 0; r < 16; ++r) x[kb][r] *= f[r / 4][r % 4];
         }
@@ -233,7 +296,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         bool raise = best > top + Mfma<T>::kSlack;
         float most = 0.0f;
         if constexpr (Mfma<T>::kNarrow) {
-          most = fabsf(at.v_scale[lane % ScalesOf<D, COARSE>::COUNT]);
+          most = fabsf(at.v_scale[lane % ScalesOf<D, MODE>::COUNT]);
           raise |= most > reach;
         }
         if (__any(raise)) {
@@ -259,7 +322,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         for (int kb = 0; kb < KB; ++kb) {
           float e[16];
           f32x4 f[4];
-          scales_at<D, COARSE>(at.v_scale, kb, lane, f);
+          scales_at<D, MODE>(at.v_scale, kb, lane, f);
           if constexpr (Mfma<T>::kNarrow) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) f[c] *= by_reach;
@@ -299,7 +362,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         }
         __builtin_amdgcn_s_setprio(0);
         if (t1 == t0) break;
-        put<T, D, E4M3, COARSE>(stage, tid, p.scale_log2, lds.buffer[~n & 1]);
+        put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, lds.buffer[~n & 1]);
         t0 = t1;
         t1 = t2;
       }
@@ -350,10 +413,10 @@ const void *pick_attention_q8(const AttnQ8Plan &p) {
 template <typename T, int D>
 const void *pick_attention_q8(const AttnQ8Plan &p) {
   if (p.rows == kQ8ManyRows) {
-#define ROPE_KR(E, C) reinterpret_cast<const void *>(&attention_q8_rows_kernel<T, D, E, C>)
-    const bool coarse = p.seq.page_size % 4 == 0 && p.block % 4 == 0;
-    if (p.e4m3) return coarse ? ROPE_KR(true, true) : ROPE_KR(true, false);
-    return coarse ? ROPE_KR(false, true) : ROPE_KR(false, false);
+#define ROPE_KR(E, MO) reinterpret_cast<const void *>(&attention_q8_rows_kernel<T, D, E, MO>)
+#define ROPE_KM(E) (p.mode == kCoarse ? ROPE_KR(E, kCoarse) : p.mode == kFine ? ROPE_KR(E, kFine) : ROPE_KR(E, kAny))
+    return p.e4m3 ? ROPE_KM(true) : ROPE_KM(false);
+#undef ROPE_KM
 #undef ROPE_KR
   }
   return p.rows == 16 ? pick_attention_q8<T, D, 1>(p) : pick_attention_q8<T, D, 2>(p);
