@@ -28,6 +28,19 @@ streams.  There is no fallback: if the library is not built this import fails.
                                  num_sequences=None, query_offsets=None, key_offsets=None,
                                  stream=None)
   latent_attention(query, key, key_rope, value, scale, ...)      (the same, with autograd)
+  rope_append_paged_cache_q8(positions, key, value, key_cache, value_cache, key_scales,
+                             value_scales, page_table, seq_lens, cos_sin_cache,
+                             query_offsets=None, query=None, query_out=None, query_rot_start=0,
+                             key_rot_start=0, is_neox_style=True, stream=None)
+  rope_attention_paged_q8(query, key_cache, value_cache, key_scales, value_scales, page_table,
+                          seq_lens, scale, query_offsets=None, out=None, lse=None, stream=None)
+  rope_copy_pages(sources, targets, caches, stream=None)
+  rope_fork_pages(page_table, seq_lens, parents, ref_counts, page_size, caches=(), grow=None,
+                  page_table_out=None, seq_lens_out=None, ref_counts_out=None, shortage=None,
+                  stream=None)
+  rope_compact_pages(page_table, ref_counts, caches=(), page_table_out=None,
+                     ref_counts_out=None, page_map=None, live=None, stream=None)
+  PageCaches(caches)                  (the caches of all layers, described once for those three)
 
 Pages defining the operations:
   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码接口详解与实现剖析"
