@@ -469,8 +469,8 @@ int rope_copy_pages(const rope_tensor *sources, const rope_tensor *targets,
  *
  * page_table     INT64 [B, maxPages]; seq_lens INT64 [B], clamped to [0, maxPages * pageSize].
  *                Entries in use outside [0, pages) stay and count nowhere.
- * parents        INT64 [R]; outside [0, B): an empty row of length 0.     grow  INT64 [R] or NULL (0);
- *                below 0: 0.
+ * parents        INT64 [R]; outside [0, B): an empty row of length 0, which gets no pages (a sequence that
+ *                begins continues one of length 0).     grow  INT64 [R] or NULL (0); below 0: 0.
  * ref_counts     INT64 [pages];  page_size: tokens of a page.
  * caches         as in rope_copy_pages, num_caches may be 0.  Of a cache [pages, n, ...] whose second
  *                dimension is the outermost of a page and n divides page_size or the reverse (rows, or

@@ -684,7 +684,8 @@ def rope_fork_pages(page_table, seq_lens, parents, ref_counts, page_size: int, c
                     grow=None, page_table_out=None, seq_lens_out=None, ref_counts_out=None,
                     shortage=None, stream=None):
     """The next step's sequences continue this step's: new row i has all seq_lens[parents[i]] tokens of
-    sequence parents[i] (an empty row where that is out of range) and room for grow[i] more.  Full pages
+    sequence parents[i] (an empty row without pages where that is out of range; a new sequence continues
+    one of length 0) and room for grow[i] more.  Full pages
     are shared, a last page that is not full is copied in all caches for every row but the first that
     continues its sequence (for that one, too, if something else holds the page), and new pages are the
     lowest with ref_counts 0.  Sequences without a row end.  All index tensors are int64: page_table

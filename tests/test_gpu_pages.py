@@ -243,6 +243,36 @@ def test_pages_beyond_4_gib():
         assert bool((x[p] == v).all()), p
 
 
+def spread(x, columns=False):
+    """The same numbers, other strides: every second element of a larger tensor, or column by column."""
+    if columns:
+        return x.t().contiguous().t()
+    wide = torch.full((*x.shape, 2), -55, dtype=x.dtype, device=DEV)
+    wide[..., 1] = x
+    return wide[..., 1]
+
+
+@pytest.mark.parametrize("columns", [False, True])
+def test_strided_tables_and_vectors(columns):
+    r = random.Random(11)
+    B, R, page, width, pages = 7, 12, 4, 6, 90
+    table, lens, parents, grow, refs = random_batch(r, B, R, page, width, pages)
+    want = fork_reference(table, lens, parents, grow, refs, page, width + 1)
+    out = spread(torch.zeros(R, width + 1, dtype=torch.int64, device=DEV), not columns)
+    vectors = [spread(ints(x)) for x in (lens, parents, grow, refs, [0] * R, [0] * pages, [0])]
+    got = ra.rope_fork_pages(spread(ints(table), columns), vectors[0], vectors[1], vectors[3], page,
+                             grow=vectors[2], page_table_out=out, seq_lens_out=vectors[4],
+                             ref_counts_out=vectors[5], shortage=vectors[6])
+    torch.cuda.synchronize()
+    assert [x.tolist() for x in got] == [want[0], want[1], want[2], [want[3]]]
+    want = compact_reference(got[0].tolist(), got[2].tolist())
+    moved = ra.rope_compact_pages(got[0], got[2], page_table_out=got[0], ref_counts_out=got[2],
+                                  page_map=spread(ints([0] * pages)), live=spread(ints([0])))
+    torch.cuda.synchronize()
+    assert [x.tolist() for x in moved] == [want[0], want[1], want[2], [want[3]]]
+    assert moved[0].data_ptr() == out.data_ptr()
+
+
 def test_graphs_replay():
     """A step's fork and compaction captured together; every replay on other lengths."""
     r = random.Random(5)
