@@ -14,8 +14,8 @@
 // of a workgroup take up to four key heads of the same tokens; those of one head, each of which
 // takes every n-th 32 tokens, join their sums at the end.
 //
-// Measured with 8 key heads of 128: 64 sequences of 200-9000 tokens 67 us (284 MB), of 9000 218 us (5.4 TB/s),
-// six of 60-131k tokens and a scale for each 276 us (5.3 TB/s).
+// Measured with 8 key heads of 128: 64 sequences of 200-9000 tokens 62.5 us (284 MB), of 9000 with 4 key heads
+// of 256 201 us (5.9 TB/s), six of 60-131k tokens and a scale for each 254 us (5.7 TB/s).
 //
 // Layout (16x16x32 products, lane l = 16 g + c):
 //   S^T = K Q^T: A[key c][8 d], lane's d = g D / 4 + 16 i + 8 e + 0..7 for product (i, e): 16 bytes a load
@@ -220,20 +220,19 @@ __device__ __forceinline__ WhereQ8<MODE> locate(const Sequences &s, int32_t b, i
   return w;
 }
 
+// W words of a row that 16 lanes load whole.  Whole lines are loaded past the caches, which no other load
+// wants them from: 64 sequences 66.8 -> 62.5 us, six of 60-131k tokens 275 -> 254 (plain loads of dense memory
+// end at 6.2 TB/s on this card, such ones at 7.0).  Half lines (heads of 64) are not, and neither are keys, two
+// loads of which share a line: they came twice (254 -> 270).
 template <int W>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&v)[W]) {
   if constexpr (W == 1) {
     v[0] = *reinterpret_cast<const uint32_t *>(p);
-  } else if constexpr (W == 2) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    v[0] = x.x;
-    v[1] = x.y;
   } else {
-    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-    v[0] = x.x;
-    v[1] = x.y;
-    v[2] = x.z;
-    v[3] = x.w;
+    typedef uint32_t words __attribute__((ext_vector_type(W)));
+    const words x = __builtin_nontemporal_load(reinterpret_cast<const words *>(p));
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = x[i];
   }
 }
 
