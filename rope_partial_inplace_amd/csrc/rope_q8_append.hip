@@ -10,9 +10,10 @@
 // nothing with powers of two, and its codes are rounded once, however often the scale grows.
 //
 // A few operations for every 3 bytes moved: bound by HBM, and for a decoding step by its launch and
-// its dependent reads.  One group of lanes (as many as a block's items of one head need, up to a
-// wavefront) owns all tokens of a block and head, so that the maximum is a few lane exchanges, and
-// nothing is shared between wavefronts: no atomics, no LDS, no order.
+// its dependent reads.  One group of lanes (as many as hold a block's elements of one head, 32 each) owns all
+// its tokens, so that the maximum is a few lane exchanges; only those of long blocks are two or four
+// wavefronts, which meet in LDS.  (11167 tokens of blocks of 32: 53.6 us with two for a head, 58.4 with four, which
+// hold half as much each.)  No atomics, no order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -313,7 +314,8 @@ __device__ inline void append_block(const AppendQ8Plan &p, const Q8Rows &r, cons
   uint8_t *rows = r.codes + page * r.page + int64_t(at.row0) * r.row + h * r.head;
   float *scale_at = r.scales + page * r.s_page + at.block * r.s_block + h * r.s_head;
   const float old = kept && mine && at.before > 0 ? *scale_at : 0.0f;
-  // the largest size, over all elements or the finite ones
+  // the largest size, over all elements or the finite ones; any_high: of the wavefronts that meet
+  uint32_t any_high = 0;
   auto largest = [&](auto only_finite) {
     constexpr bool FINITE = decltype(only_finite)::value;
     uint32_t high = 0;
@@ -345,19 +347,23 @@ __device__ inline void append_block(const AppendQ8Plan &p, const Q8Rows &r, cons
     }
     for (uint32_t d = 1; d < lanes && d < 64; d *= 2)
       high = max(high, uint32_t(__shfl_xor(int(high), int(d))));
-    if (lanes > 64) {  // the workgroup's four wavefronts
+    any_high = high;
+    if (lanes > 64) {  // with the block's other wavefronts
       __shared__ uint32_t highs[kQ8Block / 64];
       __syncthreads();
       if (lane == 0) highs[threadIdx.x >> 6] = high;
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kQ8Block / 64; ++k) high = max(high, highs[k]);
+      for (int k = 0; k < kQ8Block / 64; ++k) {
+        any_high = max(any_high, highs[k]);
+        if (lanes == kQ8Block || (k ^ int(threadIdx.x >> 6)) < 2) high = max(high, highs[k]);
+      }
     }
     return high;
   };
   uint32_t high = largest(std::false_type());
   const bool bad = high >= kNonFinite;
-  const bool check = __any(bad);  // of a long block the same for the workgroup
+  const bool check = __any(any_high >= kNonFinite);  // of several wavefronts the same for the workgroup
   if (check && E4M3) high = largest(std::true_type());
   if (!kept) return;
   float now = needed_scale<E4M3>(__uint_as_float(high));
@@ -416,12 +422,15 @@ append_q8_kernel(AppendQ8Plan p) {
     rotate_queries<T, V, NEOX>(p, block - p.kv_blocks);
     return;
   }
-  int64_t w = block;  // a workgroup's part of a place, or a wavefront's
-  if (p.lanes <= 64)
-    w = block * (kQ8Block / 64) + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  // a wavefront's part of a place, or that of two or four
+  const int each = max(6, p.lanes_log2);
+  const int64_t w = block * (kQ8Block >> each) + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> each);
   const int64_t u = p.idx32 ? int64_t(div_by(p.div_groups, uint32_t(w))) : w / p.head_groups;
   Place at;
-  if (u >= p.places || !find_place(p, u, &at)) return;
+  // (where wavefronts meet in LDS, one without a place goes on without tokens)
+  const bool some = u < p.places && find_place(p, u, &at);
+  if (!some && p.lanes != 128) return;
+  if (!some) at = Place();
   // the first half of a place's wavefronts takes keys, the second values
   int32_t group = int32_t(w - u * p.head_groups);
   const bool keys = group < p.head_groups / 2;
@@ -429,7 +438,7 @@ append_q8_kernel(AppendQ8Plan p) {
   int32_t head = group;
   if (p.lanes < 64)
     head = group * (64 >> p.lanes_log2) + ((int32_t(threadIdx.x) & 63) >> p.lanes_log2);
-  if (head >= p.heads) head = -1;
+  if (head >= p.heads || !some) head = -1;
   if (keys)
     append_block<T, V, NEOX, E4M3, true>(p, p.kv[0], at, head);
   else

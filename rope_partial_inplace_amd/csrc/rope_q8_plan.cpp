@@ -252,14 +252,13 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
                         std::min(int64_t(64), int64_t(1) << r.row_log2)});
     }
     p.lanes = 4;
-    while (p.lanes < 64 && p.lanes < lanes) p.lanes *= 2;
-    if (p.lanes < lanes) p.lanes = kQ8Block;
+    while (p.lanes < kQ8Block && p.lanes < lanes) p.lanes *= 2;
     while ((1 << p.lanes_log2) != p.lanes) ++p.lanes_log2;
     for (Q8Rows &r : p.kv) {  // a row's items of one wavefront
       r.side_by_side = (1 << r.row_log2) <= std::min(p.lanes, 64);
       if (!r.side_by_side) r.row_log2 = 0;
     }
-    const int64_t heads_each = std::max(1, 64 / p.lanes), units = p.lanes > 64 ? 1 : kQ8Block / 64;
+    const int64_t heads_each = std::max(1, 64 / p.lanes), units = kQ8Block / std::max(64, p.lanes);
     p.head_groups = 2 * int32_t((p.heads + heads_each - 1) / heads_each);
     p.div_groups = make_fastdiv(uint32_t(p.head_groups));
     p.kv_blocks = (p.places * p.head_groups + units - 1) / units;

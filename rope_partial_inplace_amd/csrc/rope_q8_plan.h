@@ -43,12 +43,13 @@ struct AppendQ8Plan {
   rope_dtype dt = ROPE_F32;
   bool neox = true, vector_io = false, noop = false, e4m3 = false;
   bool idx32 = true;  // query items and wavefronts are numbered in 32 bits
-  // A wavefront (for long blocks a workgroup) takes one place of tokens (one block of a sequence) and several of its heads.
+  // A wavefront (for long blocks two or four) takes one place of tokens (one block of a sequence) and several
+  // of its heads.
   // Places are numbered so that their sequence can be found from the offsets alone: by token, where
   // all but a block's first new token have nothing to do, or, fewer for long appends, from
   // offsets[b] / block + 2 b on, which is enough for the blocks a sequence's tokens can touch.
   bool by_token = true;
-  int32_t lanes = 64;      // threads of a head's block: a power of two up to 64, or 256
+  int32_t lanes = 64;      // threads of a head's block: a power of two from 4 to 256
   int32_t lanes_log2 = 0;
   int64_t places = 0, kv_blocks = 0, query_blocks = 0;
   int64_t first_block = 0;  // of a launch

@@ -88,7 +88,7 @@ static int64_t walk_append() {
   const int st = plan_append_q8(&pos, nullptr, &k, &v, &cs, &table, &lt, even ? nullptr : &ot, 0, 0, 1, nullptr,
                                 &kc, &vc, &ks, &vs, &p, &err);
   CHECK(st == ROPE_OK, "%s", err.c_str());
-  const int64_t units = p.lanes > 64 ? 1 : kQ8Block / 64;
+  const int64_t units = kQ8Block / std::max(64, p.lanes);
   CHECK(p.kv_blocks * units >= p.places * p.head_groups, "too few wavefronts");
   CHECK(p.head_groups / 2 * std::max(1, 64 / p.lanes) >= heads, "heads left out");
   std::map<std::pair<int64_t, int64_t>, std::pair<int64_t, int64_t>> found;  // (b, block) -> first token, count

@@ -247,6 +247,17 @@ def test_non_finite_and_extreme_values(codes, dtype):
     check(s)
 
 
+@pytest.mark.parametrize("dtype,block,width", [(BF16, 32, 128), (F16, 128, 64), (F32, 64, 128), (BF16, 128, 128)])
+@pytest.mark.parametrize("codes", [I8, E4M3])
+def test_non_finite_values_in_long_blocks(codes, dtype, block, width):
+    """Blocks of two and four wavefronts, which meet twice where one of them has such a value; places that
+    fill a workgroup partly."""
+    for heads in (1, 3):
+        s = setup([300, 777, 64, 129], [299, 500, 64, 1], 128, block, heads, width, width, codes, dtype, seed=block)
+        s["k"][5, 0, 40], s["k"][400, heads - 1, 3], s["v"][798, 0, 17] = math.nan, math.inf, -math.inf
+        check(s, neox=heads == 1)
+
+
 def test_negative_zero_and_ties():
     s = setup([4], [4], 4, 4, 1, 16, 16, I8, F32, nq=1, rd=2)
     v = torch.arange(64, device=DEV, dtype=F32).view(4, 1, 16) - 31.5
