@@ -12,8 +12,8 @@
 // A few operations for every 3 bytes moved: bound by HBM, and for a decoding step by its launch and
 // its dependent reads.  One group of lanes (as many as hold a block's elements of one head, 32 each) owns all
 // its tokens, so that the maximum is a few lane exchanges; only those of long blocks are two or four
-// wavefronts, which meet in LDS.  (11167 tokens of blocks of 32: 53.6 us with two for a head, 58.4 with four, which
-// hold half as much each.)  No atomics, no order.
+// wavefronts, which meet in LDS.  (11167 tokens of blocks of 32: 53.6 us with two for a head, 58.4 with
+// four, which hold half as much each.)  No atomics, no order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -41,13 +41,29 @@ __device__ inline void store_once(void *p, const uint4 &v) {
   __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, static_cast<u32x4 *>(p));
 }
 
-// V elements; ONCE: no other item reads them.
+// V elements as they lie in memory, and in float32.  ONCE: no other item reads them.
+template <typename T, int V>
+using Words = std::conditional_t<V == 1, typename Io<T>::raw, uint4>;
+
+template <typename T, int V, bool ONCE>
+__device__ inline Words<T, V> load_words(const T *p) {
+  if constexpr (V == 1)
+    return *reinterpret_cast<const typename Io<T>::raw *>(p);
+  else
+    return ONCE ? load_once(p) : *reinterpret_cast<const uint4 *>(p);
+}
+
+template <typename T, int V>
+__device__ inline void to_floats(const Words<T, V> &w, float *f) {
+  if constexpr (V == 1)
+    f[0] = Io<T>::from_raw(w);
+  else
+    Io<T>::unpack(w, f);
+}
+
 template <typename T, int V, bool ONCE>
 __device__ inline void load_floats(const T *p, float *f) {
-  if constexpr (V == 1)
-    f[0] = Io<T>::from_raw(*reinterpret_cast<const typename Io<T>::raw *>(p));
-  else
-    Io<T>::unpack(ONCE ? load_once(p) : *reinterpret_cast<const uint4 *>(p), f);
+  to_floats<T, V>(load_words<T, V, ONCE>(p), f);
 }
 
 // The V / 2 cos (or sin) values of a GPT-J vector: 8 bytes.
@@ -98,44 +114,55 @@ struct Turn {
   }
 };
 
-// An item in float32, rotated where it lies in the slice.
+// An item as it lies in memory (`q`: the other halves of its pairs; of one outside the slice the same
+// elements), and in float32, rotated where it lies in the slice.
 template <typename T, int V, bool NEOX>
-__device__ inline void rotated(const T *in, const Turn<T, V, NEOX> &r, const Spot &at, int32_t half,
-                               float *a, float *b) {
-  float p[V];
-  load_floats<T, V, true>(in + at.e, p);
-  if constexpr (NEOX || V == 1) {
-    float q[V];
-    load_floats<T, V, true>(in + at.e + (at.turned ? partner<NEOX>(half) : 0), q);
+struct Item {
+  static constexpr bool PAIR = NEOX || V == 1;
+  Words<T, V> p, q;
+  __device__ void load(const T *in, const Spot &at, int32_t half) {
+    p = load_words<T, V, true>(in + at.e);
+    if constexpr (PAIR) q = load_words<T, V, true>(in + at.e + (at.turned ? partner<NEOX>(half) : 0));
+  }
+  __device__ void rotate(const Turn<T, V, NEOX> &r, const Spot &at, float *a, float *b) const {
+    float x[V];
+    to_floats<T, V>(p, x);
+    if constexpr (PAIR) {
+      float y[V];
+      to_floats<T, V>(q, y);
 #pragma unroll
-    for (int m = 0; m < V; ++m) {
-      const float x = p[m] * r.c[m] - q[m] * r.s[m];
-      b[m] = q[m] * r.c[m] + p[m] * r.s[m];
-      a[m] = at.turned ? x : p[m];
-    }
-  } else {
+      for (int m = 0; m < V; ++m) {
+        const float z = x[m] * r.c[m] - y[m] * r.s[m];
+        b[m] = y[m] * r.c[m] + x[m] * r.s[m];
+        a[m] = at.turned ? z : x[m];
+      }
+    } else {
 #pragma unroll
-    for (int m = 0; m < V / 2; ++m) {
-      const float x = p[2 * m] * r.c[m] - p[2 * m + 1] * r.s[m];
-      const float y = p[2 * m + 1] * r.c[m] + p[2 * m] * r.s[m];
-      a[2 * m] = at.turned ? x : p[2 * m];
-      a[2 * m + 1] = at.turned ? y : p[2 * m + 1];
+      for (int m = 0; m < V / 2; ++m) {
+        const float y = x[2 * m] * r.c[m] - x[2 * m + 1] * r.s[m];
+        const float z = x[2 * m + 1] * r.c[m] + x[2 * m] * r.s[m];
+        a[2 * m] = at.turned ? y : x[2 * m];
+        a[2 * m + 1] = at.turned ? z : x[2 * m + 1];
+      }
     }
   }
-}
+};
 
+__device__ inline int64_t position(const AppendQ8Plan &p, int64_t token) {
+  return p.positions[token * p.pos_stride];
+}
 template <typename T>
-__device__ inline const T *angles(const AppendQ8Plan &p, int64_t token) {
-  const int64_t pos = p.positions[token * p.pos_stride];
+__device__ inline const T *angles(const AppendQ8Plan &p, int64_t pos) {
   return static_cast<const T *>(p.table) + min(max(pos, int64_t(0)), p.max_seq - 1) * p.table_stride;
 }
 
 // ---- queries ------------------------------------------------------------------------------------
-// A thread takes one item of kQueryHeads neighbouring heads, which share its cosines and sines.  (One head
-// a thread is bound by its address arithmetic: 11167 tokens of 32 heads of 128, half of each rotated
-// in pairs, 40 us.)
+// A thread takes one item of HEADS neighbouring heads, which share its cosines and sines.  All are loaded
+// before the first is stored: the output may be the input itself, so behind a store the compiler would wait with
+// the next load (11167 tokens of 32 heads of 128 and 8 + 8 in blocks of 32: 50 us so, 53.6 one by one).
 template <typename T, int V, bool NEOX>
 __device__ inline void rotate_queries(const AppendQ8Plan &p, int64_t block) {
+  constexpr int HEADS = query_heads_of(NEOX);
   const AppendRows &r = p.query;
   const int64_t it = block * kQ8Block + threadIdx.x;
   if (it >= r.all) return;
@@ -150,38 +177,39 @@ __device__ inline void rotate_queries(const AppendQ8Plan &p, int64_t block) {
     i = uint32_t(it - t * r.total);
   }
   const uint32_t hg = div_by(r.div_items, i), unit = i - hg * r.items;
-  const int64_t h = int64_t(hg) * kQueryHeads;
+  const int64_t h = int64_t(hg) * HEADS;
   const T *in = static_cast<const T *>(r.in) + t * r.in_tok + h * r.in_head;
   T *out = static_cast<T *>(r.out) + t * r.out_tok + h * r.out_head;
   const Spot at = spot_of<V, NEOX>(unit, r.rot_items, r.rot_start, p.half);
+  const int heads = int(min(p.query_heads - h, int64_t(HEADS)));
+  const int64_t pos = position(p, t);
+  Item<T, V, NEOX> x[HEADS];
+#pragma unroll
+  for (int k = 0; k < HEADS; ++k) x[k].load(in + min(k, heads - 1) * r.in_head, at, p.half);
   Turn<T, V, NEOX> turn;
-  turn.load(angles<T>(p, t), at, unit, p.half);
-  const int heads = int(min(p.query_heads - h, int64_t(kQueryHeads)));
-  auto one = [&](int k) {
-    const T *x = in + k * r.in_head;
+  turn.load(angles<T>(p, pos), at, unit, p.half);
+#pragma unroll
+  for (int k = 0; k < HEADS; ++k) {
+    if (k >= heads) break;
     T *y = out + k * r.out_head;
     float a[V], b[V];
-    rotated<T, V, NEOX>(x, turn, at, p.half, a, b);
+    x[k].rotate(turn, at, a, b);
     // what lies outside the slice is copied bit for bit (raised to float32 and rounded again, all but a
     // NaN's payload would be)
     if constexpr (V == 1) {
-      T v;
+      T v, w;
       Io<T>::store1(&v, 0, a[0]);
-      *(y + at.e) = at.turned ? v : x[at.e];
-      if (at.turned) Io<T>::store1(y + at.e + partner<NEOX>(p.half), 0, b[0]);
+      Io<T>::store1(&w, 0, b[0]);
+      *reinterpret_cast<typename Io<T>::raw *>(y + at.e) =
+          at.turned ? __builtin_bit_cast(typename Io<T>::raw, v) : x[k].p;
+      if (at.turned) *(y + at.e + partner<NEOX>(p.half)) = w;
     } else {
-      const uint4 w = load_once(x + at.e), z = Io<T>::pack(a);
+      const uint4 w = x[k].p, z = Io<T>::pack(a);
       store_once(y + at.e, make_uint4(at.turned ? z.x : w.x, at.turned ? z.y : w.y,
                                       at.turned ? z.z : w.z, at.turned ? z.w : w.w));
       if constexpr (NEOX)
         if (at.turned) store_once(y + at.e + p.half, Io<T>::pack(b));
     }
-  };
-  if (heads == kQueryHeads) {
-#pragma unroll
-    for (int k = 0; k < kQueryHeads; ++k) one(k);
-  } else {
-    for (int k = 0; k < heads; ++k) one(k);
   }
 }
 
@@ -292,8 +320,11 @@ __device__ inline void append_block(const AppendQ8Plan &p, const Q8Rows &r, cons
     const T *from = in + int64_t(row) * r.in_tok;
     if constexpr (ROT) {
       Turn<T, V, NEOX> turn;
-      turn.load(angles<T>(p, at.first + row), s, item, p.half);
-      rotated<T, V, NEOX>(from, turn, s, p.half, f, f + V);
+      Item<T, V, NEOX> x;
+      const int64_t pos = position(p, at.first + row);
+      x.load(from, s, p.half);
+      turn.load(angles<T>(p, pos), s, item, p.half);
+      x.rotate(turn, s, f, f + V);
     } else {
       load_floats<T, V, true>(from + s.e, f);
     }
@@ -414,8 +445,9 @@ __device__ inline void append_block(const AppendQ8Plan &p, const Q8Rows &r, cons
   if (mine && l == 0 && (at.before == 0 || now != old)) *scale_at = now;
 }
 
+// Five wavefronts a SIMD: with six the NeoX forms of e4m3 spill 24 registers (blocks of 16, bf16: 51 us, not 55.5).
 template <typename T, int V, bool NEOX, bool E4M3>
-__global__ __launch_bounds__(kQ8Block) __attribute__((amdgpu_waves_per_eu(6))) void
+__global__ __launch_bounds__(kQ8Block) __attribute__((amdgpu_waves_per_eu(5))) void
 append_q8_kernel(AppendQ8Plan p) {
   const int64_t block = p.first_block + blockIdx.x;
   if (block >= p.kv_blocks) {

@@ -206,7 +206,8 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
     r.rot_items = uint32_t(p.neox ? rd / 2 / step : rd / run);
     r.items = r.rot_items + (in_place ? 0u : uint32_t((query->shape[2] - rd) / step));
     p.query_heads = query->shape[1];
-    r.total = uint32_t((query->shape[1] + kQueryHeads - 1) / kQueryHeads) * r.items;
+    const int64_t each = query_heads_of(p.neox);
+    r.total = uint32_t((query->shape[1] + each - 1) / each) * r.items;
     r.all = T * int64_t(r.total);  // below 2^30 * 2^24
     r.div_items = make_fastdiv(std::max(1u, r.items));
     r.div_total = make_fastdiv(std::max(1u, r.total));

@@ -69,7 +69,9 @@ struct AppendQ8Plan {
 };
 
 constexpr int kQ8Block = 256;
-constexpr int kQueryHeads = 4;
+// Query heads of a thread, whose items are all under way at once: with the pairs' two parts apart (NeoX) two
+// heads are as many loads as four with them together.
+constexpr int query_heads_of(bool neox) { return neox ? 2 : 4; }
 constexpr int kQ8Held = 32;  // elements that a thread holds
 
 int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const rope_tensor *key,
