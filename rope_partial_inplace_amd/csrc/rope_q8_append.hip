@@ -159,7 +159,7 @@ __device__ inline const T *angles(const AppendQ8Plan &p, int64_t pos) {
 // ---- queries ------------------------------------------------------------------------------------
 // A thread takes one item of HEADS neighbouring heads, which share its cosines and sines.  All are loaded
 // before the first is stored: the output may be the input itself, so behind a store the compiler would wait with
-// the next load (11167 tokens of 32 heads of 128 and 8 + 8 in blocks of 32: 50 us so, 53.6 one by one).
+// the next load (11167 tokens of 32 heads of 128 and 8 + 8 in blocks of 32: 50.4 us so, 53.6 one by one).
 template <typename T, int V, bool NEOX>
 __device__ inline void rotate_queries(const AppendQ8Plan &p, int64_t block) {
   constexpr int HEADS = query_heads_of(NEOX);
@@ -333,11 +333,33 @@ __device__ inline void append_block(const AppendQ8Plan &p, const Q8Rows &r, cons
   const bool mine_too = mine && unit < r.items;
   float x[HELD][ITEM];
   if (held) {
+    // All rows' loads are under way before the first is needed; rows past the last one repeat it (loads behind
+    // branches wait for each other: 50.3 us, not 48.3).
     const Spot s = unit < r.items ? spot : spot_of<V, NEOX>(0, r.rot_items, r.rot_start, p.half);
+    const uint32_t item = unit < r.items ? unit : 0, last = max(count, 1u) - 1;
+    if constexpr (ROT) {
+      Item<T, V, NEOX> raw[HELD];
+      int64_t pos[HELD];
 #pragma unroll
-    for (int k = 0; k < HELD; ++k)
-      if (k * rows_at_once < count)
-        read(min(row0 + k * rows_at_once, count - 1), s, unit < r.items ? unit : 0, x[k]);
+      for (int k = 0; k < HELD; ++k) {
+        const int64_t row = min(row0 + k * rows_at_once, last);
+        pos[k] = position(p, at.first + row);
+        raw[k].load(in + row * r.in_tok, s, p.half);
+      }
+#pragma unroll
+      for (int k = 0; k < HELD; ++k) {
+        Turn<T, V, NEOX> turn;
+        turn.load(angles<T>(p, pos[k]), s, item, p.half);
+        raw[k].rotate(turn, s, x[k], x[k] + V);
+      }
+    } else {
+      Words<T, V> raw[HELD];
+#pragma unroll
+      for (int k = 0; k < HELD; ++k)
+        raw[k] = load_words<T, V, true>(in + int64_t(min(row0 + k * rows_at_once, last)) * r.in_tok + s.e);
+#pragma unroll
+      for (int k = 0; k < HELD; ++k) to_floats<T, V>(raw[k], x[k]);
+    }
   }
   // the elements are on their way: now the page
   const bool kept = at.page >= 0 && at.page < p.seq.num_pages;  // else padding; the same for all lanes
