@@ -105,7 +105,8 @@ def test_append(page, block, dtype, neox, codes):
 @pytest.mark.parametrize("neox", [True, False])
 @pytest.mark.parametrize("D,Dv,rd,start", [(128, 64, 128, 0), (128, 128, 64, 64), (96, 96, 96, 0),
                                            (80, 48, 32, 16), (256, 256, 64, 0), (72, 40, 24, 7),
-                                           (130, 66, 66, 2), (576, 16, 64, 512)])
+                                           (130, 66, 66, 2), (576, 16, 64, 512), (88, 64, 64, 8),
+                                           (136, 40, 32, 24), (160, 128, 64, 32)])
 def test_widths_and_slices(D, Dv, rd, start, neox, codes):
     s = setup(*RAGGED, 16, 8, 2, D, Dv, codes, BF16, seed=D, rd=rd)
     check(s, start, neox)
