@@ -16,8 +16,23 @@ constexpr int64_t kMaxPageWords = int64_t(1) << 31;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// A page of t as one dense block; `page_size` tokens of it (0: copied whole only).
-bool page_block(const rope_tensor *t, int64_t page_size, PageCache *c) {
+// What caches of one description have in common: a page as one dense block, `part` bytes of it for each of
+// `parts` blocks of its tokens (0: copied whole only), and the bytes from a cache's first to its last.
+struct CacheKind {
+  const rope_tensor *like = nullptr;
+  int64_t elements = 0, bytes = 0, page = 0, part = 0, reach = 0;
+  uint32_t parts = 0;
+};
+
+bool alike(const rope_tensor *a, const rope_tensor *b) {
+  if (a->ndim != b->ndim || a->dtype != b->dtype) return false;
+  for (int d = 0; d < a->ndim; ++d)
+    if (a->shape[d] != b->shape[d] || a->stride[d] != b->stride[d]) return false;
+  return true;
+}
+
+// False where a page of t is no dense block.
+bool describe(const rope_tensor *t, int64_t page_size, CacheKind *k) {
   int order[3], n = 0;
   for (int d = 1; d < t->ndim; ++d)
     if (t->shape[d] > 1) order[n++] = d;
@@ -27,24 +42,35 @@ bool page_block(const rope_tensor *t, int64_t page_size, PageCache *c) {
     if (t->stride[order[i]] != dense) return false;
     dense *= t->shape[order[i]];
   }
-  const int64_t es = bytes_of(t->dtype), bytes = dense * es;
-  c->base = static_cast<char *>(t->data);
-  c->page = t->shape[0] > 1 ? t->stride[0] * es : 0;
+  const int64_t es = bytes_of(t->dtype);
+  k->bytes = dense * es;
+  k->page = t->shape[0] > 1 ? t->stride[0] * es : 0;
   // rows outermost: the parts of a page that tokens lie in
-  int64_t part = 0;
   if (page_size > 0 && t->ndim > 1 && t->shape[1] > 0 &&
       (t->shape[1] == 1 || order[n - 1] == 1) &&
       (page_size % t->shape[1] == 0 || t->shape[1] % page_size == 0) &&
-      t->shape[1] < (int64_t(1) << 31))
-    part = bytes / t->shape[1];
-  uint64_t all = reinterpret_cast<uintptr_t>(t->data) | uint64_t(c->page) | uint64_t(bytes) |
-                 uint64_t(part);
+      t->shape[1] < (int64_t(1) << 31)) {
+    k->part = k->bytes / t->shape[1];
+    k->parts = uint32_t(t->shape[1]);
+  }
+  uintptr_t a, b;
+  extent(t, &a, &b);
+  k->reach = int64_t(b - a);
+  return true;
+}
+
+// False where a page has too many words.
+bool cache_of(const rope_tensor *t, const CacheKind &k, PageCache *c) {
+  c->base = static_cast<char *>(t->data);
+  c->page = k.page;
+  const uint64_t all = reinterpret_cast<uintptr_t>(t->data) | uint64_t(k.page) | uint64_t(k.bytes) |
+                       uint64_t(k.part);
   PageRun &r = c->run;
   while (r.width < 4 && (all >> r.width & 1) == 0) ++r.width;
-  if (bytes >> r.width >= kMaxPageWords) return false;
-  r.vecs = uint32_t(bytes >> r.width);
-  r.parts = part > 0 ? uint32_t(t->shape[1]) : 0;
-  r.part_words = uint32_t(part >> r.width);
+  if (k.bytes >> r.width >= kMaxPageWords) return false;
+  r.vecs = uint32_t(k.bytes >> r.width);
+  r.parts = k.part > 0 ? k.parts : 0;
+  r.part_words = uint32_t(k.part >> r.width);
   if (r.vecs < 64) {
     r.lanes_log2 = 0;
     while ((1u << r.lanes_log2) < r.vecs) ++r.lanes_log2;
@@ -54,65 +80,94 @@ bool page_block(const rope_tensor *t, int64_t page_size, PageCache *c) {
 
 auto order_of(const PageRun &r) { return std::tie(r.vecs, r.width, r.parts, r.part_words); }
 
-// The caches of a call: checked, and without those that hold nothing.
+// Where a cache lies.
+struct Extent {
+  uintptr_t first, end;
+  const rope_tensor *t;
+};
+
+// The caches of a call: checked, and without those that hold nothing.  All layers' are described alike, so
+// what follows from a description is worked out once for each of the last few (128 caches of a fork took 31 us
+// of the host, with the comparisons below by extents 6).
 int check_caches(const rope_tensor *caches, int64_t num_caches, int64_t *pages, int64_t page_size,
-                 std::vector<PageCache> *list, std::string *err) {
+                 std::vector<PageCache> *list, std::vector<Extent> *extents, std::string *err) {
   list->clear();
   if (num_caches < 0 || num_caches > kMaxCaches)
     return reject(err, ROPE_ERR_PARAM_INVALID, "num_caches must be in [0, 65536]");
   if (num_caches > 0 && caches == nullptr)
     return reject(err, ROPE_ERR_PARAM_NULLPTR, "caches is NULL");
-  std::vector<std::pair<uintptr_t, const rope_tensor *>> by_start;
-  by_start.reserve(size_t(num_caches));
+  extents->reserve(size_t(num_caches));
   list->reserve(size_t(num_caches));
+  constexpr int kKinds = 8;
+  CacheKind kinds[kKinds];
+  int known = 0;
   for (int64_t i = 0; i < num_caches; ++i) {
     const rope_tensor *t = caches + i;
-    const int st = common_checks({t}, err);
-    if (st != ROPE_OK) return st;
-    if (bytes_of(t->dtype) == 0)
-      return reject(err, ROPE_ERR_PARAM_INVALID, "a cache's dtype is unsupported");
-    if (*pages < 0) *pages = t->shape[0];
-    if (t->shape[0] != *pages)
-      return reject(err, ROPE_ERR_PARAM_INVALID, "the caches differ in pages");
-    if (count(t) == 0) continue;
+    const CacheKind *kind = nullptr;
+    for (int k = 0; k < std::min(known, kKinds) && kind == nullptr; ++k)
+      if (alike(kinds[k].like, t)) kind = &kinds[k];
+    if (kind == nullptr || (kind->elements > 0 && t->data == nullptr)) {
+      const int st = common_checks({t}, err);
+      if (st != ROPE_OK) return st;
+      if (bytes_of(t->dtype) == 0)
+        return reject(err, ROPE_ERR_PARAM_INVALID, "a cache's dtype is unsupported");
+      if (*pages < 0) *pages = t->shape[0];
+      if (t->shape[0] != *pages)
+        return reject(err, ROPE_ERR_PARAM_INVALID, "the caches differ in pages");
+      CacheKind &k = kinds[known++ % kKinds];
+      k = CacheKind();
+      k.like = t;
+      k.elements = count(t);
+      if (k.elements > 0 && !describe(t, page_size, &k))
+        return reject(err, ROPE_ERR_PARAM_INVALID,
+                      "a page of a cache must be one dense block of less than 2^31 words");
+      if (k.elements > 0 && !injective(t))
+        return reject(err, ROPE_ERR_PARAM_INVALID, "the pages of a cache overlap");
+      kind = &k;
+    }
+    if (kind->elements == 0) continue;
     PageCache c;
-    if (!page_block(t, page_size, &c))
+    if (!cache_of(t, *kind, &c))
       return reject(err, ROPE_ERR_PARAM_INVALID,
                     "a page of a cache must be one dense block of less than 2^31 words");
-    if (!injective(t))
-      return reject(err, ROPE_ERR_PARAM_INVALID, "the pages of a cache overlap");
-    uintptr_t a, b;
-    extent(t, &a, &b);
-    by_start.emplace_back(a, t);
+    const uintptr_t first = reinterpret_cast<uintptr_t>(t->data);
+    extents->push_back({first, first + uintptr_t(kind->reach), t});
     list->push_back(c);
   }
-  std::sort(by_start.begin(), by_start.end(),
-            [](const auto &x, const auto &y) { return x.first < y.first; });
-  for (size_t i = 0; i < by_start.size(); ++i) {
-    uintptr_t a, end;
-    extent(by_start[i].second, &a, &end);
-    for (size_t k = i + 1; k < by_start.size() && by_start[k].first < end; ++k)
-      if (!disjoint(by_start[i].second, by_start[k].second))
+  const auto before = [](const Extent &x, const Extent &y) { return x.first < y.first; };
+  if (!std::is_sorted(extents->begin(), extents->end(), before))
+    std::sort(extents->begin(), extents->end(), before);
+  for (size_t i = 0; i < extents->size(); ++i)
+    for (size_t k = i + 1; k < extents->size() && (*extents)[k].first < (*extents)[i].end; ++k)
+      if (!disjoint((*extents)[i].t, (*extents)[k].t))
         return reject(err, ROPE_ERR_PARAM_INVALID, "caches overlap");
-  }
-  // pages that are alike side by side
-  std::stable_sort(list->begin(), list->end(), [](const PageCache &x, const PageCache &y) {
-    return order_of(x.run) < order_of(y.run);
-  });
+  // pages that are alike side by side (the numbers are sorted, and the caches, of 64 bytes, put there once)
+  std::vector<uint32_t> place(list->size());
+  for (size_t i = 0; i < place.size(); ++i) place[i] = uint32_t(i);
+  const std::vector<PageCache> &c = *list;
+  std::stable_sort(place.begin(), place.end(),
+                   [&c](uint32_t x, uint32_t y) { return order_of(c[x].run) < order_of(c[y].run); });
+  std::vector<PageCache> sorted;
+  sorted.reserve(place.size());
+  for (const uint32_t i : place) sorted.push_back(c[i]);
+  list->swap(sorted);
   return ROPE_OK;
 }
 
 // Whether t, if it holds anything, shares memory with one of the caches.
-bool meets_caches(const rope_tensor *t, const rope_tensor *caches, int64_t num_caches) {
+bool meets_caches(const rope_tensor *t, const std::vector<Extent> &caches) {
   if (t == nullptr || count(t) == 0) return false;
-  for (int64_t i = 0; i < num_caches; ++i)
-    if (count(caches + i) > 0 && !disjoint(t, caches + i)) return true;
+  uintptr_t first, end;
+  extent(t, &first, &end);
+  for (const Extent &e : caches)
+    if (first < e.end && e.first < end && !disjoint(t, e.t)) return true;
   return false;
 }
 
-bool in_caches(const void *p, int64_t bytes, const rope_tensor *caches, int64_t num_caches) {
-  for (int64_t i = 0; i < num_caches; ++i)
-    if (touches(p, bytes, caches + i)) return true;
+bool in_caches(const void *p, int64_t bytes, const std::vector<Extent> &caches) {
+  const uintptr_t first = reinterpret_cast<uintptr_t>(p);
+  for (const Extent &e : caches)
+    if (bytes > 0 && first < e.end && e.first < first + uintptr_t(bytes)) return true;
   return false;
 }
 
@@ -158,11 +213,12 @@ int plan_copy_pages(const rope_tensor *sources, const rope_tensor *targets,
   if (!is_i64_vector(sources) || !is_i64_vector(targets) || sources->shape[0] != targets->shape[0])
     return reject(err, ROPE_ERR_PARAM_INVALID, "sources and targets must be int64 of one length");
   int64_t pages = -1;
-  const int ck = check_caches(caches, num_caches, &pages, 0, list, err);
+  std::vector<Extent> extents;
+  const int ck = check_caches(caches, num_caches, &pages, 0, list, &extents, err);
   if (ck != ROPE_OK) return ck;
   if (pages >= kIndexLimit || sources->shape[0] >= kIndexLimit)
     return reject(err, ROPE_ERR_PARAM_INVALID, "too many pages");
-  if (meets_caches(sources, caches, num_caches) || meets_caches(targets, caches, num_caches))
+  if (meets_caches(sources, extents) || meets_caches(targets, extents))
     return reject(err, ROPE_ERR_PARAM_INVALID, "a cache overlaps another tensor");
   plan->sources = i64(sources);
   plan->targets = i64(targets);
@@ -221,7 +277,8 @@ int plan_fork_pages(const rope_tensor *page_table, const rope_tensor *seq_lens,
       R * page_table_out->shape[1] >= (int64_t(1) << 40))
     return reject(err, ROPE_ERR_PARAM_INVALID, "too many pages, rows or tokens");
   int64_t cache_pages = pages;
-  const int ck = check_caches(caches, num_caches, &cache_pages, page_size, list, err);
+  std::vector<Extent> extents;
+  const int ck = check_caches(caches, num_caches, &cache_pages, page_size, list, &extents, err);
   if (ck != ROPE_OK) return ck;
   const rope_tensor *ins[5] = {page_table, seq_lens, parents, grow, ref_counts};
   const rope_tensor *outs[4] = {page_table_out, seq_lens_out, ref_counts_out, shortage};
@@ -241,7 +298,7 @@ int plan_fork_pages(const rope_tensor *page_table, const rope_tensor *seq_lens,
   }
   for (const rope_tensor *t : {page_table, seq_lens, parents, grow, ref_counts, page_table_out,
                                seq_lens_out, ref_counts_out, shortage})
-    if (meets_caches(t, caches, num_caches))
+    if (meets_caches(t, extents))
       return reject(err, ROPE_ERR_PARAM_INVALID, "a cache overlaps another tensor");
   const int64_t need = fork_workspace(B, R, pages);
   if (workspace == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "workspace is NULL");
@@ -251,7 +308,7 @@ int plan_fork_pages(const rope_tensor *page_table, const rope_tensor *seq_lens,
                                seq_lens_out, ref_counts_out, shortage})
     if (touches(workspace, need, t))
       return reject(err, ROPE_ERR_PARAM_INVALID, "workspace overlaps a tensor");
-  if (in_caches(workspace, need, caches, num_caches))
+  if (in_caches(workspace, need, extents))
     return reject(err, ROPE_ERR_PARAM_INVALID, "workspace overlaps a tensor");
 
   ForkPlan &p = *plan;
@@ -330,7 +387,8 @@ int plan_compact_pages(const rope_tensor *page_table, const rope_tensor *ref_cou
   if (pages >= kIndexLimit || count(page_table) >= (int64_t(1) << 40))
     return reject(err, ROPE_ERR_PARAM_INVALID, "too many pages");
   int64_t cache_pages = pages;
-  const int ck = check_caches(caches, num_caches, &cache_pages, 0, list, err);
+  std::vector<Extent> extents;
+  const int ck = check_caches(caches, num_caches, &cache_pages, 0, list, &extents, err);
   if (ck != ROPE_OK) return ck;
   const rope_tensor *ins[2] = {page_table, ref_counts};
   const rope_tensor *outs[4] = {page_table_out, ref_counts_out, page_map, live};
@@ -350,7 +408,7 @@ int plan_compact_pages(const rope_tensor *page_table, const rope_tensor *ref_cou
   }
   for (const rope_tensor *t : {page_table, ref_counts, page_table_out, ref_counts_out, page_map,
                                live})
-    if (meets_caches(t, caches, num_caches))
+    if (meets_caches(t, extents))
       return reject(err, ROPE_ERR_PARAM_INVALID, "a cache overlaps another tensor");
   const int64_t need = compact_workspace(pages);
   if (workspace == nullptr) return reject(err, ROPE_ERR_PARAM_NULLPTR, "workspace is NULL");
@@ -360,7 +418,7 @@ int plan_compact_pages(const rope_tensor *page_table, const rope_tensor *ref_cou
                                live})
     if (touches(workspace, need, t))
       return reject(err, ROPE_ERR_PARAM_INVALID, "workspace overlaps a tensor");
-  if (in_caches(workspace, need, caches, num_caches))
+  if (in_caches(workspace, need, extents))
     return reject(err, ROPE_ERR_PARAM_INVALID, "workspace overlaps a tensor");
 
   CompactPlan &p = *plan;
