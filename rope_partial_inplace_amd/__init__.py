@@ -366,8 +366,7 @@ def rope_with_cos_sin_cache_v2(positions, query_in, key_in, cos_sin_cache, mrope
 # A decoding step's calls take the GPU a few microseconds, so their marshalling is kept short:
 # descriptions are packed as bytes, and the device and stream read as numbers.
 
-_PACK = [None] + [struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack
-                  for n in range(1, 5)]
+_PACK = {n: struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack for n in range(1, 5)}
 _DTYPE_CODES = {}
 
 
@@ -375,14 +374,15 @@ def _pack(t):
     """The bytes of a ``rope_tensor`` describing a torch tensor (None stays None)."""
     if t is None:
         return None
-    n = t.dim()
-    if not 1 <= n <= 4:
+    shape = t.shape
+    n = len(shape)
+    pack = _PACK.get(n)
+    if pack is None:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "tensors must have 1 to 4 dims")
-    dtype = t.dtype
-    code = _DTYPE_CODES.get(dtype)
+    code = _DTYPE_CODES.get(t.dtype)
     if code is None:
-        code = _DTYPE_CODES[dtype] = _dtype_code(t)
-    return _PACK[n](t.data_ptr(), code, n, *t.shape, *t.stride())
+        code = _DTYPE_CODES[t.dtype] = _dtype_code(t)
+    return pack(t.data_ptr(), code, n, *shape, *t.stride())
 
 
 def _device_index(tensors) -> int:
