@@ -481,7 +481,9 @@ append_q8_kernel(AppendQ8Plan p) {
   const int64_t w = block * (kQ8Block >> each) + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> each);
   const int64_t u = p.idx32 ? int64_t(div_by(p.div_groups, uint32_t(w))) : w / p.head_groups;
   Place at;
-  // (where wavefronts meet in LDS, one without a place goes on without tokens)
+  // Wavefronts that meet in LDS are of one place, and all of its keys or all of its values (the plan sees to it), so
+  // they return together.  Those of two a head go on without tokens instead: with nothing but a return here the
+  // compiler waits for the page's number before it asks for the tokens (blocks of 16, NeoX: 52.9 us, not 49.1).
   const bool some = u < p.places && find_place(p, u, &at);
   if (!some && p.lanes != 128) return;
   if (!some) at = Place();

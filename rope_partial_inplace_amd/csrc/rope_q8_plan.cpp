@@ -260,7 +260,8 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
       if (!r.side_by_side) r.row_log2 = 0;
     }
     const int64_t heads_each = std::max(1, 64 / p.lanes), units = kQ8Block / std::max(64, p.lanes);
-    p.head_groups = 2 * int32_t((p.heads + heads_each - 1) / heads_each);
+    // whole workgroups for keys, and for values: the wavefronts of one meet in LDS
+    p.head_groups = 2 * int32_t(up((p.heads + heads_each - 1) / heads_each, p.lanes > 64 ? units : 1));
     p.div_groups = make_fastdiv(uint32_t(p.head_groups));
     p.kv_blocks = (p.places * p.head_groups + units - 1) / units;
     p.idx32 = p.idx32 && p.kv_blocks * units < (int64_t(1) << 31);

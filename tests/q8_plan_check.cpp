@@ -91,6 +91,8 @@ static int64_t walk_append() {
   const int64_t units = kQ8Block / std::max(64, p.lanes);
   CHECK(p.kv_blocks * units >= p.places * p.head_groups, "too few wavefronts");
   CHECK(p.head_groups / 2 * std::max(1, 64 / p.lanes) >= heads, "heads left out");
+  // wavefronts that meet are of one place, its keys or its values
+  CHECK(p.lanes <= 64 || p.head_groups / 2 % units == 0, "a workgroup of keys and values");
   std::map<std::pair<int64_t, int64_t>, std::pair<int64_t, int64_t>> found;  // (b, block) -> first token, count
   auto first_place = [&](int64_t offset, int64_t i) {
     return p.by_token ? offset : int64_t(div_by(p.div_block, uint32_t(offset))) + 2 * i;
