@@ -376,7 +376,8 @@ int rope_latent_attention_backward(
  * query          [T, Nq, Dq] or NULL, with query_out [T, Nq, Dq] (NULL exactly if query is; it may
  *                be the query itself).  All tokens' queries are rotated.
  * key            [T, Nk, D]; value [T, Nk, Dv]; cos_sin_cache [maxSeqLen, rotaryDim].  One dtype,
- *                F32, F16 or BF16.
+ *                F32, F16 or BF16.  Dv may be 0 (a cache of keys alone): value_scales then get the
+ *                scales of top = 0.
  * key_cache, value_cache    [pages, pageSize, Nk, D] and [.., Dv], I8 or E4M3, one of the two.
  * key_scales, value_scales  F32 [pages, blocks, Nk]; blocks divides pageSize.
  * page_table     INT64 [B, maxPages]; seq_lens INT64 [B], clamped to [0, maxPages * pageSize].

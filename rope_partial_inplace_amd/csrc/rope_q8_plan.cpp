@@ -255,8 +255,8 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
     p.lanes = 4;
     while (p.lanes < kQ8Block && p.lanes < lanes) p.lanes *= 2;
     while ((1 << p.lanes_log2) != p.lanes) ++p.lanes_log2;
-    for (Q8Rows &r : p.kv) {  // a row's items of one wavefront
-      r.side_by_side = (1 << r.row_log2) <= std::min(p.lanes, 64);
+    for (Q8Rows &r : p.kv) {  // a row's items of one wavefront; rows of width 0 have none, and no address
+      r.side_by_side = r.items > 0 && (1 << r.row_log2) <= std::min(p.lanes, 64);
       if (!r.side_by_side) r.row_log2 = 0;
     }
     const int64_t heads_each = std::max(1, 64 / p.lanes), units = kQ8Block / std::max(64, p.lanes);

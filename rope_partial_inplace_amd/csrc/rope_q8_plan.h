@@ -34,7 +34,9 @@ struct Q8Rows {
   uint32_t rot_items = 0;  // rotated items of a row, in the order of AppendRows
   uint32_t items = 0;
   bool wide_rows = false;  // code rows split into aligned 16-byte pieces
-  bool side_by_side = false;  // a row's items fit the threads of a block, 2^row_log2 of them
+  // A row's items fit the threads of a block, 2^row_log2 of them.  Such rows are loaded with no look at their
+  // items, so it is false where there are none.
+  bool side_by_side = false;
   int32_t row_log2 = 0;
   FastDiv div_items;
 };

@@ -1,0 +1,91 @@
+// Host checks of single cases of the 8-bit cache's and the page operators' launch plans, each run by its name:
+//   append_no_values   values of width 0: nothing of them may be loaded, by any launch form
+//
+// No GPU and no tensor data are involved.  Prints "ok" or the first failure.
+#include <algorithm>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <string>
+#include <vector>
+
+#include "rope.h"
+#include "rope_pages_plan.h"
+#include "rope_q8_plan.h"
+
+using namespace ropeamd;
+
+#define CHECK(c, ...)                                           \
+  do {                                                          \
+    if (!(c)) {                                                 \
+      std::printf("failed %s:%d %s: ", __FILE__, __LINE__, #c); \
+      std::printf(__VA_ARGS__);                                 \
+      std::printf("\n");                                        \
+      std::exit(1);                                             \
+    }                                                           \
+  } while (0)
+
+constexpr uintptr_t kBase = uintptr_t(1) << 40, kStep = uintptr_t(1) << 38;
+
+// Contiguous, at a place of its own; empty tensors at address 0, as torch has them.
+static rope_tensor desc(int place, rope_dtype dt, std::vector<int64_t> shape) {
+  rope_tensor t{};
+  t.dtype = dt;
+  t.ndim = int(shape.size());
+  int64_t st = 1;
+  for (int d = t.ndim - 1; d >= 0; --d) {
+    t.shape[d] = shape[size_t(d)];
+    t.stride[d] = st;
+    st *= std::max<int64_t>(shape[size_t(d)], 1);
+  }
+  bool empty = false;
+  for (int64_t n : shape) empty |= n == 0;
+  t.data = empty ? nullptr : reinterpret_cast<void *>(kBase + uintptr_t(place) * kStep);
+  return t;
+}
+
+// A plan for B sequences of `tokens` new tokens each, in blocks of `block`.
+static int append_plan(rope_dtype dt, rope_dtype codes, int64_t B, int64_t tokens, int64_t page, int64_t block,
+                       int64_t heads, int64_t D, int64_t Dv, int neox, AppendQ8Plan *p, std::string *err) {
+  const int64_t T = B * tokens;
+  const rope_tensor pos = desc(0, ROPE_I64, {T}), k = desc(1, dt, {T, heads, D}), v = desc(2, dt, {T, heads, Dv});
+  const rope_tensor cs = desc(3, dt, {100, 16}), table = desc(4, ROPE_I64, {B, 8}), lens = desc(5, ROPE_I64, {B});
+  const rope_tensor kc = desc(6, codes, {9, page, heads, D}), vc = desc(7, codes, {9, page, heads, Dv});
+  const rope_tensor ks = desc(8, ROPE_F32, {9, page / block, heads}), vs = desc(9, ROPE_F32, {9, page / block, heads});
+  return plan_append_q8(&pos, nullptr, &k, &v, &cs, &table, &lens, nullptr, 0, 0, neox, nullptr, &kc, &vc, &ks, &vs,
+                        p, err);
+}
+
+static void append_no_values() {
+  std::string err;
+  for (rope_dtype dt : {ROPE_F32, ROPE_F16, ROPE_BF16})
+    for (rope_dtype codes : {ROPE_I8, ROPE_E4M3})
+      for (int64_t tokens : {1, 7, 200})
+        for (int64_t block : {1, 4, 64})
+          for (int neox : {0, 1})
+            for (int64_t D : {16, 30, 128, 512}) {
+              AppendQ8Plan p;
+              const int st = append_plan(dt, codes, 3, tokens, 64, block, 2, D, 0, neox, &p, &err);
+              CHECK(st == ROPE_OK, "%s", err.c_str());
+              CHECK(p.kv[1].items == 0 && p.kv[1].in == nullptr, "values of width 0");
+              // rows side by side are loaded without a look at their number of items
+              CHECK(!p.kv[1].side_by_side, "rows without items are loaded");
+              CHECK(p.kv[0].items > 0, "keys");
+            }
+}
+
+int main(int argc, char **argv) {
+  const struct {
+    const char *name;
+    void (*run)();
+  } checks[] = {{"append_no_values", append_no_values}};
+  for (const auto &c : checks)
+    if (argc > 1 && std::strcmp(argv[1], c.name) == 0) {
+      c.run();
+      std::printf("ok\n");
+      return 0;
+    }
+  std::printf("no such check\n");
+  return 1;
+}
