@@ -379,7 +379,8 @@ int rope_latent_attention_backward(
  *                F32, F16 or BF16.  Dv may be 0 (a cache of keys alone): value_scales then get the
  *                scales of top = 0.
  * key_cache, value_cache    [pages, pageSize, Nk, D] and [.., Dv], I8 or E4M3, one of the two.
- * key_scales, value_scales  F32 [pages, blocks, Nk]; blocks divides pageSize.
+ * key_scales, value_scales  F32 [pages, blocks, Nk]; blocks divides pageSize.  A block has fewer than
+ *                2^30 elements of a head.
  * page_table     INT64 [B, maxPages]; seq_lens INT64 [B], clamped to [0, maxPages * pageSize].
  *                Tokens before place 0, and tokens whose page is not in [0, pages) (padding), are
  *                skipped.  A page that takes tokens belongs to one sequence only -- a precondition

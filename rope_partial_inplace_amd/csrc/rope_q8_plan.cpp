@@ -140,6 +140,10 @@ int plan_append_q8(const rope_tensor *positions, const rope_tensor *query, const
     if (t != nullptr && (t->shape[2] > kMaxWidth || t->shape[1] > kMaxWidth ||
                          t->shape[1] * t->shape[2] > kMaxWidth))
       return reject(err, ROPE_ERR_PARAM_INVALID, "too many elements per token");
+  // the kernel numbers a block's elements of a head in 32 bits
+  if (key_cache->shape[1] > 0 && key_cache->shape[1] / key_scales->shape[1] *
+                                         std::max(key->shape[2], value->shape[2]) >= kIndexLimit)
+    return reject(err, ROPE_ERR_PARAM_INVALID, "too many elements in a block of a head");
   if (key_rot_start < 0 || key_rot_start > key->shape[2] - rd)
     return reject(err, ROPE_ERR_PARAM_INVALID, "key_rot_start: the slice leaves the key head");
   if (query != nullptr && (query_rot_start < 0 || query_rot_start > query->shape[2] - rd))

@@ -1,5 +1,6 @@
 // Host checks of single cases of the 8-bit cache's and the page operators' launch plans, each run by its name:
 //   append_no_values   values of width 0: nothing of them may be loaded, by any launch form
+//   append_long_blocks blocks whose elements of a head pass the kernel's 32-bit numbers: refused
 //
 // No GPU and no tensor data are involved.  Prints "ok" or the first failure.
 #include <algorithm>
@@ -75,11 +76,34 @@ static void append_no_values() {
             }
 }
 
+static void append_long_blocks() {
+  std::string err;
+  // the kernel numbers a block's pieces of a head up to block * width, and adds the threads of a workgroup
+  const struct {
+    int64_t block, D, Dv;
+    bool fits;
+  } cases[] = {{1 << 22, 128, 128, true},  {1 << 22, 254, 16, true},  {1 << 22, 16, 254, true},
+               {1 << 22, 256, 16, false},  {1 << 22, 16, 256, false}, {1 << 24, 128, 128, false},
+               {1 << 29, 16, 16, false},   {1 << 25, 16, 0, true},    {1 << 26, 16, 0, false}};
+  for (const auto &c : cases)
+    for (rope_dtype codes : {ROPE_I8, ROPE_E4M3})
+      for (int64_t parts : {1, 2}) {
+        if (c.block * parts * 8 >= int64_t(1) << 30) continue;  // tokens of a sequence: refused for that
+        AppendQ8Plan p;
+        const int st = append_plan(ROPE_BF16, codes, 2, 3, c.block * parts, c.block, 1, c.D, c.Dv, 1, &p, &err);
+        CHECK((st == ROPE_OK) == c.fits, "block %lld of %lld and %lld: %d %s", (long long)c.block, (long long)c.D,
+              (long long)c.Dv, st, err.c_str());
+        if (st == ROPE_OK)
+          for (const Q8Rows &r : p.kv)
+            CHECK(int64_t(p.block) * std::max<int64_t>(r.dim, r.items) + kQ8Block < (int64_t(1) << 31), "numbers");
+      }
+}
+
 int main(int argc, char **argv) {
   const struct {
     const char *name;
     void (*run)();
-  } checks[] = {{"append_no_values", append_no_values}};
+  } checks[] = {{"append_no_values", append_no_values}, {"append_long_blocks", append_long_blocks}};
   for (const auto &c : checks)
     if (argc > 1 && std::strcmp(argv[1], c.name) == 0) {
       c.run();
