@@ -474,10 +474,14 @@ int rope_copy_pages(const rope_tensor *sources, const rope_tensor *targets,
  * parents        INT64 [R]; outside [0, B): an empty row of length 0, which gets no pages (a sequence that
  *                begins continues one of length 0).     grow  INT64 [R] or NULL (0); below 0: 0.
  * ref_counts     INT64 [pages];  page_size: tokens of a page.
- * caches         as in rope_copy_pages, num_caches may be 0.  Of a cache [pages, n, ...] whose second
- *                dimension is the outermost of a page and n divides page_size or the reverse (rows, or
- *                blocks of rows), only the part that holds the copied tokens is written; of others the
- *                whole page.
+ * caches         as in rope_copy_pages, num_caches may be 0.  Of two forms a copied page gets only the
+ *                part that holds the row's tokens, where the second dimension is the outermost of a page:
+ *                [pages, page_size, ...] of 3 or 4 dims, whose second dimension is taken for the page's
+ *                tokens, and F32 [pages, n, m], n a divisor of page_size, taken for the scales of n blocks
+ *                of tokens (rope_append_paged_cache_q8's).  All others are copied whole, [pages, heads,
+ *                pageSize, ...] and [pages, 2, ...] among them.  A cache that has one of the two forms and is
+ *                something else (as many heads as a page has tokens, outermost; F32 scales of a page's n
+ *                heads) is to be described as [pages, elements]: with 2 dims it is copied whole.
  * page_table_out INT64 [R, maxPages or more], seq_lens_out INT64 [R], shortage INT64 [1]: apart from
  *                all inputs.
  * ref_counts_out INT64 [pages], may be ref_counts itself.

@@ -40,7 +40,7 @@ streams.  There is no fallback: if the library is not built this import fails.
                   stream=None)
   rope_compact_pages(page_table, ref_counts, caches=(), page_table_out=None,
                      ref_counts_out=None, page_map=None, live=None, stream=None)
-  PageCaches(caches)                  (the caches of all layers, described once for those three)
+  PageCaches(caches, whole=())        (the caches of all layers, described once for those three)
 
 Pages defining the operations:
   [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace 部分旋转位置编码接口详解与实现剖析"
@@ -651,13 +651,30 @@ def rope_attention_paged_q8(query, key_cache, value_cache, key_scales, value_sca
 
 # ---- pages of a cache ------------------------------------------------------------------------------
 
+def _as_pages(t):
+    """A cache as [pages, elements of a page], whose pages are dense blocks in any order of dimensions."""
+    if t.dim() < 2 or t.numel() == 0:
+        return t
+    reach = 1
+    for stride, size in sorted((t.stride(d), t.shape[d]) for d in range(1, t.dim()) if t.shape[d] > 1):
+        if stride != reach:
+            raise RopeError(ROPE_ERR_PARAM_INVALID, "a page of a cache must be one dense block")
+        reach *= size
+    return t.as_strided((t.shape[0], reach), (t.stride(0), 1))
+
+
 class PageCaches:
     """The caches of all layers, described once: a program that copies, forks or compacts pages at
     every step makes one of its list (keys, values and scales, [pages, ...] each) and passes it in the
-    list's place.  The tensors must keep their storage while the object is used."""
+    list's place.  The tensors must keep their storage while the object is used.
 
-    def __init__(self, caches):
-        self.tensors = list(caches)
+    A fork copies only the tokens of a page that is not full where a cache is [pages, page_size, ...] (3
+    or 4 dims) or a float32 [pages, n, m], n a divisor of page_size (scales of n blocks); dimension 1 is then
+    taken for tokens.  Caches in ``whole`` are copied by whole pages whatever their shape: those where it is
+    something else, such as as many heads as a page has tokens, or scales of heads."""
+
+    def __init__(self, caches, whole=()):
+        self.tensors = [*caches, *map(_as_pages, whole)]
         self.device = _device_index(self.tensors)
         self.packed = b"".join(map(_pack, self.tensors)) or None
 
@@ -688,7 +705,10 @@ def rope_fork_pages(page_table, seq_lens, parents, ref_counts, page_size: int, c
     one of length 0) and room for grow[i] more.  Full pages
     are shared, a last page that is not full is copied in all caches for every row but the first that
     continues its sequence (for that one, too, if something else holds the page), and new pages are the
-    lowest with ref_counts 0.  Sequences without a row end.  All index tensors are int64: page_table
+    lowest with ref_counts 0.  Caches [pages, page_size, ...] of 3 or 4 dims and float32 scales [pages, n, m],
+    n a divisor of page_size, are taken to hold tokens, or blocks of them, in dimension 1, and only the
+    sequence's are copied; all others go by whole pages, and so do those that PageCaches is given as
+    ``whole``.  Sequences without a row end.  All index tensors are int64: page_table
     [B, maxPages], seq_lens [B], parents and grow [R], ref_counts [pages] (holds on each page).  Returns
     (page_table_out [R, maxPages], seq_lens_out [R], ref_counts_out [pages], shortage [1]), allocated
     where not given; ref_counts_out may be ref_counts itself, page_table_out may be wider.  shortage is

@@ -45,13 +45,15 @@ bool describe(const rope_tensor *t, int64_t page_size, CacheKind *k) {
   const int64_t es = bytes_of(t->dtype);
   k->bytes = dense * es;
   k->page = t->shape[0] > 1 ? t->stride[0] * es : 0;
-  // rows outermost: the parts of a page that tokens lie in
-  if (page_size > 0 && t->ndim > 1 && t->shape[1] > 0 &&
-      (t->shape[1] == 1 || order[n - 1] == 1) &&
-      (page_size % t->shape[1] == 0 || t->shape[1] % page_size == 0) &&
-      t->shape[1] < (int64_t(1) << 31)) {
-    k->part = k->bytes / t->shape[1];
-    k->parts = uint32_t(t->shape[1]);
+  // The parts of a page that tokens lie in, where they are outermost.  By the form alone, [pages, pageSize, ..] or
+  // scales as the 8-bit cache has them: a length that only fits may be heads, or keys and values, of which a part
+  // would lack some.
+  const int64_t n1 = t->ndim >= 3 ? t->shape[1] : 0;
+  const bool tokens = n1 > 0 && n1 == page_size;
+  const bool blocks = n1 > 0 && t->ndim == 3 && t->dtype == ROPE_F32 && page_size % n1 == 0;
+  if (page_size > 0 && (tokens || blocks) && (n1 == 1 || order[n - 1] == 1)) {
+    k->part = k->bytes / n1;
+    k->parts = uint32_t(n1);
   }
   uintptr_t a, b;
   extent(t, &a, &b);

@@ -11,7 +11,7 @@
 namespace ropeamd {
 
 // Caches whose pages are alike: `vecs` words of 2^width bytes each.  Where a page's outermost dimension
-// is its rows (or blocks of rows), the first tokens of a page are its first words: part_words of them
+// is its tokens (or blocks of them), the first tokens of a page are its first words: part_words of them
 // for each of `parts` equal parts of a page's tokens.
 //
 // A run's work is numbered cache by cache, in it move by move, in that piece by piece (move by move and

@@ -1,6 +1,8 @@
 // Host checks of single cases of the 8-bit cache's and the page operators' launch plans, each run by its name:
 //   append_no_values   values of width 0: nothing of them may be loaded, by any launch form
 //   append_long_blocks blocks whose elements of a head pass the kernel's 32-bit numbers: refused
+//   fork_layouts       which caches are copied in part: those whose second dimension is a page's tokens or
+//                      blocks of them by their form, never others that its length only fits
 //
 // No GPU and no tensor data are involved.  Prints "ok" or the first failure.
 #include <algorithm>
@@ -99,11 +101,55 @@ static void append_long_blocks() {
       }
 }
 
+static void fork_layouts() {
+  const int64_t page = 16, P = 20;
+  const struct {
+    const char *what;
+    rope_dtype dt;
+    std::vector<int64_t> shape;
+    uint32_t parts;  // 0: whole pages
+  } cases[] = {{"rows", ROPE_BF16, {P, page, 8, 128}, 16},
+               {"codes, as many heads as rows", ROPE_E4M3, {P, page, 16, 128}, 16},
+               {"latent rows", ROPE_F16, {P, page, 576}, 16},
+               {"scales of blocks of 4", ROPE_F32, {P, 4, 8}, 4},
+               {"scales of tokens", ROPE_F32, {P, page, 8}, 16},
+               {"scales of pages", ROPE_F32, {P, 1, 8}, 1},
+               {"heads outermost", ROPE_BF16, {P, 8, page, 128}, 0},
+               {"heads outermost, codes", ROPE_I8, {P, 2, page, 64}, 0},
+               {"heads outermost, longer than a page", ROPE_I8, {P, 32, page, 64}, 0},
+               {"keys and values in a page", ROPE_BF16, {P, 2, page, 1024}, 0},
+               {"keys and values in a page", ROPE_BF16, {P, 2, page * 1024}, 0},
+               {"keys' and values' scales of a page", ROPE_F32, {P, 2, 1, 8}, 0},
+               {"scales of a page by head", ROPE_F32, {P, 8}, 0},
+               {"a page as one dimension", ROPE_F32, {P, page}, 0},
+               {"a page as one dimension", ROPE_BF16, {P, page * 8 * 128}, 0},
+               {"a number a page", ROPE_I64, {P}, 0}};
+  std::string err;
+  for (const auto &c : cases) {
+    const int64_t B = 3, R = 5, width = 4;
+    const rope_tensor table = desc(0, ROPE_I64, {B, width}), lens = desc(1, ROPE_I64, {B});
+    const rope_tensor parents = desc(2, ROPE_I64, {R}), refs = desc(3, ROPE_I64, {P});
+    const rope_tensor out = desc(4, ROPE_I64, {R, width}), lens_out = desc(5, ROPE_I64, {R});
+    const rope_tensor refs_out = desc(6, ROPE_I64, {P}), one = desc(7, ROPE_I64, {1}), cache = desc(8, c.dt, c.shape);
+    ForkPlan p;
+    std::vector<PageCache> list;
+    const int st = plan_fork_pages(&table, &lens, &parents, nullptr, &refs, page, &cache, 1, &out, &lens_out,
+                                   &refs_out, &one, reinterpret_cast<void *>(kBase + 20 * kStep),
+                                   fork_workspace(B, R, P), &p, &list, &err);
+    CHECK(st == ROPE_OK && list.size() == 1, "%s: %s", c.what, err.c_str());
+    const PageRun &r = list[0].run;
+    CHECK(r.parts == c.parts || (c.parts == 1 && r.parts == 0), "%s: %u parts", c.what, r.parts);
+    CHECK(r.parts == 0 || r.parts * r.part_words == r.vecs, "%s: %u words of %u", c.what, r.part_words, r.vecs);
+  }
+}
+
 int main(int argc, char **argv) {
   const struct {
     const char *name;
     void (*run)();
-  } checks[] = {{"append_no_values", append_no_values}, {"append_long_blocks", append_long_blocks}};
+  } checks[] = {{"append_no_values", append_no_values},
+                {"append_long_blocks", append_long_blocks},
+                {"fork_layouts", fork_layouts}};
   for (const auto &c : checks)
     if (argc > 1 && std::strcmp(argv[1], c.name) == 0) {
       c.run();
