@@ -336,10 +336,11 @@ struct StateQ8 {
   f32x4 o[R][D / 16];
   float top[R], sum[R];
   int32_t limit[R];  // tokens that the lane's row may see
-  // float16: the weights p vs have to stay in its range, so vs is taken relative to a power of two not
-  // below the largest one so far
-  float reach, by_reach;
+  // float16: the weights p vs have to stay in its range, so a row takes vs relative to a power of two above the
+  // largest one that it has seen, its reach; this is the reciprocal
+  float by_reach[R];
 };
+constexpr float kFirstByReach = 0x1p120f;  // of the smallest scale
 
 // Scores of a tile in powers of two, masked where not every row sees all of it (t0 + 32 above `floor`).
 template <typename T, int D, int R, bool E4M3, int MODE>
@@ -387,6 +388,7 @@ __device__ __forceinline__ void weigh_tile(const ValuesQ8<D, MODE> &v, StateQ8<T
                                            int32_t t0, int32_t floor, int lane,
                                            const f32x4 (&x)[R][2]) {
   const int g = lane >> 4;
+  const bool masked = t0 + kTile > floor;
   float best[R];
   bool raise = false;
 #pragma unroll
@@ -398,18 +400,32 @@ __device__ __forceinline__ void weigh_tile(const ValuesQ8<D, MODE> &v, StateQ8<T
     raise |= best[r] > s.top[r] + Mfma<T>::kSlack;
   }
   constexpr int SC = MODE == kCoarse ? 2 : 1;
+  float most[R];  // float16: the largest vs of the lane's tokens, of those that its rows see where some do not
   if constexpr (Mfma<T>::kNarrow) {
 #pragma unroll
-    for (int j = 0; j < SC; ++j) raise |= fabsf(v.scale[j]) > s.reach;
+    for (int r = 0; r < R; ++r) most[r] = fmaxf(fabsf(v.scale[0]), fabsf(v.scale[SC - 1]));
+    if (masked) {
+      asm volatile("");
+#pragma unroll
+      for (int r = 0; r < R; ++r) most[r] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float vs = fabsf(scale_of<MODE>(v.scale, j, lane));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (t0 + 16 * (j / 4) + 4 * g + j % 4 < s.limit[r]) most[r] = fmaxf(most[r], vs);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) raise |= most[r] * s.by_reach[r] > 1.0f;
   }
   if (__any(raise)) {
-    float reach = s.reach;
+    float all = 0.0f;  // of the tile, which every row sees
     if constexpr (Mfma<T>::kNarrow) {
-      float most = 0.0f;
-#pragma unroll
-      for (int j = 0; j < SC; ++j) most = fmaxf(most, fabsf(v.scale[j]));
-      for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-      if (most > reach) reach = reach_above(most);
+      if (!masked) {
+        all = most[0];
+        for (int d = 1; d < 64; d *= 2) all = fmaxf(all, __shfl_xor(all, d));
+      }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -419,31 +435,30 @@ __device__ __forceinline__ void weigh_tile(const ValuesQ8<D, MODE> &v, StateQ8<T
         s.top[r] = best[r];
       }
       s.sum[r] *= f;
-      if constexpr (Mfma<T>::kNarrow) f *= s.reach * inverse_power(reach);
+      if constexpr (Mfma<T>::kNarrow) {
+        const float seen = masked ? max_quarters(most[r]) : all;
+        const float by = seen * s.by_reach[r] > 1.0f ? inverse_power(reach_above(seen)) : s.by_reach[r];
+        f *= by * inverse_power(s.by_reach[r]);
+        s.by_reach[r] = by;
+      }
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) s.o[r][n] *= f;
     }
-    if constexpr (Mfma<T>::kNarrow) {
-      s.reach = reach;
-      s.by_reach = inverse_power(reach);
-    }
   }
-  float scale[SC];
-#pragma unroll
-  for (int j = 0; j < SC; ++j) scale[j] = Mfma<T>::kNarrow ? v.scale[j] * s.by_reach : v.scale[j];
   float e[R][8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float vs = scale_of<MODE>(scale, j, lane);
+    const float scale = scale_of<MODE>(v.scale, j, lane);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const float vs = Mfma<T>::kNarrow ? scale * s.by_reach[r] : scale;
       const float ref = s.top[r] == kNegInf ? 0.0f : s.top[r] - Mfma<T>::kLift;
       const float y = __builtin_amdgcn_exp2f(x[r][j / 4][j % 4] - ref);
       s.sum[r] += y;
       e[r][j] = y * vs;
     }
   }
-  if (t0 + kTile > floor) {
+  if (masked) {
     asm volatile("");
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -708,10 +723,9 @@ attention_q8_kernel(AttnQ8Plan p) {
     const int32_t floor = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0)));
 
     StateQ8<T, D, R> s;
-    s.reach = 0x1p-120f;
-    s.by_reach = 0x1p120f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      s.by_reach[r] = kFirstByReach;
       const int32_t m = r * 16 + (lane & 15);
       const bool some = m < g.live;
       const int32_t tok = int32_t(div_by(p.div_group, uint32_t(g.row0 + (some ? m : 0))));
@@ -765,7 +779,7 @@ attention_q8_kernel(AttnQ8Plan p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float sum = sum_quarters(s.sum[r]);
-      const float unit = Mfma<T>::kNarrow ? s.reach : 1.0f;
+      const float unit = Mfma<T>::kNarrow ? inverse_power(s.by_reach[r]) : 1.0f;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < 4; ++k)

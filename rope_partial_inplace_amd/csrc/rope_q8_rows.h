@@ -216,7 +216,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         q[i] = some ? as_operand(*reinterpret_cast<const uint4 *>(from + 16 * i)) : s16x8{};
     }
     float top = kNegInf, sum = 0.0f;
-    float reach = 0x1p-120f, by_reach = 0x1p120f;  // as in StateQ8
+    float by_reach = kFirstByReach;  // as in StateQ8
     f32x16 o[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d) o[d] = f32x16{};
@@ -297,7 +297,20 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         float most = 0.0f;
         if constexpr (Mfma<T>::kNarrow) {
           most = fabsf(at.v_scale[lane % ScalesOf<D, MODE>::COUNT]);
-          raise |= most > reach;
+          if (masked) {  // of the lane's tokens that its row sees
+            asm volatile("");
+            most = 0.0f;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+              f32x4 f[4];
+              scales_at<D, MODE>(at.v_scale, kb, lane, f);
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (t0 + kb * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < limit)
+                  most = fmaxf(most, fabsf(f[r / 4][r % 4]));
+            }
+          }
+          raise |= most * by_reach > 1.0f;
         }
         if (__any(raise)) {
           float f = 1.0f;
@@ -307,11 +320,13 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
           }
           sum *= f;
           if constexpr (Mfma<T>::kNarrow) {
-            for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-            const float now = most > reach ? reach_above(most) : reach;
-            f *= reach * inverse_power(now);
-            reach = now;
-            by_reach = inverse_power(now);
+            if (masked)
+              most = max_halves(most);
+            else
+              for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+            const float by = most * by_reach > 1.0f ? inverse_power(reach_above(most)) : by_reach;
+            f *= by * inverse_power(by_reach);
+            by_reach = by;
           }
 #pragma unroll
           for (int d = 0; d < DB; ++d) o[d] *= f;
@@ -371,7 +386,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
 
     // ---- the piece's result ----
     if (some) {
-      const float unit = Mfma<T>::kNarrow ? reach : 1.0f;
+      const float unit = Mfma<T>::kNarrow ? inverse_power(by_reach) : 1.0f;
       if (g.whole()) {
         const int64_t row = output_row(p, g, g.set, sq.first, m);
         const bool any = sum > 0.0f || sum != sum;  // a row that sees nothing gets zeros

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import rope_partial_inplace_amd as ra
-from q8_ref import E4M3, I8
+from q8_ref import E4M3, I8, quantized_cache, rows_of
 from test_gpu_q8_append import BF16, DEV, F16, F32, RAGGED, append, same, setup
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +87,99 @@ def test_fork_copies_the_tokens_of_every_layout(tail, listed):
                 n = min(PAGE, lens[p] - j * PAGE)
                 a, b = (tokens(y, n).float() for y in (x[row[j]], was[table[p][j]]))
                 assert torch.equal(a, b), (what, n)
+
+
+# ---- attention: what a query does not see ------------------------------------------------------------
+
+def packed(dtype, codes, D, heads, group, lens, counts, page, block, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    n_pages = [-(-n // page) for n in lens]
+    table = torch.zeros(len(lens), max(n_pages), dtype=torch.int64, device=DEV)
+    order, at = torch.randperm(sum(n_pages), generator=g, device=DEV), 0
+    for b, c in enumerate(n_pages):
+        table[b, :c] = order[at:at + c]
+        at += c
+    kc, ks = quantized_cache(g, codes, sum(n_pages), page, block, heads, D)
+    vc, vs = quantized_cache(g, codes, sum(n_pages), page, block, heads, D)
+    q = torch.randn((sum(counts), heads * group, D), generator=g, device=DEV).to(dtype)
+    ints = lambda x: torch.tensor(x, dtype=torch.int64, device=DEV)
+    offsets = ints([0] + torch.tensor(counts).cumsum(0).tolist())
+    return dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, table=table, lens=ints(lens), offsets=offsets)
+
+
+def attend(s, **other):
+    s = {**s, **other}
+    out, lse = ra.rope_attention_paged_q8(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"],
+                                          s["q"].shape[2] ** -0.5, query_offsets=s["offsets"])
+    torch.cuda.synchronize()
+    return out, lse
+
+
+# rows of a key head: 16, 32, and the kernel for more
+ROWS = [(4, [4, 3, 4]), (8, [2, 1, 2]), (4, [8, 5, 8]), (16, [2, 2, 2]), (4, [40, 37, 70]), (1, [150, 200, 33])]
+PLACES = [(16, 16), (16, 4), (16, 1), (64, 2), (5, 5), (5, 1)]  # page, block: scales of runs, of tokens; any page
+
+
+@pytest.mark.parametrize("page,block", PLACES)
+@pytest.mark.parametrize("group,counts", ROWS)
+@pytest.mark.parametrize("dtype,codes,D", [(F16, I8, 128), (F16, E4M3, 64), (F16, E4M3, 256), (BF16, I8, 128)])
+def test_scales_of_later_tokens_reach_no_query(dtype, codes, D, group, counts, page, block):
+    """Values' scales of blocks that a query does not see, infinite or 2^40 times as large: not one bit of its
+    output changes."""
+    lens = [c + n for c, n in zip(counts, (203, 330, 64))]
+    s = packed(dtype, codes, D, 2, group, lens, counts, page, block)
+    want, want_lse = attend(s)
+    touched = 0
+    for factor in (math.inf, 2.0 ** 40):
+        for back in (1, 2, 5):  # the poisoned block is that of the back-th token from the end
+            vs = s["vs"].clone()
+            same = torch.ones(sum(counts), dtype=torch.bool, device=DEV)
+            at = 0
+            for b, (n, c) in enumerate(zip(lens, counts)):
+                begin = max(0, n - back) // block * block
+                vs[s["table"][b, begin // page], begin % page // block] *= factor
+                for i in range(c):
+                    same[at + i] = n - c + 1 + i <= begin
+                at += c
+            out, lse = attend(s, vs=vs)
+            assert torch.equal(lse, want_lse)
+            assert torch.equal(out[same], want[same]), (factor, back)
+            assert not torch.equal(out[~same], want[~same])
+            touched += int(same.sum())
+    assert touched > 0 or block == 16
+
+
+@pytest.mark.parametrize("page,block", [(16, 4), (16, 1), (5, 1)])
+@pytest.mark.parametrize("group,count", [(4, 4), (4, 8), (4, 60)])
+@pytest.mark.parametrize("codes", [I8, E4M3])
+def test_float16_beside_growing_scales(codes, group, count, page, block):
+    """Values' scales that grow 2^30 fold over a sequence's last tokens: every query is within the bound (q8_ref.py)
+    that the scales it sees give."""
+    n, D, heads = 197 + count, 64, 2
+    s = packed(F16, codes, D, heads, group, [n], [count], page, block, seed=3)
+    t = torch.arange(n, device=DEV)
+    where, row = s["table"][0][t // page], t % page // block
+    grown = (t // block - (n - count) // block).clamp_min(0)
+    grown = (grown * 30.0 / grown.max()).round()
+    s["vs"].fill_(2.0 ** -24)
+    s["vs"][where, row] = (2.0 ** (grown - 24))[:, None].expand(-1, heads)
+    out, lse = attend(s)
+    kc, kf = rows_of(s["kc"], s["ks"], s["table"][0], n)
+    vc, vf = rows_of(s["vc"], s["vs"], s["table"][0], n)
+    scale, u, e = D ** -0.5, 2.0 ** -11, 2.0 ** -24
+    for i in range(count):
+        m = n - count + 1 + i
+        for h in range(heads * group):
+            k = h // group
+            q = s["q"][i, h].double()
+            logits = (kc[:m, k] @ q) * kf[:m, k] * scale
+            mag = ((kc[:m, k].abs() @ q.abs()) * kf[:m, k] * scale).max()
+            v = vc[:m, k] * vf[:m, k, None]
+            p = torch.softmax(logits, 0)
+            ds = (D + 8) * e * mag
+            dp = 2 * ds + (m + 10) * e
+            want = p @ v
+            bound = (u * want.abs() + (u + dp) * (p @ v.abs()) + 2.0 ** -25 +
+                     m * 2.0 ** -35 * vf[:m, k].max() * vc[:m, k].abs().max())
+            assert bool(((out[i, h].double() - want).abs() <= bound).all()), (i, h)
+            assert abs(lse[i, h].double() - logits.logsumexp(0)) <= ds + (m + 10) * e + 4 * e * logits.abs().max()
