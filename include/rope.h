@@ -411,10 +411,8 @@ int rope_append_paged_cache_q8(const rope_tensor *positions, const rope_tensor *
  * float32 until one rounding to the output's dtype; the weights p_j value_scale_j are rounded to the
  * dtype for the second product.  (F16: relative to the largest value scale that the query sees, so that
  * none leaves its range; a weight is off by half a step of its own, or 2^-35 of that scale.)  A query
- * that sees no token gets zeros and lse = -infinity.  Rows past len may hold anything: they reach no
- * result.  A token that a sequence's last query sees and an earlier one does not has weight 0 for the
- * earlier one, so a NaN among its value codes makes that query's output NaN too (its scales do not reach
- * it).
+ * that sees no token gets zeros and lse = -infinity.  Tokens that a query does not see reach nothing of
+ * its results, whatever their codes and scales: rows past len, and the tokens of later queries.
  *
  * query          [T, heads, D], F16 or BF16, D 64, 128 or 256, heads a multiple of Nk, unit inner
  *                stride, rows on 16-byte boundaries, any non-negative strides.

@@ -110,6 +110,31 @@ struct Operand<T, false> {
   }
 };
 
+// Values that are NaN.  A product makes a NaN of 0 times one, and a token's codes are an operand for all rows.  So
+// that a NaN stays with the rows that see its token, in tiles that some rows see in part its code becomes that
+// of -0 (and -0 that of 0, which no sum tells apart) before the product, and outputs become NaN by a
+// product that counts, for each of them, the NaN that its row sees.
+
+// Four e4m3 codes so; not 0 where one was a NaN (a size of 127).
+__device__ inline uint32_t mark_nans(uint32_t *w) {
+  const uint32_t size = *w & 0x7f7f7f7fu;
+  const uint32_t nans = (size + 0x01010101u) & 0x80808080u, some = (size + 0x7f7f7f7fu) & 0x80808080u;
+  *w = ((size | (*w & some)) & ~((nans >> 7) * 0xffu)) | nans;
+  return nans;
+}
+
+// An operand with 1 for each -0 of another and 0 elsewhere.
+template <typename T>
+__device__ inline s16x8 marked(s16x8 x) {
+  auto ones = [](uint32_t w) {
+    const uint32_t turned = w ^ 0x80008000u;
+    const uint32_t other = ((turned & 0x7fff7fffu) + 0x7fff7fffu) | turned;  // top bits: not a -0
+    return ((~other & 0x80008000u) >> 15) * (Mfma<T>::kNarrow ? 0x3c00u : 0x3f80u);
+  };
+  const uint4 w = __builtin_bit_cast(uint4, x);
+  return as_operand(make_uint4(ones(w.x), ones(w.y), ones(w.z), ones(w.w)));
+}
+
 // What a sequence asks for: its query rows (token by token, the heads of a group one after the other) in
 // tiles.  A tile's steps end with the last token that one of its rows sees, so of causal rows a later
 // tile has more steps; the k-th tile from the end and the k-th from the front make a pair, and all
@@ -377,6 +402,48 @@ __device__ __forceinline__ void score_tile(const KeysQ8<D, MODE> &k, const State
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (t0 + 16 * (j / 4) + 4 * g + j % 4 >= s.limit[r]) x[r][j / 4][j % 4] = kNegInf;
+  }
+}
+
+// Marks NaN among a tile's values; outputs of rows that see one become NaN.
+template <typename T, int D, int R, int MODE>
+__device__ __forceinline__ void part_nans(ValuesQ8<D, MODE> &v, StateQ8<T, D, R> &s, int32_t t0, int lane) {
+  uint32_t found = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) found |= mark_nans(&v.code[j][i]);
+  if (!__any(found != 0)) return;
+  s16x8 seen[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float one[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      one[j] = t0 + 16 * (j / 4) + 4 * (lane >> 4) + j % 4 < s.limit[r] ? 1.0f : 0.0f;
+    seen[r] = round8<T>(one);
+  }
+  auto count = [&](int n, const s16x8 &a) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const f32x4 nans = Mfma<T>::mul16(marked<T>(a), seen[r], f32x4{});
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s.o[r][n][k] = nans[k] > 0.0f ? __builtin_nanf("") : s.o[r][n][k];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = v.code[j][i];
+    s16x8 a, b;
+    Operand<T, true>::template columns<false>(c, &a, &b);
+    count(4 * i, a);
+    count(4 * i + 1, b);
+    Operand<T, true>::template columns<true>(c, &a, &b);
+    count(4 * i + 2, a);
+    count(4 * i + 3, b);
   }
 }
 
@@ -721,6 +788,8 @@ attention_q8_kernel(AttnQ8Plan p) {
     const int32_t key_head = g.set * p.abreast + own;
     // fewest tokens that a row sees
     const int32_t floor = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0)));
+    // where rows may differ in the tokens that they see
+    const int32_t apart = floor < g.most ? floor : 0x7fffffff;
 
     StateQ8<T, D, R> s;
 #pragma unroll
@@ -759,6 +828,12 @@ attention_q8_kernel(AttnQ8Plan p) {
         while (true) {  // ends: t0 grows
           const int32_t t1 = t0 + step < end ? t0 + step : t0;
           next = at(t1);
+          if constexpr (E4M3) {
+            if (t0 + kTile > apart) {
+              asm volatile("");
+              part_nans<T, D, R>(v, s, t0, lane);
+            }
+          }
           f32x4 x[R][2];
           score_tile<T, D, R, E4M3, MODE>(k, s, t0, floor, p.scale_log2, lane, x);
           load_keys<D, MODE>(p, next, t1, last, head, lane, k);

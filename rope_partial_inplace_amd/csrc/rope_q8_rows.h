@@ -64,6 +64,7 @@ struct RowsLds {
   struct Buffer {
     char k[RowsShape<D>::PANELS * RowsShape<D>::PANEL], v[RowsShape<D>::PANELS * RowsShape<D>::PANEL];
     float k_scale[RowsShape<D>::TILE], v_scale[RowsShape<D>::TILE];
+    int32_t nans[kAttnWaves];  // whether a wavefront's tokens have values that are NaN (e4m3, `look` of put)
   };
   Buffer buffer[2];
   ShareLds share;
@@ -143,15 +144,26 @@ __device__ __forceinline__ void fetch(const AttnQ8Plan &p, const TokensQ8<MODE> 
   stage.scale = *scale;
 }
 
-// Into a buffer, as operands.
+// Into a buffer, as operands.  look: some rows see the tile in part, so that NaN among its values are marked.
 template <typename T, int D, bool E4M3, int MODE>
-__device__ __forceinline__ void put(const StageQ8<D> &x, int tid, float scale_log2,
+__device__ __forceinline__ void put(StageQ8<D> &x, int tid, float scale_log2, bool look,
                                     typename RowsLds<D>::Buffer &to) {
   using S = RowsShape<D>;
   using Op = Operand<T, E4M3>;
   const int wave = tid / 64, lane = tid & 63;
   const uint32_t row = uint32_t(S::run(wave) + S::token(wave, lane));
   const uint32_t piece = uint32_t(S::piece(lane));  // four to a panel's row, two chunks each
+  if constexpr (E4M3) {
+    if (look) {
+      asm volatile("");
+      uint32_t nans = 0;
+#pragma unroll
+      for (int i = 0; i < S::BYTES / 16; ++i)
+        nans |= mark_nans(&x.v[i].x) | mark_nans(&x.v[i].y) | mark_nans(&x.v[i].z) | mark_nans(&x.v[i].w);
+      const bool any = __any(nans != 0);
+      if (lane == 0) to.nans[wave] = any;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < S::BYTES / 16; ++i)
 #pragma unroll
@@ -206,6 +218,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
     const int32_t tok = int32_t(div_by(p.div_group, uint32_t(g.row0 + (some ? m : 0))));
     const int32_t limit = some ? g.hidden + tok : 0;
     const int32_t floor = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0 + min(wave * 32, g.live - 1))));
+    const int32_t lowest = g.hidden + int32_t(div_by(p.div_group, uint32_t(g.row0)));  // of all wavefronts
     s16x8 q[D / 16];
     {
       const int32_t h = g.set * p.group + g.row0 + (some ? m : 0) - tok * p.group;
@@ -232,7 +245,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
       StageQ8<D> stage;
       fetch<D, MODE>(p, at_tile(t0), head, wave, lane, stage);
       lds_barrier();  // what the last piece read of the buffers
-      put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, lds.buffer[0]);
+      put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, t0 + TILE > lowest, lds.buffer[0]);
       int32_t t1 = t0 + TILE < end ? t0 + TILE : t0;
       TokensQ8<MODE> tokens = at_tile(t1);
       for (int32_t n = 0;; ++n) {  // ends: t0 grows
@@ -246,6 +259,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         // Opaque: the places that follow from these are worked out again in every step.  Kept from step to
         // step they would take registers that the products need.
         asm volatile("" : "+v"(keys_at), "+v"(values_at));
+        const bool masked = t0 + TILE > floor;
         // S^T
         f32x16 x[KB];
 #pragma unroll
@@ -278,7 +292,6 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) x[kb][r] *= f[r / 4][r % 4];
         }
-        const bool masked = t0 + TILE > floor;
         if (masked) {
           asm volatile("");
 #pragma unroll
@@ -376,8 +389,33 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
           __builtin_amdgcn_sched_barrier(0);
         }
         __builtin_amdgcn_s_setprio(0);
+        if constexpr (E4M3) {
+          if (t0 + TILE > lowest) {  // put has looked
+            asm volatile("");
+            if (__any(at.nans[lane % kAttnWaves])) {  // outputs of rows that see a token with a NaN
+#pragma unroll
+              for (int d = 0; d < DB; ++d) {
+                f32x16 nans = {};
+#pragma unroll
+                for (int k = 0; k < 2 * KB; ++k) {
+                  const char *from = at.v + d / 2 * S::PANEL + k * 2048;
+                  const uint32_t v = values_at ^ (d % 2 * 64u);
+                  const s16x8 a = join(read_transposed(from + v), read_transposed(from + (v ^ kEightRows)));
+                  float one[8];
+#pragma unroll
+                  for (int r = 0; r < 8; ++r)
+                    one[r] = t0 + k * 16 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4 < limit ? 1.0f : 0.0f;
+                  nans = Mfma<T>::mul(marked<T>(a), round8<T>(one), nans);
+                  __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] = nans[r] > 0.0f ? __builtin_nanf("") : o[d][r];
+              }
+            }
+          }
+        }
         if (t1 == t0) break;
-        put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, lds.buffer[~n & 1]);
+        put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, t1 + TILE > lowest, lds.buffer[~n & 1]);
         t0 = t1;
         t1 = t2;
       }

@@ -183,3 +183,63 @@ def test_float16_beside_growing_scales(codes, group, count, page, block):
                      m * 2.0 ** -35 * vf[:m, k].max() * vc[:m, k].abs().max())
             assert bool(((out[i, h].double() - want).abs() <= bound).all()), (i, h)
             assert abs(lse[i, h].double() - logits.logsumexp(0)) <= ds + (m + 10) * e + 4 * e * logits.abs().max()
+
+
+def nan_where_seen(s, want, poisoned, lens, counts, block, D):
+    """(mask of the output's elements that a NaN code of the values reaches) for poisoned (sequence, token, head,
+    element) quadruples."""
+    heads = s["kc"].shape[2]
+    group = s["q"].shape[1] // heads
+    reach = torch.zeros_like(want, dtype=torch.bool)
+    for b, token, h, d in poisoned:
+        at = sum(counts[:b])
+        for i in range(counts[b]):
+            if token < lens[b] - counts[b] + 1 + i:
+                reach[at + i, h * group:(h + 1) * group, d] = True
+    return reach
+
+
+@pytest.mark.parametrize("page,block", PLACES)
+@pytest.mark.parametrize("group,counts", ROWS)
+@pytest.mark.parametrize("dtype,D", [(F16, 128), (BF16, 64), (BF16, 128), (BF16, 256), (F16, 256)])
+def test_nan_codes_of_later_tokens_reach_no_query(dtype, D, group, counts, page, block):
+    """Values' codes that are NaN: those elements of the queries that see the token are NaN, and not one bit of
+    anything else changes."""
+    lens = [c + n for c, n in zip(counts, (203, 330, 64))]
+    s = packed(dtype, E4M3, D, 2, group, lens, counts, page, block, seed=5)
+    want, want_lse = attend(s)
+    for backs in ([1], [2], [5, 1], list(range(1, 9)), [70]):
+        poisoned = [(b, n - back, (b + back) % 2, d) for b, n in enumerate(lens) for back in backs
+                    if back <= n for d in ((7 * back) % D, D - 1 - back % D, (13 * back + b) % D)]
+        vc = s["vc"].clone()
+        raw = vc.view(torch.uint8)
+        for k, (b, t, h, d) in enumerate(poisoned):
+            raw[s["table"][b, t // page], t % page, h, d] = 0x7f | (k & 1) << 7
+        out, lse = attend(s, vc=vc)
+        reach = nan_where_seen(s, want, poisoned, lens, counts, block, D)
+        assert torch.equal(lse, want_lse)
+        assert bool(torch.isnan(out[reach]).all()) and bool(reach.any()), backs
+        assert torch.equal(out[~reach], want[~reach]), backs
+
+
+@pytest.mark.parametrize("group,count", [(4, 4), (4, 8), (4, 50)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_one_bad_value_of_a_piece(bad, dtype, group, count):
+    """A non-finite value element, appended and attended to with the queries before and behind it."""
+    n, D, at = 150 + count, 128, count // 2
+    s = packed(dtype, E4M3, D, 2, group, [n], [count], 16, 16, seed=7)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    k, v = (torch.randn((count, 2, D), generator=g, device=DEV).to(dtype) for _ in range(2))
+    cs = torch.cat([torch.ones(300, 32, device=DEV), torch.zeros(300, 32, device=DEV)], 1).to(dtype)
+    results = []
+    for x in (0.0, bad):
+        v[at, 1, 77] = x
+        c = {m: s[m].clone() for m in ("kc", "vc", "ks", "vs")}
+        ra.rope_append_paged_cache_q8(torch.arange(n - count, n, device=DEV), k, v, c["kc"], c["vc"], c["ks"], c["vs"],
+                                      s["table"], s["lens"], cs)
+        results.append(attend(s, **c)[0])
+    clean, out = results
+    hit = torch.zeros_like(clean, dtype=torch.bool)
+    hit[at:, group:, 77] = True
+    assert bool(torch.isnan(out[hit]).all()) and torch.equal(out[~hit], clean[~hit])
