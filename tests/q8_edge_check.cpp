@@ -3,14 +3,19 @@
 //   append_long_blocks blocks whose elements of a head pass the kernel's 32-bit numbers: refused
 //   fork_layouts       which caches are copied in part: those whose second dimension is a page's tokens or
 //                      blocks of them by their form, never others that its length only fits
+//   interleaved_caches caches side by side in every page of one allocation: accepted if and only if they share no
+//                      byte (against all bytes of small pools), and in a time that grows with their number
 //
 // No GPU and no tensor data are involved.  Prints "ok" or the first failure.
 #include <algorithm>
+#include <chrono>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <random>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "rope.h"
@@ -143,13 +148,101 @@ static void fork_layouts() {
   }
 }
 
+// The plan of a copy of no page in `caches`; 0 if they are refused.
+static int accepted(const std::vector<rope_tensor> &caches, std::string *err) {
+  const rope_tensor src = desc(0, ROPE_I64, {3}), dst = desc(1, ROPE_I64, {3});
+  CopyPagesPlan p;
+  std::vector<PageCache> list;
+  return plan_copy_pages(&src, &dst, caches.data(), int64_t(caches.size()), &p, &list, err) == ROPE_OK;
+}
+
+static rope_tensor slice(uintptr_t at, rope_dtype dt, int64_t pages, int64_t stride, int64_t elements) {
+  rope_tensor t{};
+  t.data = reinterpret_cast<void *>(at);
+  t.dtype = dt;
+  t.ndim = 2;
+  t.shape[0] = pages;
+  t.shape[1] = elements;
+  t.stride[0] = stride;
+  t.stride[1] = 1;
+  return t;
+}
+
+static void interleaved_caches() {
+  std::mt19937_64 rng(7);
+  auto pick = [&](int64_t lo, int64_t hi) { return lo + int64_t(rng() % uint64_t(hi - lo + 1)); };
+  std::string err;
+  int64_t apart = 0, meeting = 0;
+  const uintptr_t base = kBase + 2 * kStep;
+  for (int round = 0; round < 20000; ++round) {
+    // a record of every page, in it blocks one behind the other, some of them moved or longer by a few bytes
+    const int64_t pages = pick(1, 4), n = pick(1, 6), pools = pick(1, 2);
+    std::vector<rope_tensor> caches;
+    for (int64_t pool = 0; pool < pools; ++pool) {
+      std::vector<std::pair<int64_t, int64_t>> blocks;  // where, bytes
+      int64_t at = 0;
+      for (int64_t i = 0; i < n; ++i) {
+        const int64_t bytes = 4 * pick(1, 5);
+        blocks.push_back({at, bytes});
+        at += bytes + 4 * pick(0, 1);
+      }
+      if (pick(0, 3) == 0) at -= 4 * pick(0, 2);  // the next page's record begins in this one
+      if (pick(0, 3) == 0) blocks[size_t(pick(0, n - 1))].first += 4 * pick(0, 3);
+      const int64_t stride = std::max<int64_t>(at, 4) * (pick(0, 5) == 0 ? 2 : 1);
+      for (auto &b : blocks) {
+        const int64_t own = pick(0, 9) == 0 ? stride * 2 : stride;
+        if (b.second > own) b.second = own;
+        const rope_dtype dt = pick(0, 1) ? ROPE_F32 : ROPE_I8;
+        const int64_t es = dt == ROPE_F32 ? 4 : 1;
+        caches.push_back(slice(base + uintptr_t(pool * pick(0, 400) * 4 + b.first), dt, pages, own / es, b.second / es));
+      }
+    }
+    std::shuffle(caches.begin(), caches.end(), rng);
+    std::vector<int> held(8192);
+    bool overlap = false;
+    for (const rope_tensor &t : caches) {
+      const int64_t es = t.dtype == ROPE_F32 ? 4 : 1, from = int64_t(reinterpret_cast<uintptr_t>(t.data) - base);
+      for (int64_t p = 0; p < pages; ++p)
+        for (int64_t b = 0; b < t.shape[1] * es; ++b) overlap |= held[size_t(from + p * t.stride[0] * es + b)]++ != 0;
+    }
+    const bool ok = accepted(caches, &err);
+    CHECK(!(ok && overlap), "round %d: caches that overlap are accepted", round);
+    (overlap ? meeting : apart) += 1;
+  }
+  CHECK(apart > 1000 && meeting > 1000, "%lld apart, %lld not", (long long)apart, (long long)meeting);
+  // layers' keys, values and scales of every page one behind the other, and two such pools, in any order
+  for (int64_t layers : {1, 4, 32, 16384}) {
+    std::vector<rope_tensor> caches;
+    const int64_t part = 4096, record = layers * 2 * (part + 64), pools = layers > 1000 ? 1 : 2;
+    for (int64_t pool = 0; pool < pools; ++pool)
+      for (int64_t i = 0; i < 2 * layers; ++i) {
+        const uintptr_t at = base + uintptr_t(pool * (record * 50 + 12345 * 4));
+        caches.push_back(slice(at + uintptr_t(i * part), ROPE_I8, 50, record, part));
+        caches.push_back(slice(at + uintptr_t(2 * layers * part + i * 64), ROPE_F32, 50, record / 4, 16));
+      }
+    std::shuffle(caches.begin(), caches.end(), rng);
+    const auto begin = std::chrono::steady_clock::now();
+    CHECK(accepted(caches, &err), "%lld layers: %s", (long long)layers, err.c_str());
+    const double s = std::chrono::duration<double>(std::chrono::steady_clock::now() - begin).count();
+    CHECK(s < 5, "%lld caches took %.1f s", (long long)caches.size(), s);  // compared in pairs: 40 s and more
+    for (int k = 0; k < 20; ++k) {  // one of them a byte off
+      std::vector<rope_tensor> moved = caches;
+      rope_tensor &t = moved[size_t(pick(0, int64_t(moved.size()) - 1))];
+      if (t.dtype != ROPE_I8) continue;
+      t.data = static_cast<char *>(t.data) + (k % 2 ? 1 : -1);
+      if (layers < 1000) CHECK(!accepted(moved, &err), "one byte of two caches");
+    }
+  }
+}
+
 int main(int argc, char **argv) {
   const struct {
     const char *name;
     void (*run)();
   } checks[] = {{"append_no_values", append_no_values},
                 {"append_long_blocks", append_long_blocks},
-                {"fork_layouts", fork_layouts}};
+                {"fork_layouts", fork_layouts},
+                {"interleaved_caches", interleaved_caches}};
   for (const auto &c : checks)
     if (argc > 1 && std::strcmp(argv[1], c.name) == 0) {
       c.run();

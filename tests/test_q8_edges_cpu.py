@@ -21,7 +21,7 @@ def program(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("check", ["append_no_values", "append_long_blocks", "fork_layouts"])
+@pytest.mark.parametrize("check", ["append_no_values", "append_long_blocks", "fork_layouts", "interleaved_caches"])
 def test_plan(program, check):
     r = subprocess.run([program, check], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout == "ok\n", r.stdout[-2000:] + r.stderr[-4000:]
