@@ -64,10 +64,10 @@ struct RowsLds {
   struct Buffer {
     char k[RowsShape<D>::PANELS * RowsShape<D>::PANEL], v[RowsShape<D>::PANELS * RowsShape<D>::PANEL];
     float k_scale[RowsShape<D>::TILE], v_scale[RowsShape<D>::TILE];
-    int32_t nans[kAttnWaves];  // whether a wavefront's tokens have values that are NaN (e4m3, `look` of put)
   };
   Buffer buffer[2];
   ShareLds share;
+  int32_t nans[2][kAttnWaves];  // of each buffer: whether a wavefront's tokens have NaN values (e4m3, `look` of put)
 };
 
 // Where a wavefront's tokens of a tile lie; tokens past the last one repeat it.  Pages of whole runs of 16
@@ -147,7 +147,7 @@ __device__ __forceinline__ void fetch(const AttnQ8Plan &p, const TokensQ8<MODE> 
 // Into a buffer, as operands.  look: some rows see the tile in part, so that NaN among its values are marked.
 template <typename T, int D, bool E4M3, int MODE>
 __device__ __forceinline__ void put(StageQ8<D> &x, int tid, float scale_log2, bool look,
-                                    typename RowsLds<D>::Buffer &to) {
+                                    typename RowsLds<D>::Buffer &to, int32_t *nans) {
   using S = RowsShape<D>;
   using Op = Operand<T, E4M3>;
   const int wave = tid / 64, lane = tid & 63;
@@ -156,12 +156,12 @@ __device__ __forceinline__ void put(StageQ8<D> &x, int tid, float scale_log2, bo
   if constexpr (E4M3) {
     if (look) {
       asm volatile("");
-      uint32_t nans = 0;
+      uint32_t found = 0;
 #pragma unroll
       for (int i = 0; i < S::BYTES / 16; ++i)
-        nans |= mark_nans(&x.v[i].x) | mark_nans(&x.v[i].y) | mark_nans(&x.v[i].z) | mark_nans(&x.v[i].w);
-      const bool any = __any(nans != 0);
-      if (lane == 0) to.nans[wave] = any;
+        found |= mark_nans(&x.v[i].x) | mark_nans(&x.v[i].y) | mark_nans(&x.v[i].z) | mark_nans(&x.v[i].w);
+      const bool any = __any(found != 0);
+      if (lane == 0) nans[wave] = any;
     }
   }
 #pragma unroll
@@ -245,7 +245,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
       StageQ8<D> stage;
       fetch<D, MODE>(p, at_tile(t0), head, wave, lane, stage);
       lds_barrier();  // what the last piece read of the buffers
-      put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, t0 + TILE > lowest, lds.buffer[0]);
+      put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, t0 + TILE > lowest, lds.buffer[0], lds.nans[0]);
       int32_t t1 = t0 + TILE < end ? t0 + TILE : t0;
       TokensQ8<MODE> tokens = at_tile(t1);
       for (int32_t n = 0;; ++n) {  // ends: t0 grows
@@ -259,7 +259,6 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         // Opaque: the places that follow from these are worked out again in every step.  Kept from step to
         // step they would take registers that the products need.
         asm volatile("" : "+v"(keys_at), "+v"(values_at));
-        const bool masked = t0 + TILE > floor;
         // S^T
         f32x16 x[KB];
 #pragma unroll
@@ -292,6 +291,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) x[kb][r] *= f[r / 4][r % 4];
         }
+        const bool masked = t0 + TILE > floor;
         if (masked) {
           asm volatile("");
 #pragma unroll
@@ -392,7 +392,7 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
         if constexpr (E4M3) {
           if (t0 + TILE > lowest) {  // put has looked
             asm volatile("");
-            if (__any(at.nans[lane % kAttnWaves])) {  // outputs of rows that see a token with a NaN
+            if (__any(lds.nans[n & 1][lane % kAttnWaves])) {  // outputs of rows that see a token with a NaN
 #pragma unroll
               for (int d = 0; d < DB; ++d) {
                 f32x16 nans = {};
@@ -415,7 +415,8 @@ attention_q8_rows_kernel(AttnQ8Plan p) {
           }
         }
         if (t1 == t0) break;
-        put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, t1 + TILE > lowest, lds.buffer[~n & 1]);
+        put<T, D, E4M3, MODE>(stage, tid, p.scale_log2, t1 + TILE > lowest, lds.buffer[~n & 1],
+                              lds.nans[~n & 1]);
         t0 = t1;
         t1 = t2;
       }
