@@ -422,7 +422,8 @@ int rope_append_paged_cache_q8(const rope_tensor *positions, const rope_tensor *
  * page_table, seq_lens, query_offsets, out [T, heads, D], lse, scale and workspace: as in
  *                rope_latent_attention_paged (pages out of range are clamped), the workspace of at
  *                least rope_attention_paged_q8_workspace() bytes.
- * Results do not depend on timing: every sum is taken in a fixed order.
+ * Results do not depend on timing: every sum is taken in a fixed order.  Tiles are sized by the mean
+ * number of queries of a call: sequences that decode and long pieces of prompts are faster in two calls.
  */
 int64_t rope_attention_paged_q8_workspace(int64_t num_tokens, int64_t num_heads,
                                           int64_t num_key_heads, int64_t head_size,

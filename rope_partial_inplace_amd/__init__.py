@@ -628,7 +628,8 @@ def rope_attention_paged_q8(query, key_cache, value_cache, key_scales, value_sca
     query_offsets [B + 1] are int64; without offsets every sequence has T / B queries.  Query i of n
     sees the cached tokens below seq_len - n + 1 + i.  Returns (out [T, heads, D], lse [T, heads]
     float32); rows outside all sequences are not written, so pass out and lse where they are to be
-    defined."""
+    defined.  Tiles are sized by the mean number of queries: sequences that decode and long pieces of
+    prompts are faster in two calls than in one.  Not recorded by autograd."""
     import torch
     dev = _device_index((query, key_cache, value_cache, key_scales, value_scales, page_table,
                          seq_lens, query_offsets, out, lse))

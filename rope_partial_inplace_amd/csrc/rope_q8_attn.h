@@ -14,8 +14,8 @@
 // of a workgroup take up to four key heads of the same tokens; those of one head, each of which
 // takes every n-th 32 tokens, join their sums at the end.
 //
-// Measured with 8 key heads of 128: 64 sequences of 200-9000 tokens 62.5 us (284 MB), of 9000 with 4 key heads
-// of 256 201 us (5.9 TB/s), six of 60-131k tokens and a scale for each 254 us (5.7 TB/s).
+// Measured with 8 key heads of 128: 64 sequences of 200-9000 tokens 63 us (284 MB), of 9000 201 us
+// (5.9 TB/s), six of 60-131k tokens and a scale for each 255 us (5.6 TB/s).
 //
 // Layout (16x16x32 products, lane l = 16 g + c):
 //   S^T = K Q^T: A[key c][8 d], lane's d = g D / 4 + 16 i + 8 e + 0..7 for product (i, e): 16 bytes a load

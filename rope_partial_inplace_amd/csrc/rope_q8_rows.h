@@ -8,9 +8,10 @@
 // products, so that a lane owns a query row and P goes from one to the other in registers.
 // Scales wait, as in the other kernel: keys' multiply the scores, values' the weights.
 //
-// 4 x 4096 prompt tokens of 32 heads of 128, 8 key heads: 685 us, 0.80 PFLOP/s.  The vector units work 0.61 of the
-// cycles (of 327 instructions a step 96 turn codes into operands, 161 are the softmax's), the matrix units 0.33:
-// the two wavefronts of a SIMD rarely need them at the same time, and what is left is not idle.
+// 4 x 4096 prompt tokens of 32 heads of 128, 8 key heads: 762 us a launch (725-790), 719 a call back to back,
+// 0.72-0.77 PFLOP/s.  The vector units work 0.61 of the cycles (of 327 instructions a step 96 turn codes into
+// operands, 161 are the softmax's), the matrix units 0.33: the two wavefronts of a SIMD rarely need them at the same
+// time, and what is left is not idle.
 #pragma once
 
 #include "rope_q8_attn.h"
@@ -29,8 +30,8 @@ struct RowsShape {
   // A wavefront takes tokens of 16 from run(wave) on (8 where a tile has 32); a lane one of them, and
   // every THREADS-th 16 codes from 16 piece() on.  Eight lanes write operands to LDS at a time: two tokens 8
   // apart, whose chunks of half a row of a panel lie in different banks.  (With neighbouring tokens, and a lane's
-  // codes side by side, four met in a bank: 0.22 of the cycles were such conflicts, 4 x 4096 tokens of 32
-  // heads took 742 us, not 685.)
+  // codes side by side, four met in a bank: 0.22 of the cycles were such conflicts, and 4 x 4096 tokens of 32
+  // heads took 1.82 M cycles, not 1.60 M.)
   __device__ static int run(int wave) { return D == 256 ? wave / 2 * 16 : wave * 16; }
   __device__ static int token(int wave, int lane) {
     const int x = lane >> 2;

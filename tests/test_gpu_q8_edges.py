@@ -243,3 +243,34 @@ def test_one_bad_value_of_a_piece(bad, dtype, group, count):
     hit = torch.zeros_like(clean, dtype=torch.bool)
     hit[at:, group:, 77] = True
     assert bool(torch.isnan(out[hit]).all()) and torch.equal(out[~hit], clean[~hit])
+
+
+def test_whole_pages_of_other_orders():
+    """Copies, forks and compactions of caches given as `whole`, whose pages are dense in another order."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    ints = lambda x: torch.tensor(x, dtype=torch.int64, device=DEV)
+    base = [torch.randint(0, 100, (12, PAGE, 3, 8), generator=g, device=DEV, dtype=torch.int8),
+            torch.rand((12, 2, PAGE, 4), generator=g, device=DEV)]
+    views = [base[0].permute(0, 3, 1, 2), base[1][:, 1], base[1][:, 0].transpose(1, 2)]
+    handle = ra.PageCaches([], whole=views)
+    want = [x.clone() for x in base]
+
+    def move(pairs):
+        was = [w.clone() for w in want]
+        for w, x in zip(want, was):
+            for a, b in pairs:
+                w[b] = x[a]
+
+    ra.rope_copy_pages(ints([3, 5]), ints([4, 9]), handle)
+    move([(3, 4), (5, 9)])
+    # pages 6 and 2 of one sequence, whose tail is copied to page 0
+    refs = [0, 1, 1, 1, 1, 1, 1, 0, 0, 0, 1, 0]
+    rows, lens, counts, _ = ra.rope_fork_pages(ints([[6, 2]]), ints([PAGE + 3]), ints([0, 0]), ints(refs), PAGE, handle)
+    move([(2, 0)])
+    assert rows.tolist() == [[6, 2], [6, 0]]
+    rows, counts, _, live = ra.rope_compact_pages(rows, counts, handle)
+    move([(10, 7)])
+    assert live.tolist() == [8] and rows.tolist() == [[6, 2], [6, 0]]
+    torch.cuda.synchronize()
+    for x, w in zip(base, want):
+        assert torch.equal(x, w)
